@@ -30,7 +30,8 @@
  *    With kv_dtype LAZY_FP8_E4M3 (the decodes: lazy_attn_decode, _noalloc and
  *    lazy_attn_decode_shared) the pools hold OCP e4m3 codes and the products take
  *    f16 operands (every e4m3 value is exact in f16), with fp32 accumulation and
- *    softmax.
+ *    softmax. With kv_dtype LAZY_INT4 (the same calls) the pools hold int4 records
+ *    (see "int4 pools"), the products take the codes and f16 queries and weights.
  *
  * Layout (one layer)
  * ------------------
@@ -81,7 +82,7 @@ typedef enum {
   LAZY_ERR_DEVICE = 6       /* the device status word reported a fault */
 } lazy_status;
 
-typedef enum { LAZY_F32 = 0, LAZY_BF16 = 1, LAZY_FP8_E4M3 = 2 } lazy_dtype;
+typedef enum { LAZY_F32 = 0, LAZY_BF16 = 1, LAZY_FP8_E4M3 = 2, LAZY_INT4 = 3 } lazy_dtype;
 
 /* Bits of the per-device status word. */
 #define LAZY_DEV_BAD_BLOCK_ID 0x1u /* a word's phys_id >= num_pool_blocks (block skipped) */
@@ -120,8 +121,13 @@ typedef struct {
                                  Only lazy_attn_decode (and _noalloc) and lazy_attn_decode_shared
                                  with dtype LAZY_BF16 and head_dim 128 take it; the ALiBi calls,
                                  the prefill and the materialiser return LAZY_ERR_UNSUPPORTED.
-                                 Pools 16-byte aligned. */
-  float k_scale;              /* FP8 dequantisation scales: finite, > 0; 0 selects 1 */
+                                 Pools 16-byte aligned.
+                                 LAZY_INT4: the pools hold int4 records ("int4 pools"
+                                 below). The same decodes take it with dtype LAZY_BF16 and
+                                 head_dim 64 or 128, and refuse it where they refuse e4m3.
+                                 lazy_attn_cache_write and _read take every kind of pool */
+  float k_scale;              /* FP8 dequantisation scales: finite, > 0; 0 selects 1.
+                                 LAZY_INT4: 0 or 1 (its scales are in the records) */
   float v_scale;
 } lazy_attn_params;
 
@@ -461,6 +467,58 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
                     const uint32_t *block_words_pf, const int32_t *seq_lens_pf, void *out_pf, const void *k_pool,
                     const void *v_pool, const void *rope_table, void *workspace, size_t workspace_bytes,
                     lazy_stream_t stream);
+
+/* ---------------------------------------------------------------- rows into the pools, blocks out of them
+ * The pools of every other call are filled and read back with two calls.
+ *
+ * int4 pools (kv_dtype LAZY_INT4): uint8 [num_pool_blocks][Hkv][record]; a record of
+ * lazy_attn_pool_record_bytes(p) bytes holds the 16 tokens of one block for one KV head
+ * (head_dim 128: 1152 bytes, 4.5 bits an element; 64: 576). With G = head_dim / 64
+ * groups of 64 consecutive dims per token:
+ *   - first 16 rows of head_dim / 2 bytes: head_dim / 8 little-endian 32-bit words of
+ *     eight codes, lowest bits first; word j holds the dims 64 (j % G) + 8 (j / G) + 0..7.
+ *     K: row t is token t. V: token t is in row (t & 8) + 4 (t & 1) + ((t & 7) >> 1);
+ *   - then 32-bit words [16][G], in token order: the group's scale s (bf16, low half) and
+ *     zero z (bf16, high half). The value of a code c in 0..15 is s c + z.
+ * Written groups have z = their least value, s = (greatest - least) / 15 rounded to bf16
+ * (to nearest even) and c = (x - z) / s rounded to the nearest whole number (ties to
+ * even, at most 15); s = 0 and c = 0 where all are equal. A group with an infinity or a
+ * NaN has s = z = NaN. */
+
+/* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold
+ * num_pool_blocks * Hkv times that. 0 on bad params. */
+size_t lazy_attn_pool_record_bytes(const lazy_attn_params *p);
+
+/* Writes the K and V rows of num_tokens tokens into the pools, in the pools' type:
+ * row t of head h goes to row slots[t] % 16 of block slots[t] / 16. The rows are those
+ * that every other call reads: K already rotated at its document-local position, V as
+ * it is.
+ *   k, v       rows of head_dim contiguous elements of dtype; token t, head h at
+ *              element t * token_stride + h * head_stride (>= 0; any, so that slices of
+ *              a fused product need no copy; 16-byte aligned rows are read fastest)
+ *   slots      [num_tokens] int32 device: block * 16 + row, no two the same; negative:
+ *              the token is skipped (padding). A block id outside the pool sets
+ *              LAZY_DEV_BAD_BLOCK_ID and the token is skipped
+ *   k_pool, v_pool  16-byte aligned. Only the named slots change
+ * kv_dtype 0: copies. LAZY_FP8_E4M3 (dtype bf16, head_dim 64 or 128): x / k_scale (K) or
+ * x / v_scale (V), rounded to the nearest code (ties to even) and saturated at +-448, NaN
+ * kept; scales within 2^-100 .. 2^100. LAZY_INT4 (dtype bf16): as above.
+ * Slots that occur twice hold a mixture of the two tokens. num_tokens = 0 does nothing. */
+int lazy_attn_cache_write(const lazy_attn_params *p, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void *v, int64_t v_token_stride, int64_t v_head_stride, int32_t num_tokens,
+                          const int32_t *slots, void *k_pool, void *v_pool, lazy_stream_t stream);
+
+/* Reads blocks back: block block_ids[i] of the pools to block i of k_out and v_out, in
+ * dtype and the unquantised pools' layout [num_blocks][Hkv][16][head_dim] -- a pool for
+ * the calls that take no quantised one (lazy_attn_prefill, lazy_attn_mixed,
+ * lazy_attn_materialize). All 16 rows are converted, written or not.
+ *   block_ids  [num_blocks] int32 device; negative: block i of the outputs is left as it
+ *              is (padding). An id outside the pool sets LAZY_DEV_BAD_BLOCK_ID and
+ *              leaves it too. The same id may occur several times
+ *   k_out, v_out  16-byte aligned, not overlapping the pools
+ * Values: code * scale (e4m3), s c + z (int4), formed in fp32 and rounded to dtype. */
+int lazy_attn_cache_read(const lazy_attn_params *p, const void *k_pool, const void *v_pool, int32_t num_blocks,
+                         const int32_t *block_ids, void *k_out, void *v_out, lazy_stream_t stream);
 
 /* ---------------------------------------------------------------- eager materialisation (baseline)
  * The alternative the lazy method avoids ("Declaração do Problema"): a reused

@@ -164,8 +164,11 @@ bool encode_dec_q_map(CUtensorMap* m, const void* base, uint64_t B, int hq, int 
   return encode_cached(m, 3, base, dims, strides, box);
 }
 
-// The pools hold e4m3 codes (FP8 KV; only the per-sequence decode reads them).
+// The pools hold e4m3 codes (FP8 KV; only the decodes read them).
 static bool kv_fp8(const lazy_attn_params* p) { return p->kv_dtype == LAZY_FP8_E4M3 && p->dtype != LAZY_FP8_E4M3; }
+// The pools hold int4 records.
+static bool kv_int4(const lazy_attn_params* p) { return p->kv_dtype == LAZY_INT4; }
+static bool kv_quantised(const lazy_attn_params* p) { return kv_fp8(p) || kv_int4(p); }
 
 int check_params(const lazy_attn_params* p, Checked* c) {
   if (!p) return LAZY_ERR_INVALID_ARG;
@@ -181,8 +184,13 @@ int check_params(const lazy_attn_params* p, Checked* c) {
   if (!(p->sm_scale >= 0.f) || !std::isfinite(p->sm_scale)) return LAZY_ERR_INVALID_ARG;
   if (p->num_splits < 0) return LAZY_ERR_INVALID_ARG;
   if (p->key_positions != 0 && p->key_positions != 1) return LAZY_ERR_INVALID_ARG;
-  if (p->kv_dtype != 0 && p->kv_dtype != p->dtype && p->kv_dtype != LAZY_FP8_E4M3) return LAZY_ERR_UNSUPPORTED;
+  if (p->kv_dtype != 0 && p->kv_dtype != p->dtype && p->kv_dtype != LAZY_FP8_E4M3 &&
+      p->kv_dtype != LAZY_INT4)
+    return LAZY_ERR_UNSUPPORTED;
   if (!(p->k_scale >= 0.f) || !std::isfinite(p->k_scale) || !(p->v_scale >= 0.f) || !std::isfinite(p->v_scale))
+    return LAZY_ERR_INVALID_ARG;
+  // int4 records carry their own scales
+  if (kv_int4(p) && ((p->k_scale != 0.f && p->k_scale != 1.f) || (p->v_scale != 0.f && p->v_scale != 1.f)))
     return LAZY_ERR_INVALID_ARG;
   c->id_bits = p->id_bits ? p->id_bits : kDefaultIdBits;
   if (c->id_bits < 8 || c->id_bits > 24) return LAZY_ERR_INVALID_ARG;
@@ -391,6 +399,7 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   if (alibi && p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->dtype != LAZY_BF16 || p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_int4(p) && (p->dtype != LAZY_BF16 || alibi)) return LAZY_ERR_UNSUPPORTED;
   if (p->num_seqs == 0) return LAZY_OK;
   if (!q || !k_pool || !v_pool || !block_words || !seq_lens || !q_pos || !rope_table || !out)
     return LAZY_ERR_INVALID_ARG;
@@ -432,6 +441,8 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == LAZY_F32) {
     rc = launched(lazy::launch_decode_f32(a, p->lazy != 0, cs));
+  } else if (kv_int4(p)) {
+    rc = launched(lazy::launch_decode_int4(a, p->lazy != 0, cs));
   } else if (fp8) {
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)p->num_pool_blocks * p->num_kv_heads * lazy::kBlock;
@@ -481,14 +492,14 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
       (!seg_doc || !seg_len || !doc_block_indptr || !doc_blocks || !items))
     return LAZY_ERR_INVALID_ARG;
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
-  // e4m3 pools run on the mma.sync kernel (items of at most 64 rows) at every ratio
-  const int cap = kv_fp8(p) ? 64 : lazy::shared_rows_cap(c.G, p->head_dim);
+  // e4m3 and int4 pools run on mma.sync kernels (items of at most 64 rows) at every ratio
+  const int cap = kv_quantised(p) ? 64 : lazy::shared_rows_cap(c.G, p->head_dim);
   // 0: 32 blocks for the mma.sync kernel; for the tensor-core kernel, a length that
   // gives about one item per resident CTA.
   const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 ? 0 : 32);
   const int auto_items = std::max(1, lazy::kSharedTcSlots / std::max(1, p->num_kv_heads));
   // small items spread through the launch: measured for the bf16 mma.sync kernel only
-  const bool spread = !kv_fp8(p) && cap == 64;
+  const bool spread = !kv_quantised(p) && cap == 64;
   return lazy::plan_shared_host(p->num_seqs, c.G, cap, p->max_blocks_per_seq, p->num_pool_blocks, num_docs,
                                 seg_indptr, seg_doc, seg_len, doc_block_indptr, doc_blocks, cb, auto_items, capacity,
                                 items, slot_indptr, counts, spread);
@@ -520,6 +531,7 @@ static int decode_shared_impl(const lazy_attn_params* p, const void* q, const vo
   if (p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_int4(p) && alibi) return LAZY_ERR_UNSUPPORTED;
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
   if (num_items < 0 || num_slots < 0) return LAZY_ERR_INVALID_ARG;
   if (p->num_seqs == 0) return LAZY_OK;
@@ -561,7 +573,10 @@ static int decode_shared_impl(const lazy_attn_params* p, const void* q, const vo
   a.scale_log2 = scale_log2(p);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (phase == kSharedCombine) return launched(lazy::launch_shared_combine(a, cs));
-  if (num_items > 0) {
+  if (num_items > 0 && kv_int4(p)) {
+    rc = launched(lazy::launch_decode_shared_int4(a, k_pool, v_pool, p->lazy != 0, cs));
+    if (rc != LAZY_OK) return rc;
+  } else if (num_items > 0) {
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)p->num_pool_blocks * p->num_kv_heads * lazy::kBlock;
     if (fp8) {  // e4m3 codes: one 16-row x 128-byte box per block (mma.sync kernel at every ratio)
@@ -655,7 +670,7 @@ static int prefill_impl(const lazy_attn_params* p, const void* q, const int32_t*
   Checked c;
   int rc = check_params(p, &c);
   if (rc != LAZY_OK) return rc;
-  if (p->dtype != LAZY_BF16 || p->head_dim != 128 || kv_fp8(p)) return LAZY_ERR_UNSUPPORTED;
+  if (p->dtype != LAZY_BF16 || p->head_dim != 128 || kv_quantised(p)) return LAZY_ERR_UNSUPPORTED;
   // key-position words carry no document start: only the ALiBi form reads them
   if (total_q < 0 || max_q_len < 0 || !alibi != !p->key_positions || (reinterpret_cast<uintptr_t>(alibi) & 3u))
     return LAZY_ERR_INVALID_ARG;
@@ -734,7 +749,7 @@ static bool mixed_compatible(const lazy_attn_params* pd, const lazy_attn_params*
          pd->head_dim == pp->head_dim && pd->num_pool_blocks == pp->num_pool_blocks && pd->id_bits == pp->id_bits &&
          pd->dtype == pp->dtype && pd->sm_scale == pp->sm_scale && pd->lazy == pp->lazy &&
          pd->key_positions == pp->key_positions && pd->kv_dtype == pp->kv_dtype && pd->head_dim == 128 &&
-         pd->dtype == LAZY_BF16 && !kv_fp8(pd) && pd->lazy != 0 && !pd->key_positions && cd.G % 16 == 0 &&
+         pd->dtype == LAZY_BF16 && !kv_quantised(pd) && pd->lazy != 0 && !pd->key_positions && cd.G % 16 == 0 &&
          lazy::shared_rows_cap(cd.G, pd->head_dim) == 128;
 }
 
@@ -842,7 +857,7 @@ int lazy_attn_materialize(const lazy_attn_params* p, const void* k_pool, const v
   Checked c;
   int rc = check_params(p, &c);
   if (rc != LAZY_OK) return rc;
-  if (p->dtype != LAZY_BF16 || kv_fp8(p)) return LAZY_ERR_UNSUPPORTED;
+  if (p->dtype != LAZY_BF16 || kv_quantised(p)) return LAZY_ERR_UNSUPPORTED;
   if (p->key_positions) return LAZY_ERR_INVALID_ARG;
   if (p->num_seqs == 0) return LAZY_OK;
   if (!k_pool || !v_pool || !block_words || !seq_lens || !rope_table || !k_out || !v_out || !block_words_out)
@@ -859,13 +874,113 @@ int lazy_attn_materialize(const lazy_attn_params* p, const void* k_pool, const v
   return launched(lazy::launch_materialize(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- rows into the pools, blocks out of them
+
+size_t lazy_attn_pool_record_bytes(const lazy_attn_params* p) {
+  Checked c;
+  if (check_params(p, &c) != LAZY_OK) return 0;
+  const size_t n = (size_t)lazy::kBlock * p->head_dim;
+  if (kv_int4(p)) return n / 2 + n / 64 * 4;
+  return kv_fp8(p) ? n : n * (p->dtype == LAZY_F32 ? 4 : 2);
+}
+
+// The pools' type, or a negative value for one that the cache calls do not take.
+static int cache_kv_dtype(const lazy_attn_params* p) {
+  if (!kv_quantised(p)) return p->dtype;
+  if (p->dtype != LAZY_BF16) return -1;
+  return p->kv_dtype;
+}
+
+// 0 selects 1; the e4m3 quotient needs a scale whose reciprocal is a normal number.
+static bool cache_scales(const lazy_attn_params* p, float* ks, float* vs) {
+  *ks = p->k_scale > 0.f ? p->k_scale : 1.f;
+  *vs = p->v_scale > 0.f ? p->v_scale : 1.f;
+  return *ks >= 0x1p-100f && *ks <= 0x1p100f && *vs >= 0x1p-100f && *vs <= 0x1p100f;
+}
+
+int lazy_attn_cache_write(const lazy_attn_params* p, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void* v, int64_t v_token_stride, int64_t v_head_stride, int32_t num_tokens,
+                          const int32_t* slots, void* k_pool, void* v_pool, lazy_stream_t stream) {
+  Checked c;
+  int rc = check_params(p, &c);
+  if (rc != LAZY_OK) return rc;
+  const int kind = cache_kv_dtype(p);
+  if (kind < 0) return LAZY_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+    return LAZY_ERR_INVALID_ARG;
+  if (num_tokens == 0) return LAZY_OK;
+  if (!k || !v || !slots || !k_pool || !v_pool || p->num_pool_blocks == 0) return LAZY_ERR_INVALID_ARG;
+  if ((int64_t)num_tokens * 2 * p->num_kv_heads > INT32_MAX) return LAZY_ERR_UNSUPPORTED;
+  const uintptr_t esz = p->dtype == LAZY_F32 ? 4 : 2;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || reinterpret_cast<uintptr_t>(k) % esz ||
+      reinterpret_cast<uintptr_t>(v) % esz || (reinterpret_cast<uintptr_t>(slots) & 3u))
+    return LAZY_ERR_INVALID_ARG;
+  lazy::CacheWriteArgs a{};
+  if (kind == LAZY_FP8_E4M3) {
+    if (!cache_scales(p, &a.k_scale, &a.v_scale)) return LAZY_ERR_INVALID_ARG;
+    a.k_inv = 1.f / a.k_scale;
+    a.v_inv = 1.f / a.v_scale;
+  }
+  unsigned int* st = status_ptr();
+  if (!st) return LAZY_ERR_CUDA;
+  a.k = k;
+  a.v = v;
+  a.k_token_stride = k_token_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_token_stride = v_token_stride;
+  a.v_head_stride = v_head_stride;
+  a.slots = slots;
+  a.k_pool = static_cast<uint8_t*>(k_pool);
+  a.v_pool = static_cast<uint8_t*>(v_pool);
+  a.status = st;
+  a.num_tokens = num_tokens;
+  a.Hkv = p->num_kv_heads;
+  a.D = p->head_dim;
+  a.num_pool_blocks = p->num_pool_blocks;
+  const int64_t per16 = 16 / (int64_t)esz;  // elements of a 16-byte load
+  const bool vec = aligned16(k) && aligned16(v) && k_token_stride % per16 == 0 && k_head_stride % per16 == 0 &&
+                   v_token_stride % per16 == 0 && v_head_stride % per16 == 0;
+  return launched(lazy::launch_cache_write(a, kind, vec, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int lazy_attn_cache_read(const lazy_attn_params* p, const void* k_pool, const void* v_pool, int32_t num_blocks,
+                         const int32_t* block_ids, void* k_out, void* v_out, lazy_stream_t stream) {
+  Checked c;
+  int rc = check_params(p, &c);
+  if (rc != LAZY_OK) return rc;
+  const int kind = cache_kv_dtype(p);
+  if (kind < 0) return LAZY_ERR_UNSUPPORTED;
+  if (num_blocks < 0) return LAZY_ERR_INVALID_ARG;
+  if (num_blocks == 0) return LAZY_OK;
+  if (!k_pool || !v_pool || !block_ids || !k_out || !v_out || p->num_pool_blocks == 0) return LAZY_ERR_INVALID_ARG;
+  if ((int64_t)num_blocks * 2 * p->num_kv_heads > INT32_MAX) return LAZY_ERR_UNSUPPORTED;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out) ||
+      (reinterpret_cast<uintptr_t>(block_ids) & 3u))
+    return LAZY_ERR_INVALID_ARG;
+  lazy::CacheReadArgs a{};
+  if (kind == LAZY_FP8_E4M3 && !cache_scales(p, &a.k_scale, &a.v_scale)) return LAZY_ERR_INVALID_ARG;
+  unsigned int* st = status_ptr();
+  if (!st) return LAZY_ERR_CUDA;
+  a.k_pool = static_cast<const uint8_t*>(k_pool);
+  a.v_pool = static_cast<const uint8_t*>(v_pool);
+  a.block_ids = block_ids;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.status = st;
+  a.num_blocks = num_blocks;
+  a.Hkv = p->num_kv_heads;
+  a.D = p->head_dim;
+  a.num_pool_blocks = p->num_pool_blocks;
+  return launched(lazy::launch_cache_read(a, kind, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 static int debug_gather_impl(const lazy_attn_params* p, const void* k_pool, const void* v_pool,
                              const uint32_t* block_words, const int32_t* seq_lens, void* k_out, void* v_out,
                              int32_t* pos_out, int32_t withhold_block, uint64_t wait_ns, lazy_stream_t stream) {
   Checked c;
   int rc = check_params(p, &c);
   if (rc != LAZY_OK) return rc;
-  if (kv_fp8(p)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_quantised(p)) return LAZY_ERR_UNSUPPORTED;
   if (p->num_seqs == 0) return LAZY_OK;
   if (!k_pool || !v_pool || !block_words || !seq_lens || !k_out || !v_out) return LAZY_ERR_INVALID_ARG;
   if (p->num_pool_blocks == 0 || p->max_blocks_per_seq == 0) return LAZY_ERR_INVALID_ARG;

@@ -64,24 +64,6 @@ struct DecodeCfg {
   static constexpr int SMEM = 1024 + STAGES_BYTES + QS_BYTES + BAR_BYTES;
 };
 
-__device__ __forceinline__ LaneBlock describe_block(bool live, int b, int nb, int seq_len, uint32_t w, uint32_t wn,
-                                                    int id_bits, int num_pool_blocks, unsigned int* status) {
-  LaneBlock r{num_pool_blocks, 0, 0};
-  if (!live) return r;
-  const BlockInfo bi = decode_word(w, b, id_bits);
-  const int pn = (b + 1 < nb) ? decode_word(wn, b + 1, id_bits).p : bi.p;
-  int nv = block_valid(b, nb, seq_len, bi.p, pn);
-  nv = nv < 0 ? 0 : (nv > kBlock ? kBlock : nv);
-  if (bi.phys >= num_pool_blocks) {
-    raise_status(status, LAZY_DEV_BAD_BLOCK_ID);
-    nv = 0;
-  }
-  r.phys = bi.phys < num_pool_blocks ? bi.phys : num_pool_blocks;
-  r.p = bi.p;
-  r.nv = nv;
-  return r;
-}
-
 // A fragments of scale * R_delta q for rows (mt*16 + g, mt*16 + g + 8), g = lane/4.
 // The thread owns columns 16ks + 2t + {0,1,8,9}; ks and ks + D/32 hold the two
 // halves of the same rotate-half pairs, so each pair is rotated by one thread.

@@ -269,6 +269,24 @@ struct LaneBlock {
   int phys, p, nv;
 };
 
+__device__ __forceinline__ LaneBlock describe_block(bool live, int b, int nb, int seq_len, uint32_t w, uint32_t wn,
+                                                    int id_bits, int num_pool_blocks, unsigned int* status) {
+  LaneBlock r{num_pool_blocks, 0, 0};
+  if (!live) return r;
+  const BlockInfo bi = decode_word(w, b, id_bits);
+  const int pn = (b + 1 < nb) ? decode_word(wn, b + 1, id_bits).p : bi.p;
+  int nv = block_valid(b, nb, seq_len, bi.p, pn);
+  nv = nv < 0 ? 0 : (nv > kBlock ? kBlock : nv);
+  if (bi.phys >= num_pool_blocks) {
+    raise_status(status, LAZY_DEV_BAD_BLOCK_ID);
+    nv = 0;
+  }
+  r.phys = bi.phys < num_pool_blocks ? bi.phys : num_pool_blocks;
+  r.p = bi.p;
+  r.nv = nv;
+  return r;
+}
+
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }

@@ -151,6 +151,31 @@ struct SharedFp8Args : SharedDecodeArgs {
   float k_scale, v_scale;
 };
 
+// Rows into the pools (cache_rw.cu). Strides in elements; slot = block * 16 + row.
+struct CacheWriteArgs {
+  const void* k;             // rows of D elements, contiguous
+  const void* v;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const int32_t* slots;      // [num_tokens], negative: skip
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  unsigned int* status;
+  int num_tokens, Hkv, D, num_pool_blocks;
+  float k_scale, v_scale, k_inv, v_inv;  // e4m3 pools
+};
+
+// Blocks out of the pools as `dtype`.
+struct CacheReadArgs {
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int32_t* block_ids;  // [num_blocks], negative: leave the output block as it is
+  void* k_out;               // [num_blocks][Hkv][16][D]
+  void* v_out;
+  unsigned int* status;
+  int num_blocks, Hkv, D, num_pool_blocks;
+  float k_scale, v_scale;
+};
+
 // Eager materialisation (materialize.cu): per-sequence copies with K at absolute positions.
 struct MaterializeArgs {
   const void* k_pool;        // [NB][Hkv][16][D]
@@ -235,6 +260,15 @@ cudaError_t launch_decode_shared_fp8(const SharedDecodeArgs& a, float k_scale, f
 cudaError_t launch_decode_shared_tc(const SharedDecodeArgs& a, const float* alibi, bool lazy,
                                     const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t st);
 cudaError_t launch_shared_combine(const SharedDecodeArgs& a, cudaStream_t st);
+
+// kv_dtype: the pools' type (LAZY_F32 and LAZY_BF16 copy); vec: every row is 16-byte aligned.
+cudaError_t launch_cache_write(const CacheWriteArgs& a, int kv_dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheReadArgs& a, int kv_dtype, int sms, cudaStream_t st);
+
+// int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool.
+cudaError_t launch_decode_int4(const DecodeArgs& a, bool lazy, cudaStream_t st);
+cudaError_t launch_decode_shared_int4(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,
+                                      cudaStream_t st);
 
 // Shared-memory bytes a bf16 decode CTA needs (for occupancy-based split planning).
 int decode_bf16_smem_bytes(int D, int G);

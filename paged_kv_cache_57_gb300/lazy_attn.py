@@ -24,7 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 LAZY_OK, LAZY_ERR_INVALID_ARG, LAZY_ERR_UNSUPPORTED, LAZY_ERR_WORKSPACE, LAZY_ERR_LAYOUT, LAZY_ERR_CUDA, \
     LAZY_ERR_DEVICE = range(7)
-LAZY_F32, LAZY_BF16, LAZY_FP8_E4M3 = 0, 1, 2
+LAZY_F32, LAZY_BF16, LAZY_FP8_E4M3, LAZY_INT4 = 0, 1, 2, 3
 LAZY_DEV_BAD_BLOCK_ID, LAZY_DEV_POS_RANGE, LAZY_DEV_TIMEOUT, LAZY_DEV_LAYOUT, LAZY_DEV_BAD_LEN = 1, 2, 4, 8, 16
 BLOCK = 16
 
@@ -38,7 +38,7 @@ EXPORTED = (
     "lazy_attn_rotary_layout_host", "lazy_attn_decode_shared_alibi", "lazy_attn_alibi_slopes_host",
     "lazy_attn_decode_alibi", "lazy_attn_debug_gather_withheld", "lazy_attn_prefill_alibi",
     "lazy_attn_decode_shared_partials", "lazy_attn_decode_shared_combine", "lazy_attn_mixed_workspace_bytes",
-    "lazy_attn_mixed",
+    "lazy_attn_mixed", "lazy_attn_pool_record_bytes", "lazy_attn_cache_write", "lazy_attn_cache_read",
 )
 PLAN_MAX_MEMBERS = 16
 PLAN_ITEM_BLOCK_IDS = 32
@@ -64,7 +64,7 @@ class LazyAttnError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)}")
 
 
-_vp, _sz, _i32, _u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_uint64
+_vp, _sz, _i32, _i64, _u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 _P = ctypes.POINTER(Params)
 _sig = {
     "lazy_attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -99,6 +99,9 @@ _sig = {
     "lazy_attn_mixed": (ctypes.c_int, [_P] + [_vp] * 3 + [_i32, _vp, _i32, _vp, _vp, _P] + [_vp] * 3 +
                         [_i32, _i32] + [_vp] * 6 + [_sz, _vp]),
     "lazy_attn_decode_alibi": (ctypes.c_int, [_P] + [_vp] * 9 + [_vp, _sz, _vp]),
+    "lazy_attn_pool_record_bytes": (_sz, [_P]),
+    "lazy_attn_cache_write": (ctypes.c_int, [_P, _vp, _i64, _i64, _vp, _i64, _i64, _i32] + [_vp] * 3 + [_vp]),
+    "lazy_attn_cache_read": (ctypes.c_int, [_P, _vp, _vp, _i32] + [_vp] * 3 + [_vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -118,8 +121,9 @@ def make_params(*, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim:
                 max_blocks_per_seq: int, dtype: str = "bf16", rope_theta: float = 5e5, lazy: bool = True,
                 sm_scale: float = 0.0, id_bits: int = 0, num_splits: int = 0, key_positions: bool = False,
                 kv_dtype: Optional[str] = None, k_scale: float = 0.0, v_scale: float = 0.0) -> Params:
-    """kv_dtype "fp8_e4m3": pools of e4m3 codes (torch.float8_e4m3fn), values code * k_scale / v_scale."""
-    kv = 0 if kv_dtype is None else {"fp8_e4m3": LAZY_FP8_E4M3}[kv_dtype]
+    """kv_dtype "fp8_e4m3": pools of e4m3 codes (torch.float8_e4m3fn), values code * k_scale / v_scale.
+    "int4": pools of int4 records (torch.uint8, see empty_pools), which carry their own scales."""
+    kv = 0 if kv_dtype is None else {"fp8_e4m3": LAZY_FP8_E4M3, "int4": LAZY_INT4}[kv_dtype]
     return Params(num_seqs, num_q_heads, num_kv_heads, head_dim, BLOCK, num_pool_blocks, max_blocks_per_seq,
                   id_bits, LAZY_BF16 if dtype == "bf16" else LAZY_F32, int(bool(lazy)), float(rope_theta),
                   float(sm_scale), num_splits, int(bool(key_positions)), kv, float(k_scale), float(v_scale))
@@ -149,6 +153,8 @@ def _tdt(p: Params):
 
 def _kvdt(p: Params):
     """torch dtype of the pools."""
+    if p.kv_dtype == LAZY_INT4:
+        return torch.uint8
     return torch.float8_e4m3fn if p.kv_dtype == LAZY_FP8_E4M3 else _tdt(p)
 
 
@@ -456,6 +462,80 @@ def materialize(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor, block_wor
                                     _dptr(words_out, "block_words_out"), _stream(stream))
     _check(rc, "materialize")
     return k_out, v_out, words_out
+
+
+# ---------------------------------------------------------------- rows into the pools, blocks out of them
+
+def pool_record_bytes(p: Params) -> int:
+    """Bytes of one (block, KV head) of k_pool, and of v_pool."""
+    return int(_lib.lazy_attn_pool_record_bytes(ctypes.byref(p)))
+
+
+def empty_pools(p: Params, device="cuda"):
+    """Uninitialised (k_pool, v_pool) of p's kind: [num_pool_blocks, Hkv, 16, d], or
+    [num_pool_blocks, Hkv, record] bytes for int4 pools."""
+    n = pool_record_bytes(p)
+    if n == 0:
+        raise LazyAttnError(LAZY_ERR_INVALID_ARG, "empty_pools")
+    tail = (n,) if p.kv_dtype == LAZY_INT4 else (BLOCK, p.head_dim)
+    return tuple(torch.empty((p.num_pool_blocks, p.num_kv_heads) + tail, dtype=_kvdt(p), device=device)
+                 for _ in range(2))
+
+
+def _check_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor) -> None:
+    n = p.num_pool_blocks * p.num_kv_heads * (pool_record_bytes(p) if p.kv_dtype == LAZY_INT4 else BLOCK * p.head_dim)
+    if k_pool.numel() < n or v_pool.numel() < n:
+        raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
+
+
+def token_slots(blocks, first: int, count: int) -> np.ndarray:
+    """Slots (block * 16 + row, int32) of tokens first .. first + count - 1 of a document whose
+    block ids are ``blocks`` (a cache manager's segment_blocks, for instance)."""
+    b = _i32_np(blocks)
+    if first < 0 or count < 0 or first + count > BLOCK * b.size:
+        raise ValueError(f"tokens {first} .. {first + count - 1} are outside the document's {b.size} blocks")
+    t = np.arange(first, first + count, dtype=np.int32)
+    return (b[t // BLOCK] * BLOCK + t % BLOCK).astype(np.int32)
+
+
+def cache_write(p: Params, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pool: torch.Tensor,
+                v_pool: torch.Tensor, stream=None) -> None:
+    """Writes rows k, v [T, Hkv, d] (any token and head strides, d contiguous) into the slots
+    [T] int32 of the pools, in the pools' type (lazy_attn_cache_write)."""
+    dt, shape = _tdt(p), (slots.numel(), p.num_kv_heads, p.head_dim)
+    for name, x in (("k", k), ("v", v)):
+        if not x.is_cuda or x.dtype != dt:
+            raise ValueError(f"{name} must be a {dt} CUDA tensor")
+        if x.shape != shape or (x.stride(2) != 1 and x.numel()):
+            raise ValueError(f"{name} must have shape {shape} with contiguous rows, got {tuple(x.shape)}, "
+                             f"strides {x.stride()}")
+    _check_pools(p, k_pool, v_pool)
+    kvdt = _kvdt(p)
+    rc = _lib.lazy_attn_cache_write(ctypes.byref(p), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+                                    v.stride(0), v.stride(1), shape[0], _dptr(slots, "slots", torch.int32),
+                                    _dptr(k_pool, "k_pool", kvdt), _dptr(v_pool, "v_pool", kvdt), _stream(stream))
+    _check(rc, "cache_write")
+
+
+def cache_read(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor, block_ids: torch.Tensor,
+               k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, stream=None):
+    """Blocks block_ids [n] int32 of the pools as unquantised blocks [n, Hkv, 16, d] (lazy_attn_cache_read): a
+    pool for the calls that take no quantised one, prefill above all. Returns (k_out, v_out)."""
+    dt, n = _tdt(p), block_ids.numel()
+    shape = (n, p.num_kv_heads, BLOCK, p.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+    if min(k_out.numel(), v_out.numel()) < n * p.num_kv_heads * BLOCK * p.head_dim:
+        raise ValueError(f"k_out and v_out must hold {shape} elements")
+    _check_pools(p, k_pool, v_pool)
+    kvdt = _kvdt(p)
+    rc = _lib.lazy_attn_cache_read(ctypes.byref(p), _dptr(k_pool, "k_pool", kvdt), _dptr(v_pool, "v_pool", kvdt), n,
+                                   _dptr(block_ids, "block_ids", torch.int32), _dptr(k_out, "k_out", dt),
+                                   _dptr(v_out, "v_out", dt), _stream(stream))
+    _check(rc, "cache_read")
+    return k_out, v_out
 
 
 def prefill_workspace_bytes(p: Params, total_q: int) -> int:
