@@ -23,6 +23,10 @@ struct Int4Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
+  static constexpr int SLOT = 2 * Int4Geom<D>::REC;  // a ring slot: one block's K and V records
+  static constexpr int RING = NT == 1 ? 4 : 8;       // slots per warp
+  static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
+  static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4 + kWarps * RING * 8;
 };
 
 // One warp: a query row of D bf16 values times `scale` to fp32 in shared memory, over the
@@ -73,16 +77,19 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT>& st, f
 
 // ------------------------------------------------------------------ per sequence
 // One CTA per (sequence, KV head and tile of 8 NT query heads, split), four warps with a
-// quarter of the split's blocks each, read from global memory as the fragments want them.
+// quarter of the split's blocks each. A warp is its own loader: a ring of RING blocks, each
+// refilled by two bulk copies (K and V record) as soon as it was read.
 template <int D, int NT, bool LAZY>
-__global__ void __launch_bounds__(kThreads) decode_int4_kernel(const DecodeArgs a, int head_tiles) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(const DecodeArgs a, int head_tiles) {
   using C = Int4Cfg<D, NT>;
   using G = Int4Geom<D>;
-  constexpr int HALF = D / 2;
-  __shared__ __align__(16) float qs[C::ROWS * C::QS];
-  __shared__ float row_scale[C::ROWS];
-  __shared__ float2 cs[kWarps][HALF];
-  __shared__ __align__(16) float red[kWarps * C::ROWS * C::RED];
+  constexpr int HALF = D / 2, R = C::RING;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem + C::BUF);
+  float2* cs_all = reinterpret_cast<float2*>(qs + C::ROWS * C::QS);
+  float* row_scale = reinterpret_cast<float*>(cs_all + kWarps * HALF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(row_scale + C::ROWS);
+  __shared__ int abort_flag;
   const int split = blockIdx.x, kvh = blockIdx.y / head_tiles, ht = blockIdx.y % head_tiles, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = min(C::ROWS, a.G - ht * C::ROWS);
@@ -98,6 +105,42 @@ __global__ void __launch_bounds__(kThreads) decode_int4_kernel(const DecodeArgs 
   if (n == 0 && a.splits > 1) return;  // the combine does not look here
   const int m_pos = a.q_pos[s];
   const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
+
+  // ------------------------------------------------------------ first loads
+  const int per_warp = (n + kWarps - 1) / kWarps;
+  const int kb0 = warp * per_warp;
+  const int nk = max(0, min(n, kb0 + per_warp) - kb0);  // blocks of this warp
+  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
+  const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + head_off;
+  const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + head_off;
+  uint8_t* ring = smem + warp * R * C::SLOT;
+  uint64_t* full = bars + warp * R;
+  auto load_words = [&](int kc, uint32_t& w, uint32_t& wn) {
+    const int k = kc + lane, b = b0 + kb0 + k;
+    w = k < nk ? __ldg(&wrow[b]) : 0u;
+    wn = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
+  };
+  auto describe = [&](int kc, uint32_t w, uint32_t wn) {
+    return describe_block(kc + lane < nk, b0 + kb0 + kc + lane, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
+  };
+  uint32_t w_cur, wn_cur, w_nxt = 0, wn_nxt = 0;
+  load_words(0, w_cur, wn_cur);
+  if (nk > 32) load_words(32, w_nxt, wn_nxt);
+  if (lane == 0) {
+    for (int i = 0; i < R; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) abort_flag = 0;
+  LaneBlock cur = describe(0, w_cur, wn_cur), nxt{a.num_pool_blocks, 0, 0};
+  bool nxt_ready = false;
+  __syncwarp();
+  int issued = min(R, nk);
+  for (int k = 0; k < issued; ++k) {
+    const int phys = __shfl_sync(0xffffffffu, cur.phys, k);
+    if (lane == 0) load_int4_block<D>(ring + k * C::SLOT, &full[k], phys, a.num_pool_blocks, kp, vp, blk_bytes);
+  }
+
+  // ------------------------------------------------------------ queries
   for (int r = warp; r < C::ROWS; r += kWarps) {
     if (r < heads) {
       const float sc = int4_load_row<D>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + r) * D, qs + r * C::QS, a.scale_log2, lane);
@@ -108,56 +151,99 @@ __global__ void __launch_bounds__(kThreads) decode_int4_kernel(const DecodeArgs 
     }
   }
   __syncthreads();
-
-  const int per_warp = (n + kWarps - 1) / kWarps;
-  const int kb0 = warp * per_warp;
-  const int nk = max(0, min(n, kb0 + per_warp) - kb0);
-  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
-  const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + head_off;
-  const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + head_off;
+  float2* cs = cs_all + warp * HALF;
   Int4Query<D, NT> q;
+  auto rebuild = [&](int delta) {
+    __syncwarp();
+    for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
+    __syncwarp();
+    int4_build_query<D, NT>(
+        q, lane, [&](int r, int d) { return qs[r * C::QS + d]; }, [&](int, int f) { return cs[f]; },
+        [&](int r) { return row_scale[r]; });
+  };
+  if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
+
+  // ------------------------------------------------------------ main loop
   Int4State<D, NT> st;
   int4_init(st);
-  LaneBlock cur{a.num_pool_blocks, 0, 0};
-  int delta = INT_MIN;
-  bool built = false;
-  for (int k = 0, step = 0; k < nk; k += step) {
-    const int at = k & 31;
-    if (at == 0) {
-      const int i = k + lane, b = b0 + kb0 + i;
-      const uint32_t w = i < nk ? __ldg(&wrow[b]) : 0u;
-      const uint32_t wn = (i < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
-      cur = describe_block(i < nk, b, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
-    }
-    const int p = __shfl_sync(0xffffffffu, cur.p, at);
-    const int p2 = __shfl_sync(0xffffffffu, cur.p, (at + 1) & 31);
-    const bool two = at < 31 && k + 1 < nk && (p2 == p || !LAZY);  // a tile lies in one document
-    step = two ? 2 : 1;
-    const int dnew = LAZY ? m_pos - p : m_pos;
-    if (!built || dnew != delta) {
-      delta = dnew;
-      built = true;
-      __syncwarp();
-      for (int f = lane; f < HALF; f += 32) cs[warp][f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
-      __syncwarp();
-      int4_build_query<D, NT>(
-          q, lane, [&](int r, int d) { return qs[r * C::QS + d]; }, [&](int, int f) { return cs[warp][f]; },
-          [&](int r) { return row_scale[r]; });
-    }
-    GlobalRecord kr[kTile], vr[kTile];
-    int nv[kTile];
+  int k = 0, cbase = 0, slot = 0, phase = 0;  // next block; first block of the current words
+  int p_seg = __shfl_sync(0xffffffffu, cur.p, 0);
+  bool aborted = false;
+  // One pass per document run of the warp's range (lazy only), the q re-rotation between them.
+  while (k < nk && !aborted) {
+    if constexpr (LAZY) rebuild(m_pos - p_seg);
+    while (k < nk) {
+      const int at = k & 31;
+      if (k - cbase >= 32) {  // advance the word chunk
+        if (!nxt_ready) nxt = describe(k, w_nxt, wn_nxt);
+        cur = nxt;
+        nxt_ready = false;
+        cbase += 32;
+        if (k + 32 < nk) load_words(k + 32, w_nxt, wn_nxt);
+      }
+      const int p = __shfl_sync(0xffffffffu, cur.p, at);
+      if (LAZY && p != p_seg) {  // next document: leave to re-rotate q, then resume at block k
+        p_seg = p;
+        break;
+      }
+      const int p2 = __shfl_sync(0xffffffffu, cur.p, (at + 1) & 31);
+      const bool two = at < 31 && k + 1 < nk && (!LAZY || p2 == p);  // a tile lies in one document
+      const int slot2 = slot + 1 == R ? 0 : slot + 1;
+      bool ok = warp_wait(&full[slot], phase, a.status);
+      if (two) ok = warp_wait(&full[slot2], slot2 == 0 ? phase ^ 1 : phase, a.status) && ok;
+      if (!ok) {
+        aborted = true;
+        break;
+      }
+      SharedRecord kr[kTile], vr[kTile];
+      int nv[kTile];
+      kr[0].p = ring + slot * C::SLOT;
+      kr[1].p = ring + slot2 * C::SLOT;
 #pragma unroll
-    for (int b = 0; b < kTile; ++b) {
-      const int ph = __shfl_sync(0xffffffffu, cur.phys, (at + b) & 31);
-      nv[b] = __shfl_sync(0xffffffffu, cur.nv, (at + b) & 31);
-      if (b > 0 && !two) nv[b] = 0;
-      const size_t off = (size_t)(nv[b] > 0 ? ph : 0) * blk_bytes;  // no keys: any record of the pool
-      kr[b].p = kp + off;
-      vr[b].p = vp + off;
+      for (int b = 0; b < kTile; ++b) {
+        vr[b].p = kr[b].p + G::REC;
+        nv[b] = __shfl_sync(0xffffffffu, cur.nv, (at + b) & 31);
+      }
+      if (!two) nv[1] = 0;
+      int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
+      __syncwarp();
+      // Refill the slots just read with the warp's blocks R positions ahead.
+      for (int i = 0; i < (two ? 2 : 1); ++i) {
+        const int kn = k + i + R;
+        if (kn < nk) {
+          int phys;
+          if ((kn >> 5) == (k >> 5)) {
+            phys = __shfl_sync(0xffffffffu, cur.phys, kn & 31);
+          } else {
+            if (!nxt_ready) {
+              nxt = describe(kn & ~31, w_nxt, wn_nxt);
+              nxt_ready = true;
+            }
+            phys = __shfl_sync(0xffffffffu, nxt.phys, kn & 31);
+          }
+          const int sl = i ? slot2 : slot;
+          if (lane == 0) load_int4_block<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes);
+          issued = kn + 1;
+        }
+      }
+      const int step = two ? 2 : 1;
+      k += step;
+      slot += step;
+      if (slot >= R) {
+        slot -= R;
+        phase ^= 1;
+      }
     }
-    int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
+  }
+  // Copies still in flight (only after a timeout) must land before exit (bounded).
+  if (aborted) {
+    abort_flag = 1;
+    for (int kk = k; kk < issued; ++kk) mbar_wait(&full[kk % R], (kk / R) & 1, a.status);
   }
   int4_finish(st);
+  __syncthreads();  // every warp is done with its ring: the merge takes its place
+  if (abort_flag) return;
+  float* red = reinterpret_cast<float*>(smem);
   int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
   __syncthreads();
   for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
@@ -189,35 +275,116 @@ __global__ void __launch_bounds__(kThreads) decode_int4_kernel(const DecodeArgs 
 // ------------------------------------------------------------------ shared runs
 // One CTA per (work item, KV head). The item's rows (members x heads, at most 64) are
 // tiles of 16; the warps form 4 / RT teams of RT warps, a team with a contiguous part of
-// the item's blocks and a warp with one of its tiles, as in decode_shared.cu.
+// the item's blocks and a ring for them, a warp with one of the tiles, as in
+// decode_shared.cu.
+namespace {
+
+constexpr int kShRows = 64;
+
+template <int D>
+struct Int4SharedCfg {
+  using C = Int4Cfg<D, 2>;
+  static constexpr int SLOTS = 24;  // ring slots, shared out among the teams: two CTAs fit an SM
+  static constexpr int MERGE = kShRows * C::RED * 4;  // [teams][16 RT] rows are 64 in all
+  static constexpr int BUF = SLOTS * C::SLOT > MERGE ? SLOTS * C::SLOT : MERGE;
+  static constexpr int SMEM = BUF + kShRows * C::QS * 4 + kMembers * (D / 2) * 8;
+};
+
+}  // namespace
+
 template <int D, bool LAZY>
-__global__ void __launch_bounds__(kThreads) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
-                                                                      const uint8_t* v_pool) {
+__global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
+                                                                         const uint8_t* v_pool) {
   constexpr int NT = 2;
   using C = Int4Cfg<D, NT>;
+  using S = Int4SharedCfg<D>;
   using G = Int4Geom<D>;
-  constexpr int HALF = D / 2, MAX_ROWS = 64;
-  extern __shared__ __align__(16) float smem[];
-  float* qs = smem;                             // [64][QS], then the merge area [teams][rows][RED]
-  float2* cs_tab = reinterpret_cast<float2*>(smem + MAX_ROWS * C::QS);  // [members][HALF]
-  __shared__ int rec[kItemInts], m_delta[kMembers], m_ok[kMembers];
-  __shared__ float row_scale[MAX_ROWS];
+  constexpr int HALF = D / 2;
+  extern __shared__ __align__(128) uint8_t smem[];  // the teams' rings, then the merge area
+  float* qs = reinterpret_cast<float*>(smem + S::BUF);               // [64][QS]
+  float2* cs_tab = reinterpret_cast<float2*>(qs + kShRows * C::QS);  // [members][HALF]
+  __shared__ int4 rec4[kItemInts / 4];
+  __shared__ int m_delta[kMembers], m_ok[kMembers], abort_flag;
+  __shared__ float row_scale[kShRows];
+  __shared__ uint64_t bars[S::SLOTS];
+  const int* rec = reinterpret_cast<const int*>(rec4);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < kItemInts / 4)
-    reinterpret_cast<int4*>(rec)[threadIdx.x] =
-        __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
+    rec4[threadIdx.x] = __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < S::SLOTS; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+  }
   __syncthreads();
   const int src = rec[0], b0 = rec[1], nblk = rec[2], last_nv = rec[3], nmem = rec[4];
   const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
-                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= MAX_ROWS;
+                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= kShRows;
   if (!item_ok) {  // uniform over the CTA: nothing is loaded or written
     if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
     return;
   }
   auto mem_seq = [&](int m) { return rec[8 + 4 * m]; };
   auto mem_slot = [&](int m) { return rec[8 + 4 * m + 2]; };
+
+  // ------------------------------------------------------------ teams and first loads
+  const int rows = nmem * a.G;
+  const int RT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), TEAMS = kWarps / RT;
+  const int team = warp / RT, rt = warp % RT;
+  const int R = S::SLOTS / TEAMS;  // ring slots of the team: 6, 12 or 24
+  const int per_team = (nblk + TEAMS - 1) / TEAMS;
+  const int kb0 = team * per_team;
+  const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
+  uint8_t* ring = smem + team * R * C::SLOT;
+  uint64_t* full = bars + team * R;
+  const bool leader = rt == 0 && lane == 0;
+  const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
+  const uint32_t id_mask = (1u << a.id_bits) - 1u;
+  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
+  const uint8_t* kp = k_pool + head_off;
+  const uint8_t* vp = v_pool + head_off;
+  auto rec_id = [&](int kb) { return rec[8 + 4 * kMembers + kb]; };
+  // Lane l describes team block kc + l, as in decode_shared.cu: the block word decides, and
+  // where the record names the block too the two must agree.
+  auto describe = [&](int kc, int& phys, int& nv) {
+    const int k = kc + lane;
+    phys = a.num_pool_blocks;
+    nv = 0;
+    if (k < nk) {
+      const int ph = (int)(__ldg(&wrow[k]) & id_mask);
+      if (kb0 + k < LAZY_PLAN_ITEM_BLOCK_IDS && rec_id(kb0 + k) != ph) {
+        raise_status(a.status, LAZY_DEV_LAYOUT);
+      } else if (ph < a.num_pool_blocks) {
+        phys = ph;
+        nv = kb0 + k == nblk - 1 ? last_nv : kBlock;
+      } else {
+        raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
+      }
+    }
+  };
+  auto issue = [&](int sl, int phys) {
+    load_int4_block<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes);
+  };
+  // First loads straight from the record's ids when it names all of them.
+  int issued = min(R, nk);
+  const bool rec_first = kb0 + issued <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  if (rec_first && leader)
+    for (int k = 0; k < issued; ++k) {
+      const int id = rec_id(kb0 + k);
+      issue(k, id >= 0 && id < a.num_pool_blocks ? id : a.num_pool_blocks);
+    }
+  int c_phys, c_nv, n_phys = a.num_pool_blocks, n_nv = 0;
+  describe(0, c_phys, c_nv);
+  if (nk > 32) describe(32, n_phys, n_nv);
+  if (!rec_first)
+    for (int k = 0; k < issued; ++k) {
+      const int phys = __shfl_sync(0xffffffffu, c_phys, k);
+      if (leader) issue(k, phys);
+    }
+
+  // ------------------------------------------------------------ members and queries
   if (threadIdx.x < nmem) {
     const int m = threadIdx.x, seq = mem_seq(m), bm = rec[8 + 4 * m + 1], slot = mem_slot(m);
     bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
@@ -233,9 +400,6 @@ __global__ void __launch_bounds__(kThreads) decode_shared_int4_kernel(const Shar
     m_delta[m] = delta;
   }
   __syncthreads();
-  const int rows = nmem * a.G;
-  const int RT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), TEAMS = kWarps / RT;
-  const int team = warp / RT, rt = warp % RT;
   for (int r = warp; r < 16 * RT; r += kWarps) {
     const int m = r / a.G;
     if (r < rows && m_ok[m]) {
@@ -255,47 +419,78 @@ __global__ void __launch_bounds__(kThreads) decode_shared_int4_kernel(const Shar
       q, lane, [&](int r, int d) { return qs[(16 * rt + r) * C::QS + d]; },
       [&](int r, int f) { return cs_tab[(16 * rt + r < rows ? (16 * rt + r) / a.G : 0) * HALF + f]; },
       [&](int r) { return row_scale[16 * rt + r]; });
+
+  // ------------------------------------------------------------ main loop
   Int4State<D, NT> st;
   int4_init(st);
-  const int per_team = (nblk + TEAMS - 1) / TEAMS;
-  const int kb0 = team * per_team;
-  const int nk = max(0, min(nblk, kb0 + per_team) - kb0);
-  const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
-  const uint32_t id_mask = (1u << a.id_bits) - 1u;
-  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
-  int c_phys = 0, c_nv = 0;
-  for (int k = 0; k < nk; k += kTile) {
-    if ((k & 31) == 0) {
-      const int i = k + lane;
-      c_phys = c_nv = 0;
-      if (i < nk) {
-        const int ph = (int)(__ldg(&wrow[i]) & id_mask);
-        if (kb0 + i < LAZY_PLAN_ITEM_BLOCK_IDS && rec[8 + 4 * kMembers + kb0 + i] != ph) {
-          raise_status(a.status, LAZY_DEV_LAYOUT);
-        } else if (ph < a.num_pool_blocks) {
-          c_phys = ph;
-          c_nv = kb0 + i == nblk - 1 ? last_nv : kBlock;
+  bool n_ready = true, aborted = false;
+  int k = 0, slot = 0, phase = 0;
+  for (; k < nk; k += kTile) {  // chunks of 32 and rings hold whole tiles
+    if (k > 0 && (k & 31) == 0) {
+      if (!n_ready) describe(k, n_phys, n_nv);
+      c_phys = n_phys;
+      c_nv = n_nv;
+      n_ready = false;
+    }
+    const bool two = k + 1 < nk;
+    bool ok = warp_wait(&full[slot], phase, a.status);
+    if (two) ok = warp_wait(&full[slot + 1], phase, a.status) && ok;
+    if (ok) {
+      SharedRecord kr[kTile], vr[kTile];
+      int nv[kTile];
+#pragma unroll
+      for (int b = 0; b < kTile; ++b) {
+        kr[b].p = ring + (slot + b) * C::SLOT;
+        vr[b].p = kr[b].p + G::REC;
+        nv[b] = __shfl_sync(0xffffffffu, c_nv, (k + b) & 31);
+      }
+      int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
+    }
+    // The team's warps are done with the slots (and agree to go on) before they are refilled.
+    if (RT > 1) ok = team_and(team, 32 * RT, ok);
+    if (!ok) {
+      aborted = true;
+      break;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const int kn = k + i + R;
+      if (kn < nk) {
+        int phys;
+        if ((kn >> 5) == (k >> 5)) {
+          phys = __shfl_sync(0xffffffffu, c_phys, kn & 31);
         } else {
-          raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
+          if (!n_ready) {
+            describe(kn & ~31, n_phys, n_nv);
+            n_ready = true;
+          }
+          phys = __shfl_sync(0xffffffffu, n_phys, kn & 31);
         }
+        if (leader) issue(slot + i, phys);
+        issued = kn + 1;
       }
     }
-    GlobalRecord kr[kTile], vr[kTile];
-    int nv[kTile];
-#pragma unroll
-    for (int b = 0; b < kTile; ++b) {
-      const int ph = __shfl_sync(0xffffffffu, c_phys, (k + b) & 31);
-      nv[b] = __shfl_sync(0xffffffffu, c_nv, (k + b) & 31);
-      const size_t off = (size_t)ph * blk_bytes + head_off;
-      kr[b].p = k_pool + off;
-      vr[b].p = v_pool + off;
+    slot += kTile;
+    if (slot == R) {
+      slot = 0;
+      phase ^= 1;
     }
-    int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
+  }
+  // Copies still in flight (only after a timeout) must land before exit (bounded).
+  if (aborted) {
+    abort_flag = 1;
+    if (leader)
+      for (int kk = k; kk < issued; ++kk) mbar_wait(&full[kk % R], (kk / R) & 1, a.status);
   }
   int4_finish(st);
-  __syncthreads();  // every warp has read its queries: the merge takes their place
+  __syncthreads();  // every team is done with its ring: the merge takes its place
+  if (abort_flag) return;
+
+  // ------------------------------------------------------------ partials
+  float* red = reinterpret_cast<float*>(smem);
   const int trows = 16 * RT;
-  int4_store_partial(st, smem + (team * trows + 16 * rt) * C::RED, C::RED, lane);
+  int4_store_partial(st, red + (team * trows + 16 * rt) * C::RED, C::RED, lane);
   __syncthreads();
   constexpr int PER = D / 32;
   for (int r = warp; r < rows; r += kWarps) {
@@ -303,12 +498,12 @@ __global__ void __launch_bounds__(kThreads) decode_shared_int4_kernel(const Shar
     if (mem_slot(m) < 0 || mem_slot(m) >= a.num_slots) continue;
     float M = -INFINITY, acc[PER], L = 0.f;
     if (m_ok[m])  // a member that failed its checks leaves an empty partial
-      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, smem[(tm * trows + r) * C::RED + D]);
+      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * trows + r) * C::RED + D]);
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = 0.f;
     if (m_ok[m])
       for (int tm = 0; tm < TEAMS; ++tm) {
-        const float* row = smem + (tm * trows + r) * C::RED;
+        const float* row = red + (tm * trows + r) * C::RED;
         const float w = row[D] == -INFINITY ? 0.f : fast_ex2(row[D] - M);
         L += w * row[D + 1];
 #pragma unroll
@@ -323,23 +518,29 @@ __global__ void __launch_bounds__(kThreads) decode_shared_int4_kernel(const Shar
 
 // ------------------------------------------------------------------ launchers
 
-template <int D, int NT>
-static cudaError_t launch_decode_t(const DecodeArgs& a, bool lazy, cudaStream_t st) {
-  const int ht = (a.G + 8 * NT - 1) / (8 * NT);
-  const dim3 grid(a.splits, a.Hkv * ht, a.B);
-  if (lazy) decode_int4_kernel<D, NT, true><<<grid, kThreads, 0, st>>>(a, ht);
-  else decode_int4_kernel<D, NT, false><<<grid, kThreads, 0, st>>>(a, ht);
+template <int D, int NT, bool LAZY>
+static cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
+  using C = Int4Cfg<D, NT>;
+  const int ht = (a.G + C::ROWS - 1) / C::ROWS;
+  cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, LAZY>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  decode_int4_kernel<D, NT, LAZY><<<dim3(a.splits, a.Hkv * ht, a.B), kThreads, C::SMEM, st>>>(a, ht);
   return cudaGetLastError();
 }
 
+template <int D, bool LAZY>
+static cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t st) {
+  return a.G <= 8 ? launch_decode_t<D, 1, LAZY>(a, st) : launch_decode_t<D, 2, LAZY>(a, st);
+}
+
 cudaError_t launch_decode_int4(const DecodeArgs& a, bool lazy, cudaStream_t st) {
-  if (a.D == 128) return a.G <= 8 ? launch_decode_t<128, 1>(a, lazy, st) : launch_decode_t<128, 2>(a, lazy, st);
-  return a.G <= 8 ? launch_decode_t<64, 1>(a, lazy, st) : launch_decode_t<64, 2>(a, lazy, st);
+  if (a.D == 128) return lazy ? launch_decode_d<128, true>(a, st) : launch_decode_d<128, false>(a, st);
+  return lazy ? launch_decode_d<64, true>(a, st) : launch_decode_d<64, false>(a, st);
 }
 
 template <int D, bool LAZY>
 static cudaError_t launch_shared_t(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, cudaStream_t st) {
-  constexpr int SMEM = 64 * (D + 4) * 4 + kMembers * (D / 2) * 8;
+  constexpr int SMEM = Int4SharedCfg<D>::SMEM;
   cudaError_t e = set_smem_once<decode_shared_int4_kernel<D, LAZY>>(SMEM);
   if (e != cudaSuccess) return e;
   decode_shared_int4_kernel<D, LAZY><<<(unsigned)((long long)a.num_items * a.Hkv), kThreads, SMEM, st>>>(

@@ -47,13 +47,37 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return r;
 }
 
-// Where a record lies: global memory.
-struct GlobalRecord {
+// A record in shared memory.
+struct SharedRecord {
   const uint8_t* p;
-  __device__ __forceinline__ uint4 v4(int off) const { return __ldg(reinterpret_cast<const uint4*>(p + off)); }
-  __device__ __forceinline__ uint2 v2(int off) const { return __ldg(reinterpret_cast<const uint2*>(p + off)); }
-  __device__ __forceinline__ uint32_t v1(int off) const { return __ldg(reinterpret_cast<const uint32_t*>(p + off)); }
+  __device__ __forceinline__ uint4 v4(int off) const { return *reinterpret_cast<const uint4*>(p + off); }
+  __device__ __forceinline__ uint2 v2(int off) const { return *reinterpret_cast<const uint2*>(p + off); }
+  __device__ __forceinline__ uint32_t v1(int off) const { return *reinterpret_cast<const uint32_t*>(p + off); }
 };
+
+// Copies one record (a multiple of 16 bytes at 16-byte boundaries) to shared memory;
+// completion is signalled on `bar` as transaction bytes.
+__device__ __forceinline__ void bulk_copy(uint8_t* dst, const uint8_t* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// K and V records of block `phys` (base pointers at the KV head) into a ring slot: K, then
+// V. An id outside the pool is not loaded (the barrier is just arrived).
+template <int D>
+__device__ __forceinline__ void load_int4_block(uint8_t* slot, uint64_t* bar, int phys, int num_pool_blocks,
+                                                const uint8_t* kp, const uint8_t* vp, size_t blk_bytes) {
+  constexpr int REC = Int4Geom<D>::REC;
+  if (phys < num_pool_blocks) {
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar, 2 * REC);
+    bulk_copy(slot, kp + (size_t)phys * blk_bytes, REC, bar);
+    bulk_copy(slot + REC, vp + (size_t)phys * blk_bytes, REC, bar);
+  } else {
+    mbar_arrive(bar);
+  }
+}
 
 // Query fragments of NT tiles of 8 rows (query heads), for the k-order of the codes: lane
 // (g, t) = (lane / 4, lane % 4) holds row g's dims of words D/32 t .. D/32 t + D/32 - 1 of
@@ -156,8 +180,8 @@ constexpr float kInt4ScaleHeadroom = 128.f;  // and the V scales' reference by m
 
 // One tile of TB blocks of one document. Only the first nv[b] slots of block b are keys
 // (0: the block is not there): the other slots' scales and zeros may hold anything.
-template <int D, int NT, int TB, typename Rec>
-__device__ __forceinline__ void int4_attend(const Rec (&kr)[TB], const Rec (&vr)[TB], const int (&nv)[TB],
+template <int D, int NT, int TB>
+__device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const SharedRecord (&vr)[TB], const int (&nv)[TB],
                                             const Int4Query<D, NT>& q, Int4State<D, NT>& st, int lane) {
   using G = Int4Geom<D>;
   constexpr int NG = G::NG, W = D / 32;
