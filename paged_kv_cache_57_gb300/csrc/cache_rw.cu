@@ -33,12 +33,6 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& x, float (&f)[8]) {
   }
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // x / s with the result's last bit set when it is inexact (rounded to odd), so that the
 // second rounding, to e4m3, is that of the exact quotient. Infinities and NaN pass.
 __device__ __noinline__ float div_to_odd(float x, float s) {
@@ -51,9 +45,9 @@ __device__ __noinline__ float div_to_odd(float x, float s) {
 // codes would differ within +-2^-20 of it takes the exact division.
 __device__ __forceinline__ uint32_t quantise_e4m3x2(float x, float y, float s, float inv) {
   const float a = x * inv, b = y * inv;
-  const uint32_t lo = e4m3x2(a * (1.f - 0x1p-20f), b * (1.f - 0x1p-20f));
-  const uint32_t hi = e4m3x2(a * (1.f + 0x1p-20f), b * (1.f + 0x1p-20f));
-  return lo == hi ? lo : e4m3x2(div_to_odd(x, s), div_to_odd(y, s));
+  const uint32_t lo = pack_e4m3x2(a * (1.f - 0x1p-20f), b * (1.f - 0x1p-20f));
+  const uint32_t hi = pack_e4m3x2(a * (1.f + 0x1p-20f), b * (1.f + 0x1p-20f));
+  return lo == hi ? lo : pack_e4m3x2(div_to_odd(x, s), div_to_odd(y, s));
 }
 
 // The lane's eight codes as one word, and its group's (scale, zero) word. The group's

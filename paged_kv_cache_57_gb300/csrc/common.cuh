@@ -173,6 +173,13 @@ __device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Two values to e4m3 (nearest even, saturated), `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Four e4m3 bytes (byte i = element i) to two f16x2 words (elements 0,1 and 2,3,
 // element 0 in the low half). Every e4m3 value, subnormals and zeros included, is
 // exact in f16, so the conversion is exact.

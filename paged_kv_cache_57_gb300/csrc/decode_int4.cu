@@ -14,17 +14,19 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 2;  // blocks a warp takes at a time
 constexpr int kMembers = LAZY_PLAN_MAX_MEMBERS;
 constexpr int kItemInts = LAZY_PLAN_ITEM_INTS;
 
-template <int D, int NT>
+template <int D, int NT, int HL>
 struct Int4Cfg {
-  static constexpr int ROWS = 8 * NT;
+  static constexpr int ROWS = Int4Rows<NT, HL>::ALL;
   static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
-  static constexpr int SLOT = 2 * Int4Geom<D>::REC;  // a ring slot: one block's K and V records
-  static constexpr int RING = NT == 1 ? 4 : 8;       // slots per warp
+  static constexpr int SLOT = 4 * Int4Geom<D>::REC;  // a ring stage: two blocks' K and V records
+#ifndef INT4_RING
+#define INT4_RING 2
+#endif
+  static constexpr int RING = NT == 1 ? INT4_RING : 4;  // stages per warp
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
   static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4 + kWarps * RING * 8;
 };
@@ -49,22 +51,22 @@ __device__ __forceinline__ float int4_load_row(const __nv_bfloat16* q, float* ds
   return __uint_as_float(ex << 23);
 }
 
-// A warp's (or a team's first) partial of its rows to shared memory: o[D], m, l per row.
-template <int D, int NT>
-__device__ __forceinline__ void int4_store_partial(const Int4State<D, NT>& st, float* red, int stride, int lane) {
+// A warp's partial of its rows to shared memory: o[D], m, l per row.
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& st, float* red, int stride, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float* row = red + (8 * nt + 2 * t + c) * stride;
+    for (int c = 0; c < HL; ++c) {
+      float* row = red + (8 * nt + HL * t + c) * stride;
 #pragma unroll
       for (int j = 0; j < Int4Geom<D>::NG; ++j) {
         float v[8];
         int4_out8(st, j, nt, c, v);
-        float4* dst = reinterpret_cast<float4*>(row + 64 * j + 8 * g);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        float* dst = row + int4_dims(j, g);
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(dst + kInt4Dims2) = make_float4(v[4], v[5], v[6], v[7]);
       }
       if (g == 0) {
         row[D] = st.m[nt][c];
@@ -76,12 +78,12 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT>& st, f
 }  // namespace
 
 // ------------------------------------------------------------------ per sequence
-// One CTA per (sequence, KV head and tile of 8 NT query heads, split), four warps with a
+// One CTA per (sequence, KV head and tile of 4, 8 or 16 query heads, split), four warps with a
 // quarter of the split's blocks each. A warp is its own loader: a ring of RING blocks, each
 // refilled by two bulk copies (K and V record) as soon as it was read.
-template <int D, int NT, bool LAZY>
+template <int D, int NT, int HL, bool LAZY>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(const DecodeArgs a, int head_tiles) {
-  using C = Int4Cfg<D, NT>;
+  using C = Int4Cfg<D, NT, HL>;
   using G = Int4Geom<D>;
   constexpr int HALF = D / 2, R = C::RING;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   const int per_warp = (n + kWarps - 1) / kWarps;
   const int kb0 = warp * per_warp;
   const int nk = max(0, min(n, kb0 + per_warp) - kb0);  // blocks of this warp
+  const int ns = (nk + 1) / 2;                          // stages: blocks 2i, 2i + 1
   const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
   const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + head_off;
   const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + head_off;
@@ -120,8 +123,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
     w = k < nk ? __ldg(&wrow[b]) : 0u;
     wn = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
   };
+  // Lane l describes block kc + l; valid slots of the pair (l, l + 1) in one word.
   auto describe = [&](int kc, uint32_t w, uint32_t wn) {
-    return describe_block(kc + lane < nk, b0 + kb0 + kc + lane, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
+    LaneBlock r = describe_block(kc + lane < nk, b0 + kb0 + kc + lane, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
+    r.nv |= __shfl_down_sync(0xffffffffu, r.nv, 1) << 8;
+    return r;
   };
   uint32_t w_cur, wn_cur, w_nxt = 0, wn_nxt = 0;
   load_words(0, w_cur, wn_cur);
@@ -134,11 +140,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   LaneBlock cur = describe(0, w_cur, wn_cur), nxt{a.num_pool_blocks, 0, 0};
   bool nxt_ready = false;
   __syncwarp();
-  int issued = min(R, nk);
-  for (int k = 0; k < issued; ++k) {
-    const int phys = __shfl_sync(0xffffffffu, cur.phys, k);
-    if (lane == 0) load_int4_block<D>(ring + k * C::SLOT, &full[k], phys, a.num_pool_blocks, kp, vp, blk_bytes);
-  }
+  auto load_stage = [&](int sl, int phys, int at) {  // the pair that lanes at, at + 1 describe
+    const int ph = __shfl_sync(0xffffffffu, phys, (at + lane) & 31);
+    load_int4_stage<D>(ring + sl * C::SLOT, &full[sl], ph, a.num_pool_blocks, kp, vp, blk_bytes, lane);
+  };
+  int issued = min(R, ns);
+  for (int i = 0; i < issued; ++i) load_stage(i, cur.phys, 2 * i);
 
   // ------------------------------------------------------------ queries
   for (int r = warp; r < C::ROWS; r += kWarps) {
@@ -152,93 +159,77 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   }
   __syncthreads();
   float2* cs = cs_all + warp * HALF;
-  Int4Query<D, NT> q;
+  Int4Query<D, NT, HL> q;
   auto rebuild = [&](int delta) {
     __syncwarp();
     for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
     __syncwarp();
-    int4_build_query<D, NT>(
-        q, lane, [&](int r, int d) { return qs[r * C::QS + d]; }, [&](int, int f) { return cs[f]; },
-        [&](int r) { return row_scale[r]; });
+    int4_build_query<D, NT, HL>(
+        q, lane, [&](int r) { return qs + r * C::QS; }, [&](int) { return cs; }, [&](int r) { return row_scale[r]; });
   };
-  if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
 
   // ------------------------------------------------------------ main loop
-  Int4State<D, NT> st;
+  Int4State<D, NT, HL> st;
   int4_init(st);
-  int k = 0, cbase = 0, slot = 0, phase = 0;  // next block; first block of the current words
-  int p_seg = __shfl_sync(0xffffffffu, cur.p, 0);
+  int p_cur = INT_MIN;  // the document that q is rotated for
+  if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
+  int i = 0, slot = 0, phase = 0;
   bool aborted = false;
-  // One pass per document run of the warp's range (lazy only), the q re-rotation between them.
-  while (k < nk && !aborted) {
-    if constexpr (LAZY) rebuild(m_pos - p_seg);
-    while (k < nk) {
-      const int at = k & 31;
-      if (k - cbase >= 32) {  // advance the word chunk
-        if (!nxt_ready) nxt = describe(k, w_nxt, wn_nxt);
-        cur = nxt;
-        nxt_ready = false;
-        cbase += 32;
-        if (k + 32 < nk) load_words(k + 32, w_nxt, wn_nxt);
+  for (; i < ns; ++i) {
+    const int at = (2 * i) & 31;
+    if (at == 0 && i > 0) {  // advance the word chunk
+      if (!nxt_ready) nxt = describe(2 * i, w_nxt, wn_nxt);
+      cur = nxt;
+      nxt_ready = false;
+      if (2 * i + 32 < nk) load_words(2 * i + 32, w_nxt, wn_nxt);
+    }
+    if (!warp_wait(&full[slot], phase, a.status)) {
+      aborted = true;
+      break;
+    }
+    const uint8_t* stage = ring + slot * C::SLOT;
+    const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
+    const int nvs = __shfl_sync(0xffffffffu, cur.nv, at);
+    int nv[2] = {nvs & 255, (nvs >> 8) & 255};
+    if constexpr (LAZY) {
+      // A tile lies in one document: where the second block starts another, the first is
+      // attended alone, q is rotated anew, and the second follows.
+      int p = __shfl_sync(0xffffffffu, cur.p, at);
+      const int p1 = __shfl_sync(0xffffffffu, cur.p, at + 1), nv1 = nv[1];
+      bool more = nv1 > 0 && p1 != p;
+      if (more) nv[1] = 0;
+      while (true) {
+        if (p != p_cur) rebuild(m_pos - (p_cur = p));
+        int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
+        if (!more) break;
+        more = false;
+        p = p1;
+        nv[0] = 0;
+        nv[1] = nv1;
       }
-      const int p = __shfl_sync(0xffffffffu, cur.p, at);
-      if (LAZY && p != p_seg) {  // next document: leave to re-rotate q, then resume at block k
-        p_seg = p;
-        break;
+    } else {
+      int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
+    }
+    __syncwarp();
+    // Refill the stage with the warp's pair R positions ahead.
+    if (i + R < ns) {
+      const int kn = 2 * (i + R);
+      if ((kn >> 5) != (i >> 4) && !nxt_ready) {
+        nxt = describe(kn & ~31, w_nxt, wn_nxt);
+        nxt_ready = true;
       }
-      const int p2 = __shfl_sync(0xffffffffu, cur.p, (at + 1) & 31);
-      const bool two = at < 31 && k + 1 < nk && (!LAZY || p2 == p);  // a tile lies in one document
-      const int slot2 = slot + 1 == R ? 0 : slot + 1;
-      bool ok = warp_wait(&full[slot], phase, a.status);
-      if (two) ok = warp_wait(&full[slot2], slot2 == 0 ? phase ^ 1 : phase, a.status) && ok;
-      if (!ok) {
-        aborted = true;
-        break;
-      }
-      SharedRecord kr[kTile], vr[kTile];
-      int nv[kTile];
-      kr[0].p = ring + slot * C::SLOT;
-      kr[1].p = ring + slot2 * C::SLOT;
-#pragma unroll
-      for (int b = 0; b < kTile; ++b) {
-        vr[b].p = kr[b].p + G::REC;
-        nv[b] = __shfl_sync(0xffffffffu, cur.nv, (at + b) & 31);
-      }
-      if (!two) nv[1] = 0;
-      int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
-      __syncwarp();
-      // Refill the slots just read with the warp's blocks R positions ahead.
-      for (int i = 0; i < (two ? 2 : 1); ++i) {
-        const int kn = k + i + R;
-        if (kn < nk) {
-          int phys;
-          if ((kn >> 5) == (k >> 5)) {
-            phys = __shfl_sync(0xffffffffu, cur.phys, kn & 31);
-          } else {
-            if (!nxt_ready) {
-              nxt = describe(kn & ~31, w_nxt, wn_nxt);
-              nxt_ready = true;
-            }
-            phys = __shfl_sync(0xffffffffu, nxt.phys, kn & 31);
-          }
-          const int sl = i ? slot2 : slot;
-          if (lane == 0) load_int4_block<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes);
-          issued = kn + 1;
-        }
-      }
-      const int step = two ? 2 : 1;
-      k += step;
-      slot += step;
-      if (slot >= R) {
-        slot -= R;
-        phase ^= 1;
-      }
+      load_stage(slot, (kn >> 5) == (i >> 4) ? cur.phys : nxt.phys, kn & 31);
+      issued = i + R + 1;
+    }
+    if (++slot == R) {
+      slot = 0;
+      phase ^= 1;
     }
   }
   // Copies still in flight (only after a timeout) must land before exit (bounded).
   if (aborted) {
     abort_flag = 1;
-    for (int kk = k; kk < issued; ++kk) mbar_wait(&full[kk % R], (kk / R) & 1, a.status);
+    for (int u = i; u < issued; ++u) mbar_wait(&full[u % R], (u / R) & 1, a.status);
   }
   int4_finish(st);
   __syncthreads();  // every warp is done with its ring: the merge takes its place
@@ -283,8 +274,8 @@ constexpr int kShRows = 64;
 
 template <int D>
 struct Int4SharedCfg {
-  using C = Int4Cfg<D, 2>;
-  static constexpr int SLOTS = 24;  // ring slots, shared out among the teams: two CTAs fit an SM
+  using C = Int4Cfg<D, 2, 2>;
+  static constexpr int SLOTS = 12;  // ring stages, shared out among the teams: two CTAs fit an SM
   static constexpr int MERGE = kShRows * C::RED * 4;  // [teams][16 RT] rows are 64 in all
   static constexpr int BUF = SLOTS * C::SLOT > MERGE ? SLOTS * C::SLOT : MERGE;
   static constexpr int SMEM = BUF + kShRows * C::QS * 4 + kMembers * (D / 2) * 8;
@@ -296,7 +287,8 @@ template <int D, bool LAZY>
 __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
                                                                          const uint8_t* v_pool) {
   constexpr int NT = 2;
-  using C = Int4Cfg<D, NT>;
+  constexpr int HL = 2;
+  using C = Int4Cfg<D, NT, HL>;
   using S = Int4SharedCfg<D>;
   using G = Int4Geom<D>;
   constexpr int HALF = D / 2;
@@ -333,13 +325,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   const int rows = nmem * a.G;
   const int RT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), TEAMS = kWarps / RT;
   const int team = warp / RT, rt = warp % RT;
-  const int R = S::SLOTS / TEAMS;  // ring slots of the team: 6, 12 or 24
+  const int R = S::SLOTS / TEAMS;  // ring stages of the team: 3, 6 or 12
   const int per_team = (nblk + TEAMS - 1) / TEAMS;
   const int kb0 = team * per_team;
   const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
   uint8_t* ring = smem + team * R * C::SLOT;
   uint64_t* full = bars + team * R;
-  const bool leader = rt == 0 && lane == 0;
   const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
   const uint32_t id_mask = (1u << a.id_bits) - 1u;
   const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
@@ -364,24 +355,25 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
       }
     }
   };
-  auto issue = [&](int sl, int phys) {
-    load_int4_block<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes);
+  const int ns = (nk + 1) / 2;  // stages: team blocks 2i, 2i + 1
+  auto load_stage = [&](int sl, int phys) {  // lanes 0 and 1's blocks; the team's first warp
+    load_int4_stage<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes, lane);
   };
   // First loads straight from the record's ids when it names all of them.
-  int issued = min(R, nk);
-  const bool rec_first = kb0 + issued <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
-  if (rec_first && leader)
-    for (int k = 0; k < issued; ++k) {
-      const int id = rec_id(kb0 + k);
-      issue(k, id >= 0 && id < a.num_pool_blocks ? id : a.num_pool_blocks);
+  int issued = min(R, ns);
+  const bool rec_first = kb0 + 2 * issued <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  if (rec_first && rt == 0)
+    for (int i = 0; i < issued; ++i) {
+      const int id = lane < 2 && 2 * i + lane < nk ? rec_id(kb0 + 2 * i + lane) : -1;
+      load_stage(i, id >= 0 ? id : a.num_pool_blocks);
     }
   int c_phys, c_nv, n_phys = a.num_pool_blocks, n_nv = 0;
   describe(0, c_phys, c_nv);
   if (nk > 32) describe(32, n_phys, n_nv);
   if (!rec_first)
-    for (int k = 0; k < issued; ++k) {
-      const int phys = __shfl_sync(0xffffffffu, c_phys, k);
-      if (leader) issue(k, phys);
+    for (int i = 0; i < issued; ++i) {
+      const int phys = __shfl_sync(0xffffffffu, c_phys, (2 * i + lane) & 31);
+      if (rt == 0) load_stage(i, phys);
     }
 
   // ------------------------------------------------------------ members and queries
@@ -414,65 +406,50 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads)
     cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), m_delta[idx / HALF], a.status);
   __syncthreads();
-  Int4Query<D, NT> q;
-  int4_build_query<D, NT>(
-      q, lane, [&](int r, int d) { return qs[(16 * rt + r) * C::QS + d]; },
-      [&](int r, int f) { return cs_tab[(16 * rt + r < rows ? (16 * rt + r) / a.G : 0) * HALF + f]; },
+  Int4Query<D, NT, HL> q;
+  int4_build_query<D, NT, HL>(
+      q, lane, [&](int r) { return qs + (16 * rt + r) * C::QS; },
+      [&](int r) { return cs_tab + (16 * rt + r < rows ? (16 * rt + r) / a.G : 0) * HALF; },
       [&](int r) { return row_scale[16 * rt + r]; });
 
   // ------------------------------------------------------------ main loop
-  Int4State<D, NT> st;
+  Int4State<D, NT, HL> st;
   int4_init(st);
   bool n_ready = true, aborted = false;
-  int k = 0, slot = 0, phase = 0;
-  for (; k < nk; k += kTile) {  // chunks of 32 and rings hold whole tiles
-    if (k > 0 && (k & 31) == 0) {
-      if (!n_ready) describe(k, n_phys, n_nv);
+  int i = 0, slot = 0, phase = 0;
+  for (; i < ns; ++i) {
+    const int at = (2 * i) & 31;
+    if (i > 0 && at == 0) {
+      if (!n_ready) describe(2 * i, n_phys, n_nv);
       c_phys = n_phys;
       c_nv = n_nv;
       n_ready = false;
     }
-    const bool two = k + 1 < nk;
     bool ok = warp_wait(&full[slot], phase, a.status);
-    if (two) ok = warp_wait(&full[slot + 1], phase, a.status) && ok;
     if (ok) {
-      SharedRecord kr[kTile], vr[kTile];
-      int nv[kTile];
-#pragma unroll
-      for (int b = 0; b < kTile; ++b) {
-        kr[b].p = ring + (slot + b) * C::SLOT;
-        vr[b].p = kr[b].p + G::REC;
-        nv[b] = __shfl_sync(0xffffffffu, c_nv, (k + b) & 31);
-      }
-      int4_attend<D, NT, kTile>(kr, vr, nv, q, st, lane);
+      const uint8_t* stage = ring + slot * C::SLOT;
+      const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
+      const int nv[2] = {__shfl_sync(0xffffffffu, c_nv, at), __shfl_sync(0xffffffffu, c_nv, at + 1)};
+      int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
     }
-    // The team's warps are done with the slots (and agree to go on) before they are refilled.
+    // The team's warps are done with the stage (and agree to go on) before it is refilled.
     if (RT > 1) ok = team_and(team, 32 * RT, ok);
     if (!ok) {
       aborted = true;
       break;
     }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const int kn = k + i + R;
-      if (kn < nk) {
-        int phys;
-        if ((kn >> 5) == (k >> 5)) {
-          phys = __shfl_sync(0xffffffffu, c_phys, kn & 31);
-        } else {
-          if (!n_ready) {
-            describe(kn & ~31, n_phys, n_nv);
-            n_ready = true;
-          }
-          phys = __shfl_sync(0xffffffffu, n_phys, kn & 31);
-        }
-        if (leader) issue(slot + i, phys);
-        issued = kn + 1;
+    if (i + R < ns) {
+      const int kn = 2 * (i + R);
+      if ((kn >> 5) != (i >> 4) && !n_ready) {
+        describe(kn & ~31, n_phys, n_nv);
+        n_ready = true;
       }
+      const int phys = __shfl_sync(0xffffffffu, (kn >> 5) == (i >> 4) ? c_phys : n_phys, (kn + lane) & 31);
+      if (rt == 0) load_stage(slot, phys);
+      issued = i + R + 1;
     }
-    slot += kTile;
-    if (slot == R) {
+    if (++slot == R) {
       slot = 0;
       phase ^= 1;
     }
@@ -480,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   // Copies still in flight (only after a timeout) must land before exit (bounded).
   if (aborted) {
     abort_flag = 1;
-    if (leader)
-      for (int kk = k; kk < issued; ++kk) mbar_wait(&full[kk % R], (kk / R) & 1, a.status);
+    if (rt == 0)
+      for (int u = i; u < issued; ++u) mbar_wait(&full[u % R], (u / R) & 1, a.status);
   }
   int4_finish(st);
   __syncthreads();  // every team is done with its ring: the merge takes its place
@@ -518,19 +495,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
 
 // ------------------------------------------------------------------ launchers
 
-template <int D, int NT, bool LAZY>
+template <int D, int NT, int HL, bool LAZY>
 static cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
-  using C = Int4Cfg<D, NT>;
+  using C = Int4Cfg<D, NT, HL>;
   const int ht = (a.G + C::ROWS - 1) / C::ROWS;
-  cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, LAZY>>(C::SMEM);
+  cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, HL, LAZY>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_int4_kernel<D, NT, LAZY><<<dim3(a.splits, a.Hkv * ht, a.B), kThreads, C::SMEM, st>>>(a, ht);
+  decode_int4_kernel<D, NT, HL, LAZY><<<dim3(a.splits, a.Hkv * ht, a.B), kThreads, C::SMEM, st>>>(a, ht);
   return cudaGetLastError();
 }
 
 template <int D, bool LAZY>
 static cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t st) {
-  return a.G <= 8 ? launch_decode_t<D, 1, LAZY>(a, st) : launch_decode_t<D, 2, LAZY>(a, st);
+  if (a.G <= 4) return launch_decode_t<D, 1, 1, LAZY>(a, st);
+  return a.G <= 8 ? launch_decode_t<D, 1, 2, LAZY>(a, st) : launch_decode_t<D, 2, 2, LAZY>(a, st);
 }
 
 cudaError_t launch_decode_int4(const DecodeArgs& a, bool lazy, cudaStream_t st) {

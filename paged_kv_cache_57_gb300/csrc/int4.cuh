@@ -15,9 +15,14 @@
 // taken off the other operand (q / 16, exact) or the output; 2^24 off the sums.
 //
 // Keys (or V's dims) are the A operand's 16 rows and the query heads its 8 columns: a
-// product takes 256 codes, twice what heads as rows would, and groups of up to 8 heads
-// pad nothing further. S^T = C q^T comes out with keys as rows; the weights become the
-// B operand of O^T = C_v^T P^T by an 8 x 8 transpose (movmatrix).
+// product takes 256 codes, twice what heads as rows would. S^T = C q^T comes out with keys
+// as rows; the weights become the B operand of O^T = C_v^T P^T by an 8 x 8 transpose
+// (movmatrix).
+//
+// The step is bound by the integer pipe (masks and shifts issue every second cycle), which
+// is why e4m3 codes (a byte 0..15 is c 2^-9, three such operations for eight codes) looked
+// better: mma.sync takes them here as conversions and two f16 products, 113 us against 104
+// on 64 x 4160 tokens.
 #pragma once
 
 #include "common.cuh"
@@ -32,9 +37,7 @@ struct Int4Geom {
   static constexpr int REC = META + kBlock * NG * 4;  // one (block, KV head)
 };
 
-// V row that holds token t of a block, and back. Lane t of a quad takes tokens 2t, 2t+1,
-// 2t+8, 2t+9 (the B operand's rows) from rows t, t+4, t+8, t+12: consecutive lanes read
-// consecutive rows.
+// V row that holds token t of a block, and back (the format's order).
 __host__ __device__ __forceinline__ int int4_v_row(int t) { return (t & 8) + 4 * (t & 1) + ((t & 7) >> 1); }
 __host__ __device__ __forceinline__ int int4_v_token(int r) { return (r & 8) + 2 * (r & 3) + ((r >> 2) & 1); }
 
@@ -63,65 +66,88 @@ __device__ __forceinline__ void bulk_copy(uint8_t* dst, const uint8_t* src, uint
                : "memory");
 }
 
-// K and V records of block `phys` (base pointers at the KV head) into a ring slot: K, then
-// V. An id outside the pool is not loaded (the barrier is just arrived).
+// Two blocks' K and V records into a ring stage ([block][K, V]), completing on `bar`: the
+// whole warp calls it with each block's id (lane 0's and lane 1's `phys`; an id outside the
+// pool is not loaded). Lanes 0..3 issue one copy each.
 template <int D>
-__device__ __forceinline__ void load_int4_block(uint8_t* slot, uint64_t* bar, int phys, int num_pool_blocks,
-                                                const uint8_t* kp, const uint8_t* vp, size_t blk_bytes) {
+__device__ __forceinline__ void load_int4_stage(uint8_t* stage, uint64_t* bar, int phys, int num_pool_blocks,
+                                                const uint8_t* kp, const uint8_t* vp, size_t blk_bytes, int lane) {
   constexpr int REC = Int4Geom<D>::REC;
-  if (phys < num_pool_blocks) {
+  const uint32_t live = __ballot_sync(0xffffffffu, lane < 2 && phys < num_pool_blocks);
+  const int ph = __shfl_sync(0xffffffffu, phys, lane >> 1);
+  if (lane == 0) {
     fence_proxy_async_smem();
-    mbar_arrive_expect_tx(bar, 2 * REC);
-    bulk_copy(slot, kp + (size_t)phys * blk_bytes, REC, bar);
-    bulk_copy(slot + REC, vp + (size_t)phys * blk_bytes, REC, bar);
-  } else {
-    mbar_arrive(bar);
+    mbar_arrive_expect_tx(bar, 2 * REC * __popc(live));
+  }
+  __syncwarp();
+  if (lane < 4 && ((live >> (lane >> 1)) & 1u)) {
+    if (lane) fence_proxy_async_smem();
+    bulk_copy(stage + lane * REC, ((lane & 1) ? vp : kp) + (size_t)ph * blk_bytes, REC, bar);
   }
 }
 
-// Query fragments of NT tiles of 8 rows (query heads), for the k-order of the codes: lane
-// (g, t) = (lane / 4, lane % 4) holds row g's dims of words D/32 t .. D/32 t + D/32 - 1 of
-// a K row. k-step 2i + h: word i, nibbles 2h, 2h + 4 in b0 and 2h + 1, 2h + 5 (over 16) in
-// b1. `f` scales a row's products (2^24 and the row's power of two) and `sum` holds its
-// sums per group, both for the rows 2t, 2t + 1 that the lane sees in the product.
-template <int D, int NT>
-struct Int4Query {
-  uint32_t b[NT][D / 16][2];
-  float f[NT][2];
-  float sum[NT][2][Int4Geom<D>::NG];
+// Query rows of a warp: NT tiles of 8, or (HL = 1, NT = 1) one tile of 4 in the products'
+// even columns, which halves the softmax's work per lane. A lane (g, t) = (lane / 4,
+// lane % 4) sees the rows HL t .. HL t + HL - 1 of a tile.
+template <int NT, int HL>
+struct Int4Rows {
+  static_assert(HL == 2 || (HL == 1 && NT == 1), "one row a lane: one tile of 4 rows");
+  static constexpr int TILE = 4 * HL;
+  static constexpr int ALL = NT * TILE;
 };
 
-// Rows are read from shared memory as raw, scaled fp32 values (each row over 2^e_row, so
-// that its largest is near 1) and rotated by the row's angles: value(row, dim) and
-// cs(row, frequency) give them, row_scale(row) = 2^e_row.
-template <int D, int NT, typename ValueFn, typename CsFn, typename ScaleFn>
-__device__ __forceinline__ void int4_build_query(Int4Query<D, NT>& q, int lane, ValueFn value, CsFn cs,
+// Query fragments for the k-order of the codes: lane (g, t) holds column g's dims of words
+// D/32 t .. D/32 t + D/32 - 1 of a K row. k-step 2i + h: word i, nibbles 2h, 2h + 4 in b0
+// and 2h + 1, 2h + 5 (over 16) in b1. `f` scales a row's products (2^24 and the row's power
+// of two) and `sum` holds its sums per group, for the rows that the lane sees.
+template <int D, int NT, int HL>
+struct Int4Query {
+  uint32_t b[NT][D / 16][2];
+  float f[NT][HL];
+  float sum[NT][HL][Int4Geom<D>::NG];
+};
+
+// Rows are raw, scaled fp32 values in shared memory (each over its power of two, so that
+// the largest is in 1..2), rotated by the row's angles: value(row), cs(row) point at them
+// (16-byte aligned), row_scale(row) is the power of two. The queries' rounding to f16 is
+// off by 2^-11 of an element (or 2^-21 of the row's largest).
+template <int D, int NT, int HL, typename ValueFn, typename CsFn, typename ScaleFn>
+__device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int lane, ValueFn value, CsFn cs,
                                                  ScaleFn row_scale) {
   constexpr int NG = Int4Geom<D>::NG, HALF = D / 2, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = 8 * nt + g;
+    const int row = HL == 1 ? g >> 1 : 8 * nt + g;
+    const float* qv = value(row);
+    const float2* ang = cs(row);
     float s[NG];
 #pragma unroll
     for (int j = 0; j < NG; ++j) s[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
+      asm volatile("" ::: "memory");  // one word's loads at a time: registers
       const int base = 64 * (i % NG) + 8 * ((W * t + i) / NG);
+      const float sgn = base < HALF ? -1.f : 1.f;
+      float v[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v[4];
+        const float4 x = *reinterpret_cast<const float4*>(qv + base + 4 * h);
+        const float4 y = *reinterpret_cast<const float4*>(qv + (base ^ HALF) + 4 * h);
+        const float4 c0 = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 4 * h);
+        const float4 c1 = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 4 * h + 2);
+        v[4 * h] = fmaf(x.x, c0.x, y.x * (sgn * c0.y));
+        v[4 * h + 1] = fmaf(x.y, c0.z, y.y * (sgn * c0.w));
+        v[4 * h + 2] = fmaf(x.z, c1.x, y.z * (sgn * c1.y));
+        v[4 * h + 3] = fmaf(x.w, c1.z, y.w * (sgn * c1.w));
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // nibbles 2h, 2h + 4, 2h + 1, 2h + 5
-          const int d = base + 2 * h + 4 * (e & 1) + (e >> 1);
-          const float2 c = cs(row, d & (HALF - 1));
-          const float sn = d < HALF ? -c.y : c.y;
-          v[e] = fmaf(value(row, d), c.x, value(row, d ^ HALF) * sn);
-        }
-        const uint32_t b0 = pack_f16x2(v[0], v[1]), b1 = pack_f16x2(v[2] * 0.0625f, v[3] * 0.0625f);
-        q.b[nt][2 * i + h][0] = b0;
-        q.b[nt][2 * i + h][1] = b1;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t b0 = pack_f16x2(v[2 * h], v[2 * h + 4]);
+        const uint32_t b1 = pack_f16x2(v[2 * h + 1] * 0.0625f, v[2 * h + 5] * 0.0625f);
         s[i % NG] += sum_op2<true>(b0) + 16.f * sum_op2<true>(b1);  // the rounded values, as the products see them
+        q.b[nt][2 * i + h][0] = HL == 1 && (g & 1) ? 0u : b0;
+        q.b[nt][2 * i + h][1] = HL == 1 && (g & 1) ? 0u : b1;
       }
     }
     const float rs = row_scale(row);
@@ -132,7 +158,7 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT>& q, int lane, 
       s[j] *= rs;
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {  // row 2t + c sits in the lanes 4 (2t + c) ..
+    for (int c = 0; c < HL; ++c) {  // column 2t + c's row sits in the lanes 4 (2t + c) ..
       const int src = 8 * t + 4 * c;
       q.f[nt][c] = __shfl_sync(0xffffffffu, rs, src) * 16777216.f;
 #pragma unroll
@@ -141,27 +167,29 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT>& q, int lane, 
   }
 }
 
-// Running state of NT tiles of 8 rows: per row the reference maximum m (log2 units), the
-// weight sum l and the zeros' sums z (partial over the lanes of equal t until
-// int4_finish), and O^T / 2^24 without the zeros: o[4 j + pp][nt], word j of the lane's
-// V words (group j), dims 64 j + 8 g + 2 pp in [0], [1] (rows 2t, 2t + 1) and the next
-// dim, times 16, in [2], [3]. Weights times V scales go to f16 over `inv`'s power of two
-// per group, which follows the scales as they grow: at most 2^8 (weights) x 2^7.
-template <int D, int NT>
+// Running state: per row the reference maximum m (log2 units), the weight sum l and the
+// zeros' sums z (partial over the lanes of equal t until int4_finish), and O^T / 2^24
+// without the zeros: o[4 j + pp][nt] is the products' columns 2t, 2t + 1 for the lane's dim
+// 2 pp of group j (int4_dims) in [0], [1] and for the next dim, times 16, in [2], [3]. With HL = 2
+// the columns are the rows 2t, 2t + 1; with HL = 1 they are row t under group 0's and
+// group 1's scales, and column 2t + j is the one that counts for group j. Weights times V
+// scales go to f16 over `inv`'s power of two per group, which follows the scales as they
+// grow: at most 2^8 (weights) x 2^7.
+template <int D, int NT, int HL>
 struct Int4State {
   float o[D / 16][NT][4];
-  float m[NT][2], l[NT][2], z[NT][2][Int4Geom<D>::NG];
+  float m[NT][HL], l[NT][HL], z[NT][HL][Int4Geom<D>::NG];
   float inv[Int4Geom<D>::NG], lim[Int4Geom<D>::NG];  // the same in all lanes; a scale above lim moves the reference
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void int4_init(Int4State<D, NT>& st) {
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) st.o[i][nt][0] = st.o[i][nt][1] = st.o[i][nt][2] = st.o[i][nt][3] = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < HL; ++c) {
       st.m[nt][c] = -INFINITY;
       st.l[nt][c] = 0.f;
 #pragma unroll
@@ -175,36 +203,34 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT>& st) {
   }
 }
 
-constexpr float kInt4RescaleLog2 = 8.f;    // a maximum is refreshed when it grows by more
+constexpr float kInt4RescaleLog2 = 8.f;      // a maximum is refreshed when it grows by more
 constexpr float kInt4ScaleHeadroom = 128.f;  // and the V scales' reference by more than this
 
-// One tile of TB blocks of one document. Only the first nv[b] slots of block b are keys
-// (0: the block is not there): the other slots' scales and zeros may hold anything.
-template <int D, int NT, int TB>
-__device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const SharedRecord (&vr)[TB], const int (&nv)[TB],
-                                            const Int4Query<D, NT>& q, Int4State<D, NT>& st, int lane) {
+// One tile: two blocks of one document. Only the first nv[b] slots of block b are keys (0:
+// the block is not there): the other slots' scales and zeros may hold anything.
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const SharedRecord (&vr)[2], const int (&nv)[2],
+                                            const Int4Query<D, NT, HL>& q, Int4State<D, NT, HL>& st, int lane) {
   using G = Int4Geom<D>;
   constexpr int NG = G::NG, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
-  bool partial = false;
-#pragma unroll
-  for (int b = 0; b < TB; ++b) partial |= nv[b] < kBlock;  // warp-uniform
+  const bool partial = nv[0] < kBlock || nv[1] < kBlock;  // warp-uniform
 
-  // S^T: rows g and g + 8 of each block, columns (query rows) 2t and 2t + 1.
-  float p[TB][NT][4];
+  // Scores of keys g and g + 8 of each block: p[block][key][tile][row].
+  float p[2][2][NT][HL];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    uint32_t w0[W], w1[W], m0[NG], m1[NG];
+  for (int b = 0; b < 2; ++b) {
+    uint32_t w0[W], w1[W], m[2][NG];
     if constexpr (W == 4) {
       const uint4 x = kr[b].v4(g * G::ROW + 16 * t), y = kr[b].v4((g + 8) * G::ROW + 16 * t);
       w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
       w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
       const uint2 u = kr[b].v2(G::META + g * 8), v = kr[b].v2(G::META + (g + 8) * 8);
-      m0[0] = u.x, m0[NG - 1] = u.y, m1[0] = v.x, m1[NG - 1] = v.y;
+      m[0][0] = u.x, m[0][NG - 1] = u.y, m[1][0] = v.x, m[1][NG - 1] = v.y;
     } else {
       const uint2 x = kr[b].v2(g * G::ROW + 8 * t), y = kr[b].v2((g + 8) * G::ROW + 8 * t);
       w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
-      m0[0] = kr[b].v1(G::META + g * 4), m1[0] = kr[b].v1(G::META + (g + 8) * 4);
+      m[0][0] = kr[b].v1(G::META + g * 4), m[1][0] = kr[b].v1(G::META + (g + 8) * 4);
     }
     float acc[NT][NG][4];
 #pragma unroll
@@ -215,7 +241,7 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const 
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t x = w0[i] >> (8 * h), y = w1[i] >> (8 * h);
+        const uint32_t x = h ? w0[i] >> 8 : w0[i], y = h ? w1[i] >> 8 : w1[i];
         const uint32_t a[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_16816_f16(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
@@ -223,29 +249,24 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t* m = e < 2 ? m0 : m1;
-        float s = meta_scale(m[0]) * acc[nt][0][e], zs = meta_zero(m[0]) * q.sum[nt][e & 1][0];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int j = 1; j < NG; ++j) {
-          s = fmaf(meta_scale(m[j]), acc[nt][j][e], s);
-          zs = fmaf(meta_zero(m[j]), q.sum[nt][e & 1][j], zs);
+        for (int c = 0; c < HL; ++c) {
+          float s = 0.f, zs = 0.f;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            s = fmaf(meta_scale(m[r][j]), acc[nt][j][2 * r + c], s);
+            zs = fmaf(meta_zero(m[r][j]), q.sum[nt][c][j], zs);
+          }
+          p[b][r][nt][c] = fmaf(q.f[nt][c], s, zs);
+          if (partial && g + 8 * r >= nv[b]) p[b][r][nt][c] = -INFINITY;
         }
-        p[b][nt][e] = fmaf(q.f[nt][e & 1], s, zs);
-      }
-    if (partial) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (g + 8 * (e >> 1) >= nv[b]) p[b][nt][e] = -INFINITY;
-    }
   }
 
   // V's scales and zeros of the same keys.
-  float vs[TB][2][NG], vz[TB][2][NG];
+  float vs[2][2][NG], vz[2][2][NG];
 #pragma unroll
-  for (int b = 0; b < TB; ++b)
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       uint32_t m[NG];
@@ -257,30 +278,26 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const 
       }
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        const bool live = !partial || g + 8 * r < nv[b];
-        vs[b][r][j] = live ? meta_scale(m[j]) : 0.f;
-        vz[b][r][j] = live ? meta_zero(m[j]) : 0.f;
+        if (partial && g + 8 * r >= nv[b]) m[j] = 0u;
+        vs[b][r][j] = meta_scale(m[j]);
+        vz[b][r][j] = meta_zero(m[j]);
       }
     }
 
   // Running maximum and V-scale reference: refreshed together, when some row's maximum or
   // some scale outgrew its reference (a vote; the cross-lane maxima only then).
-  float mx[NT][2], sm[NG];
+  float mx[NT][HL], sm[NG];
   bool grow = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      mx[nt][c] = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < TB; ++b) mx[nt][c] = fmaxf(mx[nt][c], fmaxf(p[b][nt][c], p[b][nt][c + 2]));
+    for (int c = 0; c < HL; ++c) {
+      mx[nt][c] = fmaxf(fmaxf(p[0][0][nt][c], p[0][1][nt][c]), fmaxf(p[1][0][nt][c], p[1][1][nt][c]));
       grow |= mx[nt][c] > st.m[nt][c] + kInt4RescaleLog2;
     }
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
-    sm[j] = 0.f;
-#pragma unroll
-    for (int b = 0; b < TB; ++b) sm[j] = fmaxf(sm[j], fmaxf(vs[b][0][j], vs[b][1][j]));
+    sm[j] = fmaxf(fmaxf(vs[0][0][j], vs[0][1][j]), fmaxf(vs[1][0][j], vs[1][1][j]));
     grow |= sm[j] > st.lim[j];
   }
   if (__any_sync(0xffffffffu, grow)) {
@@ -306,7 +323,7 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < HL; ++c) {
         float x = mx[nt][c];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -317,76 +334,89 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[TB], const 
 #pragma unroll
           for (int j = 0; j < NG; ++j) st.z[nt][c][j] *= alpha;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            st.o[i][nt][c] *= alpha;
-            st.o[i][nt][c + 2] *= alpha;
-          }
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (HL == 1 || (e & 1) == c) st.o[i][nt][e] *= alpha;
         }
       }
   }
 
-  // Weights; their sum and the zeros' part in fp32, times the scales in f16 (11 bits: an
-  // error of 2^-12 of a term, next to the 4 bits of the codes).
+  // Weights; their sum and the zeros' part in fp32.
 #pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    uint32_t pb[NT][NG][2];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int c = 0; c < HL; ++c) {
+      const float mu = st.m[nt][c] == -INFINITY ? 0.f : st.m[nt][c];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float mu = st.m[nt][e & 1] == -INFINITY ? 0.f : st.m[nt][e & 1];
-        p[b][nt][e] = fast_ex2(p[b][nt][e] - mu);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        st.l[nt][c] += p[b][nt][c] + p[b][nt][c + 2];
-#pragma unroll
-        for (int j = 0; j < NG; ++j)
-          st.z[nt][c][j] = fmaf(p[b][nt][c], vz[b][0][j], fmaf(p[b][nt][c + 2], vz[b][1][j], st.z[nt][c][j]));
-      }
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float s = vs[b][r][j] * st.inv[j];
-          pb[nt][j][r] = transpose_8x8(pack_f16x2(p[b][nt][2 * r] * s, p[b][nt][2 * r + 1] * s));
+          const float x = fast_ex2(p[b][r][nt][c] - mu);
+          p[b][r][nt][c] = x;
+          st.l[nt][c] += x;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) st.z[nt][c][j] = fmaf(x, vz[b][r][j], st.z[nt][c][j]);
         }
     }
-    // O^T += C_v^T P^T: rows are dims, the k-order tokens 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
-    uint32_t w[4][NG];
+
+  // O^T += C_v^T P^T: rows are dims, the k-order tokens 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
+  // Weights times scales in f16 (11 bits: off by 2^-11 of a term, next to the codes' 4).
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if constexpr (NG == 2) {
-        const uint2 x = vr[b].v2((4 * u + t) * G::ROW + 8 * g);
-        w[u][0] = x.x, w[u][NG - 1] = x.y;
+  for (int b = 0; b < 2; ++b) {
+    uint32_t pb[NT][NG][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float s[NG];
+#pragma unroll
+      for (int j = 0; j < NG; ++j) s[j] = vs[b][r][j] * st.inv[j];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (HL == 1) {  // both groups' columns at once
+          pb[nt][0][r] = transpose_8x8(pack_f16x2(p[b][r][nt][0] * s[0], p[b][r][nt][0] * s[NG - 1]));
+          pb[nt][NG - 1][r] = pb[nt][0][r];
+        } else {
+#pragma unroll
+          for (int j = 0; j < NG; ++j)
+            pb[nt][j][r] = transpose_8x8(pack_f16x2(p[b][r][nt][0] * s[j], p[b][r][nt][HL - 1] * s[j]));
+        }
+      }
+    }
+    // V's words, token rows g and g + 8 in lane g, become pairs of tokens (2t, 2t + 1) of the
+    // same four dims: column g is a half of word W (g / 2) + i.
+    uint32_t x[2][W];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if constexpr (W == 4) {
+        const uint4 y = vr[b].v4(int4_v_row(g + 8 * r) * G::ROW + 16 * t);
+        x[r][0] = y.x, x[r][1] = y.y, x[r][2] = y.z, x[r][3] = y.w;
       } else {
-        w[u][0] = vr[b].v1((4 * u + t) * G::ROW + 4 * g);
+        const uint2 y = vr[b].v2(int4_v_row(g + 8 * r) * G::ROW + 8 * t);
+        x[r][0] = y.x, x[r][1] = y.y;
       }
     }
 #pragma unroll
-    for (int j = 0; j < NG; ++j)
+    for (int i = 0; i < W; ++i) {
+      const uint32_t u = transpose_8x8(x[0][i]), v = transpose_8x8(x[1][i]);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t x = __byte_perm(w[0][j], w[1][j], hf ? 0x7632 : 0x5410);
-        const uint32_t y = __byte_perm(w[2][j], w[3][j], hf ? 0x7632 : 0x5410);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t xs = h ? u >> 8 : u, ys = h ? v >> 8 : v;
+        const uint32_t a[4] = {xs & 0x000f000fu, xs & 0x00f000f0u, ys & 0x000f000fu, ys & 0x00f000f0u};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t xs = x >> (8 * h), ys = y >> (8 * h);
-          const uint32_t a[4] = {xs & 0x000f000fu, xs & 0x00f000f0u, ys & 0x000f000fu, ys & 0x00f000f0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816_f16(st.o[4 * j + 2 * hf + h][nt], a, pb[nt][j][0], pb[nt][j][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          mma_16816_f16(st.o[4 * (i % NG) + 2 * (i / NG) + h][nt], a, pb[nt][i % NG][0], pb[nt][i % NG][1]);
       }
+    }
   }
 }
 
 // Sums the lanes' parts of l and z: after it every lane holds the rows' full sums.
-template <int D, int NT>
-__device__ __forceinline__ void int4_finish(Int4State<D, NT>& st) {
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_finish(Int4State<D, NT, HL>& st) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < HL; ++c)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         st.l[nt][c] += __shfl_xor_sync(0xffffffffu, st.l[nt][c], o);
@@ -395,14 +425,18 @@ __device__ __forceinline__ void int4_finish(Int4State<D, NT>& st) {
       }
 }
 
-// The lane's 8 dims 64 j + 8 g + 0..7 of row 8 nt + 2t + c: weighted values, unnormalised.
-template <int D, int NT>
-__device__ __forceinline__ void int4_out8(const Int4State<D, NT>& st, int j, int nt, int c, float (&v)[8]) {
+// Weighted values, unnormalised, of the lane's dims of group j and its row c of tile nt:
+// int4_dims(j, g) + 0..3 and int4_dims(j, g) + kInt4Dims2 + 0..3.
+constexpr int kInt4Dims2 = 8;
+__device__ __forceinline__ int int4_dims(int j, int g) { return 64 * j + 16 * (g >> 1) + 4 * (g & 1); }
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_out8(const Int4State<D, NT, HL>& st, int j, int nt, int c, float (&v)[8]) {
   const float r = 1.f / st.inv[j];
+  const int col = HL == 1 ? j : c;
 #pragma unroll
   for (int pp = 0; pp < 4; ++pp) {
-    v[2 * pp] = fmaf(st.o[4 * j + pp][nt][c] * 16777216.f, r, st.z[nt][c][j]);
-    v[2 * pp + 1] = fmaf(st.o[4 * j + pp][nt][c + 2] * 1048576.f, r, st.z[nt][c][j]);
+    v[2 * pp] = fmaf(st.o[4 * j + pp][nt][col] * 16777216.f, r, st.z[nt][c][j]);
+    v[2 * pp + 1] = fmaf(st.o[4 * j + pp][nt][col + 2] * 1048576.f, r, st.z[nt][c][j]);
   }
 }
 
