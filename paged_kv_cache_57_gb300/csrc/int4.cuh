@@ -9,10 +9,12 @@
 // weights (one per key and group), never elements.
 //
 // Codes enter mma.sync m16n8k16 as f16 without a conversion: a nibble in the low bits of
-// an f16 is the subnormal c 2^-24, one 4 bits higher 16 c 2^-24, both exact, and the
-// products are summed in fp32. (w & 0x000f000f) and (w & 0x00f000f0) are such pairs, so
-// eight codes cost four masks and a shift. The factor 16 of every second element is
-// taken off the other operand (q / 16, exact) or the output; 2^24 off the sums.
+// an f16 is the subnormal c 2^-24, a byte of two nibbles (c + 16 c') 2^-24, both exact, and
+// the products are summed in fp32. The operands are low nibbles c and whole bytes
+// c + 16 c': (w & 0x000f000f), (w & 0x00ff00ff) and the same of w's odd bytes, four
+// operations for eight codes (nibbles alone need five: a mask each and a shift). For the
+// queries c q + c' q' = c (q - q'/16) + (c + 16 c') q'/16; of the outputs the second is
+// (bytes - nibbles) / 16, in fp32. 2^24 is taken off the sums.
 //
 // Keys (or V's dims) are the A operand's 16 rows and the query heads its 8 columns: a
 // product takes 256 codes, twice what heads as rows would. S^T = C q^T comes out with keys
@@ -97,8 +99,8 @@ struct Int4Rows {
 };
 
 // Query fragments for the k-order of the codes: lane (g, t) holds column g's dims of words
-// D/32 t .. D/32 t + D/32 - 1 of a K row. k-step 2i + h: word i, nibbles 2h, 2h + 4 in b0
-// and 2h + 1, 2h + 5 (over 16) in b1. `f` scales a row's products (2^24 and the row's power
+// D/32 t .. D/32 t + D/32 - 1 of a K row. k-step 2i + h: word i, its bytes h and h + 2; b0
+// is q - q'/16 and b1 q'/16 for the dims (q, q') of each. `f` scales a row's products (2^24 and the row's power
 // of two) and `sum` holds its sums per group, for the rows that the lane sees.
 template <int D, int NT, int HL>
 struct Int4Query {
@@ -143,9 +145,10 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int la
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t b0 = pack_f16x2(v[2 * h], v[2 * h + 4]);
         const uint32_t b1 = pack_f16x2(v[2 * h + 1] * 0.0625f, v[2 * h + 5] * 0.0625f);
-        s[i % NG] += sum_op2<true>(b0) + 16.f * sum_op2<true>(b1);  // the rounded values, as the products see them
+        const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+        const uint32_t b0 = pack_f16x2(v[2 * h] - r.x, v[2 * h + 4] - r.y);
+        s[i % NG] += sum_op2<true>(b0) + 17.f * (r.x + r.y);  // the rounded values, as the products see them
         q.b[nt][2 * i + h][0] = HL == 1 && (g & 1) ? 0u : b0;
         q.b[nt][2 * i + h][1] = HL == 1 && (g & 1) ? 0u : b1;
       }
@@ -170,7 +173,7 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int la
 // Running state: per row the reference maximum m (log2 units), the weight sum l and the
 // zeros' sums z (partial over the lanes of equal t until int4_finish), and O^T / 2^24
 // without the zeros: o[4 j + pp][nt] is the products' columns 2t, 2t + 1 for the lane's dim
-// 2 pp of group j (int4_dims) in [0], [1] and for the next dim, times 16, in [2], [3]. With HL = 2
+// 2 pp of group j (int4_dims) in [0], [1] and for that plus 16 times the next in [2], [3]. With HL = 2
 // the columns are the rows 2t, 2t + 1; with HL = 1 they are row t under group 0's and
 // group 1's scales, and column 2t + j is the one that counts for group j. Weights times V
 // scales go to f16 over `inv`'s power of two per group, which follows the scales as they
@@ -206,6 +209,12 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
 constexpr float kInt4RescaleLog2 = 8.f;      // a maximum is refreshed when it grows by more
 constexpr float kInt4ScaleHeadroom = 128.f;  // and the V scales' reference by more than this
 
+// Bytes h and h + 2 of a word as f16 pairs: low nibbles, and whole bytes.
+__device__ __forceinline__ void int4_pair(uint32_t w, int h, uint32_t& nibbles, uint32_t& bytes) {
+  bytes = h ? __byte_perm(w, 0u, 0x4341) : w & 0x00ff00ffu;
+  nibbles = (h ? bytes : w) & 0x000f000fu;
+}
+
 // One tile: two blocks of one document. Only the first nv[b] slots of block b are keys (0:
 // the block is not there): the other slots' scales and zeros may hold anything.
 template <int D, int NT, int HL>
@@ -234,17 +243,17 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
     }
     float acc[NT][NG][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < NG; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.f;
-#pragma unroll
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t x = h ? w0[i] >> 8 : w0[i], y = h ? w1[i] >> 8 : w1[i];
-        const uint32_t a[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
+        uint32_t a[4];
+        int4_pair(w0[i], h, a[0], a[2]);
+        int4_pair(w1[i], h, a[1], a[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (i < NG && h == 0) mma_16816_f16_first(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
+          else mma_16816_f16(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
+        }
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -259,30 +268,51 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
             zs = fmaf(meta_zero(m[r][j]), q.sum[nt][c][j], zs);
           }
           p[b][r][nt][c] = fmaf(q.f[nt][c], s, zs);
-          if (partial && g + 8 * r >= nv[b]) p[b][r][nt][c] = -INFINITY;
         }
+  }
+  if (partial) {
+    asm volatile("" ::: "memory");  // a branch, not selects on every tile
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < HL; ++c)
+            if (g + 8 * r >= nv[b]) p[b][r][nt][c] = -INFINITY;
   }
 
   // V's scales and zeros of the same keys.
-  float vs[2][2][NG], vz[2][2][NG];
+  uint32_t vm[2][2][NG];
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      uint32_t m[NG];
       if constexpr (NG == 2) {
         const uint2 u = vr[b].v2(G::META + (g + 8 * r) * 8);
-        m[0] = u.x, m[NG - 1] = u.y;
+        vm[b][r][0] = u.x, vm[b][r][NG - 1] = u.y;
       } else {
-        m[0] = vr[b].v1(G::META + (g + 8 * r) * 4);
-      }
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        if (partial && g + 8 * r >= nv[b]) m[j] = 0u;
-        vs[b][r][j] = meta_scale(m[j]);
-        vz[b][r][j] = meta_zero(m[j]);
+        vm[b][r][0] = vr[b].v1(G::META + (g + 8 * r) * 4);
       }
     }
+  if (partial) {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < NG; ++j)
+          if (g + 8 * r >= nv[b]) vm[b][r][j] = 0u;
+  }
+  float vs[2][2][NG];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < NG; ++j) vs[b][r][j] = meta_scale(vm[b][r][j]);
 
   // Running maximum and V-scale reference: refreshed together, when some row's maximum or
   // some scale outgrew its reference (a vote; the cross-lane maxima only then).
@@ -356,7 +386,7 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
           p[b][r][nt][c] = x;
           st.l[nt][c] += x;
 #pragma unroll
-          for (int j = 0; j < NG; ++j) st.z[nt][c][j] = fmaf(x, vz[b][r][j], st.z[nt][c][j]);
+          for (int j = 0; j < NG; ++j) st.z[nt][c][j] = fmaf(x, meta_zero(vm[b][r][j]), st.z[nt][c][j]);
         }
     }
 
@@ -400,8 +430,9 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
       const uint32_t u = transpose_8x8(x[0][i]), v = transpose_8x8(x[1][i]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t xs = h ? u >> 8 : u, ys = h ? v >> 8 : v;
-        const uint32_t a[4] = {xs & 0x000f000fu, xs & 0x00f000f0u, ys & 0x000f000fu, ys & 0x00f000f0u};
+        uint32_t a[4];
+        int4_pair(u, h, a[0], a[1]);
+        int4_pair(v, h, a[2], a[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           mma_16816_f16(st.o[4 * (i % NG) + 2 * (i / NG) + h][nt], a, pb[nt][i % NG][0], pb[nt][i % NG][1]);
@@ -436,7 +467,7 @@ __device__ __forceinline__ void int4_out8(const Int4State<D, NT, HL>& st, int j,
 #pragma unroll
   for (int pp = 0; pp < 4; ++pp) {
     v[2 * pp] = fmaf(st.o[4 * j + pp][nt][col] * 16777216.f, r, st.z[nt][c][j]);
-    v[2 * pp + 1] = fmaf(st.o[4 * j + pp][nt][col + 2] * 1048576.f, r, st.z[nt][c][j]);
+    v[2 * pp + 1] = fmaf((st.o[4 * j + pp][nt][col + 2] - st.o[4 * j + pp][nt][col]) * 1048576.f, r, st.z[nt][c][j]);
   }
 }
 

@@ -126,8 +126,9 @@ def attention(w, k_values, v_values, lazy=True, freqs=None, sm_scale=0.0):
     """fp64 decode of workload ``w`` over pools of fp64 values [blocks, heads, 16, d] (torch, any device), and the bound
     on an int4 kernel's error, elementwise:
       2^-8 |out|                 the output's rounding to bf16 (half a step);
-      e sum_j w_j |v_j - out|    the query's rounding to f16: every score is off by at most
-                                 e = scale * 2^-11 * max_j sum_d |q_d k_jd|, a weight by that share;
+      e sum_j w_j |v_j - out|    the query's rounding to f16, as q - q'/16 and q'/16 of neighbouring dims (q, q'): the dims
+                                 are off by 2^-11 (|q| + |q'| / 8) and 2^-11 |q'|, every score by at most
+                                 e = scale * 2^-11 * 9/8 * |q| max_j |k_j|, a weight by that share;
       2^-11 sum_j w_j |v_j - z_j|  the weights' rounding to f16 times what they multiply, s c <= 15 s = max - min
                                  of the key's group, taken as 2 max|v_j| over the group;
       2^-18 sum_j w_j |v_j|      fp32 sums, exponentials and angles (5e-7 rad, 2^-20.9)."""
@@ -163,10 +164,7 @@ def attention(w, k_values, v_values, lazy=True, freqs=None, sm_scale=0.0):
         q = q.reshape(hkv, hq // hkv, d)
         wgt = torch.softmax(torch.einsum("hgd,thd->hgt", q, k) * scale, -1)
         o = torch.einsum("hgt,thd->hgd", wgt, v)
-        # |q| |k|: rotation keeps a pair's norm, and every rounding is in the relative frame
-        kn = torch.hypot(k[..., :d // 2], k[..., d // 2:])
-        qn = torch.hypot(q[..., :d // 2], q[..., d // 2:])
-        e = scale * 2.0 ** -11 * 2 * torch.einsum("hgd,thd->hgt", qn, kn).amax(-1)
+        e = scale * 2.0 ** -11 * 9 / 8 * q.norm(dim=-1) * k.norm(dim=-1).amax(0)[:, None]
         big = v.abs().reshape(-1, hkv, d // 64, 64).amax(-1)
         spread = torch.einsum("hgt,thj->hgj", wgt, 2 * big).repeat_interleave(64, -1)
         mean = torch.einsum("hgt,thd->hgd", wgt, v.abs())
