@@ -22,13 +22,13 @@ struct Int4Cfg {
   static constexpr int ROWS = Int4Rows<NT, HL>::ALL;
   static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
-  static constexpr int SLOT = 4 * Int4Geom<D>::REC;  // a ring stage: two blocks' K and V records
+  static constexpr int SLOT = Int4Loader<D>::STAGE;  // a ring stage: two blocks' K and V records
 #ifndef INT4_RING
 #define INT4_RING 2
 #endif
   static constexpr int RING = NT == 1 ? INT4_RING : 4;  // stages per warp
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
-  static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4 + kWarps * RING * 8;
+  static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4;
 };
 
 // One warp: a query row of D bf16 values times `scale` to fp32 in shared memory, over the
@@ -79,8 +79,8 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 
 // ------------------------------------------------------------------ per sequence
 // One CTA per (sequence, KV head and tile of 4, 8 or 16 query heads, split), four warps with a
-// quarter of the split's blocks each. A warp is its own loader: a ring of RING blocks, each
-// refilled by two bulk copies (K and V record) as soon as it was read.
+// quarter of the split's blocks each. A warp is its own loader: a ring of RING stages of
+// two blocks, each refilled as soon as it was read.
 template <int D, int NT, int HL, bool LAZY>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(const DecodeArgs a, int head_tiles) {
   using C = Int4Cfg<D, NT, HL>;
@@ -90,8 +90,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   float* qs = reinterpret_cast<float*>(smem + C::BUF);
   float2* cs_all = reinterpret_cast<float2*>(qs + C::ROWS * C::QS);
   float* row_scale = reinterpret_cast<float*>(cs_all + kWarps * HALF);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(row_scale + C::ROWS);
-  __shared__ int abort_flag;
   const int split = blockIdx.x, kvh = blockIdx.y / head_tiles, ht = blockIdx.y % head_tiles, s = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = min(C::ROWS, a.G - ht * C::ROWS);
@@ -113,39 +111,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   const int kb0 = warp * per_warp;
   const int nk = max(0, min(n, kb0 + per_warp) - kb0);  // blocks of this warp
   const int ns = (nk + 1) / 2;                          // stages: blocks 2i, 2i + 1
-  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
-  const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool) + head_off;
-  const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool) + head_off;
+  const Int4Loader<D> load(a.k_pool, a.v_pool, a.Hkv, kvh, lane);
   uint8_t* ring = smem + warp * R * C::SLOT;
-  uint64_t* full = bars + warp * R;
   auto load_words = [&](int kc, uint32_t& w, uint32_t& wn) {
     const int k = kc + lane, b = b0 + kb0 + k;
     w = k < nk ? __ldg(&wrow[b]) : 0u;
     wn = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
   };
-  // Lane l describes block kc + l; valid slots of the pair (l, l + 1) in one word.
+  // Lane l describes block kc + l; r.nv: valid slots of the blocks l and l + 1, and kSpecial
+  // where the pair is not two whole blocks of the document of block l - 1 (or l = 0).
+  constexpr int kSpecial = 1 << 16;
   auto describe = [&](int kc, uint32_t w, uint32_t wn) {
     LaneBlock r = describe_block(kc + lane < nk, b0 + kb0 + kc + lane, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
-    r.nv |= __shfl_down_sync(0xffffffffu, r.nv, 1) << 8;
+    const int nv1 = __shfl_down_sync(0xffffffffu, r.nv, 1), p1 = __shfl_down_sync(0xffffffffu, r.p, 1);
+    const int p_1 = __shfl_up_sync(0xffffffffu, r.p, 1);
+    const bool plain = r.nv == kBlock && nv1 == kBlock && (!LAZY || (lane > 0 && p1 == r.p && p_1 == r.p));
+    r.nv |= nv1 << 8 | (plain ? 0 : kSpecial);
+    if (r.phys >= a.num_pool_blocks) r.phys = 0;  // no keys in it: any block of the pool
     return r;
   };
   uint32_t w_cur, wn_cur, w_nxt = 0, wn_nxt = 0;
   load_words(0, w_cur, wn_cur);
   if (nk > 32) load_words(32, w_nxt, wn_nxt);
-  if (lane == 0) {
-    for (int i = 0; i < R; ++i) mbar_init(&full[i], 1);
-    fence_barrier_init();
-  }
-  if (threadIdx.x == 0) abort_flag = 0;
-  LaneBlock cur = describe(0, w_cur, wn_cur), nxt{a.num_pool_blocks, 0, 0};
+  LaneBlock cur = describe(0, w_cur, wn_cur), nxt{0, 0, 0};
   bool nxt_ready = false;
-  __syncwarp();
   auto load_stage = [&](int sl, int phys, int at) {  // the pair that lanes at, at + 1 describe
-    const int ph = __shfl_sync(0xffffffffu, phys, (at + lane) & 31);
-    load_int4_stage<D>(ring + sl * C::SLOT, &full[sl], ph, a.num_pool_blocks, kp, vp, blk_bytes, lane);
+    const int ph0 = __shfl_sync(0xffffffffu, phys, at), ph1 = __shfl_sync(0xffffffffu, phys, at + 1);
+    load(smem_u32(ring) + sl * C::SLOT, ph0, ph1, lane);
   };
-  int issued = min(R, ns);
-  for (int i = 0; i < issued; ++i) load_stage(i, cur.phys, 2 * i);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (i < ns) load_stage(i, cur.phys, 2 * i);
+    cp_async_commit();
+  }
 
   // ------------------------------------------------------------ queries
   for (int r = warp; r < C::ROWS; r += kWarps) {
@@ -173,9 +171,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
   int4_init(st);
   int p_cur = INT_MIN;  // the document that q is rotated for
   if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
-  int i = 0, slot = 0, phase = 0;
-  bool aborted = false;
-  for (; i < ns; ++i) {
+  for (int i = 0, slot = 0; i < ns; ++i) {
     const int at = (2 * i) & 31;
     if (at == 0 && i > 0) {  // advance the word chunk
       if (!nxt_ready) nxt = describe(2 * i, w_nxt, wn_nxt);
@@ -183,32 +179,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
       nxt_ready = false;
       if (2 * i + 32 < nk) load_words(2 * i + 32, w_nxt, wn_nxt);
     }
-    if (!warp_wait(&full[slot], phase, a.status)) {
-      aborted = true;
-      break;
-    }
+    cp_async_wait<R - 1>();
+    __syncwarp();
     const uint8_t* stage = ring + slot * C::SLOT;
     const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
-    const int nvs = __shfl_sync(0xffffffffu, cur.nv, at);
-    int nv[2] = {nvs & 255, (nvs >> 8) & 255};
-    if constexpr (LAZY) {
-      // A tile lies in one document: where the second block starts another, the first is
-      // attended alone, q is rotated anew, and the second follows.
-      int p = __shfl_sync(0xffffffffu, cur.p, at);
-      const int p1 = __shfl_sync(0xffffffffu, cur.p, at + 1), nv1 = nv[1];
-      bool more = nv1 > 0 && p1 != p;
-      if (more) nv[1] = 0;
-      while (true) {
+    const int info = __shfl_sync(0xffffffffu, cur.nv, at);
+    const bool special = __any_sync(0xffffffffu, info >= kSpecial);
+    int nv[2] = {kBlock, kBlock}, p1 = 0, nv1 = 0;
+    if (special) {
+      nv[0] = info & 255;
+      nv[1] = (info >> 8) & 255;
+      if constexpr (LAZY) {
+        // A tile lies in one document: where the second block starts another, the first is
+        // attended alone, q is rotated anew, and the second follows.
+        const int p = __shfl_sync(0xffffffffu, cur.p, at);
+        p1 = __shfl_sync(0xffffffffu, cur.p, at + 1);
         if (p != p_cur) rebuild(m_pos - (p_cur = p));
-        int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
-        if (!more) break;
-        more = false;
-        p = p1;
-        nv[0] = 0;
-        nv[1] = nv1;
+        if (nv[1] > 0 && p1 != p) {
+          nv1 = nv[1];
+          nv[1] = 0;
+        }
       }
-    } else {
-      int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
+    }
+    while (true) {
+      int4_attend<D, NT, HL>(kr, vr, special, nv, q, st, lane);
+      if (!LAZY || nv1 == 0) break;
+      nv[0] = 0;
+      nv[1] = nv1;
+      nv1 = 0;
+      rebuild(m_pos - (p_cur = p1));
     }
     __syncwarp();
     // Refill the stage with the warp's pair R positions ahead.
@@ -219,21 +218,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(
         nxt_ready = true;
       }
       load_stage(slot, (kn >> 5) == (i >> 4) ? cur.phys : nxt.phys, kn & 31);
-      issued = i + R + 1;
     }
-    if (++slot == R) {
-      slot = 0;
-      phase ^= 1;
-    }
-  }
-  // Copies still in flight (only after a timeout) must land before exit (bounded).
-  if (aborted) {
-    abort_flag = 1;
-    for (int u = i; u < issued; ++u) mbar_wait(&full[u % R], (u / R) & 1, a.status);
+    cp_async_commit();  // a group a step, empty at the end
+    if (++slot == R) slot = 0;
   }
   int4_finish(st);
   __syncthreads();  // every warp is done with its ring: the merge takes its place
-  if (abort_flag) return;
   float* red = reinterpret_cast<float*>(smem);
   int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
   __syncthreads();
@@ -296,20 +286,14 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   float* qs = reinterpret_cast<float*>(smem + S::BUF);               // [64][QS]
   float2* cs_tab = reinterpret_cast<float2*>(qs + kShRows * C::QS);  // [members][HALF]
   __shared__ int4 rec4[kItemInts / 4];
-  __shared__ int m_delta[kMembers], m_ok[kMembers], abort_flag;
+  __shared__ int m_delta[kMembers], m_ok[kMembers];
   __shared__ float row_scale[kShRows];
-  __shared__ uint64_t bars[S::SLOTS];
   const int* rec = reinterpret_cast<const int*>(rec4);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < kItemInts / 4)
     rec4[threadIdx.x] = __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < S::SLOTS; ++i) mbar_init(&bars[i], 1);
-    fence_barrier_init();
-  }
   __syncthreads();
   const int src = rec[0], b0 = rec[1], nblk = rec[2], last_nv = rec[3], nmem = rec[4];
   const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
@@ -330,19 +314,15 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   const int kb0 = team * per_team;
   const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
   uint8_t* ring = smem + team * R * C::SLOT;
-  uint64_t* full = bars + team * R;
   const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
   const uint32_t id_mask = (1u << a.id_bits) - 1u;
-  const size_t head_off = (size_t)kvh * G::REC, blk_bytes = (size_t)a.Hkv * G::REC;
-  const uint8_t* kp = k_pool + head_off;
-  const uint8_t* vp = v_pool + head_off;
+  const Int4Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
   auto rec_id = [&](int kb) { return rec[8 + 4 * kMembers + kb]; };
   // Lane l describes team block kc + l, as in decode_shared.cu: the block word decides, and
   // where the record names the block too the two must agree.
   auto describe = [&](int kc, int& phys, int& nv) {
     const int k = kc + lane;
-    phys = a.num_pool_blocks;
-    nv = 0;
+    phys = nv = 0;  // no keys: any block of the pool
     if (k < nk) {
       const int ph = (int)(__ldg(&wrow[k]) & id_mask);
       if (kb0 + k < LAZY_PLAN_ITEM_BLOCK_IDS && rec_id(kb0 + k) != ph) {
@@ -356,24 +336,27 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
     }
   };
   const int ns = (nk + 1) / 2;  // stages: team blocks 2i, 2i + 1
-  auto load_stage = [&](int sl, int phys) {  // lanes 0 and 1's blocks; the team's first warp
-    load_int4_stage<D>(ring + sl * C::SLOT, &full[sl], phys, a.num_pool_blocks, kp, vp, blk_bytes, lane);
-  };
+  // A stage is loaded by one warp of the team, in turn.
+  auto load_stage = [&](int sl, int ph0, int ph1) { load(smem_u32(ring) + sl * C::SLOT, ph0, ph1, lane); };
   // First loads straight from the record's ids when it names all of them.
-  int issued = min(R, ns);
-  const bool rec_first = kb0 + 2 * issued <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
-  if (rec_first && rt == 0)
-    for (int i = 0; i < issued; ++i) {
-      const int id = lane < 2 && 2 * i + lane < nk ? rec_id(kb0 + 2 * i + lane) : -1;
-      load_stage(i, id >= 0 ? id : a.num_pool_blocks);
+  const bool rec_first = kb0 + 2 * min(R - 1, ns) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  auto id_of = [&](int k) {
+    const int id = k < nk ? rec_id(kb0 + k) : 0;
+    return id >= 0 && id < a.num_pool_blocks ? id : 0;
+  };
+  if (rec_first)
+    for (int i = 0; i < R - 1; ++i) {
+      if (i < ns && i % RT == rt) load_stage(i, id_of(2 * i), id_of(2 * i + 1));
+      cp_async_commit();
     }
-  int c_phys, c_nv, n_phys = a.num_pool_blocks, n_nv = 0;
+  int c_phys, c_nv, n_phys = 0, n_nv = 0;
   describe(0, c_phys, c_nv);
   if (nk > 32) describe(32, n_phys, n_nv);
   if (!rec_first)
-    for (int i = 0; i < issued; ++i) {
-      const int phys = __shfl_sync(0xffffffffu, c_phys, (2 * i + lane) & 31);
-      if (rt == 0) load_stage(i, phys);
+    for (int i = 0; i < R - 1; ++i) {
+      const int ph0 = __shfl_sync(0xffffffffu, c_phys, 2 * i), ph1 = __shfl_sync(0xffffffffu, c_phys, 2 * i + 1);
+      if (i < ns && i % RT == rt) load_stage(i, ph0, ph1);
+      cp_async_commit();
     }
 
   // ------------------------------------------------------------ members and queries
@@ -415,9 +398,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   // ------------------------------------------------------------ main loop
   Int4State<D, NT, HL> st;
   int4_init(st);
-  bool n_ready = true, aborted = false;
-  int i = 0, slot = 0, phase = 0;
-  for (; i < ns; ++i) {
+  bool n_ready = true;
+  for (int i = 0, slot = 0, fill = R - 1; i < ns; ++i) {
     const int at = (2 * i) & 31;
     if (i > 0 && at == 0) {
       if (!n_ready) describe(2 * i, n_phys, n_nv);
@@ -425,44 +407,33 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
       c_nv = n_nv;
       n_ready = false;
     }
-    bool ok = warp_wait(&full[slot], phase, a.status);
-    if (ok) {
-      const uint8_t* stage = ring + slot * C::SLOT;
-      const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
-      const int nv[2] = {__shfl_sync(0xffffffffu, c_nv, at), __shfl_sync(0xffffffffu, c_nv, at + 1)};
-      int4_attend<D, NT, HL>(kr, vr, nv, q, st, lane);
-    }
-    // The team's warps are done with the stage (and agree to go on) before it is refilled.
-    if (RT > 1) ok = team_and(team, 32 * RT, ok);
-    if (!ok) {
-      aborted = true;
-      break;
-    }
-    __syncwarp();
-    if (i + R < ns) {
-      const int kn = 2 * (i + R);
+    // Stage i has landed for the warp that loaded it and, behind the barrier, for the team,
+    // all of whose warps are done with stage i - 1, which is refilled.
+    if (R == 3) cp_async_wait<1>();
+    else if (R == 6) cp_async_wait<4>();
+    else cp_async_wait<10>();
+    if (RT > 1) team_and(team, 32 * RT, true);
+    else __syncwarp();
+    if (i + R - 1 < ns) {
+      const int kn = 2 * (i + R - 1);
       if ((kn >> 5) != (i >> 4) && !n_ready) {
         describe(kn & ~31, n_phys, n_nv);
         n_ready = true;
       }
-      const int phys = __shfl_sync(0xffffffffu, (kn >> 5) == (i >> 4) ? c_phys : n_phys, (kn + lane) & 31);
-      if (rt == 0) load_stage(slot, phys);
-      issued = i + R + 1;
+      const int phys = (kn >> 5) == (i >> 4) ? c_phys : n_phys;
+      const int ph0 = __shfl_sync(0xffffffffu, phys, kn & 31), ph1 = __shfl_sync(0xffffffffu, phys, (kn & 31) + 1);
+      if ((i + R - 1) % RT == rt) load_stage(fill, ph0, ph1);
     }
-    if (++slot == R) {
-      slot = 0;
-      phase ^= 1;
-    }
-  }
-  // Copies still in flight (only after a timeout) must land before exit (bounded).
-  if (aborted) {
-    abort_flag = 1;
-    if (rt == 0)
-      for (int u = i; u < issued; ++u) mbar_wait(&full[u % R], (u / R) & 1, a.status);
+    cp_async_commit();  // a group a step, empty where another warp loads
+    const uint8_t* stage = ring + slot * C::SLOT;
+    const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
+    const int nv[2] = {__shfl_sync(0xffffffffu, c_nv, at), __shfl_sync(0xffffffffu, c_nv, at + 1)};
+    int4_attend<D, NT, HL>(kr, vr, __any_sync(0xffffffffu, nv[0] + nv[1] < 2 * kBlock), nv, q, st, lane);
+    if (++slot == R) slot = 0;
+    if (++fill == R) fill = 0;
   }
   int4_finish(st);
   __syncthreads();  // every team is done with its ring: the merge takes its place
-  if (abort_flag) return;
 
   // ------------------------------------------------------------ partials
   float* red = reinterpret_cast<float*>(smem);

@@ -27,7 +27,7 @@
 // on 64 x 4160 tokens.
 #pragma once
 
-#include "common.cuh"
+#include "decode_block.cuh"
 
 namespace lazy {
 
@@ -60,33 +60,52 @@ struct SharedRecord {
   __device__ __forceinline__ uint32_t v1(int off) const { return *reinterpret_cast<const uint32_t*>(p + off); }
 };
 
-// Copies one record (a multiple of 16 bytes at 16-byte boundaries) to shared memory;
-// completion is signalled on `bar` as transaction bytes.
-__device__ __forceinline__ void bulk_copy(uint8_t* dst, const uint8_t* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups of this thread have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two blocks' K and V records into a ring stage ([block][K, V]), completing on `bar`: the
-// whole warp calls it with each block's id (lane 0's and lane 1's `phys`; an id outside the
-// pool is not loaded). Lanes 0..3 issue one copy each.
+// A warp's copies of two blocks' records into a ring stage ([block][K, V]), 16 bytes a lane:
+// the rows of codes, then the four records' scales and zeros at once. (A bulk copy per
+// record took about 20 instructions each, one lane at a time, against 25 for all of these:
+// a step of 32 keys is bound by the instructions it issues.)
 template <int D>
-__device__ __forceinline__ void load_int4_stage(uint8_t* stage, uint64_t* bar, int phys, int num_pool_blocks,
-                                                const uint8_t* kp, const uint8_t* vp, size_t blk_bytes, int lane) {
-  constexpr int REC = Int4Geom<D>::REC;
-  const uint32_t live = __ballot_sync(0xffffffffu, lane < 2 && phys < num_pool_blocks);
-  const int ph = __shfl_sync(0xffffffffu, phys, lane >> 1);
-  if (lane == 0) {
-    fence_proxy_async_smem();
-    mbar_arrive_expect_tx(bar, 2 * REC * __popc(live));
+struct Int4Loader {
+  using G = Int4Geom<D>;
+  static constexpr int STAGE = 4 * G::REC;
+  static constexpr int MLANES = kBlock * G::NG * 4 / 16;  // lanes for a record's scales and zeros
+  const uint8_t *k, *v, *meta;  // the pools at the KV head, plus the lane's offset
+  uint32_t blk_bytes, meta_dst;
+
+  __device__ __forceinline__ Int4Loader(const void* k_pool, const void* v_pool, int hkv, int kvh, int lane) {
+    blk_bytes = (uint32_t)hkv * G::REC;
+    const size_t head = (size_t)kvh * G::REC;
+    k = static_cast<const uint8_t*>(k_pool) + head + 16 * lane;
+    v = static_cast<const uint8_t*>(v_pool) + head + 16 * lane;
+    const int rec = (lane / MLANES) & 3, off = G::META + 16 * (lane % MLANES);
+    meta = static_cast<const uint8_t*>((rec & 1) ? v_pool : k_pool) + head + off;
+    meta_dst = rec * G::REC + off;
   }
-  __syncwarp();
-  if (lane < 4 && ((live >> (lane >> 1)) & 1u)) {
-    if (lane) fence_proxy_async_smem();
-    bulk_copy(stage + lane * REC, ((lane & 1) ? vp : kp) + (size_t)ph * blk_bytes, REC, bar);
+
+  // Blocks ph0 and ph1 (both inside the pool) to the stage at shared address `dst`.
+  __device__ __forceinline__ void operator()(uint32_t dst, int ph0, int ph1, int lane) const {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const size_t off = (size_t)(uint32_t)(b ? ph1 : ph0) * blk_bytes;
+#pragma unroll
+      for (int c = 0; c < G::META; c += 512) {
+        cp_async16(dst + 16 * lane + 2 * b * G::REC + c, k + off + c);
+        cp_async16(dst + 16 * lane + (2 * b + 1) * G::REC + c, v + off + c);
+      }
+    }
+    if (4 * MLANES == 32 || lane < 4 * MLANES)
+      cp_async16(dst + meta_dst, meta + (size_t)(uint32_t)(lane < 2 * MLANES ? ph0 : ph1) * blk_bytes);
   }
-}
+};
 
 // Query rows of a warp: NT tiles of 8, or (HL = 1, NT = 1) one tile of 4 in the products'
 // even columns, which halves the softmax's work per lane. A lane (g, t) = (lane / 4,
@@ -215,15 +234,15 @@ __device__ __forceinline__ void int4_pair(uint32_t w, int h, uint32_t& nibbles, 
   nibbles = (h ? bytes : w) & 0x000f000fu;
 }
 
-// One tile: two blocks of one document. Only the first nv[b] slots of block b are keys (0:
-// the block is not there): the other slots' scales and zeros may hold anything.
+// One tile: two blocks of one document. With `partial` (the same in all lanes) only the
+// first nv[b] slots of block b are keys (0: the block is not there), and the other slots'
+// scales and zeros may hold anything.
 template <int D, int NT, int HL>
-__device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const SharedRecord (&vr)[2], const int (&nv)[2],
+__device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const SharedRecord (&vr)[2], bool partial, const int (&nv)[2],
                                             const Int4Query<D, NT, HL>& q, Int4State<D, NT, HL>& st, int lane) {
   using G = Int4Geom<D>;
   constexpr int NG = G::NG, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
-  const bool partial = nv[0] < kBlock || nv[1] < kBlock;  // warp-uniform
 
   // Scores of keys g and g + 8 of each block: p[block][key][tile][row].
   float p[2][2][NT][HL];
