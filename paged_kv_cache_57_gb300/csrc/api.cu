@@ -379,12 +379,57 @@ int lazy_attn_pack_block_words(const lazy_attn_params* p, int32_t num_docs, cons
   return launched(lazy::launch_pack(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static lazy::Int4Plan int4_plan(const lazy_attn_params* p, const Checked& c) {
+  return lazy::plan_decode_int4(p->num_seqs, c.G, p->num_kv_heads, p->max_blocks_per_seq, p->num_splits, sm_count());
+}
+
 size_t lazy_attn_decode_workspace_bytes(const lazy_attn_params* p) {
   Checked c;
   if (check_params(p, &c) != LAZY_OK) return 0;
+  if (kv_int4(p)) return lazy::decode_int4_workspace_bytes(int4_plan(p, c), p->num_seqs, p->head_dim);
   int splits, bps;
   plan_splits(p, &splits, &bps);
   return decode_ws_bytes(p, splits);
+}
+
+static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const void* q, const void* k_pool,
+                            const void* v_pool, const uint32_t* block_words, const int32_t* seq_lens,
+                            const int32_t* q_pos, const void* rope_table, void* out, void* workspace,
+                            size_t workspace_bytes, lazy_stream_t stream) {
+  lazy::Int4DecodeArgs a{};
+  a.plan = int4_plan(p, c);
+  const size_t need = lazy::decode_int4_workspace_bytes(a.plan, p->num_seqs, p->head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return LAZY_ERR_WORKSPACE;
+  unsigned int* st = status_ptr();
+  if (!st) return LAZY_ERR_CUDA;
+  a.q = q;
+  a.words = block_words;
+  a.seq_lens = seq_lens;
+  a.q_pos = q_pos;
+  a.rope = static_cast<const float2*>(rope_table);
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.out = out;
+  if (need > 0) {
+    const size_t parts = (size_t)2 * a.plan.ctas * a.plan.rows;
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_ml = a.ws_o + parts * p->head_dim;
+    a.prefix = reinterpret_cast<int*>(a.ws_ml + parts * 2);
+  }
+  a.status = st;
+  a.B = p->num_seqs;
+  a.Hq = p->num_q_heads;
+  a.Hkv = p->num_kv_heads;
+  a.G = c.G;
+  a.D = p->head_dim;
+  a.max_blocks = p->max_blocks_per_seq;
+  a.id_bits = c.id_bits;
+  a.num_pool_blocks = p->num_pool_blocks;
+  a.scale_log2 = scale_log2(p);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = launched(lazy::launch_decode_int4(a, p->lazy != 0, cs));
+  if (rc != LAZY_OK || a.plan.direct) return rc;
+  return launched(lazy::launch_combine_int4(a, cs));
 }
 
 static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_pool, const void* v_pool,
@@ -408,6 +453,9 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   if (p->dtype == LAZY_BF16 && c.G > 64) return LAZY_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(rope_table))
     return LAZY_ERR_INVALID_ARG;
+  if (kv_int4(p))
+    return decode_int4_impl(p, c, q, k_pool, v_pool, block_words, seq_lens, q_pos, rope_table, out, workspace,
+                            workspace_bytes, stream);
   int splits, bps;
   plan_splits(p, &splits, &bps);
   const size_t need = decode_ws_bytes(p, splits);
@@ -441,8 +489,6 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (p->dtype == LAZY_F32) {
     rc = launched(lazy::launch_decode_f32(a, p->lazy != 0, cs));
-  } else if (kv_int4(p)) {
-    rc = launched(lazy::launch_decode_int4(a, p->lazy != 0, cs));
   } else if (fp8) {
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)p->num_pool_blocks * p->num_kv_heads * lazy::kBlock;

@@ -2,6 +2,7 @@
 // shared document runs (lazy_attn_decode_shared). The arithmetic of a tile is in
 // int4.cuh; the query rows of a KV head are its heads (per sequence), or members x heads
 // (shared).
+#include <algorithm>
 #include <climits>
 
 #include "decode_block.cuh"
@@ -23,10 +24,8 @@ struct Int4Cfg {
   static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
   static constexpr int SLOT = Int4Loader<D>::STAGE;  // a ring stage: two blocks' K and V records
-#ifndef INT4_RING
-#define INT4_RING 2
-#endif
-  static constexpr int RING = NT == 1 ? INT4_RING : 4;  // stages per warp
+  static constexpr int RING = NT == 1 ? 2 : 4;       // stages per warp
+  static constexpr int CTAS = NT == 1 ? 4 : 2;       // per SM
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
   static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4;
 };
@@ -78,178 +77,348 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 }  // namespace
 
 // ------------------------------------------------------------------ per sequence
-// One CTA per (sequence, KV head and tile of 4, 8 or 16 query heads, split), four warps with a
-// quarter of the split's blocks each. A warp is its own loader: a ring of RING stages of
-// two blocks, each refilled as soon as it was read.
+// The units' blocks (a unit: a sequence, a KV head, a tile of 4, 8 or 16 of its query
+// heads) are laid end to end and cut into equal ranges, one per CTA, as many CTAs as are
+// resident at once: batches of any lengths give every CTA the same work. A CTA goes through
+// its range unit by unit; a unit that lies in one range is written out, the others' parts
+// go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that begins in CTA c's
+// range, 2 c for one that began before it) and are merged by combine_int4_kernel.
+//
+// Of a part the four warps take a quarter each. A warp is its own loader: a ring of RING
+// stages of two blocks, each refilled as soon as it was read.
+
+namespace {
+
+constexpr int kMinChunk = 16;      // blocks of a CTA at least (a stage or two per warp)
+constexpr int kDirectBlocks = 32;  // units of at most this many blocks get a CTA each
+
+__device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& seq_len) {
+  seq_len = __ldg(&a.seq_lens[s]);
+  if (seq_len < 0 || seq_len > kBlock * a.max_blocks) {
+    raise_status(a.status, LAZY_DEV_BAD_LEN);
+    seq_len = seq_len < 0 ? 0 : kBlock * a.max_blocks;
+  }
+  return (seq_len + kBlock - 1) / kBlock;
+}
+
+__device__ __forceinline__ int64_t chunk_of(const Int4DecodeArgs& a, int64_t total) {
+  if (a.plan.unit_len > 0) return a.plan.chunk;
+  const int64_t c = (total + a.plan.ctas - 1) / a.plan.ctas;
+  return c > a.plan.chunk ? c : a.plan.chunk;
+}
+
+}  // namespace
+
 template <int D, int NT, int HL, bool LAZY>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) decode_int4_kernel(const DecodeArgs a, int head_tiles) {
+__global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int4_kernel(const Int4DecodeArgs a) {
   using C = Int4Cfg<D, NT, HL>;
   using G = Int4Geom<D>;
   constexpr int HALF = D / 2, R = C::RING;
+  constexpr int kSpecial = 1 << 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + C::BUF);
   float2* cs_all = reinterpret_cast<float2*>(qs + C::ROWS * C::QS);
   float* row_scale = reinterpret_cast<float*>(cs_all + kWarps * HALF);
-  const int split = blockIdx.x, kvh = blockIdx.y / head_tiles, ht = blockIdx.y % head_tiles, s = blockIdx.z;
+  // Per warp, the blocks of two word chunks (64): ids, document starts, and per pair its
+  // valid slots (8 bits each) with kSpecial where the pair is not two whole blocks of the
+  // document of the block before (or begins a chunk).
+  __shared__ int2 d_phys[kWarps][32];
+  __shared__ int2 d_p[kWarps][32];
+  __shared__ int d_nv[kWarps][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = min(C::ROWS, a.G - ht * C::ROWS);
-  const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + ht * C::ROWS;  // the first row's head
-  int seq_len = a.seq_lens[s];
-  if (seq_len < 0 || seq_len > kBlock * a.max_blocks) {
-    if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_BAD_LEN);
-    seq_len = seq_len < 0 ? 0 : kBlock * a.max_blocks;
-  }
-  const int nb = (seq_len + kBlock - 1) / kBlock;
-  const int b0 = split * a.bps;
-  const int n = max(0, min(nb, b0 + a.bps) - b0);
-  if (n == 0 && a.splits > 1) return;  // the combine does not look here
-  const int m_pos = a.q_pos[s];
-  const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
+  const int U = a.plan.units, ht = U / a.Hkv;
 
-  // ------------------------------------------------------------ first loads
-  const int per_warp = (n + kWarps - 1) / kWarps;
-  const int kb0 = warp * per_warp;
-  const int nk = max(0, min(n, kb0 + per_warp) - kb0);  // blocks of this warp
-  const int ns = (nk + 1) / 2;                          // stages: blocks 2i, 2i + 1
-  const Int4Loader<D> load(a.k_pool, a.v_pool, a.Hkv, kvh, lane);
-  uint8_t* ring = smem + warp * R * C::SLOT;
-  auto load_words = [&](int kc, uint32_t& w, uint32_t& wn) {
-    const int k = kc + lane, b = b0 + kb0 + k;
-    w = k < nk ? __ldg(&wrow[b]) : 0u;
-    wn = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
-  };
-  // Lane l describes block kc + l; r.nv: valid slots of the blocks l and l + 1, and kSpecial
-  // where the pair is not two whole blocks of the document of block l - 1 (or l = 0).
-  constexpr int kSpecial = 1 << 16;
-  auto describe = [&](int kc, uint32_t w, uint32_t wn) {
-    LaneBlock r = describe_block(kc + lane < nk, b0 + kb0 + kc + lane, nb, seq_len, w, wn, a.id_bits, a.num_pool_blocks, a.status);
-    const int nv1 = __shfl_down_sync(0xffffffffu, r.nv, 1), p1 = __shfl_down_sync(0xffffffffu, r.p, 1);
-    const int p_1 = __shfl_up_sync(0xffffffffu, r.p, 1);
-    const bool plain = r.nv == kBlock && nv1 == kBlock && (!LAZY || (lane > 0 && p1 == r.p && p_1 == r.p));
-    r.nv |= nv1 << 8 | (plain ? 0 : kSpecial);
-    if (r.phys >= a.num_pool_blocks) r.phys = 0;  // no keys in it: any block of the pool
-    return r;
-  };
-  uint32_t w_cur, wn_cur, w_nxt = 0, wn_nxt = 0;
-  load_words(0, w_cur, wn_cur);
-  if (nk > 32) load_words(32, w_nxt, wn_nxt);
-  LaneBlock cur = describe(0, w_cur, wn_cur), nxt{0, 0, 0};
-  bool nxt_ready = false;
-  auto load_stage = [&](int sl, int phys, int at) {  // the pair that lanes at, at + 1 describe
-    const int ph0 = __shfl_sync(0xffffffffu, phys, at), ph1 = __shfl_sync(0xffffffffu, phys, at + 1);
-    load(smem_u32(ring) + sl * C::SLOT, ph0, ph1, lane);
-  };
+  // ------------------------------------------------------------ the CTA's range
+  int s = 0, seq_len = 0;
+  int64_t at = 0, left;  // place within sequence s (its units end to end); places left of the range
+  if (a.plan.unit_len > 0) {
+    const int64_t per_seq = (int64_t)U * a.plan.unit_len, lo = (int64_t)blockIdx.x * a.plan.chunk;
+    s = (int)(lo / per_seq);
+    at = lo - s * per_seq;
+    left = a.plan.chunk;
+  } else {  // every warp for itself: the total, then the sequence of the range's first place
+    int64_t total = 0;
+    for (int b = 0; b < a.B; b += 32) {
+      int len;
+      const int nb = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
+      int inc = nb;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (i < ns) load_stage(i, cur.phys, 2 * i);
-    cp_async_commit();
-  }
-
-  // ------------------------------------------------------------ queries
-  for (int r = warp; r < C::ROWS; r += kWarps) {
-    if (r < heads) {
-      const float sc = int4_load_row<D>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + r) * D, qs + r * C::QS, a.scale_log2, lane);
-      if (lane == 0) row_scale[r] = sc;
-    } else {
-      for (int c = lane; c < D; c += 32) qs[r * C::QS + c] = 0.f;
-      if (lane == 0) row_scale[r] = 1.f;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = (int)total + inc - nb;
+      total += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = (int)total;
+    total *= U;
+    const int64_t chunk = chunk_of(a, total), lo = blockIdx.x * chunk;
+    left = min(chunk, total - lo);
+    if (left <= 0) return;
+    int64_t before = 0;
+    for (s = 0; s < a.B; s += 32) {
+      int len;
+      const int nb = s + lane < a.B ? blocks_of(a, s + lane, len) : 0;
+      int inc = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, (before + inc) * U > lo);  // sequences that end behind lo
+      if (past) {
+        const int l = __ffs(past) - 1;
+        s += l;
+        at = lo - (before + __shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, nb, l)) * U;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
-  __syncthreads();
-  float2* cs = cs_all + warp * HALF;
-  Int4Query<D, NT, HL> q;
-  auto rebuild = [&](int delta) {
-    __syncwarp();
-    for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
-    __syncwarp();
-    int4_build_query<D, NT, HL>(
-        q, lane, [&](int r) { return qs + r * C::QS; }, [&](int) { return cs; }, [&](int r) { return row_scale[r]; });
-  };
-
-  // ------------------------------------------------------------ main loop
-  Int4State<D, NT, HL> st;
-  int4_init(st);
-  int p_cur = INT_MIN;  // the document that q is rotated for
-  if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
-  for (int i = 0, slot = 0; i < ns; ++i) {
-    const int at = (2 * i) & 31;
-    if (at == 0 && i > 0) {  // advance the word chunk
-      if (!nxt_ready) nxt = describe(2 * i, w_nxt, wn_nxt);
-      cur = nxt;
-      nxt_ready = false;
-      if (2 * i + 32 < nk) load_words(2 * i + 32, w_nxt, wn_nxt);
+  while (left > 0 && s < a.B) {
+    // ------------------------------------------------------------ the next part
+    const int nb = blocks_of(a, s, seq_len);
+    const int len = a.plan.unit_len > 0 ? a.plan.unit_len : nb;  // places of a unit
+    if (len == 0 || at >= (int64_t)U * len) {
+      at -= (int64_t)U * len;
+      ++s;
+      continue;
     }
-    cp_async_wait<R - 1>();
-    __syncwarp();
-    const uint8_t* stage = ring + slot * C::SLOT;
-    const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
-    const int info = __shfl_sync(0xffffffffu, cur.nv, at);
-    const bool special = __any_sync(0xffffffffu, info >= kSpecial);
-    int nv[2] = {kBlock, kBlock}, p1 = 0, nv1 = 0;
-    if (special) {
-      nv[0] = info & 255;
-      nv[1] = (info >> 8) & 255;
-      if constexpr (LAZY) {
-        // A tile lies in one document: where the second block starts another, the first is
-        // attended alone, q is rotated anew, and the second follows.
-        const int p = __shfl_sync(0xffffffffu, cur.p, at);
-        p1 = __shfl_sync(0xffffffffu, cur.p, at + 1);
-        if (p != p_cur) rebuild(m_pos - (p_cur = p));
-        if (nv[1] > 0 && p1 != p) {
-          nv1 = nv[1];
-          nv[1] = 0;
+    const int u = (int)(at / len), lo = (int)(at - (int64_t)u * len);
+    const int hi = (int)min((int64_t)len, lo + left);
+    at += hi - lo;
+    left -= hi - lo;
+    const int kvh = u / ht, head0 = (u - kvh * ht) * C::ROWS;
+    const int heads = min(C::ROWS, a.G - head0);
+    const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
+    const int n = max(0, min(hi, nb) - lo);                          // blocks of the part
+    const int m_pos = __ldg(&a.q_pos[s]);
+    const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
+
+    // ------------------------------------------------------------ first loads
+    // quarters of whole stages
+    const int per_warp = ((n + 2 * kWarps - 1) / (2 * kWarps)) * 2;
+    const int kb0 = lo + warp * per_warp;
+    const int nk = max(0, min(lo + n, kb0 + per_warp) - kb0);  // blocks of this warp
+    const int ns = (nk + 1) / 2;                               // stages: blocks 2i, 2i + 1
+    const Int4Loader<D> load(a.k_pool, a.v_pool, a.Hkv, kvh, lane);
+    const uint32_t ring = smem_u32(smem) + warp * R * C::SLOT;
+    uint32_t w_nxt = 0, wn_nxt = 0;
+    auto load_words = [&](int kc) {
+      const int k = kc + lane, b = kb0 + k;
+      w_nxt = k < nk ? __ldg(&wrow[b]) : 0u;
+      wn_nxt = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
+    };
+    auto describe = [&](int kc) {  // the chunk of w_nxt
+      const LaneBlock r = describe_block(kc + lane < nk, kb0 + kc + lane, nb, seq_len, w_nxt, wn_nxt, a.id_bits,
+                                         a.num_pool_blocks, a.status);
+      const int nv1 = __shfl_down_sync(0xffffffffu, r.nv, 1), p1 = __shfl_down_sync(0xffffffffu, r.p, 1);
+      const int p_1 = __shfl_up_sync(0xffffffffu, r.p, 1);
+      const bool plain = r.nv == kBlock && nv1 == kBlock && (!LAZY || (lane > 0 && p1 == r.p && p_1 == r.p));
+      const int k = (kc + lane) & 63;
+      reinterpret_cast<int*>(d_phys[warp])[k] = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block
+      reinterpret_cast<int*>(d_p[warp])[k] = r.p;
+      if (!(lane & 1)) d_nv[warp][k >> 1] = r.nv | nv1 << 8 | (plain ? 0 : kSpecial);
+      __syncwarp();
+    };
+    load_words(0);
+    describe(0);
+    load_words(32);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (i < ns) load(ring + i * C::SLOT, d_phys[warp][i].x, d_phys[warp][i].y, lane);
+      cp_async_commit();
+    }
+
+    // ------------------------------------------------------------ queries
+    for (int r = warp; r < C::ROWS; r += kWarps) {
+      if (r < heads) {
+        const float sc = int4_load_row<D>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + r) * D, qs + r * C::QS, a.scale_log2, lane);
+        if (lane == 0) row_scale[r] = sc;
+      } else {
+        for (int c = lane; c < D; c += 32) qs[r * C::QS + c] = 0.f;
+        if (lane == 0) row_scale[r] = 1.f;
+      }
+    }
+    __syncthreads();
+    float2* cs = cs_all + warp * HALF;
+    Int4Query<D, NT, HL> q;
+    auto rebuild = [&](int delta) {
+      __syncwarp();
+      for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
+      __syncwarp();
+      int4_build_query<D, NT, HL>(
+          q, lane, [&](int r) { return qs + r * C::QS; }, [&](int) { return cs; }, [&](int r) { return row_scale[r]; });
+    };
+    int p_cur = INT_MIN;  // the document that q is rotated for
+    if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
+
+    // ------------------------------------------------------------ main loop
+    Int4State<D, NT, HL> st;
+    int4_init(st);
+    for (int i = 0, slot = 0; i < ns; ++i) {
+      if ((i & 15) == 0) {  // a chunk of words ahead
+        describe(2 * i + 32);
+        load_words(2 * i + 64);
+      }
+      cp_async_wait<R - 1>();
+      __syncwarp();
+      const uint8_t* stage = smem + (warp * R + slot) * C::SLOT;
+      const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
+      const int info = d_nv[warp][i & 31];
+      const bool special = __any_sync(0xffffffffu, info >= kSpecial);
+      int nv[2] = {kBlock, kBlock}, p1 = 0, nv1 = 0;
+      if (special) {
+        nv[0] = info & 255;
+        nv[1] = (info >> 8) & 255;
+        if constexpr (LAZY) {
+          // A tile lies in one document: where the second block starts another, the first is
+          // attended alone, q is rotated anew, and the second follows.
+          const int2 p = d_p[warp][i & 31];
+          p1 = p.y;
+          if (p.x != p_cur) rebuild(m_pos - (p_cur = p.x));
+          if (nv[1] > 0 && p1 != p.x) {
+            nv1 = nv[1];
+            nv[1] = 0;
+          }
         }
       }
-    }
-    while (true) {
-      int4_attend<D, NT, HL>(kr, vr, special, nv, q, st, lane);
-      if (!LAZY || nv1 == 0) break;
-      nv[0] = 0;
-      nv[1] = nv1;
-      nv1 = 0;
-      rebuild(m_pos - (p_cur = p1));
-    }
-    __syncwarp();
-    // Refill the stage with the warp's pair R positions ahead.
-    if (i + R < ns) {
-      const int kn = 2 * (i + R);
-      if ((kn >> 5) != (i >> 4) && !nxt_ready) {
-        nxt = describe(kn & ~31, w_nxt, wn_nxt);
-        nxt_ready = true;
+      while (true) {
+        int4_attend<D, NT, HL>(kr, vr, special, nv, q, st, lane);
+        if (!LAZY || nv1 == 0) break;
+        nv[0] = 0;
+        nv[1] = nv1;
+        nv1 = 0;
+        rebuild(m_pos - (p_cur = p1));
       }
-      load_stage(slot, (kn >> 5) == (i >> 4) ? cur.phys : nxt.phys, kn & 31);
+      __syncwarp();
+      if (i + R < ns) {  // refill the stage with the warp's pair R positions ahead
+        const int2 ph = d_phys[warp][(i + R) & 31];
+        load(ring + slot * C::SLOT, ph.x, ph.y, lane);
+      }
+      cp_async_commit();  // a group a step, empty at the end
+      if (++slot == R) slot = 0;
     }
-    cp_async_commit();  // a group a step, empty at the end
-    if (++slot == R) slot = 0;
-  }
-  int4_finish(st);
-  __syncthreads();  // every warp is done with its ring: the merge takes its place
-  float* red = reinterpret_cast<float*>(smem);
-  int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
-    const int row = idx / D, col = idx % D;
-    float M = -INFINITY;
+    int4_finish(st);
+    __syncthreads();  // every warp is done with its ring: the merge takes its place
+    float* red = reinterpret_cast<float*>(smem);
+    int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
+    __syncthreads();
+    const bool whole = lo == 0 && hi == len;
+    const size_t slot0 = (size_t)(2 * blockIdx.x + (lo == 0 ? 1 : 0)) * C::ROWS;
+    for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
+      const int row = idx / D, col = idx % D;
+      float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * C::ROWS + row) * C::RED + D]);
-    float acc = 0.f, L = 0.f;
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * C::ROWS + row) * C::RED + D]);
+      if (M == -INFINITY) M = 0.f;  // no keys: all sums are 0 (or NaN, which stays)
+      float acc = 0.f, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* src = red + (w * C::ROWS + row) * C::RED;
+        const float f = fast_ex2(src[D] - M);
+        acc += f * src[col];
+        L += f * src[D + 1];
+      }
+      if (whole) {
+        static_cast<__nv_bfloat16*>(a.out)[(q0 + row) * D + col] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+      } else {
+        a.ws_o[(slot0 + row) * D + col] = acc;
+        if (col == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * (slot0 + row)) = make_float2(M, L);
+      }
+    }
+    __syncthreads();  // the next part's loads and queries take the merge's place
+  }
+}
+
+// out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit that lies in
+// several CTAs' ranges; 0 for a sequence without blocks. One CTA per (sequence, query head),
+// warps in turn over the parts, four in flight each. Launched as a programmatic dependent
+// of the decode kernel: it waits for that grid before it reads anything.
+template <int D>
+__global__ void __launch_bounds__(kThreads) combine_int4_kernel(const Int4DecodeArgs a) {
+  constexpr int PER = D / 32;
+  __shared__ float red[kWarps][D + 2];
+  const int s = blockIdx.x / a.Hq, h = blockIdx.x - s * a.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ht = a.plan.units / a.Hkv, kvh = h / a.G, t = (h - kvh * a.G) / a.plan.rows;
+  const int row = h - kvh * a.G - t * a.plan.rows, u = kvh * ht + t;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int64_t lo, len, total = 0;
+  if (a.plan.unit_len > 0) {
+    len = a.plan.unit_len;
+    lo = ((int64_t)s * a.plan.units + u) * len;
+  } else {
+    const int p0 = a.prefix[s];
+    len = a.prefix[s + 1] - p0;
+    lo = (int64_t)p0 * a.plan.units + u * len;
+    total = (int64_t)a.prefix[a.B] * a.plan.units;
+  }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)s * a.Hq + h) * D;
+  if (len == 0) {
+    for (int c = threadIdx.x; c < D; c += kThreads) out[c] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const int64_t chunk = chunk_of(a, total);
+  const int c0 = (int)(lo / chunk), c1 = (int)((lo + len - 1) / chunk);
+  if (c0 == c1) return;  // in one range: written there
+  float M = -INFINITY, L = 0.f, acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  constexpr int BATCH = 4;
+  for (int cb = c0 + warp; cb <= c1; cb += kWarps * BATCH) {
+    float2 ml[BATCH];
+    float v[BATCH][PER];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int c = cb + b * kWarps;
+      ml[b] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[b][i] = 0.f;
+      if (c <= c1) {
+        const size_t p = (size_t)(2 * c + (c == c0 ? 1 : 0)) * a.plan.rows + row;
+        ml[b] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * p);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[b][i] = a.ws_o[p * D + lane + 32 * i];
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) Mn = fmaxf(Mn, ml[b].x);
+    const float Mr = Mn == -INFINITY ? 0.f : Mn;
+    const float r = fast_ex2(M - Mr);
+    L *= r;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] *= r;
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const float w = fast_ex2(ml[b].x - Mr);  // an empty part (m = -inf) weighs 0
+      L = fmaf(w, ml[b].y, L);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, v[b][i], acc[i]);
+    }
+    M = Mn;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) red[warp][lane + 32 * i] = acc[i];
+  if (lane == 0) {
+    red[warp][D] = M;
+    red[warp][D + 1] = L;
+  }
+  __syncthreads();
+  for (int col = threadIdx.x; col < D; col += kThreads) {
+    float Ma = -INFINITY, x = 0.f, La = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) Ma = fmaxf(Ma, red[w][D]);
+    if (Ma == -INFINITY) Ma = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* src = red + (w * C::ROWS + row) * C::RED;
-      const float f = src[D] == -INFINITY ? 0.f : exp2f(src[D] - M);
-      acc += f * src[col];
-      L += f * src[D + 1];
+      const float f = fast_ex2(red[w][D] - Ma);
+      x += f * red[w][col];
+      La += f * red[w][D + 1];
     }
-    if (a.splits == 1) {
-      static_cast<__nv_bfloat16*>(a.out)[(q0 + row) * D + col] = __float2bfloat16_rn(L > 0.f || L != L ? acc / L : 0.f);
-    } else {
-      const size_t pidx = (q0 + row) * a.splits + split;
-      a.ws_o[pidx * D + col] = acc;
-      if (col == 0) {
-        a.ws_ml[2 * pidx] = M;
-        a.ws_ml[2 * pidx + 1] = L;
-      }
-    }
+    out[col] = __float2bfloat16_rn(La == 0.f ? 0.f : x / La);
   }
 }
 
@@ -449,10 +618,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
       for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * trows + r) * C::RED + D]);
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+    const float Mr = M == -INFINITY ? 0.f : M;
     if (m_ok[m])
       for (int tm = 0; tm < TEAMS; ++tm) {
         const float* row = red + (tm * trows + r) * C::RED;
-        const float w = row[D] == -INFINITY ? 0.f : fast_ex2(row[D] - M);
+        const float w = fast_ex2(row[D] - Mr);
         L += w * row[D + 1];
 #pragma unroll
         for (int c = 0; c < PER; ++c) acc[c] += w * row[lane + 32 * c];
@@ -466,25 +636,63 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
 
 // ------------------------------------------------------------------ launchers
 
+Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
+  Int4Plan p{};
+  p.rows = G <= 4 ? 4 : (G <= 8 ? 8 : 16);
+  p.units = Hkv * ((G + p.rows - 1) / p.rows);
+  const int mb = max_blocks > 0 ? max_blocks : 1;
+  const int64_t units = (int64_t)(B > 0 ? B : 1) * p.units;
+  if (num_splits > 0 || mb <= kDirectBlocks) {
+    const int s = num_splits > 0 ? std::min(num_splits, mb) : 1;
+    p.chunk = (mb + s - 1) / s;
+    const int splits = (mb + p.chunk - 1) / p.chunk;
+    p.unit_len = splits * p.chunk;
+    p.ctas = (int)std::min<int64_t>(units * splits, INT32_MAX);
+    p.direct = splits == 1;
+  } else {
+    const int64_t useful = (units * mb + kMinChunk - 1) / kMinChunk;
+    p.ctas = (int)std::min<int64_t>(useful, (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS));
+    p.chunk = kMinChunk;
+  }
+  return p;
+}
+
+size_t decode_int4_workspace_bytes(const Int4Plan& p, int B, int D) {
+  if (p.direct) return 0;
+  return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 1) * sizeof(int);
+}
+
 template <int D, int NT, int HL, bool LAZY>
-static cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t st) {
+static cudaError_t launch_decode_t(const Int4DecodeArgs& a, cudaStream_t st) {
   using C = Int4Cfg<D, NT, HL>;
-  const int ht = (a.G + C::ROWS - 1) / C::ROWS;
   cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, HL, LAZY>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_int4_kernel<D, NT, HL, LAZY><<<dim3(a.splits, a.Hkv * ht, a.B), kThreads, C::SMEM, st>>>(a, ht);
+  decode_int4_kernel<D, NT, HL, LAZY><<<a.plan.ctas, kThreads, C::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool LAZY>
-static cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t st) {
-  if (a.G <= 4) return launch_decode_t<D, 1, 1, LAZY>(a, st);
-  return a.G <= 8 ? launch_decode_t<D, 1, 2, LAZY>(a, st) : launch_decode_t<D, 2, 2, LAZY>(a, st);
+static cudaError_t launch_decode_d(const Int4DecodeArgs& a, cudaStream_t st) {
+  if (a.plan.rows == 4) return launch_decode_t<D, 1, 1, LAZY>(a, st);
+  return a.plan.rows == 8 ? launch_decode_t<D, 1, 2, LAZY>(a, st) : launch_decode_t<D, 2, 2, LAZY>(a, st);
 }
 
-cudaError_t launch_decode_int4(const DecodeArgs& a, bool lazy, cudaStream_t st) {
+cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t st) {
   if (a.D == 128) return lazy ? launch_decode_d<128, true>(a, st) : launch_decode_d<128, false>(a, st);
   return lazy ? launch_decode_d<64, true>(a, st) : launch_decode_d<64, false>(a, st);
+}
+
+cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hq));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128>, a) : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64>, a);
 }
 
 template <int D, bool LAZY>
