@@ -24,8 +24,12 @@ struct Int4Cfg {
   static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
   static constexpr int SLOT = Int4Loader<D>::STAGE;  // a ring stage: two blocks' K and V records
-  static constexpr int RING = NT == 1 ? 2 : 4;       // stages per warp
-  static constexpr int CTAS = NT == 1 ? 4 : 2;       // per SM
+#ifndef I4_CTAS
+#define I4_CTAS 4
+#define I4_RING 2
+#endif
+  static constexpr int RING = NT == 1 ? I4_RING : 4;       // stages per warp
+  static constexpr int CTAS = NT == 1 ? I4_CTAS : 2;       // per SM
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
   static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4;
 };

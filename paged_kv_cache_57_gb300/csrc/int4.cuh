@@ -244,36 +244,44 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
   constexpr int NG = G::NG, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
 
-  // Scores of keys g and g + 8 of each block: p[block][key][tile][row].
+  // Scores of keys g and g + 8 of each block: p[block][key][tile][row]. The two blocks' and
+  // the groups' products take turns: four sums side by side hide a product's latency.
   float p[2][2][NT][HL];
+  uint32_t kw[2][2][W], km[2][2][NG];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t w0[W], w1[W], m[2][NG];
-    if constexpr (W == 4) {
-      const uint4 x = kr[b].v4(g * G::ROW + 16 * t), y = kr[b].v4((g + 8) * G::ROW + 16 * t);
-      w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-      w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-      const uint2 u = kr[b].v2(G::META + g * 8), v = kr[b].v2(G::META + (g + 8) * 8);
-      m[0][0] = u.x, m[0][NG - 1] = u.y, m[1][0] = v.x, m[1][NG - 1] = v.y;
-    } else {
-      const uint2 x = kr[b].v2(g * G::ROW + 8 * t), y = kr[b].v2((g + 8) * G::ROW + 8 * t);
-      w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
-      m[0][0] = kr[b].v1(G::META + g * 4), m[1][0] = kr[b].v1(G::META + (g + 8) * 4);
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r;
+      if constexpr (W == 4) {
+        const uint4 x = kr[b].v4(row * G::ROW + 16 * t);
+        kw[b][r][0] = x.x, kw[b][r][1] = x.y, kw[b][r][2] = x.z, kw[b][r][3] = x.w;
+        const uint2 u = kr[b].v2(G::META + row * 8);
+        km[b][r][0] = u.x, km[b][r][NG - 1] = u.y;
+      } else {
+        const uint2 x = kr[b].v2(row * G::ROW + 8 * t);
+        kw[b][r][0] = x.x, kw[b][r][1] = x.y;
+        km[b][r][0] = kr[b].v1(G::META + row * 4);
+      }
     }
-    float acc[NT][NG][4];
+  float acc[2][NT][NG][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < W; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int b = 0; b < 2; ++b) {
         uint32_t a[4];
-        int4_pair(w0[i], h, a[0], a[2]);
-        int4_pair(w1[i], h, a[1], a[3]);
+        int4_pair(kw[b][0][i], h, a[0], a[2]);
+        int4_pair(kw[b][1][i], h, a[1], a[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (i < NG && h == 0) mma_16816_f16_first(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
-          else mma_16816_f16(acc[nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
+          if (i < NG && h == 0) mma_16816_f16_first(acc[b][nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
+          else mma_16816_f16(acc[b][nt][i % NG], a, q.b[nt][2 * i + h][0], q.b[nt][2 * i + h][1]);
         }
       }
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -283,12 +291,11 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
           float s = 0.f, zs = 0.f;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
-            s = fmaf(meta_scale(m[r][j]), acc[nt][j][2 * r + c], s);
-            zs = fmaf(meta_zero(m[r][j]), q.sum[nt][c][j], zs);
+            s = fmaf(meta_scale(km[b][r][j]), acc[b][nt][j][2 * r + c], s);
+            zs = fmaf(meta_zero(km[b][r][j]), q.sum[nt][c][j], zs);
           }
           p[b][r][nt][c] = fmaf(q.f[nt][c], s, zs);
         }
-  }
   if (partial) {
     asm volatile("" ::: "memory");  // a branch, not selects on every tile
 #pragma unroll
