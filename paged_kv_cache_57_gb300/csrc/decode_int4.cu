@@ -21,38 +21,13 @@ constexpr int kItemInts = LAZY_PLAN_ITEM_INTS;
 template <int D, int NT, int HL>
 struct Int4Cfg {
   static constexpr int ROWS = Int4Rows<NT, HL>::ALL;
-  static constexpr int QS = D + 4;   // fp32 query rows
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
   static constexpr int SLOT = Int4Loader<D>::STAGE;  // a ring stage: two blocks' K and V records
-#ifndef I4_CTAS
-#define I4_CTAS 4
-#define I4_RING 2
-#endif
-  static constexpr int RING = NT == 1 ? I4_RING : 4;       // stages per warp
-  static constexpr int CTAS = NT == 1 ? I4_CTAS : 2;       // per SM
+  static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp
+  static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
-  static constexpr int SMEM = BUF + ROWS * QS * 4 + kWarps * (D / 2) * 8 + ROWS * 4;
+  static constexpr int SMEM = BUF + kWarps * (D / 2) * 8;
 };
-
-// One warp: a query row of D bf16 values times `scale` to fp32 in shared memory, over the
-// power of two that brings its largest value to 1..2; returns that power.
-template <int D>
-__device__ __forceinline__ float int4_load_row(const __nv_bfloat16* q, float* dst, float scale, int lane) {
-  constexpr int PER = D / 32;
-  float v[PER], mx = 0.f;
-#pragma unroll
-  for (int c = 0; c < PER; ++c) {
-    v[c] = __bfloat162float(q[lane + 32 * c]) * scale;
-    mx = fmaxf(mx, fabsf(v[c]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 27u), 227u);  // 2^(+-100)
-  const float inv = __uint_as_float((254u - ex) << 23);
-#pragma unroll
-  for (int c = 0; c < PER; ++c) dst[lane + 32 * c] = v[c] * inv;
-  return __uint_as_float(ex << 23);
-}
 
 // A warp's partial of its rows to shared memory: o[D], m, l per row.
 template <int D, int NT, int HL>
@@ -72,7 +47,7 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
         *reinterpret_cast<float4*>(dst + kInt4Dims2) = make_float4(v[4], v[5], v[6], v[7]);
       }
       if (g == 0) {
-        row[D] = st.m[nt][c];
+        row[D] = st.top[nt][c] == -INFINITY ? -INFINITY : -st.neg_m[nt][c];
         row[D + 1] = st.l[nt][c];
       }
     }
@@ -120,9 +95,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   constexpr int HALF = D / 2, R = C::RING;
   constexpr int kSpecial = 1 << 16;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* qs = reinterpret_cast<float*>(smem + C::BUF);
-  float2* cs_all = reinterpret_cast<float2*>(qs + C::ROWS * C::QS);
-  float* row_scale = reinterpret_cast<float*>(cs_all + kWarps * HALF);
+  float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
   // Per warp, the blocks of two word chunks (64): ids, document starts, and per pair its
   // valid slots (8 bits each) with kSpecial where the pair is not two whole blocks of the
   // document of the block before (or begins a chunk).
@@ -236,24 +209,22 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     }
 
     // ------------------------------------------------------------ queries
-    for (int r = warp; r < C::ROWS; r += kWarps) {
-      if (r < heads) {
-        const float sc = int4_load_row<D>(static_cast<const __nv_bfloat16*>(a.q) + (q0 + r) * D, qs + r * C::QS, a.scale_log2, lane);
-        if (lane == 0) row_scale[r] = sc;
-      } else {
-        for (int c = lane; c < D; c += 32) qs[r * C::QS + c] = 0.f;
-        if (lane == 0) row_scale[r] = 1.f;
-      }
+    Int4QueryRows<NT> rows;
+    bool live[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2);
+      live[nt] = r < heads;
+      rows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) + (q0 + (live[nt] ? r : 0)) * D;
     }
-    __syncthreads();
+    int4_scale_rows<D, NT>(rows, live, a.scale_log2, lane);
     float2* cs = cs_all + warp * HALF;
     Int4Query<D, NT, HL> q;
     auto rebuild = [&](int delta) {
       __syncwarp();
       for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
       __syncwarp();
-      int4_build_query<D, NT, HL>(
-          q, lane, [&](int r) { return qs + r * C::QS; }, [&](int) { return cs; }, [&](int r) { return row_scale[r]; });
+      int4_build_query<D, NT, HL>(q, rows, lane, [&](int) { return cs; });
     };
     int p_cur = INT_MIN;  // the document that q is rotated for
     if constexpr (!LAZY) rebuild(m_pos);  // control: the pool holds absolute-position keys
@@ -441,7 +412,7 @@ struct Int4SharedCfg {
   static constexpr int SLOTS = 12;  // ring stages, shared out among the teams: two CTAs fit an SM
   static constexpr int MERGE = kShRows * C::RED * 4;  // [teams][16 RT] rows are 64 in all
   static constexpr int BUF = SLOTS * C::SLOT > MERGE ? SLOTS * C::SLOT : MERGE;
-  static constexpr int SMEM = BUF + kShRows * C::QS * 4 + kMembers * (D / 2) * 8;
+  static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;
 };
 
 }  // namespace
@@ -456,11 +427,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
   using G = Int4Geom<D>;
   constexpr int HALF = D / 2;
   extern __shared__ __align__(128) uint8_t smem[];  // the teams' rings, then the merge area
-  float* qs = reinterpret_cast<float*>(smem + S::BUF);               // [64][QS]
-  float2* cs_tab = reinterpret_cast<float2*>(qs + kShRows * C::QS);  // [members][HALF]
+  float2* cs_tab = reinterpret_cast<float2*>(smem + S::BUF);  // [members][HALF]
   __shared__ int4 rec4[kItemInts / 4];
   __shared__ int m_delta[kMembers], m_ok[kMembers];
-  __shared__ float row_scale[kShRows];
   const int* rec = reinterpret_cast<const int*>(rec4);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv;
@@ -548,25 +517,23 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
     m_delta[m] = delta;
   }
   __syncthreads();
-  for (int r = warp; r < 16 * RT; r += kWarps) {
-    const int m = r / a.G;
-    if (r < rows && m_ok[m]) {
-      const size_t qh = (size_t)mem_seq(m) * a.Hq + (size_t)kvh * a.G + (r - m * a.G);
-      const float sc = int4_load_row<D>(static_cast<const __nv_bfloat16*>(a.q) + qh * D, qs + r * C::QS, a.scale_log2, lane);
-      if (lane == 0) row_scale[r] = sc;
-    } else {
-      for (int c = lane; c < D; c += 32) qs[r * C::QS + c] = 0.f;
-      if (lane == 0) row_scale[r] = 1.f;
-    }
+  Int4QueryRows<NT> qrows;
+  bool live[NT];
+  int mem[NT];  // the lane's rows' members
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 16 * rt + 8 * nt + (lane >> 2), m = r / a.G;
+    live[nt] = r < rows && m_ok[r < rows ? m : 0];
+    mem[nt] = live[nt] ? m : 0;
+    qrows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) +
+                  ((live[nt] ? (size_t)mem_seq(m) * a.Hq + (r - m * a.G) : 0) + (size_t)kvh * a.G) * D;
   }
+  int4_scale_rows<D, NT>(qrows, live, a.scale_log2, lane);
   for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads)
     cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), m_delta[idx / HALF], a.status);
   __syncthreads();
   Int4Query<D, NT, HL> q;
-  int4_build_query<D, NT, HL>(
-      q, lane, [&](int r) { return qs + (16 * rt + r) * C::QS; },
-      [&](int r) { return cs_tab + (16 * rt + r < rows ? (16 * rt + r) / a.G : 0) * HALF; },
-      [&](int r) { return row_scale[16 * rt + r]; });
+  int4_build_query<D, NT, HL>(q, qrows, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
 
   // ------------------------------------------------------------ main loop
   Int4State<D, NT, HL> st;

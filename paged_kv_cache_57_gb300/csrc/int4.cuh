@@ -46,6 +46,11 @@ __host__ __device__ __forceinline__ int int4_v_token(int r) { return (r & 8) + 2
 __device__ __forceinline__ float meta_scale(uint32_t m) { return __uint_as_float(m << 16); }
 __device__ __forceinline__ float meta_zero(uint32_t m) { return __uint_as_float(m & 0xffff0000u); }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -119,8 +124,9 @@ struct Int4Rows {
 
 // Query fragments for the k-order of the codes: lane (g, t) holds column g's dims of words
 // D/32 t .. D/32 t + D/32 - 1 of a K row. k-step 2i + h: word i, its bytes h and h + 2; b0
-// is q - q'/16 and b1 q'/16 for the dims (q, q') of each. `f` scales a row's products (2^24 and the row's power
-// of two) and `sum` holds its sums per group, for the rows that the lane sees.
+// is q - q'/16 and b1 q'/16 for the dims (q, q') of each. A score, in log2 units, is f times
+// the products' sums with the keys' scales and zeros: f is 2^24 and the row's power of two,
+// `sum` the row's sums per group over f. Both are for the rows that the lane sees.
 template <int D, int NT, int HL>
 struct Int4Query {
   uint32_t b[NT][D / 16][2];
@@ -128,39 +134,73 @@ struct Int4Query {
   float sum[NT][HL][Int4Geom<D>::NG];
 };
 
-// Rows are raw, scaled fp32 values in shared memory (each over its power of two, so that
-// the largest is in 1..2), rotated by the row's angles: value(row), cs(row) point at them
-// (16-byte aligned), row_scale(row) is the power of two. The queries' rounding to f16 is
-// off by 2^-11 of an element (or 2^-21 of the row's largest).
-template <int D, int NT, int HL, typename ValueFn, typename CsFn, typename ScaleFn>
-__device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int lane, ValueFn value, CsFn cs,
-                                                 ScaleFn row_scale) {
+// The rows of the queries (bf16) that a lane reads, row 8 nt + g (or g / 2), with the factor
+// that scales them (softmax scale, log2 e, and over the row's power of two `pow2`, so that
+// the largest value is in 1..2; 0 for a row that is not there, whose pointer is another's).
+template <int NT>
+struct Int4QueryRows {
+  const __nv_bfloat16* q[NT];
+  float mul[NT], pow2[NT];
+};
+
+// First dim of a lane's word i.
+template <int D>
+__device__ __forceinline__ int int4_word_dim(int t, int i) {
+  constexpr int NG = Int4Geom<D>::NG, W = D / 32;
+  return 64 * (i % NG) + 8 * ((W * t + i) / NG);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Fills mul and pow2 from the rows' values (all lanes).
+template <int D, int NT>
+__device__ __forceinline__ void int4_scale_rows(Int4QueryRows<NT>& r, const bool (&live)[NT], float scale, int lane) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    uint32_t mx = 0u;  // |bf16| compares as its bits
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(r.q[nt] + int4_word_dim<D>(lane & 3, i)));
+      mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu)),
+                    x.w & 0x7fff7fffu);
+    }
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float m = fmaxf(bf16_lo(mx), bf16_hi(mx)) * scale;
+    const uint32_t ex = min(max(__float_as_uint(m) >> 23, 27u), 227u);  // 2^(+-100)
+    r.pow2[nt] = __uint_as_float(ex << 23);
+    r.mul[nt] = live[nt] ? scale * __uint_as_float((254u - ex) << 23) : 0.f;
+  }
+}
+
+// Rotates the rows by their angles: cs(nt) points at the (cos, sin) of the lane's row (shared
+// memory, 16-byte aligned). The rounding to f16 is off by 2^-11 of an operand.
+template <int D, int NT, int HL, typename CsFn>
+__device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, const Int4QueryRows<NT>& rows, int lane, CsFn cs) {
   constexpr int NG = Int4Geom<D>::NG, HALF = D / 2, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int row = HL == 1 ? g >> 1 : 8 * nt + g;
-    const float* qv = value(row);
-    const float2* ang = cs(row);
+    const float2* ang = cs(nt);
+    const float mul = rows.mul[nt];
     float s[NG];
 #pragma unroll
     for (int j = 0; j < NG; ++j) s[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       asm volatile("" ::: "memory");  // one word's loads at a time: registers
-      const int base = 64 * (i % NG) + 8 * ((W * t + i) / NG);
+      const int base = int4_word_dim<D>(t, i);
       const float sgn = base < HALF ? -1.f : 1.f;
+      const uint4 x4 = __ldg(reinterpret_cast<const uint4*>(rows.q[nt] + base));
+      const uint4 y4 = __ldg(reinterpret_cast<const uint4*>(rows.q[nt] + (base ^ HALF)));
+      const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
       float v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 x = *reinterpret_cast<const float4*>(qv + base + 4 * h);
-        const float4 y = *reinterpret_cast<const float4*>(qv + (base ^ HALF) + 4 * h);
-        const float4 c0 = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 4 * h);
-        const float4 c1 = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 4 * h + 2);
-        v[4 * h] = fmaf(x.x, c0.x, y.x * (sgn * c0.y));
-        v[4 * h + 1] = fmaf(x.y, c0.z, y.y * (sgn * c0.w));
-        v[4 * h + 2] = fmaf(x.z, c1.x, y.z * (sgn * c1.y));
-        v[4 * h + 3] = fmaf(x.w, c1.z, y.w * (sgn * c1.w));
+      for (int h = 0; h < 4; ++h) {
+        const float4 c = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 2 * h);
+        v[2 * h] = fmaf(bf16_lo(x[h]), c.x, bf16_lo(y[h]) * (sgn * c.y)) * mul;
+        v[2 * h + 1] = fmaf(bf16_hi(x[h]), c.z, bf16_hi(y[h]) * (sgn * c.w)) * mul;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -172,24 +212,24 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int la
         q.b[nt][2 * i + h][1] = HL == 1 && (g & 1) ? 0u : b1;
       }
     }
-    const float rs = row_scale(row);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       s[j] += __shfl_xor_sync(0xffffffffu, s[j], 1);
       s[j] += __shfl_xor_sync(0xffffffffu, s[j], 2);
-      s[j] *= rs;
+      s[j] *= 1.f / 16777216.f;
     }
 #pragma unroll
     for (int c = 0; c < HL; ++c) {  // column 2t + c's row sits in the lanes 4 (2t + c) ..
       const int src = 8 * t + 4 * c;
-      q.f[nt][c] = __shfl_sync(0xffffffffu, rs, src) * 16777216.f;
+      q.f[nt][c] = __shfl_sync(0xffffffffu, rows.pow2[nt], src) * 16777216.f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) q.sum[nt][c][j] = __shfl_sync(0xffffffffu, s[j], src);
     }
   }
 }
 
-// Running state: per row the reference maximum m (log2 units), the weight sum l and the
+// Running state: per row the reference maximum as -m (log2 units; 0 before the first key)
+// and `top`, the value of score / f that refreshes it, the weight sum l and the
 // zeros' sums z (partial over the lanes of equal t until int4_finish), and O^T / 2^24
 // without the zeros: o[4 j + pp][nt] is the products' columns 2t, 2t + 1 for the lane's dim
 // 2 pp of group j (int4_dims) in [0], [1] and for that plus 16 times the next in [2], [3]. With HL = 2
@@ -200,7 +240,7 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, int la
 template <int D, int NT, int HL>
 struct Int4State {
   float o[D / 16][NT][4];
-  float m[NT][HL], l[NT][HL], z[NT][HL][Int4Geom<D>::NG];
+  float neg_m[NT][HL], top[NT][HL], l[NT][HL], z[NT][HL][Int4Geom<D>::NG];
   float inv[Int4Geom<D>::NG], lim[Int4Geom<D>::NG];  // the same in all lanes; a scale above lim moves the reference
 };
 
@@ -212,7 +252,8 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
     for (int i = 0; i < D / 16; ++i) st.o[i][nt][0] = st.o[i][nt][1] = st.o[i][nt][2] = st.o[i][nt][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < HL; ++c) {
-      st.m[nt][c] = -INFINITY;
+      st.neg_m[nt][c] = 0.f;
+      st.top[nt][c] = -INFINITY;
       st.l[nt][c] = 0.f;
 #pragma unroll
       for (int j = 0; j < Int4Geom<D>::NG; ++j) st.z[nt][c][j] = 0.f;
@@ -244,7 +285,7 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
   constexpr int NG = G::NG, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
 
-  // Scores of keys g and g + 8 of each block: p[block][key][tile][row]. The two blocks' and
+  // Scores over f of keys g and g + 8 of each block: p[block][key][tile][row]. The two blocks' and
   // the groups' products take turns: four sums side by side hide a product's latency.
   float p[2][2][NT][HL];
   uint32_t kw[2][2][W], km[2][2][NG];
@@ -288,13 +329,13 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int c = 0; c < HL; ++c) {
-          float s = 0.f, zs = 0.f;
+          float s = meta_zero(km[b][r][0]) * q.sum[nt][c][0];
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
+            if (j > 0) s = fmaf(meta_zero(km[b][r][j]), q.sum[nt][c][j], s);
             s = fmaf(meta_scale(km[b][r][j]), acc[b][nt][j][2 * r + c], s);
-            zs = fmaf(meta_zero(km[b][r][j]), q.sum[nt][c][j], zs);
           }
-          p[b][r][nt][c] = fmaf(q.f[nt][c], s, zs);
+          p[b][r][nt][c] = s;
         }
   if (partial) {
     asm volatile("" ::: "memory");  // a branch, not selects on every tile
@@ -349,7 +390,7 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
 #pragma unroll
     for (int c = 0; c < HL; ++c) {
       mx[nt][c] = fmaxf(fmaxf(p[0][0][nt][c], p[0][1][nt][c]), fmaxf(p[1][0][nt][c], p[1][1][nt][c]));
-      grow |= mx[nt][c] > st.m[nt][c] + kInt4RescaleLog2;
+      grow |= mx[nt][c] > st.top[nt][c];
     }
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
@@ -383,9 +424,11 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
         float x = mx[nt][c];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        if (x > st.m[nt][c] + kInt4RescaleLog2) {
-          const float alpha = fast_ex2(st.m[nt][c] - x);  // 0 while the row had no key
-          st.m[nt][c] = x;
+        if (x > st.top[nt][c]) {
+          x *= q.f[nt][c];
+          const float alpha = st.top[nt][c] == -INFINITY ? 0.f : fast_ex2(-st.neg_m[nt][c] - x);
+          st.neg_m[nt][c] = -x;
+          st.top[nt][c] = __fdividef(x + kInt4RescaleLog2, q.f[nt][c]);
           st.l[nt][c] *= alpha;
 #pragma unroll
           for (int j = 0; j < NG; ++j) st.z[nt][c][j] *= alpha;
@@ -403,12 +446,11 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < HL; ++c) {
-      const float mu = st.m[nt][c] == -INFINITY ? 0.f : st.m[nt][c];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float x = fast_ex2(p[b][r][nt][c] - mu);
+          const float x = fast_ex2(fmaf(p[b][r][nt][c], q.f[nt][c], st.neg_m[nt][c]));
           p[b][r][nt][c] = x;
           st.l[nt][c] += x;
 #pragma unroll
@@ -417,24 +459,29 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
     }
 
   // O^T += C_v^T P^T: rows are dims, the k-order tokens 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
-  // Weights times scales in f16 (11 bits: off by 2^-11 of a term, next to the codes' 4).
+  // Weights, scales (exact over their reference) and their products in f16: off by 2^-10 of
+  // a term, next to the codes' 4 bits.
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     uint32_t pb[NT][NG][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float s[NG];
+      if constexpr (HL == 1) {  // both groups' columns at once
+        const uint32_t s = pack_f16x2(vs[b][r][0] * st.inv[0], vs[b][r][NG - 1] * st.inv[NG - 1]);
+        pb[0][0][r] = transpose_8x8(mul_f16x2(pack_f16x2(p[b][r][0][0], p[b][r][0][0]), s));
+        pb[0][NG - 1][r] = pb[0][0][r];
+      } else {
+        uint32_t s[NG];
 #pragma unroll
-      for (int j = 0; j < NG; ++j) s[j] = vs[b][r][j] * st.inv[j];
+        for (int j = 0; j < NG; ++j) {
+          const float x = vs[b][r][j] * st.inv[j];
+          s[j] = pack_f16x2(x, x);
+        }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (HL == 1) {  // both groups' columns at once
-          pb[nt][0][r] = transpose_8x8(pack_f16x2(p[b][r][nt][0] * s[0], p[b][r][nt][0] * s[NG - 1]));
-          pb[nt][NG - 1][r] = pb[nt][0][r];
-        } else {
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t x = pack_f16x2(p[b][r][nt][0], p[b][r][nt][HL - 1]);
 #pragma unroll
-          for (int j = 0; j < NG; ++j)
-            pb[nt][j][r] = transpose_8x8(pack_f16x2(p[b][r][nt][0] * s[j], p[b][r][nt][HL - 1] * s[j]));
+          for (int j = 0; j < NG; ++j) pb[nt][j][r] = transpose_8x8(mul_f16x2(x, s[j]));
         }
       }
     }

@@ -129,8 +129,8 @@ def attention(w, k_values, v_values, lazy=True, freqs=None, sm_scale=0.0):
       e sum_j w_j |v_j - out|    the query's rounding to f16, as q - q'/16 and q'/16 of neighbouring dims (q, q'): the dims
                                  are off by 2^-11 (|q| + |q'| / 8) and 2^-11 |q'|, every score by at most
                                  e = scale * 2^-11 * 9/8 * |q| max_j |k_j|, a weight by that share;
-      2^-11 sum_j w_j |v_j - z_j|  the weights' rounding to f16 times what they multiply, s c <= 15 s = max - min
-                                 of the key's group, taken as 2 max|v_j| over the group;
+      2^-10 sum_j w_j |v_j - z_j|  the rounding of the weights and of weight times scale to f16, times what they multiply:
+                                 s c <= 15 s = max - min of the key's group, taken as 2 max|v_j| over the group;
       2^-18 sum_j w_j |v_j|      fp32 sums, exponentials and angles (5e-7 rad, 2^-20.9)."""
     import torch
     dev = k_values.device
@@ -170,5 +170,5 @@ def attention(w, k_values, v_values, lazy=True, freqs=None, sm_scale=0.0):
         mean = torch.einsum("hgt,thd->hgd", wgt, v.abs())
         dev_o = torch.stack([torch.einsum("gt,tgd->gd", wgt[h], (v[:, h, None] - o[h][None]).abs()) for h in range(hkv)])
         out[i] = o.reshape(hq, d)
-        bound[i] = (2.0 ** -8 * o.abs() + e[..., None] * dev_o + 2.0 ** -11 * spread + 2.0 ** -18 * mean).reshape(hq, d)
+        bound[i] = (2.0 ** -8 * o.abs() + e[..., None] * dev_o + 2.0 ** -10 * spread + 2.0 ** -18 * mean).reshape(hq, d)
     return out, bound
