@@ -398,76 +398,70 @@ __global__ void __launch_bounds__(kThreads) combine_int4_kernel(const Int4Decode
 }
 
 // ------------------------------------------------------------------ shared runs
-// One CTA per (work item, KV head). The item's rows (members x heads, at most 64) are
-// tiles of 16; the warps form 4 / RT teams of RT warps, a team with a contiguous part of
-// the item's blocks and a ring for them, a warp with one of the tiles, as in
-// decode_shared.cu.
+// One CTA per (work item, KV head, 32 of its up to 64 rows). Rows are members x heads; a
+// warp takes a tile of 8 of them (of 4 where there are no more), and the warps form 4 / RT
+// teams of RT = 1, 2 or 4 warps with a contiguous part of the item's blocks and a ring of
+// stages each. Tiles of 16 rows would convert each code half as often, but hold 240
+// registers, two CTAs an SM: 197 us against LAZY_SH70 on 32 x 16384 tokens with 8 heads.
 namespace {
 
-constexpr int kShRows = 64;
+constexpr int kShRows = 32;    // rows of a CTA
+constexpr int kShStages = 8;   // ring stages, shared out among the teams
 
 template <int D>
 struct Int4SharedCfg {
-  using C = Int4Cfg<D, 2, 2>;
-  static constexpr int SLOTS = 12;  // ring stages, shared out among the teams: two CTAs fit an SM
-  static constexpr int MERGE = kShRows * C::RED * 4;  // [teams][16 RT] rows are 64 in all
-  static constexpr int BUF = SLOTS * C::SLOT > MERGE ? SLOTS * C::SLOT : MERGE;
+  static constexpr int SLOT = Int4Loader<D>::STAGE;
+  static constexpr int RED = D + 4;                   // merge rows: o[D], m, l
+  static constexpr int MERGE = kWarps * 8 * RED * 4;  // [teams][8 RT] rows are 32 in all
+  static constexpr int BUF = kShStages * SLOT > MERGE ? kShStages * SLOT : MERGE;
   static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;
+};
+
+// What the CTA's warps share of an item.
+struct Int4Item {
+  int rec[kItemInts];
+  int delta[kMembers], ok[kMembers];  // rotation offset of each member; it passed its checks
+  int2 d_phys[kWarps][32];            // per team: the blocks of two word chunks
+  int2 d_nv[kWarps][32];              // and their valid slots
 };
 
 }  // namespace
 
-template <int D, bool LAZY>
-__global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
-                                                                         const uint8_t* v_pool) {
-  constexpr int NT = 2;
-  constexpr int HL = 2;
-  using C = Int4Cfg<D, NT, HL>;
-  using S = Int4SharedCfg<D>;
+// The item's rows row0 .. row0 + 8 RT - 1 (4 with HL = 1), from `rows` of them.
+template <int D, int HL, int RT>
+__device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
+                                                 Int4Item& it, uint8_t* smem, const float2* cs_tab, int kvh, int row0,
+                                                 int rows) {
+  using C = Int4SharedCfg<D>;
   using G = Int4Geom<D>;
-  constexpr int HALF = D / 2;
-  extern __shared__ __align__(128) uint8_t smem[];  // the teams' rings, then the merge area
-  float2* cs_tab = reinterpret_cast<float2*>(smem + S::BUF);  // [members][HALF]
-  __shared__ int4 rec4[kItemInts / 4];
-  __shared__ int m_delta[kMembers], m_ok[kMembers];
-  const int* rec = reinterpret_cast<const int*>(rec4);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv;
+  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = kShStages / TEAMS, AHEAD = RT == 1 ? R : R - 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kItemInts / 4)
-    rec4[threadIdx.x] = __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
-  __syncthreads();
-  const int src = rec[0], b0 = rec[1], nblk = rec[2], last_nv = rec[3], nmem = rec[4];
-  const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
-                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= kShRows;
-  if (!item_ok) {  // uniform over the CTA: nothing is loaded or written
-    if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
-    return;
-  }
-  auto mem_seq = [&](int m) { return rec[8 + 4 * m]; };
-  auto mem_slot = [&](int m) { return rec[8 + 4 * m + 2]; };
-
-  // ------------------------------------------------------------ teams and first loads
-  const int rows = nmem * a.G;
-  const int RT = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4), TEAMS = kWarps / RT;
   const int team = warp / RT, rt = warp % RT;
-  const int R = S::SLOTS / TEAMS;  // ring stages of the team: 3, 6 or 12
-  const int per_team = (nblk + TEAMS - 1) / TEAMS;
+  const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3];
+
+  // ------------------------------------------------------------ first loads
+  // parts of whole stages
+  const int per_team = (nblk + 2 * TEAMS - 1) / (2 * TEAMS) * 2;
   const int kb0 = team * per_team;
   const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
-  uint8_t* ring = smem + team * R * C::SLOT;
+  const int ns = (nk + 1) / 2;                             // stages: team blocks 2i, 2i + 1
+  const Int4Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
+  const uint32_t ring = smem_u32(smem) + team * R * C::SLOT;
   const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
   const uint32_t id_mask = (1u << a.id_bits) - 1u;
-  const Int4Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
-  auto rec_id = [&](int kb) { return rec[8 + 4 * kMembers + kb]; };
-  // Lane l describes team block kc + l, as in decode_shared.cu: the block word decides, and
-  // where the record names the block too the two must agree.
-  auto describe = [&](int kc, int& phys, int& nv) {
+  const int* ids = it.rec + 8 + 4 * kMembers;  // the record's block ids
+  uint32_t w_nxt = 0u;
+  auto load_words = [&](int kc) {
+    if (kc + lane < nk) w_nxt = __ldg(&wrow[kc + lane]);
+  };
+  // Chunk kc of the team's words (w_nxt) to its descriptors, by every warp of the team alike.
+  // The block word decides; where the record names the block too the two must agree.
+  auto describe = [&](int kc) {
     const int k = kc + lane;
-    phys = nv = 0;  // no keys: any block of the pool
+    int phys = 0, nv = 0;  // no keys: any block of the pool
     if (k < nk) {
-      const int ph = (int)(__ldg(&wrow[k]) & id_mask);
-      if (kb0 + k < LAZY_PLAN_ITEM_BLOCK_IDS && rec_id(kb0 + k) != ph) {
+      const int ph = (int)(w_nxt & id_mask);
+      if (kb0 + k < LAZY_PLAN_ITEM_BLOCK_IDS && ids[kb0 + k] != ph) {
         raise_status(a.status, LAZY_DEV_LAYOUT);
       } else if (ph < a.num_pool_blocks) {
         phys = ph;
@@ -476,34 +470,146 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
         raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
       }
     }
+    if (rt == 0) {
+      reinterpret_cast<int*>(it.d_phys[team])[k & 63] = phys;
+      reinterpret_cast<int*>(it.d_nv[team])[k & 63] = nv;
+    }
+    __syncwarp();
   };
-  const int ns = (nk + 1) / 2;  // stages: team blocks 2i, 2i + 1
-  // A stage is loaded by one warp of the team, in turn.
-  auto load_stage = [&](int sl, int ph0, int ph1) { load(smem_u32(ring) + sl * C::SLOT, ph0, ph1, lane); };
+  load_words(0);
   // First loads straight from the record's ids when it names all of them.
-  const bool rec_first = kb0 + 2 * min(R - 1, ns) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  const bool rec_first = kb0 + 2 * min(AHEAD, ns) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
   auto id_of = [&](int k) {
-    const int id = k < nk ? rec_id(kb0 + k) : 0;
+    const int id = k < nk ? ids[kb0 + k] : 0;
     return id >= 0 && id < a.num_pool_blocks ? id : 0;
   };
-  if (rec_first)
-    for (int i = 0; i < R - 1; ++i) {
-      if (i < ns && i % RT == rt) load_stage(i, id_of(2 * i), id_of(2 * i + 1));
+  if (rec_first) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i < ns && i % RT == rt) load(ring + i * C::SLOT, id_of(2 * i), id_of(2 * i + 1), lane);
       cp_async_commit();
     }
-  int c_phys, c_nv, n_phys = 0, n_nv = 0;
-  describe(0, c_phys, c_nv);
-  if (nk > 32) describe(32, n_phys, n_nv);
-  if (!rec_first)
-    for (int i = 0; i < R - 1; ++i) {
-      const int ph0 = __shfl_sync(0xffffffffu, c_phys, 2 * i), ph1 = __shfl_sync(0xffffffffu, c_phys, 2 * i + 1);
-      if (i < ns && i % RT == rt) load_stage(i, ph0, ph1);
+  }
+  describe(0);
+  load_words(32);
+  if (RT > 1) team_and(team, 32 * RT, true);
+  if (!rec_first) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i < ns && i % RT == rt) load(ring + i * C::SLOT, it.d_phys[team][i].x, it.d_phys[team][i].y, lane);
       cp_async_commit();
     }
+  }
 
-  // ------------------------------------------------------------ members and queries
+  // ------------------------------------------------------------ queries
+  auto mem_seq = [&](int m) { return it.rec[8 + 4 * m]; };
+  auto mem_slot = [&](int m) { return it.rec[8 + 4 * m + 2]; };
+  Int4QueryRows<1> qrows;
+  const int r = row0 + (HL == 1 ? lane >> 3 : 8 * rt + (lane >> 2)), rc = r < rows ? r : row0;
+  const int mem = rc / a.G;
+  const bool live[1] = {r < rows && it.ok[mem]};
+  qrows.q[0] = static_cast<const __nv_bfloat16*>(a.q) +
+               ((live[0] ? (size_t)mem_seq(mem) * a.Hq + (rc - mem * a.G) : 0) + (size_t)kvh * a.G) * D;
+  int4_scale_rows<D, 1>(qrows, live, a.scale_log2, lane);
+  Int4Query<D, 1, HL> q;
+  int4_build_query<D, 1, HL>(q, qrows, lane, [&](int) { return cs_tab + mem * HALF; });
+
+  // ------------------------------------------------------------ main loop
+  Int4State<D, 1, HL> st;
+  int4_init(st);
+  const uint8_t* ring_p = smem + team * R * C::SLOT;
+  for (int i = 0; i < ns; ++i) {
+    // Stage i has landed for the warp that loaded it and, behind the barrier, for the team,
+    // all of whose warps are done with stage i - 1: with RT > 1 that one is refilled.
+    cp_async_wait<AHEAD - 1>();
+    if (RT > 1) team_and(team, 32 * RT, true);
+    else __syncwarp();
+    if ((i & 15) == 0) {  // a chunk of words ahead, over the one that all are done with
+      describe(2 * i + 32);
+      load_words(2 * i + 64);
+    }
+    if (RT > 1) {
+      const int n = i + AHEAD;
+      if (n < ns && n % RT == rt) {
+        const int2 ph = it.d_phys[team][n & 31];
+        load(ring + (n % R) * C::SLOT, ph.x, ph.y, lane);
+      }
+      cp_async_commit();  // a group a step, empty where another warp loads
+    }
+    const uint8_t* stage = ring_p + (i % R) * C::SLOT;
+    const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
+    const int2 v = it.d_nv[team][i & 31];
+    const int nv[2] = {v.x, v.y};
+    int4_attend<D, 1, HL>(kr, vr, __any_sync(0xffffffffu, v.x + v.y < 2 * kBlock), nv, q, st, lane);
+    if (RT == 1) {
+      __syncwarp();
+      if (i + R < ns) {
+        const int2 ph = it.d_phys[team][(i + R) & 31];
+        load(ring + (i % R) * C::SLOT, ph.x, ph.y, lane);
+      }
+      cp_async_commit();
+    }
+  }
+  int4_finish(st);
+  __syncthreads();  // every team is done with its ring: the merge takes its place
+
+  // ------------------------------------------------------------ partials
+  float* red = reinterpret_cast<float*>(smem);
+  int4_store_partial(st, red + (team * RT + rt) * 8 * C::RED, C::RED, lane);
+  __syncthreads();
+  constexpr int PER = D / 32;
+  const int n = min(rows - row0, HL == 1 ? 4 : 8 * RT);
+  for (int x = warp; x < n; x += kWarps) {
+    const int m = (row0 + x) / a.G, h = row0 + x - m * a.G;
+    if (mem_slot(m) < 0 || mem_slot(m) >= a.num_slots) continue;
+    float M = -INFINITY, acc[PER], L = 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+    if (it.ok[m]) {  // a member that failed its checks leaves an empty partial
+#pragma unroll
+      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * RT * 8 + x) * C::RED + D]);
+      const float Mr = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int tm = 0; tm < TEAMS; ++tm) {
+        const float* row = red + (tm * RT * 8 + x) * C::RED;
+        const float w = fast_ex2(row[D] - Mr);
+        L += w * row[D + 1];
+#pragma unroll
+        for (int c = 0; c < PER; ++c) acc[c] += w * row[lane + 32 * c];
+      }
+    }
+    const size_t pidx = (size_t)mem_slot(m) * a.Hq + (size_t)kvh * a.G + h;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) a.ws_o[pidx * D + lane + 32 * c] = acc[c];
+    if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * pidx) = make_float2(M, L);
+  }
+}
+
+template <int D, bool LAZY>
+__global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
+                                                                         const uint8_t* v_pool, int halves) {
+  using C = Int4SharedCfg<D>;
+  constexpr int HALF = D / 2;
+  extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
+  float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][HALF]
+  __shared__ __align__(16) Int4Item it;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv / halves, half = blockIdx.x / a.Hkv % halves;
+  if (threadIdx.x < kItemInts / 4)
+    reinterpret_cast<int4*>(it.rec)[threadIdx.x] =
+        __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
+  __syncthreads();
+  const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3], nmem = it.rec[4];
+  const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
+                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= 2 * kShRows;
+  if (!item_ok) {  // uniform over the CTA: nothing is loaded or written
+    if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
+    return;
+  }
+  const int row0 = half * kShRows, all = nmem * a.G, rows = min(all, row0 + kShRows);
+  if (row0 >= all) return;
   if (threadIdx.x < nmem) {
-    const int m = threadIdx.x, seq = mem_seq(m), bm = rec[8 + 4 * m + 1], slot = mem_slot(m);
+    const int m = threadIdx.x, seq = it.rec[8 + 4 * m], bm = it.rec[8 + 4 * m + 1], slot = it.rec[8 + 4 * m + 2];
     bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
     int delta = 0;
     if (good) {
@@ -513,96 +619,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_shared_int4_kernel(const S
       delta = LAZY ? qp - mi.p : qp;
     }
     if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
-    m_ok[m] = good;
-    m_delta[m] = delta;
+    it.ok[m] = good;
+    it.delta[m] = delta;
   }
   __syncthreads();
-  Int4QueryRows<NT> qrows;
-  bool live[NT];
-  int mem[NT];  // the lane's rows' members
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 16 * rt + 8 * nt + (lane >> 2), m = r / a.G;
-    live[nt] = r < rows && m_ok[r < rows ? m : 0];
-    mem[nt] = live[nt] ? m : 0;
-    qrows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) +
-                  ((live[nt] ? (size_t)mem_seq(m) * a.Hq + (r - m * a.G) : 0) + (size_t)kvh * a.G) * D;
-  }
-  int4_scale_rows<D, NT>(qrows, live, a.scale_log2, lane);
-  for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads)
-    cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), m_delta[idx / HALF], a.status);
+  // the angles of the CTA's members
+  const int m0 = row0 / a.G, m1 = (rows - 1) / a.G;
+  for (int idx = m0 * HALF + threadIdx.x; idx < (m1 + 1) * HALF; idx += kThreads)
+    cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), it.delta[idx / HALF], a.status);
   __syncthreads();
-  Int4Query<D, NT, HL> q;
-  int4_build_query<D, NT, HL>(q, qrows, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
-
-  // ------------------------------------------------------------ main loop
-  Int4State<D, NT, HL> st;
-  int4_init(st);
-  bool n_ready = true;
-  for (int i = 0, slot = 0, fill = R - 1; i < ns; ++i) {
-    const int at = (2 * i) & 31;
-    if (i > 0 && at == 0) {
-      if (!n_ready) describe(2 * i, n_phys, n_nv);
-      c_phys = n_phys;
-      c_nv = n_nv;
-      n_ready = false;
-    }
-    // Stage i has landed for the warp that loaded it and, behind the barrier, for the team,
-    // all of whose warps are done with stage i - 1, which is refilled.
-    if (R == 3) cp_async_wait<1>();
-    else if (R == 6) cp_async_wait<4>();
-    else cp_async_wait<10>();
-    if (RT > 1) team_and(team, 32 * RT, true);
-    else __syncwarp();
-    if (i + R - 1 < ns) {
-      const int kn = 2 * (i + R - 1);
-      if ((kn >> 5) != (i >> 4) && !n_ready) {
-        describe(kn & ~31, n_phys, n_nv);
-        n_ready = true;
-      }
-      const int phys = (kn >> 5) == (i >> 4) ? c_phys : n_phys;
-      const int ph0 = __shfl_sync(0xffffffffu, phys, kn & 31), ph1 = __shfl_sync(0xffffffffu, phys, (kn & 31) + 1);
-      if ((i + R - 1) % RT == rt) load_stage(fill, ph0, ph1);
-    }
-    cp_async_commit();  // a group a step, empty where another warp loads
-    const uint8_t* stage = ring + slot * C::SLOT;
-    const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
-    const int nv[2] = {__shfl_sync(0xffffffffu, c_nv, at), __shfl_sync(0xffffffffu, c_nv, at + 1)};
-    int4_attend<D, NT, HL>(kr, vr, __any_sync(0xffffffffu, nv[0] + nv[1] < 2 * kBlock), nv, q, st, lane);
-    if (++slot == R) slot = 0;
-    if (++fill == R) fill = 0;
-  }
-  int4_finish(st);
-  __syncthreads();  // every team is done with its ring: the merge takes its place
-
-  // ------------------------------------------------------------ partials
-  float* red = reinterpret_cast<float*>(smem);
-  const int trows = 16 * RT;
-  int4_store_partial(st, red + (team * trows + 16 * rt) * C::RED, C::RED, lane);
-  __syncthreads();
-  constexpr int PER = D / 32;
-  for (int r = warp; r < rows; r += kWarps) {
-    const int m = r / a.G, h = r - m * a.G;
-    if (mem_slot(m) < 0 || mem_slot(m) >= a.num_slots) continue;
-    float M = -INFINITY, acc[PER], L = 0.f;
-    if (m_ok[m])  // a member that failed its checks leaves an empty partial
-      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * trows + r) * C::RED + D]);
-#pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = 0.f;
-    const float Mr = M == -INFINITY ? 0.f : M;
-    if (m_ok[m])
-      for (int tm = 0; tm < TEAMS; ++tm) {
-        const float* row = red + (tm * trows + r) * C::RED;
-        const float w = fast_ex2(row[D] - Mr);
-        L += w * row[D + 1];
-#pragma unroll
-        for (int c = 0; c < PER; ++c) acc[c] += w * row[lane + 32 * c];
-      }
-    const size_t pidx = (size_t)mem_slot(m) * a.Hq + (size_t)kvh * a.G + h;
-#pragma unroll
-    for (int c = 0; c < PER; ++c) a.ws_o[pidx * D + lane + 32 * c] = acc[c];
-    if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * pidx) = make_float2(M, L);
-  }
+  const int n = rows - row0;
+  if (n <= 4) shared_int4_rows<D, 1, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
+  else if (n <= 8) shared_int4_rows<D, 2, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
+  else if (n <= 16) shared_int4_rows<D, 2, 2>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
+  else shared_int4_rows<D, 2, 4>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -671,8 +701,11 @@ static cudaError_t launch_shared_t(const SharedDecodeArgs& a, const void* k_pool
   constexpr int SMEM = Int4SharedCfg<D>::SMEM;
   cudaError_t e = set_smem_once<decode_shared_int4_kernel<D, LAZY>>(SMEM);
   if (e != cudaSuccess) return e;
-  decode_shared_int4_kernel<D, LAZY><<<(unsigned)((long long)a.num_items * a.Hkv), kThreads, SMEM, st>>>(
-      a, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool));
+  const int halves = std::min(kMembers * a.G, 2 * kShRows) > kShRows ? 2 : 1;
+  const long long grid = (long long)a.num_items * a.Hkv * halves;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  decode_shared_int4_kernel<D, LAZY><<<(unsigned)grid, kThreads, SMEM, st>>>(
+      a, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), halves);
   return cudaGetLastError();
 }
 
