@@ -427,16 +427,19 @@ struct Int4Item {
 
 }  // namespace
 
-// The item's rows row0 .. row0 + 8 RT - 1 (4 with HL = 1), from `rows` of them.
-template <int D, int HL, int RT>
+// The item's rows row0 .. row0 + 8 RT - 1 (4 with HL = 1, where RT = 1), from `rows` of them.
+// One body for every RT: one per RT made the four warps of a scheduler wait two cycles an
+// instruction for their code.
+template <int D, int HL>
 __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
                                                  Int4Item& it, uint8_t* smem, const float2* cs_tab, int kvh, int row0,
-                                                 int rows) {
+                                                 int rows, int RT) {
   using C = Int4SharedCfg<D>;
   using G = Int4Geom<D>;
-  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = kShStages / TEAMS, AHEAD = RT == 1 ? R : R - 1;
+  constexpr int HALF = D / 2;
+  const int TEAMS = kWarps / RT, R = kShStages / TEAMS, AHEAD = R - 1;  // R = 2, 4 or 8
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = warp / RT, rt = warp % RT;
+  const int team = warp / RT, rt = warp & (RT - 1);
   const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3];
 
   // ------------------------------------------------------------ first loads
@@ -484,9 +487,8 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
     return id >= 0 && id < a.num_pool_blocks ? id : 0;
   };
   if (rec_first) {
-#pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      if (i < ns && i % RT == rt) load(ring + i * C::SLOT, id_of(2 * i), id_of(2 * i + 1), lane);
+      if (i < ns && (i & (RT - 1)) == rt) load(ring + i * C::SLOT, id_of(2 * i), id_of(2 * i + 1), lane);
       cp_async_commit();
     }
   }
@@ -494,9 +496,8 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   load_words(32);
   if (RT > 1) team_and(team, 32 * RT, true);
   if (!rec_first) {
-#pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      if (i < ns && i % RT == rt) load(ring + i * C::SLOT, it.d_phys[team][i].x, it.d_phys[team][i].y, lane);
+      if (i < ns && (i & (RT - 1)) == rt) load(ring + i * C::SLOT, it.d_phys[team][i].x, it.d_phys[team][i].y, lane);
       cp_async_commit();
     }
   }
@@ -520,35 +521,30 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   const uint8_t* ring_p = smem + team * R * C::SLOT;
   for (int i = 0; i < ns; ++i) {
     // Stage i has landed for the warp that loaded it and, behind the barrier, for the team,
-    // all of whose warps are done with stage i - 1: with RT > 1 that one is refilled.
-    cp_async_wait<AHEAD - 1>();
-    if (RT > 1) team_and(team, 32 * RT, true);
-    else __syncwarp();
+    // all of whose warps are done with stage i - 1, which is refilled.
+    if (RT == 1) {
+      cp_async_wait<0>();
+      __syncwarp();
+    } else {
+      if (RT == 2) cp_async_wait<2>();
+      else cp_async_wait<6>();
+      team_and(team, 32 * RT, true);
+    }
     if ((i & 15) == 0) {  // a chunk of words ahead, over the one that all are done with
       describe(2 * i + 32);
       load_words(2 * i + 64);
     }
-    if (RT > 1) {
-      const int n = i + AHEAD;
-      if (n < ns && n % RT == rt) {
-        const int2 ph = it.d_phys[team][n & 31];
-        load(ring + (n % R) * C::SLOT, ph.x, ph.y, lane);
-      }
-      cp_async_commit();  // a group a step, empty where another warp loads
+    const int n = i + AHEAD;
+    if (n < ns && (n & (RT - 1)) == rt) {
+      const int2 ph = it.d_phys[team][n & 31];
+      load(ring + (n & (R - 1)) * C::SLOT, ph.x, ph.y, lane);
     }
-    const uint8_t* stage = ring_p + (i % R) * C::SLOT;
+    cp_async_commit();  // a group a step, empty where another warp loads
+    const uint8_t* stage = ring_p + (i & (R - 1)) * C::SLOT;
     const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
     const int2 v = it.d_nv[team][i & 31];
     const int nv[2] = {v.x, v.y};
     int4_attend<D, 1, HL>(kr, vr, __any_sync(0xffffffffu, v.x + v.y < 2 * kBlock), nv, q, st, lane);
-    if (RT == 1) {
-      __syncwarp();
-      if (i + R < ns) {
-        const int2 ph = it.d_phys[team][(i + R) & 31];
-        load(ring + (i % R) * C::SLOT, ph.x, ph.y, lane);
-      }
-      cp_async_commit();
-    }
   }
   int4_finish(st);
   __syncthreads();  // every team is done with its ring: the merge takes its place
@@ -566,10 +562,8 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = 0.f;
     if (it.ok[m]) {  // a member that failed its checks leaves an empty partial
-#pragma unroll
       for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * RT * 8 + x) * C::RED + D]);
       const float Mr = M == -INFINITY ? 0.f : M;
-#pragma unroll
       for (int tm = 0; tm < TEAMS; ++tm) {
         const float* row = red + (tm * RT * 8 + x) * C::RED;
         const float w = fast_ex2(row[D] - Mr);
@@ -629,10 +623,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
     cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), it.delta[idx / HALF], a.status);
   __syncthreads();
   const int n = rows - row0;
-  if (n <= 4) shared_int4_rows<D, 1, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
-  else if (n <= 8) shared_int4_rows<D, 2, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
-  else if (n <= 16) shared_int4_rows<D, 2, 2>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
-  else shared_int4_rows<D, 2, 4>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows);
+  if (n <= 4) shared_int4_rows<D, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, 1);
+  else shared_int4_rows<D, 2>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, n <= 8 ? 1 : (n <= 16 ? 2 : 4));
 }
 
 // ------------------------------------------------------------------ launchers
