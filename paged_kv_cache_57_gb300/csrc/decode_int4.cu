@@ -23,7 +23,7 @@ struct Int4Cfg {
   static constexpr int ROWS = Int4Rows<NT, HL>::ALL;
   static constexpr int RED = D + 4;  // merge rows: o[D], m, l
   static constexpr int SLOT = Int4Loader<D>::STAGE;  // a ring stage: two blocks' K and V records
-  static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp
+  static constexpr int RING = 2;                // stages per warp
   static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
   static constexpr int SMEM = BUF + kWarps * (D / 2) * 8;

@@ -141,8 +141,14 @@ def _dptr(t: Optional[torch.Tensor], name: str, dtype=None, device_required=True
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (3 us of a call's 10), where torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -271,9 +277,10 @@ def decode(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tenso
     dt = _tdt(p)
     if out is None:
         out = torch.empty_like(q)
-    nws = decode_workspace_bytes(p)
-    if workspace is None and nws:
-        workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
+    if workspace is None:  # the library checks a given workspace's size itself
+        nws = decode_workspace_bytes(p)
+        if nws:
+            workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     head = (ctypes.byref(p), _dptr(q, "q", dt), _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p)),
             _dptr(block_words, "block_words"), _dptr(seq_lens, "seq_lens", torch.int32),
@@ -482,10 +489,13 @@ def empty_pools(p: Params, device="cuda"):
                  for _ in range(2))
 
 
-def _check_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor) -> None:
-    n = p.num_pool_blocks * p.num_kv_heads * (pool_record_bytes(p) if p.kv_dtype == LAZY_INT4 else BLOCK * p.head_dim)
+def _cache_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
+    """The pools' pointers, checked: type, device, size."""
+    dt = _kvdt(p)
+    n = p.num_pool_blocks * p.num_kv_heads * (p.head_dim * 9 if p.kv_dtype == LAZY_INT4 else BLOCK * p.head_dim)
     if k_pool.numel() < n or v_pool.numel() < n:
         raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
+    return _dptr(k_pool, "k_pool", dt), _dptr(v_pool, "v_pool", dt)
 
 
 def token_slots(blocks, first: int, count: int) -> np.ndarray:
@@ -503,17 +513,15 @@ def cache_write(p: Params, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     """Writes rows k, v [T, Hkv, d] (any token and head strides, d contiguous) into the slots
     [T] int32 of the pools, in the pools' type (lazy_attn_cache_write)."""
     dt, shape = _tdt(p), (slots.numel(), p.num_kv_heads, p.head_dim)
-    for name, x in (("k", k), ("v", v)):
-        if not x.is_cuda or x.dtype != dt:
-            raise ValueError(f"{name} must be a {dt} CUDA tensor")
-        if x.shape != shape or (x.stride(2) != 1 and x.numel()):
-            raise ValueError(f"{name} must have shape {shape} with contiguous rows, got {tuple(x.shape)}, "
-                             f"strides {x.stride()}")
-    _check_pools(p, k_pool, v_pool)
-    kvdt = _kvdt(p)
-    rc = _lib.lazy_attn_cache_write(ctypes.byref(p), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                                    v.stride(0), v.stride(1), shape[0], _dptr(slots, "slots", torch.int32),
-                                    _dptr(k_pool, "k_pool", kvdt), _dptr(v_pool, "v_pool", kvdt), _stream(stream))
+    if not (k.is_cuda and v.is_cuda) or k.dtype != dt or v.dtype != dt:
+        raise ValueError(f"k and v must be {dt} CUDA tensors")
+    sk, sv = k.stride(), v.stride()
+    if k.shape != shape or v.shape != shape or ((sk[2] != 1 or sv[2] != 1) and k.numel()):
+        raise ValueError(f"k and v must have shape {shape} and contiguous rows, got {tuple(k.shape)}, strides {sk} and "
+                         f"{tuple(v.shape)}, strides {sv}")
+    kp, vp = _cache_pools(p, k_pool, v_pool)
+    rc = _lib.lazy_attn_cache_write(ctypes.byref(p), k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], shape[0],
+                                    _dptr(slots, "slots", torch.int32), kp, vp, _stream(stream))
     _check(rc, "cache_write")
 
 
@@ -523,17 +531,15 @@ def cache_read(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor, block_ids:
     pool for the calls that take no quantised one, prefill above all. Returns (k_out, v_out)."""
     dt, n = _tdt(p), block_ids.numel()
     shape = (n, p.num_kv_heads, BLOCK, p.head_dim)
+    kp, vp = _cache_pools(p, k_pool, v_pool)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+        k_out = k_pool.new_empty(shape, dtype=dt)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
+        v_out = k_pool.new_empty(shape, dtype=dt)
     if min(k_out.numel(), v_out.numel()) < n * p.num_kv_heads * BLOCK * p.head_dim:
         raise ValueError(f"k_out and v_out must hold {shape} elements")
-    _check_pools(p, k_pool, v_pool)
-    kvdt = _kvdt(p)
-    rc = _lib.lazy_attn_cache_read(ctypes.byref(p), _dptr(k_pool, "k_pool", kvdt), _dptr(v_pool, "v_pool", kvdt), n,
-                                   _dptr(block_ids, "block_ids", torch.int32), _dptr(k_out, "k_out", dt),
-                                   _dptr(v_out, "v_out", dt), _stream(stream))
+    rc = _lib.lazy_attn_cache_read(ctypes.byref(p), kp, vp, n, _dptr(block_ids, "block_ids", torch.int32),
+                                   _dptr(k_out, "k_out", dt), _dptr(v_out, "v_out", dt), _stream(stream))
     _check(rc, "cache_read")
     return k_out, v_out
 
