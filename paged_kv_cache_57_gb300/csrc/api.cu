@@ -964,6 +964,11 @@ int lazy_attn_cache_write(const lazy_attn_params* p, const void* k, int64_t k_to
   lazy::CacheWriteArgs a{};
   if (kind == LAZY_FP8_E4M3) {
     if (!cache_scales(p, &a.k_scale, &a.v_scale)) return LAZY_ERR_INVALID_ARG;
+    // small scales, and the rows with them, are lifted so that remainders stay exact
+    a.k_pre = a.k_scale < 0x1p-32f ? 0x1p64f : 1.f;
+    a.v_pre = a.v_scale < 0x1p-32f ? 0x1p64f : 1.f;
+    a.k_scale *= a.k_pre;
+    a.v_scale *= a.v_pre;
     a.k_inv = 1.f / a.k_scale;
     a.v_inv = 1.f / a.v_scale;
   }

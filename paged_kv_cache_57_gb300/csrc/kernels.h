@@ -161,7 +161,9 @@ struct CacheWriteArgs {
   uint8_t* v_pool;
   unsigned int* status;
   int num_tokens, Hkv, D, num_pool_blocks;
-  float k_scale, v_scale, k_inv, v_inv;  // e4m3 pools
+  // e4m3 pools: the scales times a power of two `pre`, and their reciprocals
+  float k_scale, v_scale, k_inv, v_inv, k_pre, v_pre;
+  uint32_t div_mul, div_shift;           // division by 2 Hkv (the launch fills them)
 };
 
 // Blocks out of the pools as `dtype`.

@@ -533,9 +533,9 @@ def cache_read(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor, block_ids:
     shape = (n, p.num_kv_heads, BLOCK, p.head_dim)
     kp, vp = _cache_pools(p, k_pool, v_pool)
     if k_out is None:
-        k_out = k_pool.new_empty(shape, dtype=dt)
+        k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     if v_out is None:
-        v_out = k_pool.new_empty(shape, dtype=dt)
+        v_out = torch.empty_like(k_out)
     if min(k_out.numel(), v_out.numel()) < n * p.num_kv_heads * BLOCK * p.head_dim:
         raise ValueError(f"k_out and v_out must hold {shape} elements")
     rc = _lib.lazy_attn_cache_read(ctypes.byref(p), kp, vp, n, _dptr(block_ids, "block_ids", torch.int32),
