@@ -26,7 +26,8 @@ struct Int4Cfg {
   static constexpr int RING = 2;                // stages per warp
   static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM
   static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
-  static constexpr int SMEM = BUF + kWarps * (D / 2) * 8;
+  static constexpr int KEPT = int4_kept_floats<D, NT, HL>();  // per warp (int4.cuh)
+  static constexpr int SMEM = BUF + kWarps * (D / 2) * 8 + kWarps * KEPT * 4;
 };
 
 // A warp's partial of its rows to shared memory: o[D], m, l per row.
@@ -96,11 +97,10 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   constexpr int kSpecial = 1 << 16;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
-  // Per warp, the blocks of two word chunks (64): ids, document starts, and per pair its
-  // valid slots (8 bits each) with kSpecial where the pair is not two whole blocks of the
-  // document of the block before (or begins a chunk).
+  // Per warp, the blocks of two word chunks (64): ids, and per pair its valid slots (8 bits
+  // each) with kSpecial where the pair is not two whole blocks of the document of the block
+  // before (or begins a chunk).
   __shared__ int2 d_phys[kWarps][32];
-  __shared__ int2 d_p[kWarps][32];
   __shared__ int d_nv[kWarps][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
       const bool plain = r.nv == kBlock && nv1 == kBlock && (!LAZY || (lane > 0 && p1 == r.p && p_1 == r.p));
       const int k = (kc + lane) & 63;
       reinterpret_cast<int*>(d_phys[warp])[k] = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block
-      reinterpret_cast<int*>(d_p[warp])[k] = r.p;
       if (!(lane & 1)) d_nv[warp][k >> 1] = r.nv | nv1 << 8 | (plain ? 0 : kSpecial);
       __syncwarp();
     };
@@ -219,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     }
     int4_scale_rows<D, NT>(rows, live, a.scale_log2, lane);
     float2* cs = cs_all + warp * HALF;
+    float* kept = reinterpret_cast<float*>(cs_all + kWarps * HALF) + warp * C::KEPT;
     Int4Query<D, NT, HL> q;
     auto rebuild = [&](int delta) {
       __syncwarp();
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
       if ((i & 15) == 0) {  // a chunk of words ahead
         describe(2 * i + 32);
         load_words(2 * i + 64);
+        if (i > 0 && i % kInt4Flush == 0) int4_flush(st, kept, i > kInt4Flush, lane);
       }
       cp_async_wait<R - 1>();
       __syncwarp();
@@ -250,17 +251,17 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
         if constexpr (LAZY) {
           // A tile lies in one document: where the second block starts another, the first is
           // attended alone, q is rotated anew, and the second follows.
-          const int2 p = d_p[warp][i & 31];
-          p1 = p.y;
-          if (p.x != p_cur) rebuild(m_pos - (p_cur = p.x));
-          if (nv[1] > 0 && p1 != p.x) {
+          const int b = kb0 + 2 * i, p0 = decode_word(__ldg(&wrow[b]), b, a.id_bits).p;
+          if (p0 != p_cur) rebuild(m_pos - (p_cur = p0));
+          p1 = nv[1] > 0 ? decode_word(__ldg(&wrow[b + 1]), b + 1, a.id_bits).p : p0;
+          if (p1 != p0) {
             nv1 = nv[1];
             nv[1] = 0;
           }
         }
       }
       while (true) {
-        int4_attend<D, NT, HL>(kr, vr, special, nv, q, st, lane);
+        int4_attend<D, NT, HL>(kr, vr, special, nv, q, st, lane, i >= kInt4Flush ? kept : nullptr);
         if (!LAZY || nv1 == 0) break;
         nv[0] = 0;
         nv[1] = nv1;
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
       cp_async_commit();  // a group a step, empty at the end
       if (++slot == R) slot = 0;
     }
+    if (ns > kInt4Flush) int4_unflush(st, kept, lane);
     int4_finish(st);
     __syncthreads();  // every warp is done with its ring: the merge takes its place
     float* red = reinterpret_cast<float*>(smem);

@@ -266,6 +266,45 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
   }
 }
 
+// O^T's running sums hold codes, not values: they grow with the keys and cancel against the
+// zeros' part, and the products truncate them (2^-24 of the sum each time, always towards
+// zero). Over 5000 keys of a 65000-key context that was 2.6e-3 of the output instead of the
+// output rounding's 1.7e-3, so long runs move them to shared memory every kInt4Flush tiles,
+// where they are summed by rounding additions: `kept` is the warp's area, value n of lane l at
+// 32 n + l (with HL = 1 only the columns that count).
+constexpr int kInt4Flush = 32;
+template <int D, int NT, int HL>
+constexpr int int4_kept_floats() { return 32 * (D / 16) * NT * 2 * HL; }
+
+// f(n, o): value n of the kept ones and its running sum.
+template <int D, int NT, int HL, typename Fn>
+__device__ __forceinline__ void int4_each_kept(Int4State<D, NT, HL>& st, Fn f) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < HL; ++c) f(((i * NT + nt) * 2 + r) * HL + c, i / 4, nt, c, st.o[i][nt][2 * r + (HL == 1 ? i / 4 : c)]);
+}
+
+// Moves the running sums to the kept ones (which are there already: `again`).
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_flush(Int4State<D, NT, HL>& st, float* kept, bool again, int lane) {
+  int4_each_kept<D, NT, HL>(st, [&](int n, int, int, int, float& o) {
+    float* k = kept + 32 * n + lane;
+    *k = again ? *k + o : o;
+    o = 0.f;
+  });
+}
+
+// And back, at the end.
+template <int D, int NT, int HL>
+__device__ __forceinline__ void int4_unflush(Int4State<D, NT, HL>& st, const float* kept, int lane) {
+  int4_each_kept<D, NT, HL>(st, [&](int n, int, int, int, float& o) { o += kept[32 * n + lane]; });
+}
+
 constexpr float kInt4RescaleLog2 = 8.f;      // a maximum is refreshed when it grows by more
 constexpr float kInt4ScaleHeadroom = 128.f;  // and the V scales' reference by more than this
 
@@ -277,10 +316,12 @@ __device__ __forceinline__ void int4_pair(uint32_t w, int h, uint32_t& nibbles, 
 
 // One tile: two blocks of one document. With `partial` (the same in all lanes) only the
 // first nv[b] slots of block b are keys (0: the block is not there), and the other slots'
-// scales and zeros may hold anything.
+// scales and zeros may hold anything. `kept`: sums moved out of the state, to be rescaled
+// with it (null: none).
 template <int D, int NT, int HL>
 __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const SharedRecord (&vr)[2], bool partial, const int (&nv)[2],
-                                            const Int4Query<D, NT, HL>& q, Int4State<D, NT, HL>& st, int lane) {
+                                            const Int4Query<D, NT, HL>& q, Int4State<D, NT, HL>& st, int lane,
+                                            float* kept = nullptr) {
   using G = Int4Geom<D>;
   constexpr int NG = G::NG, W = D / 32;
   const int g = lane >> 2, t = lane & 3;
@@ -415,6 +456,10 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) st.o[4 * j + i][nt][e] *= r;
+        if (kept)
+          int4_each_kept<D, NT, HL>(st, [&](int n, int jj, int, int, float&) {
+            if (jj == j) kept[32 * n + lane] *= r;
+          });
       }
     }
 #pragma unroll
@@ -437,6 +482,10 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (HL == 1 || (e & 1) == c) st.o[i][nt][e] *= alpha;
+          if (kept)
+            int4_each_kept<D, NT, HL>(st, [&](int n, int, int t2, int c2, float&) {
+              if (t2 == nt && c2 == c) kept[32 * n + lane] *= alpha;
+            });
         }
       }
   }

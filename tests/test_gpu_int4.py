@@ -103,6 +103,21 @@ def test_decode_long_context():
     check(decode(dv, k4, v4), M.attention(w, kv, vv), "40000 tokens")
 
 
+@pytest.mark.parametrize("hq", [1, 8, 16])
+def test_long_sums_stay_exact(hq):
+    # 131072 keys of nearly equal weight in one part, 2048 blocks a warp: outputs of about 1/200 of a value, from sums of
+    # codes that cancel against the zeros'. In the 2-norm the output's rounding to bf16 is at most 2^-8 (a half step of a
+    # power of two's least value) and the rounding of weights and of weight times scale to f16 (2^-11 each, independent)
+    # at most 2^-10 of s c, 1.7 standard deviations of a value for normal values: 2^-8 + 1.7 * 2^-10 < 2^-7.
+    # Truncated sums would be off by 2048 * 2^-25 of 1.35 ranges' middle, 2 % of the output.
+    w = W.decode_zipf("i4sum", batch=1, hq=hq, hkv=1, d=128, docs_per_seq=32, doc_tokens=4096, pool_docs=1, zipf_s=1.0,
+                      share=False, seed=723)
+    dv, k4, v4, kv, vv = on_device(w, num_splits=1)
+    want, _ = M.attention(w, kv, vv)
+    out = decode(dv, k4, v4).double()
+    assert ((out - want).norm() / want.norm()).item() < 2.0 ** -7
+
+
 def _rescaled(w, k_mul, v_mul):
     """The workload with each token's stored rows multiplied (per block and slot)."""
     w.k_pool = (w.k_pool.double() * k_mul).to(torch.bfloat16)
