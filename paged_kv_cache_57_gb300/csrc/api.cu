@@ -414,7 +414,7 @@ static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const v
     const size_t parts = (size_t)2 * a.plan.ctas * a.plan.rows;
     a.ws_o = static_cast<float*>(workspace);
     a.ws_ml = a.ws_o + parts * p->head_dim;
-    a.prefix = reinterpret_cast<int*>(a.ws_ml + parts * 2);
+    a.prefix = reinterpret_cast<int64_t*>(a.ws_ml + parts * 2);
   }
   a.status = st;
   a.B = p->num_seqs;

@@ -116,33 +116,29 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     left = a.plan.chunk;
   } else {  // every warp for itself: the total, then the sequence of the range's first place
     int64_t total = 0;
-    for (int b = 0; b < a.B; b += 32) {
+    int nb = 0, inc = 0;  // of the last 32 sequences: the lane's blocks, and up to them
+    auto scan = [&](int b) {
       int len;
-      const int nb = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
-      int inc = nb;
+      inc = nb = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
       }
-      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = (int)total + inc - nb;
+    };
+    for (int b = 0; b < a.B; b += 32) {
+      scan(b);
+      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = total + inc - nb;
       total += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = (int)total;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = total;
     total *= U;
     const int64_t chunk = chunk_of(a, total), lo = blockIdx.x * chunk;
     left = min(chunk, total - lo);
     if (left <= 0) return;
     int64_t before = 0;
     for (s = 0; s < a.B; s += 32) {
-      int len;
-      const int nb = s + lane < a.B ? blocks_of(a, s + lane, len) : 0;
-      int inc = nb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
+      if (a.B > 32) scan(s);
       const uint32_t past = __ballot_sync(0xffffffffu, (before + inc) * U > lo);  // sequences that end behind lo
       if (past) {
         const int l = __ffs(past) - 1;
@@ -172,6 +168,19 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     const int n = max(0, min(hi, nb) - lo);                          // blocks of the part
     const int m_pos = __ldg(&a.q_pos[s]);
     const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
+
+    Int4QueryRows<NT> rows;
+    bool live[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2);
+      live[nt] = r < heads;
+      rows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) + (q0 + (live[nt] ? r : 0)) * D;
+    }
+    const Int4RawRows<D, NT> raw(rows, lane);  // loads that nothing waits for yet
+    float2 rate[HALF / 32];
+#pragma unroll
+    for (int j = 0; j < HALF / 32; ++j) rate[j] = __ldg(&a.rope[lane + 32 * j]);
 
     // ------------------------------------------------------------ first loads
     // quarters of whole stages
@@ -208,21 +217,14 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     }
 
     // ------------------------------------------------------------ queries
-    Int4QueryRows<NT> rows;
-    bool live[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2);
-      live[nt] = r < heads;
-      rows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) + (q0 + (live[nt] ? r : 0)) * D;
-    }
-    int4_scale_rows<D, NT>(rows, live, a.scale_log2, lane);
+    int4_scale_rows<D, NT>(rows, raw, live, a.scale_log2);
     float2* cs = cs_all + warp * HALF;
     float* kept = reinterpret_cast<float*>(cs_all + kWarps * HALF) + warp * C::KEPT;
     Int4Query<D, NT, HL> q;
     auto rebuild = [&](int delta) {
       __syncwarp();
-      for (int f = lane; f < HALF; f += 32) cs[f] = rope_cs(__ldg(&a.rope[f]), delta, a.status);
+#pragma unroll
+      for (int j = 0; j < HALF / 32; ++j) cs[lane + 32 * j] = rope_cs(rate[j], delta, a.status);
       __syncwarp();
       int4_build_query<D, NT, HL>(q, rows, lane, [&](int) { return cs; });
     };
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
     __syncthreads();
     const bool whole = lo == 0 && hi == len;
-    const size_t slot0 = (size_t)(2 * blockIdx.x + (lo == 0 ? 1 : 0)) * C::ROWS;
+    const size_t slot0 = (2 * (size_t)blockIdx.x + (lo == 0 ? 1 : 0)) * C::ROWS;
     for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
       const int row = idx / D, col = idx % D;
       float M = -INFINITY;
@@ -310,92 +312,137 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
 }
 
 // out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit that lies in
-// several CTAs' ranges; 0 for a sequence without blocks. One CTA per (sequence, query head),
-// warps in turn over the parts, four in flight each. Launched as a programmatic dependent
-// of the decode kernel: it waits for that grid before it reads anything.
+// several CTAs' ranges; 0 for a sequence without blocks. A CTA looks after PAIRS (sequence,
+// query head) pairs: a warp finds a pair's parts and merges up to kCombineBatch of them by
+// itself; more are shared by the CTA's warps. Launched as a programmatic dependent of the
+// decode kernel: it waits for that grid before it reads anything.
+//
+// Up to kCombineAlone pairs, as many CTAs as are resident at once, get a CTA each: whole
+// calls of 32 heads take 21 us at 1 x 16k tokens and 21 at 4 x 4k, with PAIRS = 8 30 and 29.
+// Most of a large batch's pairs have nothing to merge, and CTAs that find that out come in
+// waves: at 64 x 8k (4 heads a KV head) PAIRS = 8 takes 73.5 us, a CTA per pair 80.
+constexpr int kCombineWarps = 8, kCombineBatch = 8, kCombineAlone = 3 * 152;
+
+namespace {
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) combine_int4_kernel(const Int4DecodeArgs a) {
+struct Merged {
+  static constexpr int PER = D / 32;
+  float M, L, acc[PER];
+  // Parts c0 + first, c0 + first + step, ... c1 of a row, a lane the columns lane + 32 i.
+  __device__ __forceinline__ Merged(const Int4DecodeArgs& a, int row, int c0, int c1, int first, int step) {
+    const int lane = threadIdx.x & 31;
+    M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    for (int cb = c0 + first; cb <= c1; cb += step * kCombineBatch) {
+      float2 ml[kCombineBatch];
+      float v[kCombineBatch][PER];
+#pragma unroll
+      for (int b = 0; b < kCombineBatch; ++b) {
+        const int c = cb + b * step;
+        ml[b] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[b][i] = 0.f;
+        if (c <= c1) {
+          const size_t p = (2 * (size_t)c + (c == c0 ? 1 : 0)) * a.plan.rows + row;
+          ml[b] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * p);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) v[b][i] = a.ws_o[p * D + lane + 32 * i];
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int b = 0; b < kCombineBatch; ++b) Mn = fmaxf(Mn, ml[b].x);
+      const float Mr = Mn == -INFINITY ? 0.f : Mn;
+      const float r = fast_ex2(M - Mr);
+      L *= r;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] *= r;
+#pragma unroll
+      for (int b = 0; b < kCombineBatch; ++b) {
+        const float w = fast_ex2(ml[b].x - Mr);  // an empty part (m = -inf) weighs 0
+        L = fmaf(w, ml[b].y, L);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, v[b][i], acc[i]);
+      }
+      M = Mn;
+    }
+  }
+};
+
+}  // namespace
+
+template <int D, int PAIRS>
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const Int4DecodeArgs a) {
   constexpr int PER = D / 32;
-  __shared__ float red[kWarps][D + 2];
-  const int s = blockIdx.x / a.Hq, h = blockIdx.x - s * a.Hq;
+  __shared__ float red[kCombineWarps][D + 2];
+  __shared__ int2 parts[PAIRS];  // what the CTA's warps share: first and last part
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ht = a.plan.units / a.Hkv, kvh = h / a.G, t = (h - kvh * a.G) / a.plan.rows;
-  const int row = h - kvh * a.G - t * a.plan.rows, u = kvh * ht + t;
+  const int64_t pair0 = (int64_t)blockIdx.x * PAIRS, pairs = (int64_t)a.B * a.Hq;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+  auto row_of = [&](int64_t pair) { return (int)(pair % a.Hq) % a.G % a.plan.rows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int64_t lo, len, total = 0;
-  if (a.plan.unit_len > 0) {
-    len = a.plan.unit_len;
-    lo = ((int64_t)s * a.plan.units + u) * len;
-  } else {
-    const int p0 = a.prefix[s];
-    len = a.prefix[s + 1] - p0;
-    lo = (int64_t)p0 * a.plan.units + u * len;
-    total = (int64_t)a.prefix[a.B] * a.plan.units;
-  }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)s * a.Hq + h) * D;
-  if (len == 0) {
-    for (int c = threadIdx.x; c < D; c += kThreads) out[c] = __float2bfloat16_rn(0.f);
-    return;
-  }
-  const int64_t chunk = chunk_of(a, total);
-  const int c0 = (int)(lo / chunk), c1 = (int)((lo + len - 1) / chunk);
-  if (c0 == c1) return;  // in one range: written there
-  float M = -INFINITY, L = 0.f, acc[PER];
+  if (warp < PAIRS) {
+    const int64_t pair = pair0 + warp;
+    int2 mine = make_int2(0, 0);
+    if (pair < pairs) {
+      const int s = (int)(pair / a.Hq), h = (int)(pair - (int64_t)s * a.Hq), kvh = h / a.G;
+      const int u = kvh * (a.plan.units / a.Hkv) + (h - kvh * a.G) / a.plan.rows;
+      int64_t lo, len, total = 0;
+      if (a.plan.unit_len > 0) {
+        len = a.plan.unit_len;
+        lo = ((int64_t)s * a.plan.units + u) * len;
+      } else {
+        const int64_t p0 = a.prefix[s];
+        len = a.prefix[s + 1] - p0;
+        lo = p0 * a.plan.units + u * len;
+        total = a.prefix[a.B] * a.plan.units;
+      }
+      if (len == 0) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  constexpr int BATCH = 4;
-  for (int cb = c0 + warp; cb <= c1; cb += kWarps * BATCH) {
-    float2 ml[BATCH];
-    float v[BATCH][PER];
+        for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(0.f);
+      } else {
+        const int64_t chunk = chunk_of(a, total);
+        mine = make_int2((int)(lo / chunk), (int)((lo + len - 1) / chunk));  // in one range: written there
+        if (PAIRS > 1 && mine.x < mine.y && mine.y - mine.x < kCombineBatch) {
+          const Merged<D> m(a, row_of(pair), mine.x, mine.y, 0, 1);
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const int c = cb + b * kWarps;
-      ml[b] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) v[b][i] = 0.f;
-      if (c <= c1) {
-        const size_t p = (size_t)(2 * c + (c == c0 ? 1 : 0)) * a.plan.rows + row;
-        ml[b] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * p);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[b][i] = a.ws_o[p * D + lane + 32 * i];
+          for (int i = 0; i < PER; ++i)
+            out[pair * D + lane + 32 * i] = __float2bfloat16_rn(m.L == 0.f ? 0.f : m.acc[i] / m.L);
+          mine.y = mine.x;
+        }
       }
     }
-    float Mn = M;
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) Mn = fmaxf(Mn, ml[b].x);
-    const float Mr = Mn == -INFINITY ? 0.f : Mn;
-    const float r = fast_ex2(M - Mr);
-    L *= r;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] *= r;
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const float w = fast_ex2(ml[b].x - Mr);  // an empty part (m = -inf) weighs 0
-      L = fmaf(w, ml[b].y, L);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, v[b][i], acc[i]);
-    }
-    M = Mn;
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) red[warp][lane + 32 * i] = acc[i];
-  if (lane == 0) {
-    red[warp][D] = M;
-    red[warp][D + 1] = L;
+    if (lane == 0) parts[warp] = mine;
   }
   __syncthreads();
-  for (int col = threadIdx.x; col < D; col += kThreads) {
-    float Ma = -INFINITY, x = 0.f, La = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < PAIRS; ++i) {
+    const int c0 = parts[i].x, c1 = parts[i].y;
+    if (c0 == c1) continue;
+    const Merged<D> m(a, row_of(pair0 + i), c0, c1, warp, kCombineWarps);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) Ma = fmaxf(Ma, red[w][D]);
-    if (Ma == -INFINITY) Ma = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = fast_ex2(red[w][D] - Ma);
-      x += f * red[w][col];
-      La += f * red[w][D + 1];
+    for (int j = 0; j < PER; ++j) red[warp][lane + 32 * j] = m.acc[j];
+    if (lane == 0) {
+      red[warp][D] = m.M;
+      red[warp][D + 1] = m.L;
     }
-    out[col] = __float2bfloat16_rn(La == 0.f ? 0.f : x / La);
+    __syncthreads();
+    for (int col = threadIdx.x; col < D; col += 32 * kCombineWarps) {
+      float Ma = -INFINITY, x = 0.f, La = 0.f;
+#pragma unroll
+      for (int w = 0; w < kCombineWarps; ++w) Ma = fmaxf(Ma, red[w][D]);
+      if (Ma == -INFINITY) Ma = 0.f;
+#pragma unroll
+      for (int w = 0; w < kCombineWarps; ++w) {
+        const float f = fast_ex2(red[w][D] - Ma);
+        x += f * red[w][col];
+        La += f * red[w][D + 1];
+      }
+      out[(pair0 + i) * D + col] = __float2bfloat16_rn(La == 0.f ? 0.f : x / La);
+    }
+    __syncthreads();
   }
 }
 
@@ -514,7 +561,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   const bool live[1] = {r < rows && it.ok[mem]};
   qrows.q[0] = static_cast<const __nv_bfloat16*>(a.q) +
                ((live[0] ? (size_t)mem_seq(mem) * a.Hq + (rc - mem * a.G) : 0) + (size_t)kvh * a.G) * D;
-  int4_scale_rows<D, 1>(qrows, live, a.scale_log2, lane);
+  int4_scale_rows<D, 1>(qrows, Int4RawRows<D, 1>(qrows, lane), live, a.scale_log2);
   Int4Query<D, 1, HL> q;
   int4_build_query<D, 1, HL>(q, qrows, lane, [&](int) { return cs_tab + mem * HALF; });
 
@@ -643,11 +690,11 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
     p.chunk = (mb + s - 1) / s;
     const int splits = (mb + p.chunk - 1) / p.chunk;
     p.unit_len = splits * p.chunk;
-    p.ctas = (int)std::min<int64_t>(units * splits, INT32_MAX);
+    p.ctas = units * splits;
     p.direct = splits == 1;
   } else {
     const int64_t useful = (units * mb + kMinChunk - 1) / kMinChunk;
-    p.ctas = (int)std::min<int64_t>(useful, (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS));
+    p.ctas = std::min<int64_t>(useful, (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS));
     p.chunk = kMinChunk;
   }
   return p;
@@ -655,15 +702,16 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
 
 size_t decode_int4_workspace_bytes(const Int4Plan& p, int B, int D) {
   if (p.direct) return 0;
-  return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 1) * sizeof(int);
+  return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 1) * sizeof(int64_t);
 }
 
 template <int D, int NT, int HL, bool LAZY>
 static cudaError_t launch_decode_t(const Int4DecodeArgs& a, cudaStream_t st) {
   using C = Int4Cfg<D, NT, HL>;
+  if (a.plan.ctas > INT_MAX) return cudaErrorInvalidConfiguration;
   cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, HL, LAZY>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_int4_kernel<D, NT, HL, LAZY><<<a.plan.ctas, kThreads, C::SMEM, st>>>(a);
+  decode_int4_kernel<D, NT, HL, LAZY><<<(unsigned)a.plan.ctas, kThreads, C::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -680,15 +728,23 @@ cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t 
 
 cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.B * a.Hq));
-  cfg.blockDim = dim3(kThreads);
+  const long long pairs = (long long)a.B * a.Hq;
+  const bool one = pairs <= kCombineAlone;
+  const long long grid = one ? pairs : (pairs + kCombineWarps - 1) / kCombineWarps;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128>, a) : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64>, a);
+  if (one)
+    return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128, 1>, a)
+                      : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64, 1>, a);
+  return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128, kCombineWarps>, a)
+                    : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64, kCombineWarps>, a);
 }
 
 template <int D, bool LAZY>

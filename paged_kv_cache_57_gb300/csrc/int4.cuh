@@ -153,15 +153,29 @@ __device__ __forceinline__ int int4_word_dim(int t, int i) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// A lane's own dims of its rows, loaded ahead of their use.
+template <int D, int NT>
+struct Int4RawRows {
+  uint4 x[NT][D / 32];
+  __device__ __forceinline__ explicit Int4RawRows(const Int4QueryRows<NT>& r, int lane) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        x[nt][i] = __ldg(reinterpret_cast<const uint4*>(r.q[nt] + int4_word_dim<D>(lane & 3, i)));
+  }
+};
+
 // Fills mul and pow2 from the rows' values (all lanes).
 template <int D, int NT>
-__device__ __forceinline__ void int4_scale_rows(Int4QueryRows<NT>& r, const bool (&live)[NT], float scale, int lane) {
+__device__ __forceinline__ void int4_scale_rows(Int4QueryRows<NT>& r, const Int4RawRows<D, NT>& raw, const bool (&live)[NT],
+                                                float scale) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t mx = 0u;  // |bf16| compares as its bits
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(r.q[nt] + int4_word_dim<D>(lane & 3, i)));
+      const uint4 x = raw.x[nt][i];
       mx = __vmaxu2(__vmaxu2(__vmaxu2(mx, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu)),
                     x.w & 0x7fff7fffu);
     }

@@ -273,14 +273,14 @@ cudaError_t launch_cache_read(const CacheReadArgs& a, int kv_dtype, int sms, cud
 struct Int4Plan {
   int rows;        // query heads of a unit: 4, 8 or 16
   int units;       // units of a sequence: KV heads x head tiles
-  int ctas;
+  int64_t ctas;    // refused past INT_MAX
   int unit_len;    // > 0: every unit has this many places (split into equal parts); 0: its blocks
   int chunk;       // places of a CTA with unit_len, else the least a CTA takes
   bool direct;     // every CTA has one whole unit: no partials
 };
 struct Int4DecodeArgs : DecodeArgs {
   Int4Plan plan;
-  int* prefix;  // [B + 1] blocks of the sequences before each (unit_len = 0); in the workspace
+  int64_t* prefix;  // [B + 1] blocks of the sequences before each (unit_len = 0); in the workspace
 };
 // num_splits > 0: that many equal parts of max_blocks; else chosen. sms: the device's.
 Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
