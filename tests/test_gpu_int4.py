@@ -78,6 +78,60 @@ def test_decode_ragged_batch_with_empty_sequences():
         check(out[keep], (want[keep], bound[keep]), "beside empty sequences")
 
 
+# (sequences, query heads) on both sides of 456 pairs, where a join's CTA takes eight pairs; batches of more than 32
+# sequences (several scans of the lengths), runs of empty ones before, between and behind the others, parts of one
+# sequence in more than eight ranges, and a workspace that held NaN
+@pytest.mark.parametrize("batch,hq", [(33, 8), (57, 8), (58, 8), (90, 14)])
+def test_decode_many_sequences(batch, hq):
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=batch, n_prefill=1, chunk=16, hq=hq, hkv=2, d=64, pool_docs=60, ctx_lo=1, ctx_hi=6000,
+                        doc_lo=1, doc_hi=300, seed=712 + batch)
+    dv, k4, v4, kv, vv = on_device(dw)
+    want, bound = M.attention(dw, kv, vv)
+    ws = torch.full((L.decode_workspace_bytes(dv.p),), 255, dtype=torch.uint8, device="cuda")
+    first = decode(dv, k4, v4, workspace=ws)
+    check(first, (want, bound), "all")
+    assert torch.equal(decode(dv, k4, v4, workspace=ws), first)
+    for keep in ([batch - 1], [0], [3, batch // 2], list(range(32, batch)), []):
+        lens = torch.zeros_like(dv.seq_lens)
+        lens[keep] = dv.seq_lens[keep]
+        ws.fill_(255)
+        out = L.decode(dv.p, dv.q, k4, v4, dv.words, lens, dv.q_pos, dv.rope, workspace=ws)
+        check(out[keep], (want[keep], bound[keep]), f"only {keep[:3]}")
+        assert torch.count_nonzero(out).item() == torch.count_nonzero(out[keep]).item()
+
+
+def test_two_decodes_at_once():
+    # each call with its own workspace, on its own stream, several in flight
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=20, n_prefill=1, chunk=16, hq=16, hkv=2, d=128, pool_docs=40, ctx_lo=1, ctx_hi=4000,
+                        doc_lo=1, doc_hi=300, seed=716)
+    dv, k4, v4, kv, vv = on_device(dw)
+    alone = decode(dv, k4, v4)
+    check(alone, M.attention(dw, kv, vv), "alone")
+    n = L.decode_workspace_bytes(dv.p)
+    runs = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(dv.q)) for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, ws, out in runs:
+            decode(dv, k4, v4, out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for _, _, out in runs:
+        assert torch.equal(out, alone)
+
+
+def test_decode_more_splits_than_blocks_and_small_workspace():
+    L = la()
+    w = W.decode_zipf("i4sp", batch=2, hq=8, hkv=2, d=128, docs_per_seq=2, doc_tokens=60, pool_docs=4, zipf_s=0.5, seed=717)
+    dv, k4, v4, kv, vv = on_device(w, num_splits=1000)
+    check(decode(dv, k4, v4), M.attention(w, kv, vv), "1000 splits")
+    need = L.decode_workspace_bytes(dv.p)
+    with pytest.raises(L.LazyAttnError, match="WORKSPACE"):
+        decode(dv, k4, v4, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(L.LazyAttnError, match="WORKSPACE"):
+        decode(dv, k4, v4, workspace=torch.empty(need + 16, dtype=torch.uint8, device="cuda")[8:])
+
+
 def test_decode_far_positions_and_control():
     w = W.decode_zipf("i4far", batch=2, hq=16, hkv=4, d=128, docs_per_seq=3, doc_tokens=70, pool_docs=4, zipf_s=1.0,
                       suffix_tokens=9, seed=720, shift=100000)
