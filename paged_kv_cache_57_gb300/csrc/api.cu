@@ -540,10 +540,13 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
   // e4m3 and int4 pools run on mma.sync kernels (items of at most 64 rows) at every ratio
   const int cap = kv_quantised(p) ? 64 : lazy::shared_rows_cap(c.G, p->head_dim);
-  // 0: 32 blocks for the mma.sync kernel; for the tensor-core kernel, a length that
-  // gives about one item per resident CTA.
-  const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 ? 0 : 32);
-  const int auto_items = std::max(1, lazy::kSharedTcSlots / std::max(1, p->num_kv_heads));
+  // 0: 32 blocks for the bf16 and e4m3 mma.sync kernel; for the tensor-core kernel and int4
+  // pools, a length that gives about one item per resident CTA. int4 (8 KV heads, 64-block
+  // documents): 136 us against 156 with 32 blocks and 218 with 16; 8 sequences of 256-block
+  // documents 45 against 44, 52 with 16, 108 with 256.
+  const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 || kv_int4(p) ? 0 : 32);
+  const int slots = kv_int4(p) ? lazy::kSharedInt4Slots : lazy::kSharedTcSlots;
+  const int auto_items = std::max(1, slots / std::max(1, p->num_kv_heads));
   // small items spread through the launch: measured for the bf16 mma.sync kernel only
   const bool spread = !kv_quantised(p) && cap == 64;
   return lazy::plan_shared_host(p->num_seqs, c.G, cap, p->max_blocks_per_seq, p->num_pool_blocks, num_docs,

@@ -204,6 +204,8 @@ inline int shared_rows_cap(int G, int D) { return (G >= 8 && D == 128) ? 128 : 6
 // automatic chunk length aims at about this many CTAs, so that each CTA's fixed
 // cost (record, query rotation, partials) is paid as few times as the machine allows.
 constexpr int kSharedTcSlots = 2 * 152;
+// The same of the int4 kernel.
+constexpr int kSharedInt4Slots = 4 * 152;
 
 // Host planner of the shared-run decode (shared_plan.cu). counts = {items, slots}.
 // chunk_blocks <= 0 picks the chunk from the batch: about auto_items items in all,
