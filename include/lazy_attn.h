@@ -265,12 +265,12 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  * split into sets of at most LAZY_PLAN_MAX_MEMBERS members and at most R query
  * rows (members x query heads per KV head), and each set's blocks are cut into
  * chunks of chunk_blocks logical blocks. R is 128 when a KV head serves at least
- * 8 query heads, head_dim is 128 and the pools are not e4m3 (the decode then runs
- * on the 5th-generation tensor cores, one 128-row tile per item), else 64 (plan
- * with the kv_dtype the decode will use). chunk_blocks 0 selects 32,
- * or, for R = 128, about one item per resident CTA (2 x 152 / num_kv_heads items):
- * the sets' blocks summed, divided by that count, rounded up to a multiple of 4
- * and kept within 32 .. 256. It writes
+ * 8 query heads, head_dim is 128 and the pools are neither e4m3 nor int4 (the decode
+ * then runs on the 5th-generation tensor cores, one 128-row tile per item), else 64
+ * (plan with the kv_dtype the decode will use). chunk_blocks 0 selects 32,
+ * or, for R = 128 and for int4 pools, about one item per resident CTA (2 x 152 /
+ * num_kv_heads items, int4: 4 x 152 / num_kv_heads): the sets' blocks summed, divided
+ * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. It writes
  *   items_host [num_items][LAZY_PLAN_ITEM_INTS] int32, one work item each:
  *     [0] src_seq, [1] b0, [2] nblk, [3] last_valid, [4] nmem, [5] c0, [6..7] 0:
  *         nblk logical blocks of sequence src_seq from block b0, all full but
@@ -483,7 +483,11 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * Written groups have z = their least value, s = (greatest - least) / 15 rounded to bf16
  * (to nearest even) and c = (x - z) / s rounded to the nearest whole number (ties to
  * even, at most 15); s = 0 and c = 0 where all are equal. A group with an infinity or a
- * NaN has s = z = NaN. */
+ * NaN has s = z = NaN.
+ *
+ * The decodes on them (at most 65535 KV heads) round weight times V scale to f16, over a power
+ * of two near the largest V scale of a sequence's part: to 2^-11 of each for scales within
+ * 2^14 of the largest, below that to 2^-25 of the largest. */
 
 /* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold
  * num_pool_blocks * Hkv times that. 0 on bad params. */
@@ -497,8 +501,8 @@ size_t lazy_attn_pool_record_bytes(const lazy_attn_params *p);
  *              element t * token_stride + h * head_stride (>= 0; any, so that slices of
  *              a fused product need no copy; 16-byte aligned rows are read fastest)
  *   slots      [num_tokens] int32 device: block * 16 + row, no two the same; negative:
- *              the token is skipped (padding). A block id outside the pool sets
- *              LAZY_DEV_BAD_BLOCK_ID and the token is skipped
+ *              the token is skipped (padding; its rows are read all the same). A block id
+ *              outside the pool sets LAZY_DEV_BAD_BLOCK_ID and the token is skipped
  *   k_pool, v_pool  16-byte aligned. Only the named slots change
  * kv_dtype 0: copies. LAZY_FP8_E4M3 (dtype bf16, head_dim 64 or 128): x / k_scale (K) or
  * x / v_scale (V), rounded to the nearest code (ties to even) and saturated at +-448, NaN

@@ -166,6 +166,8 @@ bool encode_dec_q_map(CUtensorMap* m, const void* base, uint64_t B, int hq, int 
 
 // The pools hold e4m3 codes (FP8 KV; only the decodes read them).
 static bool kv_fp8(const lazy_attn_params* p) { return p->kv_dtype == LAZY_FP8_E4M3 && p->dtype != LAZY_FP8_E4M3; }
+// int4 records of one block are addressed with 32 bits.
+constexpr int kInt4MaxKvHeads = 65535;
 // The pools hold int4 records.
 static bool kv_int4(const lazy_attn_params* p) { return p->kv_dtype == LAZY_INT4; }
 static bool kv_quantised(const lazy_attn_params* p) { return kv_fp8(p) || kv_int4(p); }
@@ -398,6 +400,7 @@ static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const v
                             size_t workspace_bytes, lazy_stream_t stream) {
   lazy::Int4DecodeArgs a{};
   a.plan = int4_plan(p, c);
+  if (a.plan.ctas > INT32_MAX) return LAZY_ERR_UNSUPPORTED;
   const size_t need = lazy::decode_int4_workspace_bytes(a.plan, p->num_seqs, p->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return LAZY_ERR_WORKSPACE;
   unsigned int* st = status_ptr();
@@ -444,7 +447,7 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   if (alibi && p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->dtype != LAZY_BF16 || p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
-  if (kv_int4(p) && (p->dtype != LAZY_BF16 || alibi)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_int4(p) && (p->dtype != LAZY_BF16 || alibi || p->num_kv_heads > kInt4MaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
   if (p->num_seqs == 0) return LAZY_OK;
   if (!q || !k_pool || !v_pool || !block_words || !seq_lens || !q_pos || !rope_table || !out)
     return LAZY_ERR_INVALID_ARG;
@@ -580,7 +583,7 @@ static int decode_shared_impl(const lazy_attn_params* p, const void* q, const vo
   if (p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
-  if (kv_int4(p) && alibi) return LAZY_ERR_UNSUPPORTED;
+  if (kv_int4(p) && (alibi || p->num_kv_heads > kInt4MaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
   if (num_items < 0 || num_slots < 0) return LAZY_ERR_INVALID_ARG;
   if (p->num_seqs == 0) return LAZY_OK;

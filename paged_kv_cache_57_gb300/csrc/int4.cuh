@@ -23,8 +23,14 @@
 //
 // The step is bound by the integer pipe (masks and shifts issue every second cycle), which
 // is why e4m3 codes (a byte 0..15 is c 2^-9, three such operations for eight codes) looked
-// better: mma.sync takes them here as conversions and two f16 products, 113 us against 104
-// on 64 x 4160 tokens.
+// better: mma.sync takes them here as conversions and two f16 products (113 us against 104 on
+// 64 x 4160 tokens, when the rest of the step was slower than it is now).
+//
+// tcgen05 needs the codes as f16 in shared memory and did not pay: with the values s c + z
+// unpacked once per 64-key tile for up to 64 rows of an item (f16 over a power of two per
+// token), items of more than 16 rows took 129 us against 135 on 32 x 16384 Zipf-drawn tokens
+// with 8 heads per KV head and 68 against 62 on 64 x 4160 with 4; two CTAs an SM spent 2700
+// cycles a tile, half of it in the softmax of one warp's keys and half unpacking.
 #pragma once
 
 #include "decode_block.cuh"
@@ -283,8 +289,8 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
 // O^T's running sums hold codes, not values: they grow with the keys and cancel against the
 // zeros' part, and the products truncate them (2^-24 of the sum each time, always towards
 // zero). Over 5000 keys of a 65000-key context that was 2.6e-3 of the output instead of the
-// output rounding's 1.7e-3, so long runs move them to shared memory every kInt4Flush tiles,
-// where they are summed by rounding additions: `kept` is the warp's area, value n of lane l at
+// output rounding's 1.7e-3, so long runs move them to shared memory every kInt4Flush stages
+// (64 blocks), where they are summed by rounding additions: `kept` is the warp's area, value n of lane l at
 // 32 n + l (with HL = 1 only the columns that count).
 constexpr int kInt4Flush = 32;
 template <int D, int NT, int HL>

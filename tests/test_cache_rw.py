@@ -109,6 +109,10 @@ def test_int4_argument_rules():
     p = _params(num_q_heads=32, num_kv_heads=2)
     assert L._lib.lazy_attn_mixed(ctypes.byref(p), *([fake] * 3), 1, fake, 1, fake, fake, ctypes.byref(p),
                                   *([fake] * 3), 1, 1, *([fake] * 6), 1 << 30, None) == un
+    # more work units than a grid has CTAs (each needs a row of q: none is launched)
+    assert decode(_params(num_seqs=2 ** 30, max_blocks_per_seq=4)) == un
+    for many in (_params(num_q_heads=65536, num_kv_heads=65536), _params(num_q_heads=131072, num_kv_heads=65536)):
+        assert decode(many) == un and shared(many) == un
     # an unaligned pool, workspace too small
     p = _params()
     assert L._lib.lazy_attn_decode(ctypes.byref(p), fake, ctypes.c_void_p(FAKE + 8), *([fake] * 6), fake, 1 << 20,
