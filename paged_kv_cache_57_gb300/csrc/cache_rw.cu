@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteA
   // skipped token's row is read (not behind its slot's load) and dropped.
   uint4 x[U][ESZ / 2];
   int slot[U];
+  wait_for_launch_before();
 #pragma unroll
   for (int n = 0; n < U; ++n) {
     slot[n] = -1;
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadArg
   constexpr int LPR = D / 8, RPW = 32 / LPR;  // rows a warp takes at a time
   const int lane = threadIdx.x & 31, u = lane % LPR;
   const uint32_t recs = (uint32_t)a.num_blocks * 2u * (uint32_t)a.Hkv;
+  wait_for_launch_before();
   for (uint32_t rec = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); rec < recs; rec += gridDim.x * (kThreads / 32)) {
     const uint32_t i = rec / (2u * a.Hkv), rem = rec - i * (2u * a.Hkv);
     const bool is_v = rem >= (uint32_t)a.Hkv;
@@ -307,9 +309,7 @@ cudaError_t write_u(CacheWriteArgs a, bool vec, cudaStream_t st) {
   a.div_shift = 0;
   while ((1ull << a.div_shift) < d) ++a.div_shift;
   a.div_mul = (uint32_t)(((1ull << 32) * ((1ull << a.div_shift) - d)) / d + 1);
-  if (vec) cache_write_kernel<KIND, D, true, U><<<grid, kThreads, 0, st>>>(a);
-  else cache_write_kernel<KIND, D, false, U><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(vec ? cache_write_kernel<KIND, D, true, U> : cache_write_kernel<KIND, D, false, U>, grid, kThreads, 0, st, a);
 }
 
 // Four tokens per lane share its addresses and keep four loads in flight (8192 tokens of 8
@@ -325,8 +325,7 @@ template <int KIND, int D>
 cudaError_t read_t(const CacheReadArgs& a, int sms, cudaStream_t st) {
   const int64_t recs = (int64_t)a.num_blocks * 2 * a.Hkv, per = kThreads / 32;
   const int64_t want = (recs + per - 1) / per, most = (int64_t)sms * 64;
-  cache_read_kernel<KIND, D><<<(unsigned)(want < most ? want : most), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(cache_read_kernel<KIND, D>, (unsigned)(want < most ? want : most), kThreads, 0, st, a);
 }
 
 }  // namespace

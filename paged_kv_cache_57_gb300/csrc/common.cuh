@@ -100,6 +100,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return true;
 }
 
+// Of a kernel started by launch_behind, in every thread and before any access to global memory:
+// the launch before it is complete and its writes are visible.
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Orders this thread's generic-proxy shared-memory accesses before later
 // async-proxy (TMA / tensor core) accesses.
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   // before (or begins a chunk).
   __shared__ int2 d_phys[kWarps][32];
   __shared__ int d_nv[kWarps][32];
+  wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int U = a.plan.units, ht = U / a.Hkv;
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const 
   const int64_t pair0 = (int64_t)blockIdx.x * PAIRS, pairs = (int64_t)a.B * a.Hq;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   auto row_of = [&](int64_t pair) { return (int)(pair % a.Hq) % a.G % a.plan.rows; };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_launch_before();
   if (warp < PAIRS) {
     const int64_t pair = pair0 + warp;
     int2 mine = make_int2(0, 0);
@@ -647,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
   extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
   float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][HALF]
   __shared__ __align__(16) Int4Item it;
+  wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv / halves, half = blockIdx.x / a.Hkv % halves;
   if (threadIdx.x < kItemInts / 4)
@@ -720,8 +722,7 @@ static cudaError_t launch_decode_t(const Int4DecodeArgs& a, cudaStream_t st) {
   using C = Int4Cfg<D, NT, HL>;
   cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, HL, LAZY>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  decode_int4_kernel<D, NT, HL, LAZY><<<(unsigned)a.plan.ctas, kThreads, C::SMEM, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(decode_int4_kernel<D, NT, HL, LAZY>, (unsigned)a.plan.ctas, kThreads, C::SMEM, st, a);
 }
 
 template <int D, bool LAZY>
@@ -736,24 +737,13 @@ cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t 
 }
 
 cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
   const long long pairs = (long long)a.B * a.Hq;
   const bool one = pairs <= kCombineAlone;
   const long long grid = one ? pairs : (pairs + kCombineWarps - 1) / kCombineWarps;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(32 * kCombineWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (one)
-    return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128, 1>, a)
-                      : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64, 1>, a);
-  return a.D == 128 ? cudaLaunchKernelEx(&cfg, combine_int4_kernel<128, kCombineWarps>, a)
-                    : cudaLaunchKernelEx(&cfg, combine_int4_kernel<64, kCombineWarps>, a);
+  auto kern = a.D == 128 ? (one ? combine_int4_kernel<128, 1> : combine_int4_kernel<128, kCombineWarps>)
+                         : (one ? combine_int4_kernel<64, 1> : combine_int4_kernel<64, kCombineWarps>);
+  return launch_behind(kern, (unsigned)grid, 32 * kCombineWarps, 0, st, a);
 }
 
 template <int D, bool LAZY>
@@ -764,9 +754,8 @@ static cudaError_t launch_shared_t(const SharedDecodeArgs& a, const void* k_pool
   const int halves = std::min(kMembers * a.G, 2 * kShRows) > kShRows ? 2 : 1;
   const long long grid = (long long)a.num_items * a.Hkv * halves;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  decode_shared_int4_kernel<D, LAZY><<<(unsigned)grid, kThreads, SMEM, st>>>(
-      a, static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), halves);
-  return cudaGetLastError();
+  return launch_behind(decode_shared_int4_kernel<D, LAZY>, (unsigned)grid, kThreads, SMEM, st, a,
+                       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), halves);
 }
 
 cudaError_t launch_decode_shared_int4(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,

@@ -26,6 +26,23 @@ inline cudaError_t set_smem_once(int bytes) {
   return e;
 }
 
+// Launches a kernel that calls wait_for_launch_before (common.cuh): its CTAs may start while
+// the launch before it in the stream ends, and wait there for the end of it.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_behind(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                                 const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 struct DecodeArgs {
   const void* q;             // [B][Hq][D] unrotated
