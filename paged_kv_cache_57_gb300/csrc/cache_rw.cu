@@ -10,11 +10,13 @@
 //  - e4m3: code = x / scale, correctly rounded (ties to even), saturated at +-448;
 //  - int4: per group of 64 dims z = min, s = bf16((max - min) / 15), code =
 //    rint((x - z) / s).
-// Quotients are formed by an approximate reciprocal in fp32, and only where the result is
-// next to a border between two codes (or two scales) exactly, so the codes are those of the
-// definition. That arithmetic is what bounds the kernel: about 230 instructions for eight
-// int4 codes of 32 lanes, 190 for e4m3. Writing 8192 tokens of 8 heads takes 16 us (int4,
-// 43 MB), 16384 tokens 31 us (e4m3, 101 MB), the rows coming from L2.
+// Quotients are formed by an approximate reciprocal and exact remainders in fp32, and where
+// that does not tell a border between two codes (or two scales) in 64 bits, so the codes are
+// those of the definition. That arithmetic is what bounds the kernel (75% of the issue slots
+// taken): 173 instructions for eight int4 codes of 32 lanes, 150 for e4m3. Writing 8192
+// tokens of 8 heads takes 12.8 us (int4, 43 MB), 16384 tokens 21.6 us (e4m3, 101 MB), the
+// rows coming from L2. Both worked on borders as they came, 15.5 and 30.7 us, before ties
+// fell out of a corrected quotient (int4) and the odd bit out of two roundings (e4m3).
 // Read: one warp per (block, head, K or V) record, eight dims per lane, written as `dtype`;
 // bound by bandwidth.
 #include "int4.cuh"
@@ -37,47 +39,53 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& x, float (&f)[8]) {
   }
 }
 
-// x / s rounded to odd (the last bit set where it is inexact), so that a second rounding,
-// to e4m3, is that of the exact quotient: scales like amax / 448 put one bf16 value in some
-// hundred on a tie or next to it. q and its remainders by two multiply-adds each; exact for
-// 2^-36 <= s <= 2^100 and the quotients that matter (the caller scales x and s to that).
-// Quotients past the range, infinities and NaN pass as the product.
-__device__ __forceinline__ float div_to_odd(float x, float s, float inv) {
-  const float q0 = x * inv;
-  float q = fmaf(fmaf(-q0, s, x), inv, q0);
-  const float rest = fmaf(-q, s, x);
-  const uint32_t b = __float_as_uint(q);
-  // towards the exact value, where q is even: one up in magnitude if rest has q's sign
-  const uint32_t odd = b + 1u - 2u * ((__float_as_uint(rest) ^ b) >> 31);
-  if (rest != 0.f && !(b & 1u)) q = __uint_as_float(odd);
-  q = __uint_as_float((__float_as_uint(q) & 0x7fffffffu) | (__float_as_uint(x) & 0x80000000u));  // -0 stays
-  return fabsf(q0) < 1024.f ? q : q0;
+// x / s rounded to odd (the last bit set where it is inexact), so that a second rounding, to
+// e4m3, is that of the exact quotient: scales like amax / 448 put one bf16 value in some
+// hundred on a tie or next to it. A product, corrected by its remainder to the nearest fp32
+// value; that one's remainder, rounded towards zero on top of it, gives the truncated
+// quotient, and whether it is 0 the odd bit. Remainders are exact for 2^-36 <= s <= 2^100 and
+// the quotients that matter (the caller scales x and s to that); rounded down they keep the
+// sign of a -0. The bit is all that the integer pipe does, which bounds the kernel.
+__device__ __forceinline__ float div_to_odd(float x, float s, float inv, float q0) {
+  const float q = fmaf(__fmaf_rd(-q0, s, x), inv, q0), rest = __fmaf_rd(-q, s, x);
+  const float a = __fmaf_rz(rest, inv, q);
+  return rest != 0.f ? __uint_as_float(__float_as_uint(a) | 1u) : a;
 }
 
 __device__ __forceinline__ uint2 quantise_e4m3x8(const float (&x)[8], float pre, float s, float inv) {
+  float q[8], big = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = x[i] * pre, q0 = v * inv;
+    big = fmaf(q0, 0.f, big);
+    q[i] = div_to_odd(v, s, inv, q0);
+  }
+  if (!(big == 0.f)) {  // a product past fp32's range, an infinity or a NaN: passes as it is
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = x[i] * pre * inv;
+      if (!(fabsf(q0) < INFINITY)) q[i] = q0;
+    }
+  }
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(div_to_odd(x[2 * i] * pre, s, inv), div_to_odd(x[2 * i + 1] * pre, s, inv));
+  for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(q[2 * i], q[2 * i + 1]);
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+// NaN where either is.
 __device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The scale of a range next to a tie of two bf16 values, or of one that overflows.
-__device__ __noinline__ float int4_scale_exact(float hi, float lo) {
-  return __bfloat162float(__float2bfloat16_rn(static_cast<float>((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0)));
-}
-
-// The code c of a quotient next to a border, corrected by |(x - lo) - s c| - s / 2, which
-// fp32 holds without an error (x - lo as a sum of two, the product of 8 and 5 bits, a
-// difference of near values). A tie goes to the even code.
+// The code c (as a float, cf) of a quotient next to a border, corrected by
+// |(x - lo) - s c| - s / 2, which fp32 holds without an error (x - lo as a sum of two, the
+// product of 8 and 5 bits, a difference of near values). A tie goes to the even code.
 __device__ __forceinline__ uint32_t int4_code_border(float x, float lo, float s, uint32_t c, float cf) {
   const float d = x - lo, b = d - x, rest = (x - (d - b)) + (-lo - b);
   const float r = fmaf(-s, cf, d), off = (fabsf(r) - 0.5f * s) + (r < 0.f ? -rest : rest);
@@ -85,10 +93,23 @@ __device__ __forceinline__ uint32_t int4_code_border(float x, float lo, float s,
   return off > 0.f || (off == 0.f && (c & 1u)) ? to : c;
 }
 
-// The code of a quotient whose parts leave fp32's normal range.
-__device__ __noinline__ uint32_t int4_code_exact(float x, float lo, float s) {
-  const double c = rint((static_cast<double>(x) - static_cast<double>(lo)) / static_cast<double>(s));
-  return static_cast<uint32_t>(fmin(fmax(c, 0.0), 15.0));
+// quantise_int4x8 behind its minima in 64 bits: groups that are not finite, of one value, of
+// a range that overflows or whose parts leave fp32's normal numbers, or with a scale next to
+// a tie.
+__device__ __noinline__ uint2 int4_word_exact(uint4 v, float lo, float hi) {
+  if (!(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY)) return make_uint2(0u, 0x7fc07fc0u);  // reads back as NaN
+  if (hi == lo) return make_uint2(0u, pack_bf16x2(0.f, lo));
+  const uint32_t meta = pack_bf16x2(static_cast<float>((static_cast<double>(hi) - static_cast<double>(lo)) / 15.0), lo);
+  const float s = meta_scale(meta);
+  if (s == 0.f) return make_uint2(0u, meta);  // nearer than bf16 tells
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t word = 0u;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const double x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    word = word << 4 | static_cast<uint32_t>(fmin(rint((x - static_cast<double>(lo)) / static_cast<double>(s)), 15.0));
+  }
+  return make_uint2(word, meta);
 }
 
 // The lane's eight codes as one word, and its group's (scale, zero) word, from eight bf16
@@ -100,46 +121,45 @@ __device__ __forceinline__ uint32_t quantise_int4x8(const uint4& v, uint32_t& me
   uint32_t m = bmin2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = bmin2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // infinities and NaN (which minima pass over): exponent bits all set in some half
-  uint32_t top = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top |= ((w[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-  const uint32_t bad = __ballot_sync(0xffffffffu, top != 0u);
   const float lo = bf16_lo(m), hi = -bf16_hi(m);
-  if (bad >> (threadIdx.x & 24) & 0xffu) {  // not finite: the group reads back as NaN
-    meta = 0x7fc07fc0u;
-    return 0u;
-  }
   // range / 15 by a product, off by 2^-22: rounds to bf16 as the quotient does unless its
-  // low 16 bits are next to a tie's (and it is finite)
-  const float range = hi - lo;
-  float s = range * (1.f / 15.f);
-  if (((__float_as_uint(s) + 8u) & 0xffffu) - 0x8000u <= 16u || !(range < INFINITY)) s = int4_scale_exact(hi, lo);
-  meta = pack_bf16x2(s, lo);
-  s = meta_scale(meta);
-  if (s == 0.f) return 0u;  // all equal (or nearer than bf16 tells): the zero is the value
+  // low 16 bits are next to a tie's
+  const float range = hi - lo, s0 = range * (1.f / 15.f);
+  const uint32_t sb = __float_as_uint(s0);
+  constexpr uint32_t kLeastScale = (127u - 99u) << 23, kInf = 255u << 23;
+  if (((sb + 8u) & 0xffffu) - 0x8000u <= 16u || sb - kLeastScale >= kInf - kLeastScale) {
+    const uint2 r = int4_word_exact(v, lo, hi);
+    meta = r.y;
+    return r.x;
+  }
+  meta = pack_bf16x2(s0, lo);
+  const float s = meta_scale(meta);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  // d inv + 1.5 x 2^23 has the code, rounded to nearest even, in its last bits; e is what the
-  // rounding left. The quotient is off by less than 15.1 x 1.5 x 2^-23 < 2^-18.
-  constexpr float kMagic = 12582912.f, kNear = 0.5f - 0x1p-18f;
-  float x[8], e[8], worst = 0.f;
+  // q, the quotient of d = x - lo corrected by its remainder (exact: 24 + 8 bits less what
+  // cancels), is (x - lo) / s rounded to fp32 wherever that decides a code: ties come out as
+  // such, and q + 1.5 x 2^23 has the code, rounded to nearest even, in its last bits. It
+  // takes a d without a rounding and quotients that are ties or 2^-21 (half a step of q) away
+  // from one. Both hold for |x| and |lo| of 2^-16 of the range or more (or lo = 0): their last
+  // bits, and d, are multiples of a power of two above 2^-24 range, so 2 d - (2 k + 1) s is 0
+  // or above 2^-23 range, over 2 s < 2.02 range / 15 more than 2^-20.1.
+  constexpr float kMagic = 12582912.f;
+  auto quotient = [&](float x) {
+    const float d = x - lo, q = d * inv;
+    return fmaf(fmaf(-q, s, d), inv, q);
+  };
   uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    const float d = x[i] - lo, r = fmaf(d, inv, kMagic);
-    e[i] = fmaf(d, inv, kMagic - r);
-    worst = fmaxf(worst, fabsf(e[i]));
-    c[i] = __float_as_uint(r);
-  }
-  if (s < 0x1p-100f || !(range < INFINITY)) {
+  for (int i = 0; i < 8; ++i)
+    c[i] = __float_as_uint(quotient((i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1])) + kMagic);
+  const uint32_t least = bmin2(bmin2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), bmin2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  const float tiny = range * 0x1p-16f;
+  if (fminf(bf16_lo(least), bf16_hi(least)) < tiny || (fabsf(lo) < tiny && lo != 0.f)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(kMagic) + int4_code_exact(x[i], lo, s);
-  } else if (!(worst < kNear)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!(fabsf(e[i]) < kNear)) c[i] = int4_code_border(x[i], lo, s, c[i], __uint_as_float(c[i]) - kMagic);
+    for (int i = 0; i < 8; ++i) {
+      const float x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]), cf = __uint_as_float(c[i]) - kMagic;
+      if (!(fabsf(quotient(x) - cf) < 0.5f - 0x1p-18f)) c[i] = int4_code_border(x, lo, s, c[i], cf);
+    }
   }
   uint32_t word = c[7], off = __float_as_uint(kMagic);
 #pragma unroll
@@ -313,7 +333,7 @@ cudaError_t write_u(CacheWriteArgs a, bool vec, cudaStream_t st) {
 }
 
 // Four tokens per lane share its addresses and keep four loads in flight (8192 tokens of 8
-// heads: 16.0 us against 17.5 with one); one where four would leave threads of the device
+// heads: 16.0 us against 17.5 with one, when a code took a third more); one where four would leave threads of the device
 // idle.
 template <int KIND, int D>
 cudaError_t write_t(const CacheWriteArgs& a, bool vec, int sms, cudaStream_t st) {

@@ -89,6 +89,32 @@ def test_int4_write_bytes(kind, hkv, d, t):
         assert (((a == b) | ((a & 0x7FFF) + (b & 0x7FFF) == 0))).all()
 
 
+def test_int4_codes_beside_ties():
+    # groups from -(j + 1/2) s to (14.5 - j) s with s a power of two: 0 is a tie of two codes, and a value 2^-k s off it,
+    # k = 0 .. 40, lies on one side however little it moves the difference to the least value; beside them the least
+    # value itself off zero by as little, with ties and halves elsewhere
+    L = la()
+    rng = np.random.default_rng(11)
+    t, h, d = 400, 2, 64
+    p = params("int4", h, d, t // 16)
+    x = rng.choice([-1.0, 1.0], (t, h, d)) * 2.0 ** -rng.integers(0, 41, (t, h, d))
+    x[rng.random(x.shape) < 0.1] = 0.0
+    j = rng.integers(0, 15, (t, h))
+    x[..., 0], x[..., 1] = -(j + 0.5), 14.5 - j
+    off = x[::4, :, 2].copy()
+    x[::4] = rng.integers(0, 31, x[::4].shape) / 2.0
+    x[::4, :, 0], x[::4, :, 1] = off * 2.0 ** -6, 15.0
+    x *= 2.0 ** rng.integers(-60, 61, (t, h, 1))
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    (kp, vp), (k0, v0) = filled_pools(p, 12)
+    slots = np.arange(t, dtype=np.int32)
+    L.cache_write(p, x.cuda(), x.cuda(), torch.from_numpy(slots).cuda(), kp, vp)
+    for got, want, is_v in ((kp, k0.numpy(), False), (vp, v0.numpy(), True)):
+        scatter(slots, want, x, is_v, "int4", d)
+        m = M.BLOCK * d // 2
+        assert np.array_equal(got.cpu().numpy()[..., :m], want[..., :m])
+
+
 @pytest.mark.parametrize("scale", [1.0, 2.0 ** -6, 5.5 / 448, 3.3e-7, 7.0 / 448, 1.1e20])
 def test_e4m3_write_of_every_bf16_value(scale):
     # 65536 patterns: ties, subnormal codes, saturation, infinities and NaN
