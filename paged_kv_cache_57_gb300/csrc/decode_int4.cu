@@ -491,9 +491,9 @@ struct Int4Item {
 // The item's rows row0 .. row0 + 8 RT - 1 (4 with HL = 1, where RT = 1), from `rows` of them.
 // One body for every RT: one per RT made the four warps of a scheduler wait two cycles an
 // instruction for their code.
-template <int D, int HL>
+template <int D, int HL, bool LAZY>
 __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
-                                                 Int4Item& it, uint8_t* smem, const float2* cs_tab, int kvh, int row0,
+                                                 Int4Item& it, uint8_t* smem, float2* cs_tab, int kvh, int row0,
                                                  int rows, int RT) {
   using C = Int4SharedCfg<D>;
   using G = Int4Geom<D>;
@@ -562,6 +562,29 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
       cp_async_commit();
     }
   }
+
+  // ------------------------------------------------------------ members
+  const int nmem = it.rec[4];
+  if (threadIdx.x < nmem) {
+    const int m = threadIdx.x, seq = it.rec[8 + 4 * m], bm = it.rec[8 + 4 * m + 1], slot = it.rec[8 + 4 * m + 2];
+    bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
+    int delta = 0;
+    if (good) {
+      const BlockInfo mi = decode_word(__ldg(&a.words[(size_t)seq * a.max_blocks + bm]), bm, a.id_bits);
+      good = mi.phys == decode_word(__ldg(&a.words[(size_t)src * a.max_blocks + b0]), b0, a.id_bits).phys;
+      const int qp = __ldg(&a.q_pos[seq]);
+      delta = LAZY ? qp - mi.p : qp;
+    }
+    if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
+    it.ok[m] = good;
+    it.delta[m] = delta;
+  }
+  __syncthreads();
+  // the angles of the CTA's members
+  const int m0 = row0 / a.G, m1 = (rows - 1) / a.G;
+  for (int idx = m0 * HALF + threadIdx.x; idx < (m1 + 1) * HALF; idx += kThreads)
+    cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), it.delta[idx / HALF], a.status);
+  __syncthreads();
 
   // ------------------------------------------------------------ queries
   auto mem_seq = [&](int m) { return it.rec[8 + 4 * m]; };
@@ -646,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
   using C = Int4SharedCfg<D>;
   constexpr int HALF = D / 2;
   extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
-  float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][HALF]
+  float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][D / 2]
   __shared__ __align__(16) Int4Item it;
   wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -664,29 +687,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
   }
   const int row0 = half * kShRows, all = nmem * a.G, rows = min(all, row0 + kShRows);
   if (row0 >= all) return;
-  if (threadIdx.x < nmem) {
-    const int m = threadIdx.x, seq = it.rec[8 + 4 * m], bm = it.rec[8 + 4 * m + 1], slot = it.rec[8 + 4 * m + 2];
-    bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
-    int delta = 0;
-    if (good) {
-      const BlockInfo mi = decode_word(__ldg(&a.words[(size_t)seq * a.max_blocks + bm]), bm, a.id_bits);
-      good = mi.phys == decode_word(__ldg(&a.words[(size_t)src * a.max_blocks + b0]), b0, a.id_bits).phys;
-      const int qp = __ldg(&a.q_pos[seq]);
-      delta = LAZY ? qp - mi.p : qp;
-    }
-    if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
-    it.ok[m] = good;
-    it.delta[m] = delta;
-  }
-  __syncthreads();
-  // the angles of the CTA's members
-  const int m0 = row0 / a.G, m1 = (rows - 1) / a.G;
-  for (int idx = m0 * HALF + threadIdx.x; idx < (m1 + 1) * HALF; idx += kThreads)
-    cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), it.delta[idx / HALF], a.status);
-  __syncthreads();
   const int n = rows - row0;
-  if (n <= 4) shared_int4_rows<D, 1>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, 1);
-  else shared_int4_rows<D, 2>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, n <= 8 ? 1 : (n <= 16 ? 2 : 4));
+  if (n <= 4) shared_int4_rows<D, 1, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, 1);
+  else shared_int4_rows<D, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, row0, rows, n <= 8 ? 1 : (n <= 16 ? 2 : 4));
 }
 
 // ------------------------------------------------------------------ launchers
