@@ -287,8 +287,8 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  *   slot_indptr_host [B+1]: the slots of sequence s are slot_indptr[s] ..
  *     slot_indptr[s+1]-1;
  *   counts_host [2] = {num_items, num_slots}.
- * Items are ordered by decreasing block count (ties in the order of first
- * appearance of their document).
+ * Items are ordered by decreasing block count, for int4 pools times 1, 2 or 4 for up to 8,
+ * up to 16 or more query rows (ties in the order of first appearance of their document).
  * `capacity` bounds the item count (the number
  * of logical blocks in the batch always suffices). Returns LAZY_ERR_LAYOUT on the
  * packer's layout errors, and LAZY_ERR_WORKSPACE if capacity is too small.

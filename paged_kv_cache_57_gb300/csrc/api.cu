@@ -554,7 +554,7 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
   const bool spread = !kv_quantised(p) && cap == 64;
   return lazy::plan_shared_host(p->num_seqs, c.G, cap, p->max_blocks_per_seq, p->num_pool_blocks, num_docs,
                                 seg_indptr, seg_doc, seg_len, doc_block_indptr, doc_blocks, cb, auto_items, capacity,
-                                items, slot_indptr, counts, spread);
+                                items, slot_indptr, counts, spread, kv_int4(p));
 }
 
 size_t lazy_attn_decode_shared_workspace_bytes(const lazy_attn_params* p, int32_t num_slots) {

@@ -22,6 +22,11 @@
 // blocks are the exception: they are spread evenly through the order (measured:
 // 66.0 -> 65.0 us per step on the 8B decode, whose 64-token private tails make 31%
 // of the items; the e4m3 instantiation ran slower that way, 75 -> 81 us).
+// The int4 kernel's CTAs share an item's blocks among 4, 2 or 1 teams of warps by its rows (up
+// to 8, 16, more): with cost_of_rows items go by block count times 1, 2 or 4, so that the
+// launch does not end on the long ones (32 x 16384 Zipf-drawn tokens 136 -> 129 us, 8 x 16384
+// of 256-block documents 44 -> 39; cutting wide items shorter instead cost more in partials
+// than it evened out, 143 us).
 #include <algorithm>
 #include <utility>
 #include <vector>
@@ -33,7 +38,7 @@ namespace lazy {
 int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_blocks, int num_docs, const int32_t* seg_indptr,
                      const int32_t* seg_doc, const int32_t* seg_len, const int32_t* doc_block_indptr,
                      const int32_t* doc_blocks, int chunk_blocks, int auto_items, int capacity, int32_t* items,
-                     int32_t* slot_indptr, int32_t* counts, bool spread_small) {
+                     int32_t* slot_indptr, int32_t* counts, bool spread_small, bool cost_of_rows) {
   struct Occ {
     int seq, b0;
   };
@@ -104,7 +109,7 @@ int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_bl
     for (int j0 = 0; j0 < gsize(gi); j0 += per_set) {
       const int n = std::min(per_set, gsize(gi) - j0);
       const int rows = n * G;
-      const int rt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+      const int rt = !cost_of_rows || rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
       sets.push_back(Set{gi, gstart[gi] + j0, n, rt, cb});
       for (int j = 0; j < n; ++j) nslots[occ[gstart[gi] + j0 + j].seq] += (nbk + cb - 1) / cb;
     }
@@ -123,7 +128,7 @@ int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_bl
     for (int c0 = 0; c0 < nbk; c0 += st.cb) {
       const int nb = std::min(st.cb, nbk - c0);
       const int last = (c0 + nb == nbk) ? ((len - 1) & (kBlk - 1)) + 1 : kBlk;
-      its.push_back(Item{si, c0, nb, last, nb});
+      its.push_back(Item{si, c0, nb, last, nb * st.rt});
     }
   }
   if ((int64_t)its.size() > capacity) return LAZY_ERR_WORKSPACE;

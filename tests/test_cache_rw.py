@@ -128,6 +128,9 @@ def test_int4_plan_keeps_items_of_at_most_64_rows():
     items, _ = L.plan_shared_host(p, len(w.doc_len), w.seg_indptr, w.seg_doc, w.seg_len, w.doc_block_indptr,
                                   w.doc_blocks)
     assert (items[:, 4] * 16 <= 64).all() and (items[:, 4] > 1).any()
+    # the widest and longest first
+    cost = items[:, 2] * np.array([1, 2, 4])[np.searchsorted([8, 16], items[:, 4] * 16)]
+    assert (np.diff(cost) <= 0).all()
 
 
 def test_token_slots():
