@@ -478,6 +478,11 @@ struct Int4SharedCfg {
   static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;
 };
 
+// The n threads of team t meet (barrier 0 is the CTA's).
+__device__ __forceinline__ void team_sync(int t, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(t + 1), "r"(n) : "memory");
+}
+
 // What the CTA's warps share of an item.
 struct Int4Item {
   int rec[kItemInts];
@@ -555,7 +560,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   }
   describe(0);
   load_words(32);
-  if (RT > 1) team_and(team, 32 * RT, true);
+  if (RT > 1) team_sync(team, 32 * RT);
   if (!rec_first) {
     for (int i = 0; i < AHEAD; ++i) {
       if (i < ns && (i & (RT - 1)) == rt) load(ring + i * C::SLOT, it.d_phys[team][i].x, it.d_phys[team][i].y, lane);
@@ -612,7 +617,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
     } else {
       if (RT == 2) cp_async_wait<2>();
       else cp_async_wait<6>();
-      team_and(team, 32 * RT, true);
+      team_sync(team, 32 * RT);
     }
     if ((i & 15) == 0) {  // a chunk of words ahead, over the one that all are done with
       describe(2 * i + 32);
