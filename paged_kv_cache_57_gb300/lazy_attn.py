@@ -491,8 +491,8 @@ def empty_pools(p: Params, device="cuda"):
 
 def _cache_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
     """The pools' pointers, checked: type, device, size."""
-    dt = _kvdt(p)
-    n = p.num_pool_blocks * p.num_kv_heads * (p.head_dim * 9 if p.kv_dtype == LAZY_INT4 else BLOCK * p.head_dim)
+    rows, int4 = p.num_pool_blocks * p.num_kv_heads, p.kv_dtype == LAZY_INT4
+    n, dt = rows * p.head_dim * (9 if int4 else BLOCK), torch.uint8 if int4 else _kvdt(p)
     if k_pool.numel() < n or v_pool.numel() < n:
         raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
     return _dptr(k_pool, "k_pool", dt), _dptr(v_pool, "v_pool", dt)
@@ -532,12 +532,13 @@ def cache_read(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor, block_ids:
     dt, n = _tdt(p), block_ids.numel()
     shape = (n, p.num_kv_heads, BLOCK, p.head_dim)
     kp, vp = _cache_pools(p, k_pool, v_pool)
+    for x in (k_out, v_out):
+        if x is not None and x.numel() < n * p.num_kv_heads * BLOCK * p.head_dim:
+            raise ValueError(f"k_out and v_out must hold {shape} elements")
     if k_out is None:
         k_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
-    if min(k_out.numel(), v_out.numel()) < n * p.num_kv_heads * BLOCK * p.head_dim:
-        raise ValueError(f"k_out and v_out must hold {shape} elements")
+        v_out = torch.empty(shape, dtype=dt, device=k_pool.device)
     rc = _lib.lazy_attn_cache_read(ctypes.byref(p), kp, vp, n, _dptr(block_ids, "block_ids", torch.int32),
                                    _dptr(k_out, "k_out", dt), _dptr(v_out, "v_out", dt), _stream(stream))
     _check(rc, "cache_read")
