@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
 // decode kernel: it waits for that grid before it reads anything.
 //
 // Up to kCombineAlone pairs, as many CTAs as are resident at once, get a CTA each: whole
-// calls of 32 heads take 21 us at 1 x 16k tokens and 21 at 4 x 4k, with PAIRS = 8 30 and 29.
+// calls of 32 heads took 21 us at 1 x 16384 tokens and at 4 x 4096, with PAIRS = 8 30 and 29.
 // Most of a large batch's pairs have nothing to merge, and CTAs that find that out come in
-// waves: at 64 x 8k (4 heads a KV head) PAIRS = 8 takes 73.5 us, a CTA per pair 80.
+// waves: at 64 x 4160 tokens PAIRS = 8 took 73.5 us, a CTA per pair 80.
 constexpr int kCombineWarps = 8, kCombineBatch = 8, kCombineAlone = 3 * 152;
 
 namespace {
@@ -461,9 +461,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const 
 // teams of RT = 1, 2 or 4 warps with a contiguous part of the item's blocks and a ring of
 // stages each. Tiles of 16 rows would unpack each code half as often, but hold 240
 // registers, two CTAs an SM: 197 us against 154 on 32 x 16384 tokens of Zipf-drawn
-// documents with 8 query heads per KV head, in items of 32 blocks. In items of 64 the 8-row
-// tiles take 134 us, 1.6 TB/s of unique records: bound by the instructions of unpacking
-// and softmax, once per 8 rows.
+// documents with 8 query heads per KV head, in items of 32 blocks. In items of 64, the long
+// and wide ones first, the 8-row tiles take 122 us, 1.8 TB/s of unique records: bound by the
+// instructions of unpacking and softmax, once per 8 rows (60% of the issue slots).
 namespace {
 
 constexpr int kShRows = 32;    // rows of a CTA

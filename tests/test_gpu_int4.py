@@ -410,6 +410,67 @@ def test_captured_steps_replay():
         assert torch.equal(st["kp"], k4)
 
 
+def test_captured_behind_copies_and_joined_streams():
+    # In a captured step every call follows what a launch may not overlap: a copy, a fill, two streams that join; and its
+    # inputs come from right before it. Replayed on new inputs, twice in a row.
+    L = la()
+    w = _model(3, 8, 2, 128, 792)
+    dv, k4, v4, kv, vv = on_device(w)
+    ids = torch.arange(w.num_pool_blocks, dtype=torch.int32, device="cuda")
+    plan = shared_plan(dv)
+    src = [k4.clone(), v4.clone(), dv.q.clone()]
+    kp, vp, q = torch.zeros_like(k4), torch.zeros_like(v4), torch.zeros_like(dv.q)
+    out, outs = torch.empty_like(dv.q), torch.empty_like(dv.q)
+    rows = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    slots = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(256, L.decode_workspace_bytes(dv.p)), dtype=torch.uint8, device="cuda")
+    wss = torch.empty(L.decode_shared_workspace_bytes(dv.p, plan.num_slots), dtype=torch.uint8, device="cuda")
+    ko = torch.empty(w.num_pool_blocks, 2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    vo = torch.empty_like(ko)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        kp.copy_(src[0])  # a copy, then the join of two streams
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            vp.copy_(src[1])
+        q.copy_(src[2]).mul_(1)
+        here.wait_stream(side)
+        L.decode(dv.p, q, kp, vp, dv.words, dv.seq_lens, dv.q_pos, dv.rope, out=out, workspace=ws)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            L.cache_read(dv.p, kp, vp, ids, ko, vo)
+        rows.zero_()
+        L.cache_write(dv.p, rows, rows, slots, kp, vp)
+        here.wait_stream(side)
+        L.decode_shared(dv.p, q, kp, vp, dv.words, dv.q_pos, dv.rope, plan, out=outs, workspace=wss)
+        ws.fill_(255)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for scale in (1, 2):
+        src[2].copy_(dv.q * scale)
+        for x in (kp, vp, out, outs, ko, vo):
+            x.zero_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        w2 = _model(3, 8, 2, 128, 792)
+        w2.q = (w2.q.float() * scale).to(torch.bfloat16)
+        ref = M.attention(w2, kv, vv)
+        check(out, ref, f"replay, queries times {scale}")
+        check(outs, ref, f"shared replay, queries times {scale}")
+        assert torch.equal(torch.nan_to_num(ko.float()), torch.nan_to_num(kv.float().to(torch.bfloat16).float()))
+        assert torch.equal(torch.nan_to_num(vo.float()), torch.nan_to_num(vv.float().to(torch.bfloat16).float()))
+
+
 def test_side_stream():
     L = la()
     w = _model(3, 8, 2, 64, 791)
