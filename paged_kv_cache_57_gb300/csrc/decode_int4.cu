@@ -57,20 +57,38 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 }  // namespace
 
 // ------------------------------------------------------------------ per sequence
-// The units' blocks (a unit: a sequence, a KV head, a tile of 4, 8 or 16 of its query
-// heads) are laid end to end and cut into equal ranges, one per CTA, as many CTAs as are
-// resident at once: batches of any lengths give every CTA the same work. A CTA goes through
-// its range unit by unit; a unit that lies in one range is written out, the others' parts
-// go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that begins in CTA c's
-// range, 2 c for one that began before it) and are merged by combine_int4_kernel.
+// A unit is a sequence, a KV head and a tile of 4, 8 or 16 of its query heads. Tiles of 8
+// where 4 would do take 83 us against 77 on 64 x 4160 tokens, tiles of 8 instead of 16 345
+// against 258 on 32 heads per KV head.
+//
+// Equal pieces: every unit is cut into the same number of pieces of a length that the host
+// knows, one CTA each, as many as fill the resident CTAs once (at least kMinPiece blocks a
+// piece, and whole units where there are more of them than resident CTAs: those are written
+// out, without parts and a join).
+//
+// Ranges: where a piece could be longer than kMaxPiece, the length of the longest sequence
+// says too little about the others. The units' blocks are laid end to end and cut into equal
+// ranges, one per resident CTA: batches of any lengths give every CTA the same work. A CTA
+// goes through its range unit by unit; a unit that lies in one range is written out.
+//
+// Measured from HBM (pieces, ranges; us): 64 sequences up to 2048 tokens 33 57, up to 4096 60
+// 75, up to 8192 91 93, all of 4160 74 77; 256 of 1024 73 89; 8 of 4096 21 26; one of 16384 17
+// 19; 48 up to 131072 with one KV head (pieces of 2731 blocks) 460 255.
+//
+// The other parts go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that
+// begins in CTA c's places, 2 c for one that began before) and are merged by
+// combine_int4_kernel.
 //
 // Of a part the four warps take a quarter each. A warp is its own loader: a ring of RING
-// stages of two blocks, each refilled as soon as it was read.
+// stages of two blocks, each refilled as soon as it was read. 64 sequences of 4160 tokens, 32
+// heads on 8, take 63 us a call, 4.9 TB/s of records: no pipe is full (integer 55%), and 16
+// warps an SM, which is what 128 registers allow, do not hide a tile's chain.
 
 namespace {
 
-constexpr int kMinChunk = 16;      // blocks of a CTA at least (a stage or two per warp)
-constexpr int kDirectBlocks = 32;  // units of at most this many blocks get a CTA each
+constexpr int kMinPiece = 32;   // blocks of a piece at least: one of 16384 tokens 17 us, with 16 or 64 19
+constexpr int kMaxPiece = 512;
+constexpr int kMinChunk = 16;   // blocks of a range at least
 
 __device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& seq_len) {
   seq_len = __ldg(&a.seq_lens[s]);
@@ -705,8 +723,10 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
   p.units = Hkv * ((G + p.rows - 1) / p.rows);
   const int mb = max_blocks > 0 ? max_blocks : 1;
   const int64_t units = (int64_t)(B > 0 ? B : 1) * p.units;
-  if (num_splits > 0 || mb <= kDirectBlocks) {
-    const int s = num_splits > 0 ? std::min(num_splits, mb) : 1;
+  const int64_t resident = (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS);
+  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(resident / units, mb / kMinPiece));
+  if (num_splits > 0 || (mb + pieces - 1) / pieces <= kMaxPiece) {
+    const int s = num_splits > 0 ? std::min(num_splits, mb) : (int)pieces;
     p.chunk = (mb + s - 1) / s;
     const int splits = (mb + p.chunk - 1) / p.chunk;
     p.unit_len = splits * p.chunk;
@@ -714,7 +734,7 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
     p.direct = splits == 1;
   } else {
     const int64_t useful = (units * mb + kMinChunk - 1) / kMinChunk;
-    p.ctas = std::min<int64_t>(useful, (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS));
+    p.ctas = std::min<int64_t>(useful, resident);
     p.chunk = kMinChunk;
   }
   return p;

@@ -101,6 +101,30 @@ def test_decode_many_sequences(batch, hq):
         assert torch.count_nonzero(out).item() == torch.count_nonzero(out[keep]).item()
 
 
+# more units than a device has resident CTAs and sequences of more than 512 blocks among short ones: ranges of the units'
+# blocks laid end to end, several units or parts of one in a CTA's range
+@pytest.mark.parametrize("batch,hq,hkv,d", [(330, 8, 2, 64), (330, 12, 2, 128), (160, 32, 1, 128)])
+def test_decode_ranges_of_ragged_batches(batch, hq, hkv, d):
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=batch, n_prefill=1, chunk=16, hq=hq, hkv=hkv, d=d, pool_docs=60, ctx_lo=1, ctx_hi=9500,
+                        doc_lo=1, doc_hi=700, seed=713 + hq)
+    dv, k4, v4, kv, vv = on_device(dw)
+    assert dw.max_blocks_per_seq > 512 and 0 < L.decode_workspace_bytes(dv.p)
+    want, bound = M.attention(dw, kv, vv)
+    ws = torch.full((L.decode_workspace_bytes(dv.p),), 255, dtype=torch.uint8, device="cuda")
+    first = decode(dv, k4, v4, workspace=ws)
+    check(first, (want, bound), "all")
+    assert torch.equal(decode(dv, k4, v4, workspace=ws), first)
+    long = int(dv.seq_lens.argmax())
+    for keep in ([batch - 1], [0], [long], [3, batch // 2, long], list(range(40, batch)), []):
+        lens = torch.zeros_like(dv.seq_lens)
+        lens[keep] = dv.seq_lens[keep]
+        ws.fill_(255)
+        out = L.decode(dv.p, dv.q, k4, v4, dv.words, lens, dv.q_pos, dv.rope, workspace=ws)
+        check(out[keep], (want[keep], bound[keep]), f"only {keep[:3]}")
+        assert torch.count_nonzero(out).item() == torch.count_nonzero(out[keep]).item()
+
+
 def test_two_decodes_at_once():
     # each call with its own workspace, on its own stream, several in flight
     L = la()
