@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * C::ROWS + row) * C::RED + D]);
-      if (M == -INFINITY) M = 0.f;  // no keys: all sums are 0 (or NaN, which stays)
+      const float Mr = M == -INFINITY ? 0.f : M;  // no keys: all sums are 0 (or NaN, which stays)
       float acc = 0.f, L = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* src = red + (w * C::ROWS + row) * C::RED;
-        const float f = fast_ex2(src[D] - M);
+        const float f = fast_ex2(src[D] - Mr);
         acc += f * src[col];
         L += f * src[D + 1];
       }
