@@ -678,6 +678,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
 #pragma unroll
         for (int c = 0; c < PER; ++c) acc[c] += w * row[lane + 32 * c];
       }
+      if (L != 0.f) M = Mr;  // all scores NaN: not an empty slot, which the combine would pass over
     }
     const size_t pidx = (size_t)mem_slot(m) * a.Hq + (size_t)kvh * a.G + h;
 #pragma unroll

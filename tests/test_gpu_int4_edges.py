@@ -46,3 +46,28 @@ def test_low_scores_beside_parts_without_keys(hq, hkv, d, c):
         check(decode(dv, k4, v4), ref, f"ragged, splits {splits}")
     for chunk in (0, 4):
         check(la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv, chunk)), ref, f"shared, chunk {chunk}")
+
+
+# a query with a NaN, and a sequence whose keys are all NaN for one KV head: their rows are NaN, on both decodes, the others
+# as without them
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (2, 2, 64), (48, 2, 128)])
+def test_rows_without_a_finite_score_are_nan(hq, hkv, d):
+    w = W.decode_zipf("i4n", batch=3, hq=hq, hkv=hkv, d=d, docs_per_seq=2, doc_tokens=90, pool_docs=3, zipf_s=0.5, share=False,
+                      suffix_tokens=7, seed=820)
+    G = hq // hkv
+    for doc, _ in w.seq_segments(2):  # KV head 0 of sequence 2
+        w.k_pool[w.doc_blocks[int(w.doc_block_indptr[doc]):int(w.doc_block_indptr[doc + 1])].astype(np.int64), 0] = float("nan")
+    w.q[1, hq - 1, 5] = float("nan")
+    dv, k4, v4, kv, vv = on_device(w)
+    want, bound = M.attention(w, kv, vv)
+    nan = torch.zeros(3, hq, dtype=torch.bool, device="cuda")
+    nan[1, hq - 1] = nan[2, :G] = True
+    outs = {}
+    for splits in (0, 1, 3):
+        dv.p.num_splits = splits
+        outs[f"splits {splits}"] = decode(dv, k4, v4)
+    for chunk in (0, 2):
+        outs[f"chunk {chunk}"] = la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv, chunk))
+    for what, out in outs.items():
+        assert torch.isnan(out[nan]).all(), what
+        check(out[~nan], (want[~nan], bound[~nan]), what)
