@@ -493,7 +493,10 @@ struct Int4SharedCfg {
   static constexpr int RED = D + 4;                   // merge rows: o[D], m, l
   static constexpr int MERGE = kWarps * 8 * RED * 4;  // [teams][8 RT] rows are 32 in all
   static constexpr int BUF = kShStages * SLOT > MERGE ? kShStages * SLOT : MERGE;
-  static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;
+  // the members' angles, then, once the queries are built, the warps' kept sums (int4.cuh)
+  static constexpr int KEPT = int4_kept_floats<D, 1, 2>();
+  static constexpr int ANGLES = kMembers * (D / 2) * 8;
+  static constexpr int SMEM = BUF + (ANGLES > kWarps * KEPT * 4 ? ANGLES : kWarps * KEPT * 4);
 };
 
 // The n threads of team t meet (barrier 0 is the CTA's).
@@ -623,6 +626,8 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   int4_build_query<D, 1, HL>(q, qrows, lane, [&](int) { return cs_tab + mem * HALF; });
 
   // ------------------------------------------------------------ main loop
+  float* kept = reinterpret_cast<float*>(cs_tab) + warp * C::KEPT;
+  if (per_team > 2 * kInt4Flush) __syncthreads();  // sums will be kept where the angles were
   Int4State<D, 1, HL> st;
   int4_init(st);
   const uint8_t* ring_p = smem + team * R * C::SLOT;
@@ -640,6 +645,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
     if ((i & 15) == 0) {  // a chunk of words ahead, over the one that all are done with
       describe(2 * i + 32);
       load_words(2 * i + 64);
+      if (i > 0 && i % kInt4Flush == 0) int4_flush(st, kept, i > kInt4Flush, lane);
     }
     const int n = i + AHEAD;
     if (n < ns && (n & (RT - 1)) == rt) {
@@ -651,8 +657,10 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
     const SharedRecord kr[2] = {{stage}, {stage + 2 * G::REC}}, vr[2] = {{stage + G::REC}, {stage + 3 * G::REC}};
     const int2 v = it.d_nv[team][i & 31];
     const int nv[2] = {v.x, v.y};
-    int4_attend<D, 1, HL>(kr, vr, __any_sync(0xffffffffu, v.x + v.y < 2 * kBlock), nv, q, st, lane);
+    int4_attend<D, 1, HL>(kr, vr, __any_sync(0xffffffffu, v.x + v.y < 2 * kBlock), nv, q, st, lane,
+                          i >= kInt4Flush ? kept : nullptr);
   }
+  if (ns > kInt4Flush) int4_unflush(st, kept, lane);
   int4_finish(st);
   __syncthreads();  // every team is done with its ring: the merge takes its place
 

@@ -71,3 +71,64 @@ def test_rows_without_a_finite_score_are_nan(hq, hkv, d):
     for what, out in outs.items():
         assert torch.isnan(out[nan]).all(), what
         check(out[~nan], (want[~nan], bound[~nan]), what)
+
+
+# one long document: its blocks' words take id_bits = 14 (18 bits of offset from its start)
+def one_document(tokens, hq, seed, d=128):
+    return W.decode_zipf("i4one", batch=1, hq=hq, hkv=1, d=d, docs_per_seq=1, doc_tokens=tokens, pool_docs=1, zipf_s=1.0, seed=seed)
+
+
+# 131072 keys of nearly equal weight as one item: 8192, 4096 or 2048 blocks a team of warps for more than 16, up to 16 and up
+# to 8 rows (4 rows: another tile), and two CTAs' rows. In the 2-norm the output's rounding to bf16 is at most 2^-8 and that
+# of the weights' f16 products 1.7 * 2^-10 (see test_long_sums_stay_exact); sums that the products truncate would be off by
+# 2048 * 2^-25 of 1.35 ranges' middle and more, 2 to 8 % of the output.
+@pytest.mark.parametrize("hq", [3, 8, 16, 32, 48])
+def test_shared_long_items_stay_exact(hq):
+    w = one_document(131072, hq, 830)
+    dv, k4, v4, kv, vv = on_device(w, id_bits=14)
+    want, _ = M.attention(w, kv, vv)
+    plan = shared_plan(dv, 8192)
+    assert plan.num_items == 1
+    out = la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, plan).double()
+    assert ((out - want).norm() / want.norm()).item() < 2.0 ** -7
+
+
+# The same keys in items of 256 blocks, the automatic plan's longest, for more than 16 rows, from the fp32 partials (no
+# rounding to bf16). A term w s c is off by two roundings of 2^-11 at most, each of standard deviation 2^-11 / sqrt(3) or
+# less, and s c has 2.6 standard deviations of a value in the root mean square (codes from 0, 7.5 steps their middle): like
+# the output itself these errors add up as independent ones, 2.6 sqrt(2 / 3) 2^-11 = 2.1 * 2^-11 of it; the queries' rounding
+# to f16 moves the weights by less than 2^-11 of each. sqrt(2.1^2 + 1) * 2^-11 = 2.3 * 2^-11 < 2^-9. Truncated over 256
+# blocks the sums would be off by 1.5 times that bound.
+@pytest.mark.parametrize("hq", [32, 48])
+def test_shared_partials_of_256_blocks_stay_exact(hq):
+    L = la()
+    w = one_document(131072, hq, 831)
+    dv, k4, v4, kv, vv = on_device(w, id_bits=14)
+    want, _ = M.attention(w, kv, vv)
+    plan = shared_plan(dv, 256)
+    assert plan.num_items == 32
+    ws = torch.full((L.decode_shared_workspace_bytes(dv.p, plan.num_slots) // 4,), float("nan"), device="cuda")
+    L.decode_shared_partials(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, plan, ws)
+    n = plan.num_slots * hq
+    acc = ws[:n * 128].view(plan.num_slots, hq, 128).double()
+    m, l = ws[n * 128:n * 130].view(plan.num_slots, hq, 2).double().unbind(-1)
+    f = torch.exp2(m - m.amax(0))
+    out = (f[..., None] * acc).sum(0) / (f * l).sum(0)[..., None]
+    assert ((out - want[0]).norm() / want.norm()).item() < 2.0 ** -9
+
+
+# maxima and V scales that keep growing behind the first 64 blocks of a warp: sums that were set aside follow them
+@pytest.mark.parametrize("hq,d", [(3, 128), (8, 128), (16, 64), (32, 128)])
+def test_set_aside_sums_follow_new_maxima_and_scales(hq, d):
+    w = one_document(16000, hq, 832, d)
+    nb = w.num_pool_blocks
+    at = torch.empty(nb, dtype=torch.float64)
+    at[torch.from_numpy(w.doc_blocks.astype(np.int64))] = torch.arange(nb, dtype=torch.float64)
+    at = at.view(-1, 1, 1, 1)
+    w.k_pool = (w.k_pool.double() * (0.25 + 2 * at / nb)).to(torch.bfloat16)
+    w.v_pool = (w.v_pool.double() * 2.0 ** (at // 64)).to(torch.bfloat16)
+    dv, k4, v4, kv, vv = on_device(w, num_splits=1, id_bits=14)
+    ref = M.attention(w, kv, vv)
+    check(decode(dv, k4, v4), ref, "per sequence")
+    for chunk in (1000, 130):
+        check(la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv, chunk)), ref, f"chunk {chunk}")
