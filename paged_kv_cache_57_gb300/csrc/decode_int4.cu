@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
       const LaneBlock r = describe_block(kc + lane < nk, kb0 + kc + lane, nb, seq_len, w_nxt, wn_nxt, a.id_bits,
                                          a.num_pool_blocks, a.status);
       const int nv1 = __shfl_down_sync(0xffffffffu, r.nv, 1), p1 = __shfl_down_sync(0xffffffffu, r.p, 1);
-      const int p_1 = __shfl_up_sync(0xffffffffu, r.p, 1);
+      // a block without keys, left out perhaps, did not have q rotated for its document
+      const int p_1 = __shfl_up_sync(0xffffffffu, r.nv > 0 ? r.p : INT_MIN, 1);
       const bool plain = r.nv == kBlock && nv1 == kBlock && (!LAZY || (lane > 0 && p1 == r.p && p_1 == r.p));
       const int k = (kc + lane) & 63;
       reinterpret_cast<int*>(d_phys[warp])[k] = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block

@@ -21,6 +21,37 @@ def _clean_status():
     assert la().device_status(clear=True) == 0, "device status word set"
 
 
+def attend(w, s, kv, vv, keep=None):
+    """M.attention of sequence s alone over the keys that `keep` (one truth value per token) names: output, bound, weights."""
+    hkv, d = w.num_kv_heads, w.head_dim
+    f = torch.as_tensor(w.rope_theta ** (-2.0 * np.arange(d // 2) / d), dtype=torch.float64, device="cuda")
+
+    def rotate(x, n):
+        c, r = torch.cos(n[:, None, None] * f), torch.sin(n[:, None, None] * f)
+        a, b = x[..., :d // 2], x[..., d // 2:]
+        return torch.cat((a * c - b * r, a * r + b * c), -1)
+
+    ks, vs, pos, p = [], [], [], int(w.seq_pos0[s])
+    for doc, n in w.seq_segments(s):
+        blk = torch.as_tensor(w.doc_blocks[int(w.doc_block_indptr[doc]):][:(n + 15) // 16].astype(np.int64), device="cuda")
+        ks.append(kv[blk].transpose(1, 2).reshape(-1, hkv, d)[:n])
+        vs.append(vv[blk].transpose(1, 2).reshape(-1, hkv, d)[:n])
+        pos.append(torch.full((n,), float(p), dtype=torch.float64, device="cuda"))
+        p += n
+    k, v = rotate(torch.cat(ks), torch.cat(pos)), torch.cat(vs)
+    if keep is not None:
+        k, v = k[keep], v[keep]
+    q = rotate(w.q[s].double().cuda()[None], torch.tensor([float(w.q_pos[s])], dtype=torch.float64, device="cuda"))[0].reshape(hkv, -1, d)
+    wgt = torch.softmax(torch.einsum("hgd,thd->hgt", q, k) * d ** -0.5, -1)
+    o = torch.einsum("hgt,thd->hgd", wgt, v)
+    e = d ** -0.5 * 2.0 ** -11 * 9 / 8 * q.norm(dim=-1) * k.norm(dim=-1).amax(0)[:, None]
+    big = 2 * v.abs().reshape(-1, hkv, d // 64, 64).amax(-1)
+    spread = torch.einsum("hgt,thj->hgj", wgt, big).repeat_interleave(64, -1)
+    dev = torch.stack([torch.einsum("gt,tgd->gd", wgt[h], (v[:, h, None] - o[h][None]).abs()) for h in range(hkv)])
+    bound = 2.0 ** -8 * o.abs() + e[..., None] * dev + 2.0 ** -10 * spread + 2.0 ** -18 * torch.einsum("hgt,thd->hgd", wgt, v.abs())
+    return o.reshape(-1, d), bound.reshape(-1, d), wgt
+
+
 def opposed(w, c=8.0):
     """The workload with every key's slowest dims (the last quarter of each half) near c and every query's near -c: all
     scores lie near -d c^2 / 4 / sqrt(d), far below 2^-126 of a weight of 1. V lies near 1, so that an output of 0 is
@@ -132,3 +163,24 @@ def test_set_aside_sums_follow_new_maxima_and_scales(hq, d):
     check(decode(dv, k4, v4), ref, "per sequence")
     for chunk in (1000, 130):
         check(la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv, chunk)), ref, f"chunk {chunk}")
+
+
+# a document whose first block, the second of a pair, is not in the pool: that block is left out, and the document's others
+# are attended at their own positions
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 64), (32, 1, 128)])
+@pytest.mark.parametrize("bad", [3, 4, 10])
+def test_blocks_behind_a_bad_one_keep_their_positions(hq, hkv, d, bad):
+    L = la()
+    w = W.decode_zipf("i4bad", batch=2, hq=hq, hkv=hkv, d=d, docs_per_seq=1, doc_tokens=48, pool_docs=2, zipf_s=0.5, share=False,
+                      suffix_tokens=900, seed=840, shift=5000)
+    dv, k4, v4, kv, vv = on_device(w, num_splits=1)
+    words = dv.words.clone()
+    words[1, bad] |= (1 << 18) - 1
+    out = L.decode(dv.p, dv.q, k4, v4, words, dv.seq_lens, dv.q_pos, dv.rope)
+    assert L.device_status(clear=True) == L.LAZY_DEV_BAD_BLOCK_ID
+    for s in range(2):
+        keep = torch.ones(948, dtype=torch.bool, device="cuda")
+        if s == 1:
+            keep[16 * bad:16 * bad + 16] = False
+        want, bound, _ = attend(w, s, kv, vv, keep)
+        check(out[s], (want, bound), f"sequence {s}")
