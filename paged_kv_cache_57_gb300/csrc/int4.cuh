@@ -52,11 +52,6 @@ __host__ __device__ __forceinline__ int int4_v_token(int r) { return (r & 8) + 2
 __device__ __forceinline__ float meta_scale(uint32_t m) { return __uint_as_float(m << 16); }
 __device__ __forceinline__ float meta_zero(uint32_t m) { return __uint_as_float(m & 0xffff0000u); }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -528,30 +523,25 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
     }
 
   // O^T += C_v^T P^T: rows are dims, the k-order tokens 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
-  // Weights, scales (exact over their reference) and their products in f16: off by 2^-10 of
+  // Weights times scales (exact over their reference) are rounded to f16 once: off by 2^-11 of
   // a term, next to the codes' 4 bits.
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     uint32_t pb[NT][NG][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      float s[NG];
+#pragma unroll
+      for (int j = 0; j < NG; ++j) s[j] = vs[b][r][j] * st.inv[j];
       if constexpr (HL == 1) {  // both groups' columns at once
-        const uint32_t s = pack_f16x2(vs[b][r][0] * st.inv[0], vs[b][r][NG - 1] * st.inv[NG - 1]);
-        pb[0][0][r] = transpose_8x8(mul_f16x2(pack_f16x2(p[b][r][0][0], p[b][r][0][0]), s));
+        const float x = p[b][r][0][0];
+        pb[0][0][r] = transpose_8x8(pack_f16x2(x * s[0], x * s[NG - 1]));
         pb[0][NG - 1][r] = pb[0][0][r];
       } else {
-        uint32_t s[NG];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          const float x = vs[b][r][j] * st.inv[j];
-          s[j] = pack_f16x2(x, x);
-        }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t x = pack_f16x2(p[b][r][nt][0], p[b][r][nt][HL - 1]);
-#pragma unroll
-          for (int j = 0; j < NG; ++j) pb[nt][j][r] = transpose_8x8(mul_f16x2(x, s[j]));
-        }
+          for (int j = 0; j < NG; ++j) pb[nt][j][r] = transpose_8x8(pack_f16x2(p[b][r][nt][0] * s[j], p[b][r][nt][HL - 1] * s[j]));
       }
     }
     // V's words, token rows g and g + 8 in lane g, become pairs of tokens (2t, 2t + 1) of the

@@ -21,10 +21,12 @@ def _clean_status():
     assert la().device_status(clear=True) == 0, "device status word set"
 
 
-def attend(w, s, kv, vv, keep=None):
-    """M.attention of sequence s alone over the keys that `keep` (one truth value per token) names: output, bound, weights."""
+def attend(w, s, kv, vv, keep=None, freqs=None, scale=None):
+    """M.attention of sequence s alone over the keys that `keep` (one truth value per token) names: output, bound, and
+    weights [hkv, G, t]."""
     hkv, d = w.num_kv_heads, w.head_dim
-    f = torch.as_tensor(w.rope_theta ** (-2.0 * np.arange(d // 2) / d), dtype=torch.float64, device="cuda")
+    scale = d ** -0.5 if scale is None else scale
+    f = torch.as_tensor(w.rope_theta ** (-2.0 * np.arange(d // 2) / d) if freqs is None else freqs, dtype=torch.float64, device="cuda")
 
     def rotate(x, n):
         c, r = torch.cos(n[:, None, None] * f), torch.sin(n[:, None, None] * f)
@@ -42,14 +44,35 @@ def attend(w, s, kv, vv, keep=None):
     if keep is not None:
         k, v = k[keep], v[keep]
     q = rotate(w.q[s].double().cuda()[None], torch.tensor([float(w.q_pos[s])], dtype=torch.float64, device="cuda"))[0].reshape(hkv, -1, d)
-    wgt = torch.softmax(torch.einsum("hgd,thd->hgt", q, k) * d ** -0.5, -1)
+    wgt = torch.softmax(torch.einsum("hgd,thd->hgt", q, k) * scale, -1)
     o = torch.einsum("hgt,thd->hgd", wgt, v)
-    e = d ** -0.5 * 2.0 ** -11 * 9 / 8 * q.norm(dim=-1) * k.norm(dim=-1).amax(0)[:, None]
+    e = scale * 2.0 ** -11 * 9 / 8 * q.norm(dim=-1) * k.norm(dim=-1).amax(0)[:, None]
     big = 2 * v.abs().reshape(-1, hkv, d // 64, 64).amax(-1)
     spread = torch.einsum("hgt,thj->hgj", wgt, big).repeat_interleave(64, -1)
     dev = torch.stack([torch.einsum("gt,tgd->gd", wgt[h], (v[:, h, None] - o[h][None]).abs()) for h in range(hkv)])
     bound = 2.0 ** -8 * o.abs() + e[..., None] * dev + 2.0 ** -10 * spread + 2.0 ** -18 * torch.einsum("hgt,thd->hgd", wgt, v.abs())
     return o.reshape(-1, d), bound.reshape(-1, d), wgt
+
+
+def partials_out(dv, k4, v4, plan, rope=None):
+    """The shared-run decode's fp32 partials merged in 64 bits: [B, Hq, d], without the output's rounding to bf16."""
+    L = la()
+    hq, d, n = dv.p.num_q_heads, dv.p.head_dim, plan.num_slots
+    ws = torch.full((L.decode_shared_workspace_bytes(dv.p, n) // 4,), float("nan"), device="cuda")
+    L.decode_shared_partials(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope if rope is None else rope, plan, ws)
+    acc = ws[:n * hq * d].view(n, hq, d).double()
+    m, l = ws[n * hq * d:n * hq * (d + 2)].view(n, hq, 2).double().unbind(-1)
+    out = []
+    for a, b in zip(plan.slot_indptr_host, plan.slot_indptr_host[1:]):
+        f = torch.exp2(m[a:b] - m[a:b].amax(0))
+        out.append((f[..., None] * acc[a:b]).sum(0) / (f * l[a:b]).sum(0)[..., None])
+    return torch.stack(out)
+
+
+def spans(v4, w):
+    """Per key and dim s c, the part of a V value above its group's zero, of a pool [blocks, heads, 16, d]."""
+    z = M.int4_values(np.concatenate((np.zeros_like(v4[..., :16 * w.head_dim // 2]), v4[..., 16 * w.head_dim // 2:]), -1), w.head_dim, True)
+    return torch.from_numpy(np.nan_to_num(M.int4_values(v4, w.head_dim, True) - z)).cuda()
 
 
 def opposed(w, c=8.0):
@@ -132,19 +155,12 @@ def test_shared_long_items_stay_exact(hq):
 # blocks the sums would be off by 1.5 times that bound.
 @pytest.mark.parametrize("hq", [32, 48])
 def test_shared_partials_of_256_blocks_stay_exact(hq):
-    L = la()
     w = one_document(131072, hq, 831)
     dv, k4, v4, kv, vv = on_device(w, id_bits=14)
     want, _ = M.attention(w, kv, vv)
     plan = shared_plan(dv, 256)
     assert plan.num_items == 32
-    ws = torch.full((L.decode_shared_workspace_bytes(dv.p, plan.num_slots) // 4,), float("nan"), device="cuda")
-    L.decode_shared_partials(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, plan, ws)
-    n = plan.num_slots * hq
-    acc = ws[:n * 128].view(plan.num_slots, hq, 128).double()
-    m, l = ws[n * 128:n * 130].view(plan.num_slots, hq, 2).double().unbind(-1)
-    f = torch.exp2(m - m.amax(0))
-    out = (f[..., None] * acc).sum(0) / (f * l).sum(0)[..., None]
+    out = partials_out(dv, k4, v4, plan)[0]
     assert ((out - want[0]).norm() / want.norm()).item() < 2.0 ** -9
 
 
@@ -184,3 +200,42 @@ def test_blocks_behind_a_bad_one_keep_their_positions(hq, hkv, d, bad):
             keep[16 * bad:16 * bad + 16] = False
         want, bound, _ = attend(w, s, kv, vv, keep)
         check(out[s], (want, bound), f"sequence {s}")
+
+
+# A weight times a V scale is rounded to f16 once. Every row has one key that outweighs the others by 2^4 to 2^7.9, in a tile
+# behind the first (so its weight is no power of two); no rotation, queries and keys of a single dim. Elementwise the fp32
+# partials are off by 2^-11 of sum_j w_j s c, by fp32's 2^-18 of sum_j w_j |v_j|, and by the rounding of the query times the
+# softmax scale to f16: 2^-11 of that key's score x in its exponent, which moves the output by 2^-11 x sum_j w_j |v_j - out|
+# at most. With a softmax scale of ln 2 / 8 the products are the queries times a power of two: nothing is rounded there.
+@pytest.mark.parametrize("hq,hkv,d", [(64, 1, 128), (32, 8, 128), (32, 2, 64)])
+@pytest.mark.parametrize("exact_scores", [False, True])
+def test_weight_times_scale_is_rounded_once(hq, hkv, d, exact_scores):
+    w = W.decode_zipf("i4w", batch=12, hq=hq, hkv=hkv, d=d, docs_per_seq=1, doc_tokens=41, pool_docs=1, zipf_s=1.0, share=False, seed=850)
+    last = w.doc_blocks[w.doc_block_indptr[1:][np.diff(w.doc_block_indptr) > 0] - 1].astype(np.int64)
+    w.k_pool = torch.where(torch.isnan(w.k_pool), w.k_pool, torch.zeros_like(w.k_pool))
+    w.k_pool[last, :, 8, 0] = 15.0  # token 40: code 15 of scale 1
+    w.q.zero_()
+    g = torch.Generator().manual_seed(851)
+    score = 4 + 3.9 * torch.rand(12, hq, generator=g, dtype=torch.float64)  # in log2 units
+    scale = float(np.float32(np.log(2.0) / 8)) if exact_scores else d ** -0.5
+    w.q[..., 0] = (score / scale / 15 / np.log2(np.e)).to(torch.bfloat16)
+    dv, k4, v4, kv, vv = on_device(w)
+    if exact_scores:
+        dv.p.sm_scale = scale
+    zero = np.zeros(d // 2)
+    out = partials_out(dv, k4, v4, shared_plan(dv), la().rope_table_init(dv.p, freqs=zero))
+    sc = spans(v4.cpu().numpy(), w)
+    worst = 0.0
+    for s in range(12):
+        want, _, wgt = attend(w, s, kv, vv, freqs=zero, scale=scale)
+        part = attend(w, s, kv, sc, freqs=zero, scale=scale)[0]
+        mean = attend(w, s, kv, vv.abs(), freqs=zero, scale=scale)[0]
+        bound = 2.0 ** -11 * part + 2.0 ** -18 * mean
+        if not exact_scores:
+            blk = torch.as_tensor(w.doc_blocks[int(w.doc_block_indptr[w.seq_segments(s)[0][0]]):][:3].astype(np.int64), device="cuda")
+            v = vv[blk].transpose(1, 2).reshape(-1, hkv, d)[:41]
+            x = w.q[s, :, 0].double().cuda() * 15 * scale
+            dev = torch.einsum("hgt,thgd->hgd", wgt, (v[:, :, None] - want.view(1, hkv, -1, d)).abs()).reshape(hq, d)
+            bound = bound + 2.0 ** -11 * x[:, None] * dev
+        worst = max(worst, ((out[s] - want).abs() / bound).max().item())
+    assert worst <= 1.0, f"off by {worst:.2f} of the bound"
