@@ -485,9 +485,10 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * even, at most 15); s = 0 and c = 0 where all are equal. A group with an infinity or a
  * NaN has s = z = NaN.
  *
- * The decodes on them (at most 65535 KV heads) round weight times V scale to f16, over a power
- * of two near the largest V scale of a sequence's part: to 2^-11 of each for scales within
- * 2^14 of the largest, below that to 2^-25 of the largest. */
+ * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
+ * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale of
+ * that group where that is more (weights over the row's largest in the part; a part is what one
+ * warp attends). Sums, maxima and zeros are fp32. */
 
 /* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold
  * num_pool_blocks * Hkv times that. 0 on bad params. */

@@ -239,3 +239,84 @@ def test_weight_times_scale_is_rounded_once(hq, hkv, d, exact_scores):
             bound = bound + 2.0 ** -11 * x[:, None] * dev
         worst = max(worst, ((out[s] - want).abs() / bound).max().item())
     assert worst <= 1.0, f"off by {worst:.2f} of the bound"
+
+
+def product_bound(w, s, v4, wgt):
+    """The bound on sequence s's fp32 partials that lazy_attn.h states for the weights' products, elementwise [hq, d]: with W
+    the weights over the row's largest, sum_j max(2^-11 W_j s_j, 2^-29 max s) c_j / sum_j W_j. wgt: softmax weights [hkv, G, t]."""
+    d, hkv = w.head_dim, w.num_kv_heads
+    pool = v4.cpu().numpy()
+    one = pool.copy()  # scales of 1, zeros of 0: the values are the codes; and codes of 1: the values are scales
+    meta = one[..., 8 * d:].reshape(*one.shape[:-1], -1, 4)
+    meta[...] = np.array([0x80, 0x3F, 0, 0], np.uint8)
+    codes = M.int4_values(one, d, True)
+    sc = pool.copy()
+    sc[..., :8 * d] = 0x11
+    sc[..., 8 * d:].reshape(*sc.shape[:-1], -1, 4)[..., 2:] = 0
+    scales = np.nan_to_num(M.int4_values(sc, d, True))
+
+    def tokens(x):
+        x, got = torch.from_numpy(x), []
+        for doc, n in w.seq_segments(s):
+            blk = torch.as_tensor(w.doc_blocks[int(w.doc_block_indptr[doc]):][:(n + 15) // 16].astype(np.int64))
+            got.append(x[blk].transpose(1, 2).reshape(-1, hkv, d)[:n])
+        return torch.cat(got).cuda()
+
+    c, sc = tokens(codes), tokens(scales)
+    top = sc.amax(0)
+    W = wgt / wgt.amax(-1, keepdim=True)
+    out = torch.empty(hkv, W.shape[1], d, dtype=torch.float64, device="cuda")
+    for h in range(hkv):
+        for g in range(W.shape[1]):
+            x = torch.maximum(2.0 ** -11 * W[h, g, :, None] * sc[:, h], 2.0 ** -29 * top[h]) * c[:, h]
+            out[h, g] = x.sum(0) / W[h, g].sum()
+    return out.reshape(-1, d)
+
+
+# One key far above a long flat tail, whose weights of 2^-20 to 2^-28 add up to between 2^-11 and 2^-3 of it: one team of warps
+# attends all of them (32 rows in one item). Scores without a rounding, as above. A lane adds the weights, and the weights times
+# zeros, of an eighth of the 131072 keys one by one in fp32, each sum off by 2^-24 of itself at most: 2^14 * 2^-24 of the sums
+# in all, which is 2^-10 (|out| + max |z|) of the output. (Tails below 2^-25 of the first key are lost there in its own lane.)
+def test_long_tail_of_small_weights():
+    w = one_document(131072, 32, 860)
+    w.k_pool.zero_()
+    w.k_pool[int(w.doc_blocks[0]), :, 0, 0] = 15.0  # the first key: code 15 of scale 1
+    scale = float(np.float32(np.log(2.0) / 8))
+    w.q.zero_()
+    w.q[0, :, 0] = (torch.linspace(20, 28, 32, dtype=torch.float64) * 8 / 15).to(torch.bfloat16)
+    dv, k4, v4, kv, vv = on_device(w, id_bits=14)
+    dv.p.sm_scale = scale
+    zero = np.zeros(64)
+    plan = shared_plan(dv, 8192)
+    out = partials_out(dv, k4, v4, plan, la().rope_table_init(dv.p, freqs=zero))[0]
+    want, _, wgt = attend(w, 0, kv, vv, freqs=zero, scale=scale)
+    bound = product_bound(w, 0, v4, wgt) + 2.0 ** -18 * attend(w, 0, kv, vv.abs(), freqs=zero, scale=scale)[0]
+    least = (vv - spans(v4.cpu().numpy(), w)).abs().max()
+    bound = bound + 2.0 ** -10 * (want.abs() + least)
+    worst = ((out - want).abs() / bound).max().item()
+    assert worst <= 1.0, f"off by {worst:.2f} of the bound"
+
+
+# A key that no query attends to (weight 2^-120) has V values of 2^10, 2^17 and 2^24 times the others', all of weight 1: what
+# it leaves of their products. Scores without a rounding, as above.
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (32, 2, 128), (16, 2, 64)])
+@pytest.mark.parametrize("big", [10, 17, 24])
+def test_large_v_scale_without_weight(hq, hkv, d, big):
+    w = W.decode_zipf("i4big", batch=2, hq=hq, hkv=hkv, d=d, docs_per_seq=1, doc_tokens=20, pool_docs=1, zipf_s=1.0, share=False, seed=861)
+    w.k_pool = torch.where(torch.isnan(w.k_pool), w.k_pool, torch.zeros_like(w.k_pool))
+    for s in range(2):
+        blk = int(w.doc_blocks[int(w.doc_block_indptr[w.seq_segments(s)[0][0]])])
+        w.k_pool[blk, :, 5, 0] = -60.0  # exact: the group's least value
+        w.v_pool[blk, :, 5] = (w.v_pool[blk, :, 5].double() * 2.0 ** big).to(torch.bfloat16)
+    w.q.zero_()
+    w.q[..., 0] = 16.0
+    dv, k4, v4, kv, vv = on_device(w)
+    dv.p.sm_scale = scale = float(np.float32(np.log(2.0) / 8))
+    zero = np.zeros(d // 2)
+    out = partials_out(dv, k4, v4, shared_plan(dv), la().rope_table_init(dv.p, freqs=zero))
+    for s in range(2):
+        want, _, wgt = attend(w, s, kv, vv, freqs=zero, scale=scale)
+        assert (wgt[:, :, 5] < 2.0 ** -119).all()
+        bound = product_bound(w, s, v4, wgt) + 2.0 ** -18 * attend(w, s, kv, vv.abs(), freqs=zero, scale=scale)[0]
+        worst = ((out[s] - want).abs() / bound).max().item()
+        assert worst <= 1.0, f"off by {worst:.2f} of the bound"
