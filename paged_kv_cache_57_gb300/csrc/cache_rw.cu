@@ -197,21 +197,21 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteA
 #pragma unroll
     for (int i = 0; i < ESZ / 2; ++i) x[n][i] = make_uint4(0, 0, 0, 0);
     if (t0 + n < a.num_tokens) {
-      slot[n] = __ldg(&a.slots[t0 + n]);
+      slot[n] = a.slots[t0 + n];
       const uint8_t* row = src + n * step;
       if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < ESZ / 2; ++i) x[n][i] = __ldg(reinterpret_cast<const uint4*>(row) + i);
+        for (int i = 0; i < ESZ / 2; ++i) x[n][i] = reinterpret_cast<const uint4*>(row)[i];
       } else if constexpr (ESZ == 4) {
         uint32_t* w = reinterpret_cast<uint32_t*>(x[n]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + i);
+        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[i];
       } else {
         uint32_t* w = reinterpret_cast<uint32_t*>(x[n]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          w[i] = __ldg(reinterpret_cast<const uint16_t*>(row) + 2 * i) |
-                 (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + 2 * i + 1) << 16;
+          w[i] = reinterpret_cast<const uint16_t*>(row)[2 * i] |
+                 (uint32_t)reinterpret_cast<const uint16_t*>(row)[2 * i + 1] << 16;
       }
     }
   }
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadArg
     const uint32_t i = rec / (2u * a.Hkv), rem = rec - i * (2u * a.Hkv);
     const bool is_v = rem >= (uint32_t)a.Hkv;
     const uint32_t h = is_v ? rem - a.Hkv : rem;
-    const int blk = __ldg(&a.block_ids[i]);
+    const int blk = a.block_ids[i];
     if (blk < 0) continue;  // padding: its rows stay as they are
     if (blk >= a.num_pool_blocks) {
       if (lane == 0) raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
@@ -270,23 +270,27 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadArg
     uint8_t* out = static_cast<uint8_t*>(is_v ? a.v_out : a.k_out);
     if constexpr (KIND == kCopy16 || KIND == kCopy32) {
       constexpr int BYTES = kBlock * D * (KIND == kCopy32 ? 4 : 2);
+      constexpr int PER = BYTES / 16 / 32;
+      const uint4* src = reinterpret_cast<const uint4*>(pool + src_rec * BYTES) + lane;
+      uint4 x[PER];
 #pragma unroll
-      for (int c = lane; c < BYTES / 16; c += 32)
-        reinterpret_cast<uint4*>(out + dst_rec * BYTES)[c] = __ldg(reinterpret_cast<const uint4*>(pool + src_rec * BYTES) + c);
+      for (int c = 0; c < PER; ++c) x[c] = src[32 * c];
+#pragma unroll
+      for (int c = 0; c < PER; ++c) reinterpret_cast<uint4*>(out + dst_rec * BYTES)[lane + 32 * c] = x[c];
     } else {
       uint32_t w[kBlock / RPW][2];
 #pragma unroll
       for (int n = 0; n < kBlock / RPW; ++n) {
         const int row = n * RPW + lane / LPR;
         if constexpr (KIND == kE4m3) {
-          const uint2 c = __ldg(reinterpret_cast<const uint2*>(pool + (src_rec * kBlock + row) * D + 8 * u));
+          const uint2 c = *reinterpret_cast<const uint2*>(pool + (src_rec * kBlock + row) * D + 8 * u);
           w[n][0] = c.x, w[n][1] = c.y;
         } else {
           using G = Int4Geom<D>;
           const uint8_t* base = pool + src_rec * G::REC;
           const int tok = is_v ? int4_v_token(row) : row;
-          w[n][0] = __ldg(reinterpret_cast<const uint32_t*>(base + row * G::ROW + 4 * u));
-          w[n][1] = __ldg(reinterpret_cast<const uint32_t*>(base + G::META + 4 * (tok * G::NG + u % G::NG)));
+          w[n][0] = *reinterpret_cast<const uint32_t*>(base + row * G::ROW + 4 * u);
+          w[n][1] = *reinterpret_cast<const uint32_t*>(base + G::META + 4 * (tok * G::NG + u % G::NG));
         }
       }
 #pragma unroll

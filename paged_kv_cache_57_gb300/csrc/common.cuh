@@ -101,7 +101,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
 }
 
 // Of a kernel started by launch_behind, in every thread and before any access to global memory:
-// the launch before it is complete and its writes are visible.
+// the launch before it is complete and its writes are visible. Such a kernel reads by ordinary
+// loads: the read-only path (ld.global.nc) is for data that nothing writes while the kernel
+// lives, and the launch before may write its inputs until this returns.
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Orders this thread's generic-proxy shared-memory accesses before later

@@ -91,7 +91,7 @@ constexpr int kMaxPiece = 512;
 constexpr int kMinChunk = 16;   // blocks of a range at least
 
 __device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& seq_len) {
-  seq_len = __ldg(&a.seq_lens[s]);
+  seq_len = a.seq_lens[s];
   if (seq_len < 0 || seq_len > kBlock * a.max_blocks) {
     raise_status(a.status, LAZY_DEV_BAD_LEN);
     seq_len = seq_len < 0 ? 0 : kBlock * a.max_blocks;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     const int heads = min(C::ROWS, a.G - head0);
     const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
     const int n = max(0, min(hi, nb) - lo);                          // blocks of the part
-    const int m_pos = __ldg(&a.q_pos[s]);
+    const int m_pos = a.q_pos[s];
     const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
 
     Int4QueryRows<NT> rows;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     const Int4RawRows<D, NT> raw(rows, lane);  // loads that nothing waits for yet
     float2 rate[HALF / 32];
 #pragma unroll
-    for (int j = 0; j < HALF / 32; ++j) rate[j] = __ldg(&a.rope[lane + 32 * j]);
+    for (int j = 0; j < HALF / 32; ++j) rate[j] = a.rope[lane + 32 * j];
 
     // ------------------------------------------------------------ first loads
     // quarters of whole stages
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     uint32_t w_nxt = 0, wn_nxt = 0;
     auto load_words = [&](int kc) {
       const int k = kc + lane, b = kb0 + k;
-      w_nxt = k < nk ? __ldg(&wrow[b]) : 0u;
-      wn_nxt = (k < nk && b + 1 < nb) ? __ldg(&wrow[b + 1]) : 0u;
+      w_nxt = k < nk ? wrow[b] : 0u;
+      wn_nxt = (k < nk && b + 1 < nb) ? wrow[b + 1] : 0u;
     };
     auto describe = [&](int kc) {  // the chunk of w_nxt
       const LaneBlock r = describe_block(kc + lane < nk, kb0 + kc + lane, nb, seq_len, w_nxt, wn_nxt, a.id_bits,
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     // the loop has no register for it. Control: the pool holds absolute-position keys.
     int p_cur = 0;  // the document that q is rotated for
     if (ns > 0) {
-      if constexpr (LAZY) p_cur = decode_word(__ldg(&wrow[kb0]), kb0, a.id_bits).p;
+      if constexpr (LAZY) p_cur = decode_word(wrow[kb0], kb0, a.id_bits).p;
       rebuild(m_pos - p_cur);
     }
 
@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
         if constexpr (LAZY) {
           // A tile lies in one document: where the second block starts another, the first is
           // attended alone, q is rotated anew, and the second follows.
-          const int b = kb0 + 2 * i, p0 = decode_word(__ldg(&wrow[b]), b, a.id_bits).p;
-          if (p0 != p_cur) rebuild(__ldg(&a.q_pos[s]) - (p_cur = p0));
-          p1 = nv[1] > 0 ? decode_word(__ldg(&wrow[b + 1]), b + 1, a.id_bits).p : p0;
+          const int b = kb0 + 2 * i, p0 = decode_word(wrow[b], b, a.id_bits).p;
+          if (p0 != p_cur) rebuild(a.q_pos[s] - (p_cur = p0));
+          p1 = nv[1] > 0 ? decode_word(wrow[b + 1], b + 1, a.id_bits).p : p0;
           if (p1 != p0) {
             nv1 = nv[1];
             nv[1] = 0;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
         nv[0] = 0;
         nv[1] = nv1;
         nv1 = 0;
-        rebuild(__ldg(&a.q_pos[s]) - (p_cur = p1));
+        rebuild(a.q_pos[s] - (p_cur = p1));
       }
       __syncwarp();
       if (i + R < ns) {  // refill the stage with the warp's pair R positions ahead
@@ -543,7 +543,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   const int* ids = it.rec + 8 + 4 * kMembers;  // the record's block ids
   uint32_t w_nxt = 0u;
   auto load_words = [&](int kc) {
-    if (kc + lane < nk) w_nxt = __ldg(&wrow[kc + lane]);
+    if (kc + lane < nk) w_nxt = wrow[kc + lane];
   };
   // Chunk kc of the team's words (w_nxt) to its descriptors, by every warp of the team alike.
   // The block word decides; where the record names the block too the two must agree.
@@ -597,9 +597,9 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
     bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
     int delta = 0;
     if (good) {
-      const BlockInfo mi = decode_word(__ldg(&a.words[(size_t)seq * a.max_blocks + bm]), bm, a.id_bits);
-      good = mi.phys == decode_word(__ldg(&a.words[(size_t)src * a.max_blocks + b0]), b0, a.id_bits).phys;
-      const int qp = __ldg(&a.q_pos[seq]);
+      const BlockInfo mi = decode_word(a.words[(size_t)seq * a.max_blocks + bm], bm, a.id_bits);
+      good = mi.phys == decode_word(a.words[(size_t)src * a.max_blocks + b0], b0, a.id_bits).phys;
+      const int qp = a.q_pos[seq];
       delta = LAZY ? qp - mi.p : qp;
     }
     if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
@@ -610,7 +610,7 @@ __device__ __forceinline__ void shared_int4_rows(const SharedDecodeArgs& a, cons
   // the angles of the CTA's members
   const int m0 = row0 / a.G, m1 = (rows - 1) / a.G;
   for (int idx = m0 * HALF + threadIdx.x; idx < (m1 + 1) * HALF; idx += kThreads)
-    cs_tab[idx] = rope_cs(__ldg(&a.rope[idx % HALF]), it.delta[idx / HALF], a.status);
+    cs_tab[idx] = rope_cs(a.rope[idx % HALF], it.delta[idx / HALF], a.status);
   __syncthreads();
 
   // ------------------------------------------------------------ queries
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
   const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv / halves, half = blockIdx.x / a.Hkv % halves;
   if (threadIdx.x < kItemInts / 4)
     reinterpret_cast<int4*>(it.rec)[threadIdx.x] =
-        __ldg(reinterpret_cast<const int4*>(a.items) + (size_t)item * (kItemInts / 4) + threadIdx.x);
+        reinterpret_cast<const int4*>(a.items)[(size_t)item * (kItemInts / 4) + threadIdx.x];
   __syncthreads();
   const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3], nmem = it.rec[4];
   const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&

@@ -163,7 +163,7 @@ struct Int4RawRows {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        x[nt][i] = __ldg(reinterpret_cast<const uint4*>(r.q[nt] + int4_word_dim<D>(lane & 3, i)));
+        x[nt][i] = *reinterpret_cast<const uint4*>(r.q[nt] + int4_word_dim<D>(lane & 3, i));
   }
 };
 
@@ -207,8 +207,8 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, const 
       asm volatile("" ::: "memory");  // one word's loads at a time: registers
       const int base = int4_word_dim<D>(t, i);
       const float sgn = base < HALF ? -1.f : 1.f;
-      const uint4 x4 = __ldg(reinterpret_cast<const uint4*>(rows.q[nt] + base));
-      const uint4 y4 = __ldg(reinterpret_cast<const uint4*>(rows.q[nt] + (base ^ HALF)));
+      const uint4 x4 = *reinterpret_cast<const uint4*>(rows.q[nt] + base);
+      const uint4 y4 = *reinterpret_cast<const uint4*>(rows.q[nt] + (base ^ HALF));
       const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
       float v[8];
 #pragma unroll
