@@ -164,6 +164,22 @@ def _kvdt(p: Params):
     return torch.float8_e4m3fn if p.kv_dtype == LAZY_FP8_E4M3 else _tdt(p)
 
 
+def _cache_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
+    """The pools' pointers, checked: type, device, size."""
+    rows, int4 = p.num_pool_blocks * p.num_kv_heads, p.kv_dtype == LAZY_INT4
+    n, dt = rows * p.head_dim * (9 if int4 else BLOCK), torch.uint8 if int4 else _kvdt(p)
+    if k_pool.numel() < n or v_pool.numel() < n:
+        raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
+    return _dptr(k_pool, "k_pool", dt), _dptr(v_pool, "v_pool", dt)
+
+
+def _pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
+    """The decodes' pools. int4 records are plain bytes, which any uint8 tensor is: their number is checked too."""
+    if p.kv_dtype == LAZY_INT4:
+        return _cache_pools(p, k_pool, v_pool)
+    return _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p))
+
+
 # ---------------------------------------------------------------- rotation table
 
 def rope_table_bytes(p: Params) -> int:
@@ -274,7 +290,7 @@ def decode(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tenso
            workspace: Optional[torch.Tensor] = None, stream=None,
            alibi_slopes: Optional[torch.Tensor] = None) -> torch.Tensor:
     """alibi_slopes (fp32 [Hq]) selects lazy_attn_decode_alibi: words packed with key_positions=True."""
-    dt = _tdt(p)
+    dt, pools = _tdt(p), _pools(p, k_pool, v_pool)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:  # the library checks a given workspace's size itself
@@ -282,7 +298,7 @@ def decode(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tenso
         if nws:
             workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    head = (ctypes.byref(p), _dptr(q, "q", dt), _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p)),
+    head = (ctypes.byref(p), _dptr(q, "q", dt), *pools,
             _dptr(block_words, "block_words"), _dptr(seq_lens, "seq_lens", torch.int32),
             _dptr(q_pos, "q_pos", torch.int32), _dptr(rope_table, "rope_table"))
     tail = (_dptr(out, "out", dt), _dptr(workspace, "workspace"), wsz, _stream(stream))
@@ -302,9 +318,8 @@ def decode_noalloc(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: tor
     """Decode whose split-K scratch is the library's static device array (for callers
     that cannot allocate a workspace). ``out`` is required: the call allocates nothing.
     Calls that overlap on the GPU share that array and must not run concurrently."""
-    dt = _tdt(p)
-    rc = _lib.lazy_attn_decode_noalloc(ctypes.byref(p), _dptr(q, "q", dt), _dptr(k_pool, "k_pool", _kvdt(p)),
-                                       _dptr(v_pool, "v_pool", _kvdt(p)), _dptr(block_words, "block_words"),
+    dt, pools = _tdt(p), _pools(p, k_pool, v_pool)
+    rc = _lib.lazy_attn_decode_noalloc(ctypes.byref(p), _dptr(q, "q", dt), *pools, _dptr(block_words, "block_words"),
                                        _dptr(seq_lens, "seq_lens", torch.int32), _dptr(q_pos, "q_pos", torch.int32),
                                        _dptr(rope_table, "rope_table"), _dptr(out, "out", dt), _stream(stream))
     _check(rc, "decode_noalloc")
@@ -366,7 +381,7 @@ def decode_shared(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torc
                   workspace: Optional[torch.Tensor] = None, stream=None,
                   alibi_slopes: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Shared-run decode; ``alibi_slopes`` (device fp32 [Hq]) selects the ALiBi call."""
-    dt = _tdt(p)
+    dt, pools = _tdt(p), _pools(p, k_pool, v_pool)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:  # the library checks a given workspace's size itself
@@ -375,7 +390,7 @@ def decode_shared(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torc
             workspace = torch.empty(nws, dtype=torch.uint8, device=q.device)
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     i32 = torch.int32
-    args = (ctypes.byref(p), _dptr(q, "q", dt), _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p)),
+    args = (ctypes.byref(p), _dptr(q, "q", dt), *pools,
             _dptr(block_words, "block_words"), _dptr(q_pos, "q_pos", i32), _dptr(rope_table, "rope_table"),
             plan.num_items, _dptr(plan.items, "items", i32), plan.num_slots,
             _dptr(plan.slot_indptr, "slot_indptr", i32))
@@ -394,10 +409,11 @@ def decode_shared_partials(p: Params, q: torch.Tensor, k_pool: torch.Tensor, v_p
                            block_words: torch.Tensor, q_pos: torch.Tensor, rope_table: torch.Tensor, plan: SharedPlan,
                            workspace: torch.Tensor, stream=None) -> torch.Tensor:
     """First pass of decode_shared: fp32 partials of every slot into ``workspace``."""
+    pools = _pools(p, k_pool, v_pool)
     wsz = workspace.numel() * workspace.element_size()
     i32 = torch.int32
     rc = _lib.lazy_attn_decode_shared_partials(
-        ctypes.byref(p), _dptr(q, "q", _tdt(p)), _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p)),
+        ctypes.byref(p), _dptr(q, "q", _tdt(p)), *pools,
         _dptr(block_words, "block_words"), _dptr(q_pos, "q_pos", i32), _dptr(rope_table, "rope_table"),
         plan.num_items, _dptr(plan.items, "items", i32), plan.num_slots, _dptr(workspace, "workspace"), wsz,
         _stream(stream))
@@ -487,15 +503,6 @@ def empty_pools(p: Params, device="cuda"):
     tail = (n,) if p.kv_dtype == LAZY_INT4 else (BLOCK, p.head_dim)
     return tuple(torch.empty((p.num_pool_blocks, p.num_kv_heads) + tail, dtype=_kvdt(p), device=device)
                  for _ in range(2))
-
-
-def _cache_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
-    """The pools' pointers, checked: type, device, size."""
-    rows, int4 = p.num_pool_blocks * p.num_kv_heads, p.kv_dtype == LAZY_INT4
-    n, dt = rows * p.head_dim * (9 if int4 else BLOCK), torch.uint8 if int4 else _kvdt(p)
-    if k_pool.numel() < n or v_pool.numel() < n:
-        raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
-    return _dptr(k_pool, "k_pool", dt), _dptr(v_pool, "v_pool", dt)
 
 
 def token_slots(blocks, first: int, count: int) -> np.ndarray:
