@@ -414,7 +414,7 @@ static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const v
   a.v_pool = v_pool;
   a.out = out;
   if (need > 0) {
-    const size_t parts = (size_t)2 * a.plan.ctas * a.plan.rows;
+    const size_t parts = (size_t)2 * a.plan.parts * a.plan.rows;
     a.ws_o = static_cast<float*>(workspace);
     a.ws_ml = a.ws_o + parts * p->head_dim;
     a.prefix = reinterpret_cast<int64_t*>(a.ws_ml + parts * 2);
@@ -431,7 +431,7 @@ static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const v
   a.scale_log2 = scale_log2(p);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int rc = launched(lazy::launch_decode_int4(a, p->lazy != 0, cs));
-  if (rc != LAZY_OK || a.plan.direct) return rc;
+  if (rc != LAZY_OK || a.plan.parts == 0) return rc;
   return launched(lazy::launch_combine_int4(a, cs));
 }
 

@@ -61,19 +61,21 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 // where 4 would do take 83 us against 77 on 64 x 4160 tokens, tiles of 8 instead of 16 345
 // against 258 on 32 heads per KV head.
 //
-// Equal pieces: every unit is cut into the same number of pieces of a length that the host
-// knows, one CTA each, as many as fill the resident CTAs once (at least kMinPiece blocks a
-// piece, and whole units where there are more of them than resident CTAs: those are written
-// out, without parts and a join).
+// Equal pieces: a unit is cut into pieces of the same length, one CTA each: as many as let all
+// units fill the resident CTAs once, of at least 32 blocks by the sequence's own length
+// (a block table is as wide as a captured step may need; CTAs that its sequence leaves without
+// a piece end at once). Units of one piece are written out, without parts and a join.
 //
-// Ranges: where a piece could be longer than kMaxPiece, the length of the longest sequence
+// Ranges: where a piece would be longer than kMaxPiece, the length of the longest sequence
 // says too little about the others. The units' blocks are laid end to end and cut into equal
 // ranges, one per resident CTA: batches of any lengths give every CTA the same work. A CTA
-// goes through its range unit by unit; a unit that lies in one range is written out.
+// goes through its range unit by unit; a unit that lies in one range is written out. Where the
+// table's width does not rule ranges out the kernel looks for the longest sequence itself.
 //
-// Measured from HBM (pieces, ranges; us): 64 sequences up to 2048 tokens 33 57, up to 4096 60
-// 75, up to 8192 91 93, all of 4160 74 77; 256 of 1024 73 89; 8 of 4096 21 26; one of 16384 17
-// 19; 48 up to 131072 with one KV head (pieces of 2731 blocks) 460 255.
+// Measured from HBM (pieces, ranges; us), 32 heads on 8: 64 sequences of 256 blocks 63 68, of 512
+// 118 113, of 600 139 130, of 1000 225 210, of 2000 439 397; of up to 512 106 96, of up to 1024
+// 189 138; 4 of 8192 (pieces of 432) 105 109. 32 heads on one: 16 of 2000 (pieces of 106) 63 69,
+// 48 of up to 3750 (pieces of 1250) 215 145.
 //
 // The other parts go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that
 // begins in CTA c's places, 2 c for one that began before) and are merged by
@@ -86,7 +88,7 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 
 namespace {
 
-constexpr int kMinPiece = 32;   // blocks of a piece at least: one of 16384 tokens 17 us, with 16 or 64 19
+constexpr int kMinPieceLog2 = 5;  // 32 blocks of a piece at least: one of 16384 tokens 17 us, with 16 or 64 19
 constexpr int kMaxPiece = 512;
 constexpr int kMinChunk = 16;   // blocks of a range at least
 
@@ -99,10 +101,28 @@ __device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& se
   return (seq_len + kBlock - 1) / kBlock;
 }
 
+// Blocks of a piece of a sequence of nb blocks.
+__host__ __device__ __forceinline__ int piece_of(const Int4Plan& p, int nb) {
+  if (p.splits == 1) return nb;
+  const int n = max(1, min(p.splits, nb >> p.least_log2));
+  return (int)((unsigned)(nb + n - 1) / (unsigned)n);
+}
+
+// Blocks of a range, of `total` in all.
 __device__ __forceinline__ int64_t chunk_of(const Int4DecodeArgs& a, int64_t total) {
-  if (a.plan.unit_len > 0) return a.plan.chunk;
-  const int64_t c = (total + a.plan.ctas - 1) / a.plan.ctas;
-  return c > a.plan.chunk ? c : a.plan.chunk;
+  const int64_t c = (total + a.plan.range_ctas - 1) / a.plan.range_ctas;
+  return c > kMinChunk ? c : kMinChunk;
+}
+
+// Whether the batch is cut into ranges (every warp by itself).
+__device__ __forceinline__ bool takes_ranges(const Int4DecodeArgs& a, int lane) {
+  int longest = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    int len;
+    longest = max(longest, blocks_of(a, b, len));
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  return piece_of(a.plan, longest) > kMaxPiece;
 }
 
 }  // namespace
@@ -125,20 +145,26 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int U = a.plan.units, ht = U / a.Hkv;
 
-  // ------------------------------------------------------------ the CTA's range
-  int s = 0, seq_len = 0;
-  int64_t at = 0, left;  // place within sequence s (its units end to end); places left of the range
-  if (a.plan.unit_len > 0) {
-    const int64_t per_seq = (int64_t)U * a.plan.unit_len, lo = (int64_t)blockIdx.x * a.plan.chunk;
-    s = (int)(lo / per_seq);
-    at = lo - s * per_seq;
-    left = a.plan.chunk;
+  // ------------------------------------------------------------ the CTA's piece or range
+  int s = 0, seq_len = 0, nb = 0, u = 0, lo = 0, hi = 0;  // the part: blocks lo .. hi - 1 of unit u of s
+  int64_t at = 0, left = 0;  // place within sequence s (its units end to end); places left of the range
+  const bool ranges = a.plan.range_ctas > 0 && takes_ranges(a, lane);
+  if (a.plan.range_ctas > 0 && blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B + 1] = ranges;
+  if (!ranges) {  // first pieces first: CTAs without one are the last, not between those of one SM
+    const unsigned units = (unsigned)a.B * U, piece = blockIdx.x / units, unit = blockIdx.x - piece * units;
+    s = unit / U;
+    u = unit - s * U;
+    nb = blocks_of(a, s, seq_len);
+    const int len = piece_of(a.plan, nb);
+    lo = piece * len;
+    hi = min(nb, lo + len);
+    if (piece > 0 && lo >= nb) return;
   } else {  // every warp for itself: the total, then the sequence of the range's first place
     int64_t total = 0;
-    int nb = 0, inc = 0;  // of the last 32 sequences: the lane's blocks, and up to them
+    int own = 0, inc = 0;  // of the last 32 sequences: the lane's blocks, and up to them
     auto scan = [&](int b) {
       int len;
-      inc = nb = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
+      inc = own = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -147,44 +173,46 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     };
     for (int b = 0; b < a.B; b += 32) {
       scan(b);
-      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = total + inc - nb;
+      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = total + inc - own;
       total += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = total;
     total *= U;
-    const int64_t chunk = chunk_of(a, total), lo = blockIdx.x * chunk;
-    left = min(chunk, total - lo);
+    const int64_t chunk = chunk_of(a, total), first = blockIdx.x * chunk;
+    left = min(chunk, total - first);
     if (left <= 0) return;
     int64_t before = 0;
     for (s = 0; s < a.B; s += 32) {
       if (a.B > 32) scan(s);
-      const uint32_t past = __ballot_sync(0xffffffffu, (before + inc) * U > lo);  // sequences that end behind lo
+      const uint32_t past = __ballot_sync(0xffffffffu, (before + inc) * U > first);  // sequences that end behind it
       if (past) {
         const int l = __ffs(past) - 1;
         s += l;
-        at = lo - (before + __shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, nb, l)) * U;
+        at = first - (before + __shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, own, l)) * U;
         break;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
-  while (left > 0 && s < a.B) {
+  while (true) {
     // ------------------------------------------------------------ the next part
-    const int nb = blocks_of(a, s, seq_len);
-    const int len = a.plan.unit_len > 0 ? a.plan.unit_len : nb;  // places of a unit
-    if (len == 0 || at >= (int64_t)U * len) {
-      at -= (int64_t)U * len;
-      ++s;
-      continue;
+    if (left > 0) {
+      if (s >= a.B) return;
+      nb = blocks_of(a, s, seq_len);
+      if (nb == 0 || at >= (int64_t)U * nb) {
+        at -= (int64_t)U * nb;
+        ++s;
+        continue;
+      }
+      u = (int)(at / nb), lo = (int)(at - (int64_t)u * nb);
+      hi = (int)min((int64_t)nb, lo + left);
+      at += hi - lo;
+      left -= hi - lo;
     }
-    const int u = (int)(at / len), lo = (int)(at - (int64_t)u * len);
-    const int hi = (int)min((int64_t)len, lo + left);
-    at += hi - lo;
-    left -= hi - lo;
     const int kvh = u / ht, head0 = (u - kvh * ht) * C::ROWS;
     const int heads = min(C::ROWS, a.G - head0);
     const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
-    const int n = max(0, min(hi, nb) - lo);                          // blocks of the part
+    const int n = hi - lo;                                           // blocks of the part
     const int m_pos = a.q_pos[s];
     const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
 
@@ -312,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
     float* red = reinterpret_cast<float*>(smem);
     int4_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
     __syncthreads();
-    const bool whole = lo == 0 && hi == len;
+    const bool whole = lo == 0 && hi == nb;
     const size_t slot0 = (2 * (size_t)blockIdx.x + (lo == 0 ? 1 : 0)) * C::ROWS;
     for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
       const int row = idx / D, col = idx % D;
@@ -335,12 +363,13 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
         if (col == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * (slot0 + row)) = make_float2(M, L);
       }
     }
+    if (left <= 0) return;
     __syncthreads();  // the next part's loads and queries take the merge's place
   }
 }
 
-// out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit that lies in
-// several CTAs' ranges; 0 for a sequence without blocks. A CTA looks after PAIRS (sequence,
+// out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit of several pieces
+// or in several ranges; with ranges 0 for a sequence without blocks. A CTA looks after PAIRS (sequence,
 // query head) pairs: a warp finds a pair's parts and merges up to kCombineBatch of them by
 // itself; more are shared by the CTA's warps. Launched as a programmatic dependent of the
 // decode kernel: it waits for that grid before it reads anything.
@@ -357,13 +386,13 @@ template <int D>
 struct Merged {
   static constexpr int PER = D / 32;
   float M, L, acc[PER];
-  // Parts c0 + first, c0 + first + step, ... c1 of a row, a lane the columns lane + 32 i.
-  __device__ __forceinline__ Merged(const Int4DecodeArgs& a, int row, int c0, int c1, int first, int step) {
+  // Parts first, first + step, ... of a row's n, a lane the columns lane + 32 i. Part i is CTA c0 + i stride's.
+  __device__ __forceinline__ Merged(const Int4DecodeArgs& a, int row, int c0, int n, int stride, int first, int step) {
     const int lane = threadIdx.x & 31;
     M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int cb = c0 + first; cb <= c1; cb += step * kCombineBatch) {
+    for (int cb = first; cb < n; cb += step * kCombineBatch) {
       float2 ml[kCombineBatch];
       float v[kCombineBatch][PER];
 #pragma unroll
@@ -372,8 +401,8 @@ struct Merged {
         ml[b] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int i = 0; i < PER; ++i) v[b][i] = 0.f;
-        if (c <= c1) {
-          const size_t p = (2 * (size_t)c + (c == c0 ? 1 : 0)) * a.plan.rows + row;
+        if (c < n) {
+          const size_t p = (2 * ((size_t)c0 + (size_t)c * stride) + (c == 0 ? 1 : 0)) * a.plan.rows + row;
           ml[b] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * p);
 #pragma unroll
           for (int i = 0; i < PER; ++i) v[b][i] = a.ws_o[p * D + lane + 32 * i];
@@ -405,41 +434,40 @@ template <int D, int PAIRS>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const Int4DecodeArgs a) {
   constexpr int PER = D / 32;
   __shared__ float red[kCombineWarps][D + 2];
-  __shared__ int2 parts[PAIRS];  // what the CTA's warps share: first and last part
+  __shared__ int2 parts[PAIRS];  // what the CTA's warps share: first part's CTA and parts; 0 or 1: nothing to merge
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t pair0 = (int64_t)blockIdx.x * PAIRS, pairs = (int64_t)a.B * a.Hq;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   auto row_of = [&](int64_t pair) { return (int)(pair % a.Hq) % a.G % a.plan.rows; };
   wait_for_launch_before();
+  const bool ranges = a.plan.range_ctas > 0 && a.prefix[a.B + 1] != 0;
+  const int stride = ranges ? 1 : a.B * a.plan.units;
   if (warp < PAIRS) {
     const int64_t pair = pair0 + warp;
     int2 mine = make_int2(0, 0);
     if (pair < pairs) {
       const int s = (int)(pair / a.Hq), h = (int)(pair - (int64_t)s * a.Hq), kvh = h / a.G;
       const int u = kvh * (a.plan.units / a.Hkv) + (h - kvh * a.G) / a.plan.rows;
-      int64_t lo, len, total = 0;
-      if (a.plan.unit_len > 0) {
-        len = a.plan.unit_len;
-        lo = ((int64_t)s * a.plan.units + u) * len;
-      } else {
-        const int64_t p0 = a.prefix[s];
-        len = a.prefix[s + 1] - p0;
-        lo = p0 * a.plan.units + u * len;
-        total = a.prefix[a.B] * a.plan.units;
-      }
-      if (len == 0) {
+      if (ranges) {
+        const int64_t p0 = a.prefix[s], len = a.prefix[s + 1] - p0, lo = p0 * a.plan.units + u * len;
+        const int64_t chunk = chunk_of(a, a.prefix[a.B] * a.plan.units);
+        if (len == 0) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(0.f);
-      } else {
-        const int64_t chunk = chunk_of(a, total);
-        mine = make_int2((int)(lo / chunk), (int)((lo + len - 1) / chunk));  // in one range: written there
-        if (PAIRS > 1 && mine.x < mine.y && mine.y - mine.x < kCombineBatch) {
-          const Merged<D> m(a, row_of(pair), mine.x, mine.y, 0, 1);
-#pragma unroll
-          for (int i = 0; i < PER; ++i)
-            out[pair * D + lane + 32 * i] = __float2bfloat16_rn(m.L == 0.f ? 0.f : m.acc[i] / m.L);
-          mine.y = mine.x;
+          for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(0.f);
+        } else {
+          const int64_t c0 = lo / chunk;
+          mine = make_int2((int)c0, (int)((lo + len - 1) / chunk - c0) + 1);  // in one range: written there
         }
+      } else {
+        int seq_len;
+        const int nb = blocks_of(a, s, seq_len), len = piece_of(a.plan, nb);
+        mine = make_int2(s * a.plan.units + u, nb > len ? (nb + len - 1) / len : 1);  // of one piece: written there
+      }
+      if (PAIRS > 1 && mine.y > 1 && mine.y <= kCombineBatch) {
+        const Merged<D> m(a, row_of(pair), mine.x, mine.y, stride, 0, 1);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(m.L == 0.f ? 0.f : m.acc[i] / m.L);
+        mine.y = 0;
       }
     }
     if (lane == 0) parts[warp] = mine;
@@ -447,9 +475,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const 
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < PAIRS; ++i) {
-    const int c0 = parts[i].x, c1 = parts[i].y;
-    if (c0 == c1) continue;
-    const Merged<D> m(a, row_of(pair0 + i), c0, c1, warp, kCombineWarps);
+    const int2 p = parts[i];
+    if (p.y <= 1) continue;
+    const Merged<D> m(a, row_of(pair0 + i), p.x, p.y, stride, warp, kCombineWarps);
 #pragma unroll
     for (int j = 0; j < PER; ++j) red[warp][lane + 32 * j] = m.acc[j];
     if (lane == 0) {
@@ -700,7 +728,6 @@ template <int D, bool LAZY>
 __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
                                                                          const uint8_t* v_pool, int halves) {
   using C = Int4SharedCfg<D>;
-  constexpr int HALF = D / 2;
   extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
   float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][D / 2]
   __shared__ __align__(16) Int4Item it;
@@ -734,25 +761,22 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
   const int mb = max_blocks > 0 ? max_blocks : 1;
   const int64_t units = (int64_t)(B > 0 ? B : 1) * p.units;
   const int64_t resident = (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS);
-  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(resident / units, mb / kMinPiece));
-  if (num_splits > 0 || (mb + pieces - 1) / pieces <= kMaxPiece) {
-    const int s = num_splits > 0 ? std::min(num_splits, mb) : (int)pieces;
-    p.chunk = (mb + s - 1) / s;
-    const int splits = (mb + p.chunk - 1) / p.chunk;
-    p.unit_len = splits * p.chunk;
-    p.ctas = units * splits;
-    p.direct = splits == 1;
-  } else {
-    const int64_t useful = (units * mb + kMinChunk - 1) / kMinChunk;
-    p.ctas = std::min<int64_t>(useful, resident);
-    p.chunk = kMinChunk;
+  p.least_log2 = num_splits > 0 ? 0 : kMinPieceLog2;
+  p.splits = num_splits > 0 ? std::min(num_splits, mb)
+                            : (int)std::max<int64_t>(1, std::min<int64_t>(resident / units, mb >> kMinPieceLog2));
+  p.ctas = units * p.splits;
+  p.parts = p.splits > 1 ? p.ctas : 0;
+  if (num_splits <= 0 && piece_of(p, mb) > kMaxPiece) {
+    p.range_ctas = std::min<int64_t>((units * mb + kMinChunk - 1) / kMinChunk, resident);
+    p.ctas = std::max(p.ctas, p.range_ctas);
+    p.parts = std::max(p.parts, p.range_ctas);
   }
   return p;
 }
 
 size_t decode_int4_workspace_bytes(const Int4Plan& p, int B, int D) {
-  if (p.direct) return 0;
-  return (size_t)2 * p.ctas * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 1) * sizeof(int64_t);
+  if (p.parts == 0) return 0;
+  return (size_t)2 * p.parts * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(int64_t);
 }
 
 template <int D, int NT, int HL, bool LAZY>

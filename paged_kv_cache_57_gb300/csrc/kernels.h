@@ -288,24 +288,28 @@ cudaError_t launch_cache_write(const CacheWriteArgs& a, int kv_dtype, bool vec, 
 cudaError_t launch_cache_read(const CacheReadArgs& a, int kv_dtype, int sms, cudaStream_t st);
 
 // int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool.
-// A unit is one sequence's blocks for one KV head and tile of `rows` query heads; the units'
-// blocks, laid end to end, are cut into equal ranges, one per CTA.
+// A unit is one sequence's blocks for one KV head and tile of `rows` query heads. Each is cut
+// into pieces of equal length, one per CTA, by its own sequence's length; or, where the longest
+// sequence would have pieces of more than 512 blocks, the units' blocks are laid end to end and
+// cut into equal ranges, one per CTA. Both are settled on the device.
 struct Int4Plan {
-  int rows;        // query heads of a unit: 4, 8 or 16
-  int units;       // units of a sequence: KV heads x head tiles
-  int64_t ctas;    // refused past INT_MAX
-  int unit_len;    // > 0: every unit has this many places (split into equal parts); 0: its blocks
-  int chunk;       // places of a CTA with unit_len, else the least a CTA takes
-  bool direct;     // every CTA has one whole unit: no partials
+  int rows;            // query heads of a unit: 4, 8 or 16
+  int units;           // units of a sequence: KV heads x head tiles
+  int splits;          // pieces of a unit at most
+  int least_log2;      // log2 of the blocks of a piece at least
+  int64_t ctas;        // refused past INT_MAX
+  int64_t range_ctas;  // CTAs that share the batch as ranges; 0: no sequence can be that long
+  int64_t parts;       // CTAs that may leave a part of a unit; 0: every unit is one piece, without a join
 };
 struct Int4DecodeArgs : DecodeArgs {
   Int4Plan plan;
-  int64_t* prefix;  // [B + 1] blocks of the sequences before each (unit_len = 0); in the workspace
+  int64_t* prefix;  // with range_ctas: [B + 1] blocks of the sequences before each, and whether ranges were taken
 };
-// num_splits > 0: that many equal parts of max_blocks; else chosen. sms: the device's.
+// num_splits > 0: that many pieces of every unit (fewer of a sequence with fewer blocks); else chosen.
+// sms: the device's.
 Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
 size_t decode_int4_workspace_bytes(const Int4Plan& plan, int B, int D);
-// a.ws_o: [2 ctas][rows][D], a.ws_ml: [2 ctas][rows][2], then a.prefix, where not direct.
+// a.ws_o: [2 parts][rows][D], a.ws_ml: [2 parts][rows][2], then a.prefix, where there are parts.
 cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t st);
 cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_shared_int4(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,

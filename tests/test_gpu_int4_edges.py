@@ -320,3 +320,28 @@ def test_large_v_scale_without_weight(hq, hkv, d, big):
         bound = product_bound(w, s, v4, wgt) + 2.0 ** -18 * attend(w, s, kv, vv.abs(), freqs=zero, scale=scale)[0]
         worst = ((out[s] - want).abs() / bound).max().item()
         assert worst <= 1.0, f"off by {worst:.2f} of the bound"
+
+
+# A captured step's block table is as wide as its longest sequence may become: pieces and ranges go by the sequences' own
+# lengths, so the same bits come out at every width. 4, 3 and 96 sequences: several pieces a unit, one piece a unit, and ranges
+# (a sequence of more than 512 blocks a piece); entries behind a sequence are never read.
+@pytest.mark.parametrize("batch,hq,hkv,d,hi", [(4, 32, 8, 128, 4200), (3, 8, 1, 64, 9000), (96, 16, 8, 64, 3000), (96, 16, 8, 64, 12000),
+                                               (20, 32, 1, 128, 60000)])
+def test_width_of_the_table_changes_nothing(batch, hq, hkv, d, hi):
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=batch, n_prefill=1, chunk=16, hq=hq, hkv=hkv, d=d, pool_docs=40, ctx_lo=1, ctx_hi=hi, doc_lo=1,
+                        doc_hi=700, seed=870 + batch)
+    dv, k4, v4, kv, vv = on_device(dw)
+    tight, ref = decode(dv, k4, v4), M.attention(dw, kv, vv)
+    check(tight, ref, "tight")
+    mb, words = dv.p.max_blocks_per_seq, dv.words
+    for wide in (mb + 1, 2048, 8192, 30000):
+        if wide <= mb:
+            continue
+        dv.p.max_blocks_per_seq = wide
+        dv.words = torch.full((batch, wide), -1, dtype=torch.int32, device="cuda")
+        dv.words[:, :mb] = words
+        ws = torch.full((L.decode_workspace_bytes(dv.p),), 255, dtype=torch.uint8, device="cuda")
+        out = decode(dv, k4, v4, workspace=ws)
+        check(out, ref, f"{wide} blocks wide")
+        assert torch.equal(out.view(torch.int16), tight.view(torch.int16)), f"{wide} blocks wide"
