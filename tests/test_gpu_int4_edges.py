@@ -345,3 +345,44 @@ def test_width_of_the_table_changes_nothing(batch, hq, hkv, d, hi):
         out = decode(dv, k4, v4, workspace=ws)
         check(out, ref, f"{wide} blocks wide")
         assert torch.equal(out.view(torch.int16), tight.view(torch.int16)), f"{wide} blocks wide"
+
+
+def test_captured_step_follows_its_lengths():
+    # one capture, a wide table, lengths that pass from ranges to whole units, to pieces, to nothing and back; the workspace is
+    # another captured call's too
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=96, n_prefill=1, chunk=16, hq=16, hkv=8, d=64, pool_docs=40, ctx_lo=1, ctx_hi=12000, doc_lo=1,
+                        doc_hi=700, seed=880)
+    dv, k4, v4, _, _ = on_device(dw)
+    mb, full = dv.p.max_blocks_per_seq, dv.seq_lens.clone()
+    assert mb > 512
+    words = torch.full((96, 4096), -1, dtype=torch.int32, device="cuda")
+    words[:, :mb] = dv.words
+    dv.words, dv.p.max_blocks_per_seq = words, 4096
+    ws = torch.empty(L.decode_workspace_bytes(dv.p), dtype=torch.uint8, device="cuda")
+    small = L.Params.from_buffer_copy(dv.p)
+    small.num_seqs = 2  # many pieces a unit
+    lens, out, out2 = full.clone(), torch.empty_like(dv.q), torch.empty_like(dv.q[:2])
+
+    def step():
+        L.decode(dv.p, dv.q, k4, v4, dv.words, lens, dv.q_pos, dv.rope, out=out, workspace=ws)
+        L.decode(small, dv.q[:2], k4, v4, dv.words[:2], lens[:2], dv.q_pos[:2], dv.rope, out=out2, workspace=ws)
+
+    assert L.decode_workspace_bytes(small) <= ws.numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for what, new in (("ranges", full), ("whole units", full.clamp(max=16 * 500)), ("nothing", full * 0), ("ranges again", full),
+                      ("one long", torch.where(full == full.max(), full, 0)), ("tokens", full.clamp(max=1))):
+        lens.copy_(new)
+        want, want2 = (L.decode(p, dv.q[:n], k4, v4, dv.words[:n], lens[:n], dv.q_pos[:n], dv.rope) for p, n in ((dv.p, 96), (small, 2)))
+        out.fill_(7), out2.fill_(7), ws.fill_(255)
+        g.replay()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(out2.view(torch.int16), want2.view(torch.int16)), what
+        # (a length cut at 500 blocks may name a document's unwritten slots as keys: NaN, the same on both sides)
+        assert torch.count_nonzero(out[new == 0]) == 0 and not (out == 7).flatten(1).all(1).any(), what
