@@ -31,7 +31,8 @@
  *    lazy_attn_decode_shared) the pools hold OCP e4m3 codes and the products take
  *    f16 operands (every e4m3 value is exact in f16), with fp32 accumulation and
  *    softmax. With kv_dtype LAZY_INT4 (the same calls) the pools hold int4 records
- *    (see "int4 pools"), the products take the codes and f16 queries and weights.
+ *    (see "int4 pools"), the products take the codes, f16 queries and f16 weights times
+ *    scales.
  *
  * Layout (one layer)
  * ------------------
@@ -505,9 +506,10 @@ size_t lazy_attn_pool_record_bytes(const lazy_attn_params *p);
  *              the token is skipped (padding; its rows are read all the same). A block id
  *              outside the pool sets LAZY_DEV_BAD_BLOCK_ID and the token is skipped
  *   k_pool, v_pool  16-byte aligned. Only the named slots change
- * kv_dtype 0: copies. LAZY_FP8_E4M3 (dtype bf16, head_dim 64 or 128): x / k_scale (K) or
- * x / v_scale (V), rounded to the nearest code (ties to even) and saturated at +-448, NaN
- * kept; scales within 2^-100 .. 2^100. LAZY_INT4 (dtype bf16): as above.
+ * kv_dtype 0: copies. LAZY_FP8_E4M3 (dtype bf16, head_dim 64 or 128, of which the decodes
+ * take 128): x / k_scale (K) or x / v_scale (V), rounded to the nearest code (ties to even)
+ * and saturated at +-448, NaN kept; scales within 2^-100 .. 2^100. LAZY_INT4 (dtype bf16):
+ * as above.
  * Slots that occur twice hold a mixture of the two tokens. num_tokens = 0 does nothing. */
 int lazy_attn_cache_write(const lazy_attn_params *p, const void *k, int64_t k_token_stride, int64_t k_head_stride,
                           const void *v, int64_t v_token_stride, int64_t v_head_stride, int32_t num_tokens,

@@ -12,13 +12,15 @@
 //    rint((x - z) / s).
 // Quotients are formed by an approximate reciprocal and exact remainders in fp32, and where
 // that does not tell a border between two codes (or two scales) in 64 bits, so the codes are
-// those of the definition. That arithmetic is what bounds the kernel (75% of the issue slots
-// taken): 173 instructions for eight int4 codes of 32 lanes, 150 for e4m3. Writing 8192
-// tokens of 8 heads takes 12.8 us (int4, 43 MB), 16384 tokens 21.6 us (e4m3, 101 MB), the
-// rows coming from L2. Both worked on borders as they came, 15.5 and 30.7 us, before ties
-// fell out of a corrected quotient (int4) and the odd bit out of two roundings (e4m3).
-// Read: one warp per (block, head, K or V) record, eight dims per lane, written as `dtype`;
-// bound by bandwidth.
+// those of the definition. That arithmetic is what bounds the kernel (74% of the issue slots
+// taken, e4m3 77%): 173 instructions for eight int4 codes of 32 lanes, 149 for e4m3. Writing 8192
+// tokens of 8 heads takes 13.4 us (int4, 43 MB), 16384 tokens 22.6 us (e4m3, 101 MB), the
+// rows coming from L2; 8192 as they are 11.5 us (bf16, 5.8 TB/s). Both worked on borders as they
+// came, a fifth and two fifths slower, before ties fell out of a corrected quotient (int4) and
+// the odd bit out of two roundings (e4m3).
+// Read: one warp per (block, head, K or V) record, eight dims per lane (4 bytes of int4 codes, 8
+// of e4m3, 16-byte loads of a copied record), written as `dtype` in 16-byte stores; bound by
+// bandwidth (16384 int4 blocks of 8 heads 206 us, 6.7 TB/s; bf16 6.9).
 #include "int4.cuh"
 #include "kernels.h"
 

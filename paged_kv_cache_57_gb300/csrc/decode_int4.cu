@@ -83,8 +83,10 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 //
 // Of a part the four warps take a quarter each. A warp is its own loader: a ring of RING
 // stages of two blocks, each refilled as soon as it was read. 64 sequences of 4160 tokens, 32
-// heads on 8, take 63 us a call, 4.9 TB/s of records: no pipe is full (integer 55%), and 16
-// warps an SM, which is what 128 registers allow, do not hide a tile's chain.
+// heads on 8, take 64 us a call, 4.8 TB/s of records: no pipe is full (integer 55%, issue slots
+// 55%), and 16 warps an SM, which is what 128 registers allow, do not hide a tile's chain. With
+// 32 heads on one KV head both tiles of 16 heads read the records (872 MB for 466), at 8 warps
+// an SM: 250 us, issue slots 51%, tensor 38%.
 
 namespace {
 
@@ -369,10 +371,11 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
 }
 
 // out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit of several pieces
-// or in several ranges; with ranges 0 for a sequence without blocks. A CTA looks after PAIRS (sequence,
-// query head) pairs: a warp finds a pair's parts and merges up to kCombineBatch of them by
-// itself; more are shared by the CTA's warps. Launched as a programmatic dependent of the
-// decode kernel: it waits for that grid before it reads anything.
+// or in several ranges; with ranges 0 for a sequence without blocks (with pieces its unit's CTA
+// writes that). A CTA looks after PAIRS (sequence, query head) pairs: a warp finds a pair's parts
+// and merges up to kCombineBatch of them by itself; more are shared by the CTA's warps. Launched
+// as a programmatic dependent of the decode kernel: it waits for that grid before it reads
+// anything.
 //
 // Up to kCombineAlone pairs, as many CTAs as are resident at once, get a CTA each: whole
 // calls of 32 heads took 21 us at 1 x 16384 tokens and at 4 x 4096, with PAIRS = 8 30 and 29.
@@ -509,8 +512,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const 
 // stages each. Tiles of 16 rows would unpack each code half as often, but hold 240
 // registers, two CTAs an SM: 197 us against 154 on 32 x 16384 tokens of Zipf-drawn
 // documents with 8 query heads per KV head, in items of 32 blocks. In items of 64, the long
-// and wide ones first, the 8-row tiles take 122 us, 1.8 TB/s of unique records: bound by the
-// instructions of unpacking and softmax, once per 8 rows (60% of the issue slots).
+// and wide ones first, the 8-row tiles take 126 us, 1.7 TB/s of unique records: bound by the
+// instructions of a tile, once per 8 rows (59% of the issue slots, integer 56%, tensor 25%).
 namespace {
 
 constexpr int kShRows = 32;    // rows of a CTA

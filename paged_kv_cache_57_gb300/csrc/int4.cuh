@@ -21,9 +21,10 @@
 // as rows; the weights become the B operand of O^T = C_v^T P^T by an 8 x 8 transpose
 // (movmatrix).
 //
-// The step is bound by the integer pipe (masks and shifts issue every second cycle), which
-// is why e4m3 codes (a byte 0..15 is c 2^-9, three such operations for eight codes) looked
-// better: mma.sync takes them here as conversions and two f16 products (113 us against 104 on
+// A tile of 32 keys and 8 rows is about 590 instructions of a warp: 128 unpack codes, 32 are
+// products and 24 transposes, the rest scales, zeros and softmax in fp32. Masks and shifts issue
+// every second cycle and keep the integer pipe 44 to 56% busy, more than any other. e4m3 codes (a
+// byte 0..15 is c 2^-9, three such operations for eight codes) looked better: mma.sync takes them here as conversions and two f16 products (113 us against 104 on
 // 64 x 4160 tokens, when the rest of the step was slower than it is now).
 //
 // tcgen05 needs the codes as f16 in shared memory and did not pay: with the values s c + z
@@ -287,9 +288,11 @@ __device__ __forceinline__ void int4_init(Int4State<D, NT, HL>& st) {
 // O^T's running sums hold codes, not values: they grow with the keys and cancel against the
 // zeros' part, and the products truncate them (2^-24 of the sum each time, always towards
 // zero). Over 5000 keys of a 65000-key context that was 2.6e-3 of the output instead of the
-// output rounding's 1.7e-3, so long runs move them to shared memory every kInt4Flush stages
-// (64 blocks), where they are summed by rounding additions: `kept` is the warp's area, value n of lane l at
-// 32 n + l (with HL = 1 only the columns that count).
+// output rounding's 1.7e-3, over 8192 blocks of one warp of the shared-run decode 41% of it, so
+// long runs move them to shared memory every kInt4Flush stages (64 blocks), where they are summed
+// by rounding additions: `kept` is the warp's area, value n of lane l at 32 n + l (with HL = 1
+// only the columns that count). It costs the shared-run decode 2 to 3%: 56.4 us against 54.2,
+// 125.2 against 122.4.
 constexpr int kInt4Flush = 32;
 template <int D, int NT, int HL>
 constexpr int int4_kept_floats() { return 32 * (D / 16) * NT * 2 * HL; }
