@@ -244,18 +244,18 @@ __device__ __forceinline__ void int4_build_query(Int4Query<D, NT, HL>& q, const 
   }
 }
 
-// Running state: per row the reference maximum m as kInt4WeightLog2 - m (log2 units; 0 before
-// the first key) and `top`, the value of score / f that refreshes it, the weight sum l and the
+// Running state: per row the reference maximum as -m (log2 units; 0 before the first key)
+// and `top`, the value of score / f that refreshes it, the weight sum l and the
 // zeros' sums z (partial over the lanes of equal t until int4_finish), and O^T / 2^24
 // without the zeros: o[4 j + pp][nt] is the products' columns 2t, 2t + 1 for the lane's dim
 // 2 pp of group j (int4_dims) in [0], [1] and for that plus 16 times the next in [2], [3]. With HL = 2
 // the columns are the rows 2t, 2t + 1; with HL = 1 they are row t under group 0's and
 // group 1's scales, and column 2t + j is the one that counts for group j. Weights times V
 // scales go to f16 over `inv`'s power of two per group, which follows the scales as they
-// grow: at most 2^(5 + 8) (weights: 2^5 at the reference maximum) x 2^2. What f16 has below
-// them is for the long tails: a product keeps its 11 bits from 2^-19 of weight 1 times the
-// scales' power of two, and is off by 2^-30 of that below (weights of 1 at the reference
-// with 2^7 for the scales' growth lost 2^5 of it: a tail of 131072 keys of 2^-25.5 was gone).
+// grow: the largest scale is 2^4 to 2^5 then, at most 2^7 before the reference moves, and weights
+// at most 2^8. What f16 has below is for the long tails: a product keeps its 11 bits from 2^-18
+// of weight 1 times the largest scale, and is off by 2^-29 of that below (with the largest scale
+// at 1 a tail of 131072 keys of weight 2^-25.5 was gone).
 template <int D, int NT, int HL>
 struct Int4State {
   float o[D / 16][NT][4];
@@ -326,9 +326,8 @@ __device__ __forceinline__ void int4_unflush(Int4State<D, NT, HL>& st, const flo
   int4_each_kept<D, NT, HL>(st, [&](int n, int, int, int, float& o) { o += kept[32 * n + lane]; });
 }
 
-constexpr float kInt4WeightLog2 = 5.f;     // a weight at the reference maximum is 2^5
-constexpr float kInt4RescaleLog2 = 8.f;    // a maximum is refreshed when it grows by more
-constexpr float kInt4ScaleHeadroom = 4.f;  // and the V scales' reference by more than this
+constexpr float kInt4RescaleLog2 = 8.f;  // a maximum is refreshed when it grows by more
+constexpr float kInt4ScaleTop = 128.f;   // the V scales' reference moves when one times inv is more
 
 // Bytes h and h + 2 of a word as f16 pairs: low nibbles, and whole bytes.
 __device__ __forceinline__ void int4_pair(uint32_t w, int h, uint32_t& nibbles, uint32_t& bytes) {
@@ -466,12 +465,12 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sm[j] = fmaxf(sm[j], __shfl_xor_sync(0xffffffffu, sm[j], o));
       if (sm[j] > st.lim[j]) {
-        // 2^-(e + 1) for sm in [2^e, 2^(e+1)): between 1/2 and 1 now. Kept a normal number.
-        const uint32_t ex = min(max(__float_as_uint(sm[j]) >> 23, 8u), 246u);
-        const float inv = __uint_as_float((253u - ex) << 23);
+        // 2^(4 - e) for sm in [2^e, 2^(e+1)): between 2^4 and 2^5 now. Kept a normal number.
+        const uint32_t ex = min(max(__float_as_uint(sm[j]) >> 23, 8u), 252u);
+        const float inv = __uint_as_float((258u - ex) << 23);
         const float r = inv / st.inv[j];
         st.inv[j] = inv;
-        st.lim[j] = kInt4ScaleHeadroom / inv;
+        st.lim[j] = kInt4ScaleTop / inv;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -493,8 +492,8 @@ __device__ __forceinline__ void int4_attend(const SharedRecord (&kr)[2], const S
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
         if (x > st.top[nt][c]) {
           x *= q.f[nt][c];
-          const float alpha = st.top[nt][c] == -INFINITY ? 0.f : fast_ex2(kInt4WeightLog2 - st.neg_m[nt][c] - x);
-          st.neg_m[nt][c] = kInt4WeightLog2 - x;
+          const float alpha = st.top[nt][c] == -INFINITY ? 0.f : fast_ex2(-st.neg_m[nt][c] - x);
+          st.neg_m[nt][c] = -x;
           st.top[nt][c] = __fdividef(x + kInt4RescaleLog2, q.f[nt][c]);
           st.l[nt][c] *= alpha;
 #pragma unroll

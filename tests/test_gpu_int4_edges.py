@@ -386,3 +386,17 @@ def test_captured_step_follows_its_lengths():
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(out2.view(torch.int16), want2.view(torch.int16)), what
         # (a length cut at 500 blocks may name a document's unwritten slots as keys: NaN, the same on both sides)
         assert torch.count_nonzero(out[new == 0]) == 0 and not (out == 7).flatten(1).all(1).any(), what
+
+
+# V values of 2^118 over 20 keys: the sums of codes times scales reach 20 * 5 * 2^118 < 2^125, inside fp32 (a weight of 1 may
+# not be held as more). And of 2^124 on a single key, whose scale is among the largest that a group of bf16 values has.
+@pytest.mark.parametrize("hq,hkv,d", [(3, 1, 128), (8, 1, 64), (32, 2, 128)])
+@pytest.mark.parametrize("tokens,power", [(20, 118), (1, 124)])
+def test_v_values_near_the_end_of_fp32(hq, hkv, d, tokens, power):
+    w = W.decode_zipf("i4top", batch=2, hq=hq, hkv=hkv, d=d, docs_per_seq=1, doc_tokens=tokens, pool_docs=1, zipf_s=1.0, share=False,
+                      seed=890)
+    w.v_pool = (w.v_pool.double() * 2.0 ** power).to(torch.bfloat16)
+    dv, k4, v4, kv, vv = on_device(w)
+    ref = M.attention(w, kv, vv)
+    check(decode(dv, k4, v4), ref, "per sequence")
+    check(la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv)), ref, "shared")
