@@ -70,7 +70,10 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 // says too little about the others. The units' blocks are laid end to end and cut into equal
 // ranges, one per resident CTA: batches of any lengths give every CTA the same work. A CTA
 // goes through its range unit by unit; a unit that lies in one range is written out. Where the
-// table's width does not rule ranges out the kernel looks for the longest sequence itself.
+// table's width does not rule ranges out every CTA looks for the longest sequence, in batches of
+// up to kMaxLook; larger ones are cut into ranges (tables of 4096 blocks, 32 heads on 8, us with the
+// look and with ranges at once: 512 sequences of 64 tokens 56 61, of 1024 134 150; 1024 of 64
+// 123 110, of 256 158 154, of 1024 272 290; 2048 of 64 303 213, of 1024 582 563).
 //
 // Measured from HBM (pieces, ranges; us), 32 heads on 8: 64 sequences of 256 blocks 63 68, of 512
 // 118 113, of 600 139 130, of 1000 225 210, of 2000 439 397; of up to 512 106 96, of up to 1024
@@ -93,6 +96,7 @@ namespace {
 constexpr int kMinPieceLog2 = 5;  // 32 blocks of a piece at least: one of 16384 tokens 17 us, with 16 or 64 19
 constexpr int kMaxPiece = 512;
 constexpr int kMinChunk = 16;   // blocks of a range at least
+constexpr int kMaxLook = 1024;  // sequences that every CTA looks through
 
 __device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& seq_len) {
   seq_len = a.seq_lens[s];
@@ -116,15 +120,17 @@ __device__ __forceinline__ int64_t chunk_of(const Int4DecodeArgs& a, int64_t tot
   return c > kMinChunk ? c : kMinChunk;
 }
 
-// Whether the batch is cut into ranges (every warp by itself).
+// Whether the batch is cut into ranges: some sequence's pieces would be too long (every warp
+// looks by itself).
 __device__ __forceinline__ bool takes_ranges(const Int4DecodeArgs& a, int lane) {
+  if (a.plan.range_ctas == 0) return false;
+  if (a.B > kMaxLook) return true;
   int longest = 0;
   for (int b = lane; b < a.B; b += 32) {
     int len;
     longest = max(longest, blocks_of(a, b, len));
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  return piece_of(a.plan, longest) > kMaxPiece;
+  return __reduce_max_sync(0xffffffffu, longest) > kMaxPiece * a.plan.splits;
 }
 
 }  // namespace
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   // ------------------------------------------------------------ the CTA's piece or range
   int s = 0, seq_len = 0, nb = 0, u = 0, lo = 0, hi = 0;  // the part: blocks lo .. hi - 1 of unit u of s
   int64_t at = 0, left = 0;  // place within sequence s (its units end to end); places left of the range
-  const bool ranges = a.plan.range_ctas > 0 && takes_ranges(a, lane);
+  const bool ranges = takes_ranges(a, lane);
   if (a.plan.range_ctas > 0 && blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B + 1] = ranges;
   if (!ranges) {  // first pieces first: CTAs without one are the last, not between those of one SM
     const unsigned units = (unsigned)a.B * U, piece = blockIdx.x / units, unit = blockIdx.x - piece * units;
@@ -769,9 +775,9 @@ Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits,
                             : (int)std::max<int64_t>(1, std::min<int64_t>(resident / units, mb >> kMinPieceLog2));
   p.ctas = units * p.splits;
   p.parts = p.splits > 1 ? p.ctas : 0;
-  if (num_splits <= 0 && piece_of(p, mb) > kMaxPiece) {
+  if (num_splits <= 0 && mb > kMaxPiece * p.splits) {
     p.range_ctas = std::min<int64_t>((units * mb + kMinChunk - 1) / kMinChunk, resident);
-    p.ctas = std::max(p.ctas, p.range_ctas);
+    p.ctas = B > kMaxLook ? p.range_ctas : std::max(p.ctas, p.range_ctas);
     p.parts = std::max(p.parts, p.range_ctas);
   }
   return p;

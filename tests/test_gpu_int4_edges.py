@@ -400,3 +400,18 @@ def test_v_values_near_the_end_of_fp32(hq, hkv, d, tokens, power):
     ref = M.attention(w, kv, vv)
     check(decode(dv, k4, v4), ref, "per sequence")
     check(la().decode_shared(dv.p, dv.q, k4, v4, dv.words, dv.q_pos, dv.rope, shared_plan(dv)), ref, "shared")
+
+
+def test_wide_table_of_many_sequences():
+    # more sequences than every CTA looks through: ranges, whatever the lengths
+    L = la()
+    dw, _ = W.mixed_mqa(n_decode=2100, n_prefill=1, chunk=16, hq=2, hkv=1, d=64, pool_docs=20, ctx_lo=1, ctx_hi=90, doc_lo=1, doc_hi=40,
+                        seed=871)
+    dv, k4, v4, kv, vv = on_device(dw)
+    ref = M.attention(dw, kv, vv)
+    check(decode(dv, k4, v4), ref, "tight")
+    words = torch.full((2100, 600), -1, dtype=torch.int32, device="cuda")
+    words[:, :dv.p.max_blocks_per_seq] = dv.words
+    dv.words, dv.p.max_blocks_per_seq = words, 600
+    ws = torch.full((L.decode_workspace_bytes(dv.p),), 255, dtype=torch.uint8, device="cuda")
+    check(decode(dv, k4, v4, workspace=ws), ref, "600 blocks wide")
