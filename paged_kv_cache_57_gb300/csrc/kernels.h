@@ -290,8 +290,9 @@ cudaError_t launch_cache_read(const CacheReadArgs& a, int kv_dtype, int sms, cud
 // int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool.
 // A unit is one sequence's blocks for one KV head and tile of `rows` query heads. Each is cut
 // into pieces of equal length, one per CTA, by its own sequence's length; or, where the longest
-// sequence would have pieces of more than 512 blocks, the units' blocks are laid end to end and
-// cut into equal ranges, one per CTA. Both are settled on the device.
+// sequence would have pieces of more than 512 blocks (or the table allows it and the batch is
+// large), the units' blocks are laid end to end and cut into equal ranges, one per CTA. Both are
+// settled on the device.
 struct Int4Plan {
   int rows;            // query heads of a unit: 4, 8 or 16
   int units;           // units of a sequence: KV heads x head tiles
