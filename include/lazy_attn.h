@@ -32,7 +32,8 @@
  *    f16 operands (every e4m3 value is exact in f16), with fp32 accumulation and
  *    softmax. With kv_dtype LAZY_INT4 (the same calls) the pools hold int4 records
  *    (see "int4 pools"), the products take the codes, f16 queries and f16 weights times
- *    scales.
+ *    scales. With kv_dtype LAZY_FP8_E4M3_BLOCK (the same calls) the pools hold records of
+ *    e4m3 codes with a scale per block and head (see "e4m3 pools with block scales").
  *
  * Layout (one layer)
  * ------------------
@@ -83,7 +84,7 @@ typedef enum {
   LAZY_ERR_DEVICE = 6       /* the device status word reported a fault */
 } lazy_status;
 
-typedef enum { LAZY_F32 = 0, LAZY_BF16 = 1, LAZY_FP8_E4M3 = 2, LAZY_INT4 = 3 } lazy_dtype;
+typedef enum { LAZY_F32 = 0, LAZY_BF16 = 1, LAZY_FP8_E4M3 = 2, LAZY_INT4 = 3, LAZY_FP8_E4M3_BLOCK = 5 } lazy_dtype; /* 4 is refused */
 
 /* Bits of the per-device status word. */
 #define LAZY_DEV_BAD_BLOCK_ID 0x1u /* a word's phys_id >= num_pool_blocks (block skipped) */
@@ -91,6 +92,7 @@ typedef enum { LAZY_F32 = 0, LAZY_BF16 = 1, LAZY_FP8_E4M3 = 2, LAZY_INT4 = 3 } l
 #define LAZY_DEV_TIMEOUT 0x4u      /* a pipeline wait gave up after its limit */
 #define LAZY_DEV_LAYOUT 0x8u       /* the device packer met an invalid layout */
 #define LAZY_DEV_BAD_LEN 0x10u     /* seq_lens < 0 or > 16*max_blocks_per_seq (clamped) */
+#define LAZY_DEV_NO_BLOCKS 0x20u   /* the free list has too few blocks for a sequence's new tokens (not added) */
 
 /* Largest |offset| the rotation table covers (positions and offsets). */
 #define LAZY_MAX_ROPE_OFFSET (1 << 24)
@@ -126,9 +128,13 @@ typedef struct {
                                  LAZY_INT4: the pools hold int4 records ("int4 pools"
                                  below). The same decodes take it with dtype LAZY_BF16 and
                                  head_dim 64 or 128, and refuse it where they refuse e4m3.
+                                 LAZY_FP8_E4M3_BLOCK: the pools hold records of e4m3 codes
+                                 with a scale each ("e4m3 pools with block scales"), taken
+                                 and refused where LAZY_INT4 is.
                                  lazy_attn_cache_write and _read take every kind of pool */
   float k_scale;              /* FP8 dequantisation scales: finite, > 0; 0 selects 1.
-                                 LAZY_INT4: 0 or 1 (its scales are in the records) */
+                                 LAZY_INT4, LAZY_FP8_E4M3_BLOCK: 0 or 1 (the scales are in
+                                 the records) */
   float v_scale;
 } lazy_attn_params;
 
@@ -231,6 +237,47 @@ int lazy_attn_pack_block_words(const lazy_attn_params *p, int32_t num_docs, cons
                                const int32_t *doc_block_indptr, const int32_t *doc_blocks,
                                uint32_t *block_words, int32_t *seq_lens, lazy_stream_t stream);
 
+/* ---------------------------------------------------------------- room for new tokens
+ * The tables of a step, from the sequences' lengths alone and on the device: a captured step
+ * needs no host in between. Every sequence s gets new_lens[s] tokens (a prompt, a chunk of one,
+ * a decoded token, drafts; 0: none) behind what it holds. Its own tokens start at position
+ * tail_start[s] and lie in blocks of their own, behind the blocks of the documents that it cites:
+ * token i of them (position tail_start[s] + i) is row i % 16 of logical block b0 + i / 16, where
+ * b0 is the block behind the cited documents. They form documents of doc_tokens tokens (a
+ * multiple of 16, the same in every call for a sequence; 0: one document), so that the words'
+ * offsets stay small: token i is stored rotated at i % doc_tokens, which is local_pos.
+ *   new_lens    [B] int32
+ *   seq_lens    [B] slots in use, as the packer writes them
+ *   pos         [B] position of the next token: tail_start plus the sequence's own tokens so far
+ *   tail_start  [B]; = pos: its own tokens begin with this call, in a fresh block (a prefill
+ *               chunk, which has to be a document of its own, is given that way, with
+ *               doc_tokens 0 or at least its length)
+ *   free_blocks [num_free] physical ids; the call takes them in order from index *first_free
+ *               (device; NULL: 0), sequence by sequence, one as a token enters its row 0
+ *   block_words [B][max_blocks_per_seq]: the words of the blocks taken are written (in either
+ *               form, see key_positions), the others stay
+ *   seq_lens_out, pos_out [B]: after the call; may be seq_lens and pos themselves
+ *   q_start     [B] the old pos (a chunk's q_start; the q_pos of a single token)
+ *   cu_rows     [B+1] sums of new_lens: rows cu_rows[s] .. cu_rows[s+1] - 1 are sequence s's (the
+ *               prefill's cu_seqlens_q)
+ *   block_indptr [B+1]: sequence s was given free_blocks[block_indptr[s] .. block_indptr[s+1] - 1];
+ *               the last entry is where the next call goes on, and may be its first_free
+ *   slots       [num_rows] the rows' slots for lazy_attn_cache_write; -1 behind the last row
+ *   local_pos   [num_rows] or NULL: the positions that the rows' K is rotated at; 0 behind the last row
+ * A sequence whose tokens cannot be added keeps its lengths and words, its rows get slots of -1,
+ * and the status word says why: LAZY_DEV_NO_BLOCKS (the list ends; later sequences get no blocks
+ * either), LAZY_DEV_BAD_LEN (negative new_lens, seq_lens outside the table, rows past num_rows),
+ * LAZY_DEV_LAYOUT (pos and tail_start do not fit seq_lens, the table or a word's offset field is
+ * full, *first_free outside the list). An id outside the pool sets LAZY_DEV_BAD_BLOCK_ID; its
+ * rows get slots of -1.
+ * Outputs other than the two named must not overlap inputs. num_seqs may be 0. */
+int lazy_attn_append_tokens(const lazy_attn_params *p, const int32_t *new_lens, const int32_t *seq_lens,
+                            const int32_t *pos, const int32_t *tail_start, const int32_t *free_blocks,
+                            int32_t num_free, const int32_t *first_free, int32_t doc_tokens, int32_t num_rows,
+                            uint32_t *block_words, int32_t *seq_lens_out, int32_t *pos_out, int32_t *q_start,
+                            int32_t *cu_rows, int32_t *block_indptr, int32_t *slots, int32_t *local_pos,
+                            lazy_stream_t stream);
+
 /* ---------------------------------------------------------------- decode
  * One query per sequence ("Implementação Técnica", item 2, Decoding: query tile
  * M = 1; the query is re-rotated only when the relative offset changes, i.e. at
@@ -266,11 +313,12 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  * split into sets of at most LAZY_PLAN_MAX_MEMBERS members and at most R query
  * rows (members x query heads per KV head), and each set's blocks are cut into
  * chunks of chunk_blocks logical blocks. R is 128 when a KV head serves at least
- * 8 query heads, head_dim is 128 and the pools are neither e4m3 nor int4 (the decode
+ * 8 query heads, head_dim is 128 and the pools are not quantised (the decode
  * then runs on the 5th-generation tensor cores, one 128-row tile per item), else 64
  * (plan with the kv_dtype the decode will use). chunk_blocks 0 selects 32,
- * or, for R = 128 and for int4 pools, about one item per resident CTA (2 x 152 /
- * num_kv_heads items, int4: 4 x 152 / num_kv_heads): the sets' blocks summed, divided
+ * or, for R = 128 and for pools of records (int4, e4m3 with block scales), about one item per
+ * resident CTA (2 x 152 / num_kv_heads items, int4: 4 x 152 / num_kv_heads, e4m3 with block
+ * scales: 3 x 152 / num_kv_heads): the sets' blocks summed, divided
  * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. It writes
  *   items_host [num_items][LAZY_PLAN_ITEM_INTS] int32, one work item each:
  *     [0] src_seq, [1] b0, [2] nblk, [3] last_valid, [4] nmem, [5] c0, [6..7] 0:
@@ -288,7 +336,7 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  *   slot_indptr_host [B+1]: the slots of sequence s are slot_indptr[s] ..
  *     slot_indptr[s+1]-1;
  *   counts_host [2] = {num_items, num_slots}.
- * Items are ordered by decreasing block count, for int4 pools times 1, 2 or 4 for up to 8,
+ * Items are ordered by decreasing block count, for pools of records times 1, 2 or 4 for up to 8,
  * up to 16 or more query rows (ties in the order of first appearance of their document).
  * `capacity` bounds the item count (the number
  * of logical blocks in the batch always suffices). Returns LAZY_ERR_LAYOUT on the
@@ -489,7 +537,24 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
  * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale of
  * that group where that is more (weights over the row's largest in the part; a part is what one
- * warp attends). Sums, maxima and zeros are fp32. */
+ * warp attends). Sums, maxima and zeros are fp32.
+ *
+ * e4m3 pools with block scales (kv_dtype LAZY_FP8_E4M3_BLOCK): uint8 [num_pool_blocks][Hkv][record];
+ * a record of 16 head_dim + 32 bytes holds the 16 tokens of one block for one KV head: their OCP
+ * e4m3 codes, then the scale 2^e (fp32) and 28 bytes that nothing reads. A value is code * 2^e.
+ *   - K: bytes 16 (32 j + 4 g + t) .. + 15, j < head_dim / 32, g < 8, t < 4, are the dims
+ *     16 (t + 4 (j / 2)) .. + 15 of token g + 8 (j % 2);
+ *   - V: with G = head_dim / 64, bytes 16 (32 j + 4 g + t) + 2 i + b, i < 8, b < 2, are dim
+ *     8 (g + 8 (j % G)) + i of token 2 (t + 4 (j / G)) + b.
+ * A call that writes rows of a block gives it the least e for which 448 * 2^e is no less than any
+ * of those rows' finite values (-100 <= e <= 119), and, unless row 0 is among them, no less than the
+ * block's e before. Codes are x / 2^e to the nearest (ties to even, saturated at +-448); infinities
+ * and NaN are written as NaN. The rows that the call does not write keep their codes, rounded again
+ * where e grew (which changes a code only where it falls below e4m3's least normal number). A
+ * block whose row 0 is written begins anew: its other rows, unless written too, are 0.
+ * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
+ * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale where that
+ * is more (weights over the row's largest in the part). Sums and maxima are fp32. */
 
 /* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold
  * num_pool_blocks * Hkv times that. 0 on bad params. */
@@ -509,7 +574,9 @@ size_t lazy_attn_pool_record_bytes(const lazy_attn_params *p);
  * kv_dtype 0: copies. LAZY_FP8_E4M3 (dtype bf16, head_dim 64 or 128, of which the decodes
  * take 128): x / k_scale (K) or x / v_scale (V), rounded to the nearest code (ties to even)
  * and saturated at +-448, NaN kept; scales within 2^-100 .. 2^100. LAZY_INT4 (dtype bf16):
- * as above.
+ * as above. LAZY_FP8_E4M3_BLOCK (dtype bf16): as above; the tokens that go into one block are
+ * within 32 consecutive entries of slots (skipped ones count; the tokens of a document in their
+ * order are), else their records are unspecified.
  * Slots that occur twice hold a mixture of the two tokens. num_tokens = 0 does nothing. */
 int lazy_attn_cache_write(const lazy_attn_params *p, const void *k, int64_t k_token_stride, int64_t k_head_stride,
                           const void *v, int64_t v_token_stride, int64_t v_head_stride, int32_t num_tokens,
@@ -523,7 +590,8 @@ int lazy_attn_cache_write(const lazy_attn_params *p, const void *k, int64_t k_to
  *              is (padding). An id outside the pool sets LAZY_DEV_BAD_BLOCK_ID and
  *              leaves it too. The same id may occur several times
  *   k_out, v_out  16-byte aligned, not overlapping the pools
- * Values: code * scale (e4m3), s c + z (int4), formed in fp32 and rounded to dtype. */
+ * Values: code * scale (e4m3), code * 2^e (e4m3 with block scales), s c + z (int4), formed in fp32
+ * and rounded to dtype. */
 int lazy_attn_cache_read(const lazy_attn_params *p, const void *k_pool, const void *v_pool, int32_t num_blocks,
                          const int32_t *block_ids, void *k_out, void *v_out, lazy_stream_t stream);
 

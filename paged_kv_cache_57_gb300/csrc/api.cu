@@ -166,11 +166,15 @@ bool encode_dec_q_map(CUtensorMap* m, const void* base, uint64_t B, int hq, int 
 
 // The pools hold e4m3 codes (FP8 KV; only the decodes read them).
 static bool kv_fp8(const lazy_attn_params* p) { return p->kv_dtype == LAZY_FP8_E4M3 && p->dtype != LAZY_FP8_E4M3; }
-// int4 records of one block are addressed with 32 bits.
-constexpr int kInt4MaxKvHeads = 65535;
+// Records of one block are addressed with 32 bits.
+constexpr int kRecordMaxKvHeads = 65535;
 // The pools hold int4 records.
 static bool kv_int4(const lazy_attn_params* p) { return p->kv_dtype == LAZY_INT4; }
-static bool kv_quantised(const lazy_attn_params* p) { return kv_fp8(p) || kv_int4(p); }
+// The pools hold records of e4m3 codes with a scale each.
+static bool kv_fp8_block(const lazy_attn_params* p) { return p->kv_dtype == LAZY_FP8_E4M3_BLOCK; }
+// The pools hold records that carry their scales.
+static bool kv_records(const lazy_attn_params* p) { return kv_int4(p) || kv_fp8_block(p); }
+static bool kv_quantised(const lazy_attn_params* p) { return kv_fp8(p) || kv_records(p); }
 
 int check_params(const lazy_attn_params* p, Checked* c) {
   if (!p) return LAZY_ERR_INVALID_ARG;
@@ -187,12 +191,12 @@ int check_params(const lazy_attn_params* p, Checked* c) {
   if (p->num_splits < 0) return LAZY_ERR_INVALID_ARG;
   if (p->key_positions != 0 && p->key_positions != 1) return LAZY_ERR_INVALID_ARG;
   if (p->kv_dtype != 0 && p->kv_dtype != p->dtype && p->kv_dtype != LAZY_FP8_E4M3 &&
-      p->kv_dtype != LAZY_INT4)
+      !kv_records(p))
     return LAZY_ERR_UNSUPPORTED;
   if (!(p->k_scale >= 0.f) || !std::isfinite(p->k_scale) || !(p->v_scale >= 0.f) || !std::isfinite(p->v_scale))
     return LAZY_ERR_INVALID_ARG;
-  // int4 records carry their own scales
-  if (kv_int4(p) && ((p->k_scale != 0.f && p->k_scale != 1.f) || (p->v_scale != 0.f && p->v_scale != 1.f)))
+  // records carry their own scales
+  if (kv_records(p) && ((p->k_scale != 0.f && p->k_scale != 1.f) || (p->v_scale != 0.f && p->v_scale != 1.f)))
     return LAZY_ERR_INVALID_ARG;
   c->id_bits = p->id_bits ? p->id_bits : kDefaultIdBits;
   if (c->id_bits < 8 || c->id_bits > 24) return LAZY_ERR_INVALID_ARG;
@@ -381,27 +385,52 @@ int lazy_attn_pack_block_words(const lazy_attn_params* p, int32_t num_docs, cons
   return launched(lazy::launch_pack(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-static lazy::Int4Plan int4_plan(const lazy_attn_params* p, const Checked& c) {
-  return lazy::plan_decode_int4(p->num_seqs, c.G, p->num_kv_heads, p->max_blocks_per_seq, p->num_splits, sm_count());
+int lazy_attn_append_tokens(const lazy_attn_params* p, const int32_t* new_lens, const int32_t* seq_lens, const int32_t* pos,
+                            const int32_t* tail_start, const int32_t* free_blocks, int32_t num_free,
+                            const int32_t* first_free, int32_t doc_tokens, int32_t num_rows, uint32_t* block_words,
+                            int32_t* seq_lens_out, int32_t* pos_out, int32_t* q_start, int32_t* cu_rows,
+                            int32_t* block_indptr, int32_t* slots, int32_t* local_pos, lazy_stream_t stream) {
+  Checked c;
+  int rc = check_params(p, &c);
+  if (rc != LAZY_OK) return rc;
+  if (num_free < 0 || num_rows < 0 || doc_tokens < 0 || doc_tokens % lazy::kBlock != 0) return LAZY_ERR_INVALID_ARG;
+  if (!cu_rows || !block_indptr || (num_free > 0 && !free_blocks) || (num_rows > 0 && !slots)) return LAZY_ERR_INVALID_ARG;
+  if (p->num_seqs > 0 && (!new_lens || !seq_lens || !pos || !tail_start || !block_words || !seq_lens_out || !pos_out || !q_start))
+    return LAZY_ERR_INVALID_ARG;
+  unsigned int* st = status_ptr();
+  if (!st) return LAZY_ERR_CUDA;
+  lazy::AppendArgs a{new_lens, seq_lens, pos, tail_start, free_blocks, first_free, block_words, seq_lens_out, pos_out, q_start,
+                     cu_rows, block_indptr, slots, local_pos, st, p->num_seqs, num_free, num_rows, doc_tokens,
+                     p->max_blocks_per_seq, c.id_bits, p->num_pool_blocks, p->key_positions,
+                     aligned16(slots) && aligned16(local_pos)};
+  int launches = 0;
+  rc = launched(lazy::launch_append_tokens(a, &launches, reinterpret_cast<cudaStream_t>(stream)));
+  if (rc == LAZY_OK && launches > 1) g_launches.fetch_add(launches - 1, std::memory_order_relaxed);
+  return rc;
+}
+
+static lazy::UnitPlan unit_plan(const lazy_attn_params* p, const Checked& c) {
+  return (kv_int4(p) ? lazy::plan_decode_int4 : lazy::plan_decode_fp8_block)(p->num_seqs, c.G, p->num_kv_heads, p->max_blocks_per_seq,
+                                                                             p->num_splits, sm_count());
 }
 
 size_t lazy_attn_decode_workspace_bytes(const lazy_attn_params* p) {
   Checked c;
   if (check_params(p, &c) != LAZY_OK) return 0;
-  if (kv_int4(p)) return lazy::decode_int4_workspace_bytes(int4_plan(p, c), p->num_seqs, p->head_dim);
+  if (kv_records(p)) return lazy::unit_workspace_bytes(unit_plan(p, c), p->num_seqs, p->head_dim);
   int splits, bps;
   plan_splits(p, &splits, &bps);
   return decode_ws_bytes(p, splits);
 }
 
-static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const void* q, const void* k_pool,
-                            const void* v_pool, const uint32_t* block_words, const int32_t* seq_lens,
-                            const int32_t* q_pos, const void* rope_table, void* out, void* workspace,
-                            size_t workspace_bytes, lazy_stream_t stream) {
-  lazy::Int4DecodeArgs a{};
-  a.plan = int4_plan(p, c);
+static int decode_records_impl(const lazy_attn_params* p, const Checked& c, const void* q, const void* k_pool,
+                               const void* v_pool, const uint32_t* block_words, const int32_t* seq_lens,
+                               const int32_t* q_pos, const void* rope_table, void* out, void* workspace,
+                               size_t workspace_bytes, lazy_stream_t stream) {
+  lazy::UnitDecodeArgs a{};
+  a.plan = unit_plan(p, c);
   if (a.plan.ctas > INT32_MAX) return LAZY_ERR_UNSUPPORTED;
-  const size_t need = lazy::decode_int4_workspace_bytes(a.plan, p->num_seqs, p->head_dim);
+  const size_t need = lazy::unit_workspace_bytes(a.plan, p->num_seqs, p->head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return LAZY_ERR_WORKSPACE;
   unsigned int* st = status_ptr();
   if (!st) return LAZY_ERR_CUDA;
@@ -430,9 +459,9 @@ static int decode_int4_impl(const lazy_attn_params* p, const Checked& c, const v
   a.num_pool_blocks = p->num_pool_blocks;
   a.scale_log2 = scale_log2(p);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const int rc = launched(lazy::launch_decode_int4(a, p->lazy != 0, cs));
+  const int rc = launched((kv_int4(p) ? lazy::launch_decode_int4 : lazy::launch_decode_fp8_block)(a, p->lazy != 0, cs));
   if (rc != LAZY_OK || a.plan.parts == 0) return rc;
-  return launched(lazy::launch_combine_int4(a, cs));
+  return launched(lazy::launch_combine_units(a, cs));
 }
 
 static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_pool, const void* v_pool,
@@ -447,7 +476,7 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   if (alibi && p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->dtype != LAZY_BF16 || p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
-  if (kv_int4(p) && (p->dtype != LAZY_BF16 || alibi || p->num_kv_heads > kInt4MaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_records(p) && (p->dtype != LAZY_BF16 || alibi || p->num_kv_heads > kRecordMaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
   if (p->num_seqs == 0) return LAZY_OK;
   if (!q || !k_pool || !v_pool || !block_words || !seq_lens || !q_pos || !rope_table || !out)
     return LAZY_ERR_INVALID_ARG;
@@ -456,9 +485,9 @@ static int decode_impl(const lazy_attn_params* p, const void* q, const void* k_p
   if (p->dtype == LAZY_BF16 && c.G > 64) return LAZY_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(rope_table))
     return LAZY_ERR_INVALID_ARG;
-  if (kv_int4(p))
-    return decode_int4_impl(p, c, q, k_pool, v_pool, block_words, seq_lens, q_pos, rope_table, out, workspace,
-                            workspace_bytes, stream);
+  if (kv_records(p))
+    return decode_records_impl(p, c, q, k_pool, v_pool, block_words, seq_lens, q_pos, rope_table, out, workspace,
+                               workspace_bytes, stream);
   int splits, bps;
   plan_splits(p, &splits, &bps);
   const size_t need = decode_ws_bytes(p, splits);
@@ -541,20 +570,20 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
       (!seg_doc || !seg_len || !doc_block_indptr || !doc_blocks || !items))
     return LAZY_ERR_INVALID_ARG;
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
-  // e4m3 and int4 pools run on mma.sync kernels (items of at most 64 rows) at every ratio
+  // quantised pools run on mma.sync kernels (items of at most 64 rows) at every ratio
   const int cap = kv_quantised(p) ? 64 : lazy::shared_rows_cap(c.G, p->head_dim);
   // 0: 32 blocks for the bf16 and e4m3 mma.sync kernel; for the tensor-core kernel and int4
   // pools, a length that gives about one item per resident CTA. int4 (8 KV heads, 64-block
   // documents): 136 us against 156 with 32 blocks and 218 with 16; 8 sequences of 256-block
   // documents 45 against 44, 52 with 16, 108 with 256.
-  const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 || kv_int4(p) ? 0 : 32);
-  const int slots = kv_int4(p) ? lazy::kSharedInt4Slots : lazy::kSharedTcSlots;
+  const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 || kv_records(p) ? 0 : 32);
+  const int slots = kv_int4(p) ? lazy::kSharedInt4Slots : kv_fp8_block(p) ? lazy::kSharedFp8BlockSlots : lazy::kSharedTcSlots;
   const int auto_items = std::max(1, slots / std::max(1, p->num_kv_heads));
   // small items spread through the launch: measured for the bf16 mma.sync kernel only
   const bool spread = !kv_quantised(p) && cap == 64;
   return lazy::plan_shared_host(p->num_seqs, c.G, cap, p->max_blocks_per_seq, p->num_pool_blocks, num_docs,
                                 seg_indptr, seg_doc, seg_len, doc_block_indptr, doc_blocks, cb, auto_items, capacity,
-                                items, slot_indptr, counts, spread, kv_int4(p));
+                                items, slot_indptr, counts, spread, kv_records(p));
 }
 
 size_t lazy_attn_decode_shared_workspace_bytes(const lazy_attn_params* p, int32_t num_slots) {
@@ -583,7 +612,7 @@ static int decode_shared_impl(const lazy_attn_params* p, const void* q, const vo
   if (p->dtype != LAZY_BF16) return LAZY_ERR_UNSUPPORTED;
   const bool fp8 = kv_fp8(p);
   if (fp8 && (p->head_dim != 128 || alibi)) return LAZY_ERR_UNSUPPORTED;
-  if (kv_int4(p) && (alibi || p->num_kv_heads > kInt4MaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
+  if (kv_records(p) && (alibi || p->num_kv_heads > kRecordMaxKvHeads)) return LAZY_ERR_UNSUPPORTED;
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
   if (num_items < 0 || num_slots < 0) return LAZY_ERR_INVALID_ARG;
   if (p->num_seqs == 0) return LAZY_OK;
@@ -625,8 +654,9 @@ static int decode_shared_impl(const lazy_attn_params* p, const void* q, const vo
   a.scale_log2 = scale_log2(p);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (phase == kSharedCombine) return launched(lazy::launch_shared_combine(a, cs));
-  if (num_items > 0 && kv_int4(p)) {
-    rc = launched(lazy::launch_decode_shared_int4(a, k_pool, v_pool, p->lazy != 0, cs));
+  if (num_items > 0 && kv_records(p)) {
+    rc = launched((kv_int4(p) ? lazy::launch_decode_shared_int4 : lazy::launch_decode_shared_fp8_block)(a, k_pool, v_pool,
+                                                                                                      p->lazy != 0, cs));
     if (rc != LAZY_OK) return rc;
   } else if (num_items > 0) {
     CUtensorMap kmap, vmap;
@@ -933,6 +963,7 @@ size_t lazy_attn_pool_record_bytes(const lazy_attn_params* p) {
   if (check_params(p, &c) != LAZY_OK) return 0;
   const size_t n = (size_t)lazy::kBlock * p->head_dim;
   if (kv_int4(p)) return n / 2 + n / 64 * 4;
+  if (kv_fp8_block(p)) return n + 32;
   return kv_fp8(p) ? n : n * (p->dtype == LAZY_F32 ? 4 : 2);
 }
 
@@ -997,7 +1028,9 @@ int lazy_attn_cache_write(const lazy_attn_params* p, const void* k, int64_t k_to
   const int64_t per16 = 16 / (int64_t)esz;  // elements of a 16-byte load
   const bool vec = aligned16(k) && aligned16(v) && k_token_stride % per16 == 0 && k_head_stride % per16 == 0 &&
                    v_token_stride % per16 == 0 && v_head_stride % per16 == 0;
-  return launched(lazy::launch_cache_write(a, kind, vec, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (kind == LAZY_FP8_E4M3_BLOCK) return launched(lazy::launch_cache_write_fp8_block(a, vec, sm_count(), cs));
+  return launched(lazy::launch_cache_write(a, kind, vec, sm_count(), cs));
 }
 
 int lazy_attn_cache_read(const lazy_attn_params* p, const void* k_pool, const void* v_pool, int32_t num_blocks,
@@ -1028,7 +1061,9 @@ int lazy_attn_cache_read(const lazy_attn_params* p, const void* k_pool, const vo
   a.Hkv = p->num_kv_heads;
   a.D = p->head_dim;
   a.num_pool_blocks = p->num_pool_blocks;
-  return launched(lazy::launch_cache_read(a, kind, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (kind == LAZY_FP8_E4M3_BLOCK) return launched(lazy::launch_cache_read_fp8_block(a, sm_count(), cs));
+  return launched(lazy::launch_cache_read(a, kind, sm_count(), cs));
 }
 
 static int debug_gather_impl(const lazy_attn_params* p, const void* k_pool, const void* v_pool,

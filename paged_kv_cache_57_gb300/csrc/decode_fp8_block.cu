@@ -1,0 +1,469 @@
+// decode_fp8_block.cu -- the decodes over pools of e4m3 codes with a scale per block and head:
+// per sequence (lazy_attn_decode) and over shared document runs (lazy_attn_decode_shared). The
+// arithmetic of a block is in fp8_block.cuh; the query rows of a KV head are its heads (per
+// sequence), or members x heads (shared).
+//
+// Both kernels: four warps form 4 / RT teams of RT = 1, 2 or 4. A team takes a contiguous part of
+// the CTA's blocks through a ring of stages in shared memory; each of its warps has its own tile
+// of 4, 8 or 16 query rows. A block's copies are one warp's, in turn.
+#include <algorithm>
+#include <climits>
+
+#include "decode_units.cuh"
+#include "fp8_block.cuh"
+
+namespace lazy {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMembers = LAZY_PLAN_MAX_MEMBERS;
+constexpr int kItemInts = LAZY_PLAN_ITEM_INTS;
+constexpr int kShRing = 2;  // stages per warp of a team (shared runs)
+
+// The n threads of team t meet (barrier 0 is the CTA's).
+__device__ __forceinline__ void team_sync(int t, int n) { asm volatile("bar.sync %0, %1;" ::"r"(t + 1), "r"(n) : "memory"); }
+
+template <int D, int NT, int HL>
+struct Fp8Cfg {
+  static constexpr int ROWS = Fp8Rows<NT, HL>::ALL;  // of a warp
+  static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
+  static constexpr int SLOT = Fp8Loader<D>::STAGE;
+  static constexpr int CTAS = NT == 1 ? 4 : 3;  // per SM
+  static constexpr int RING = 2;                // stages per warp of a team
+  static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
+  static constexpr int KEPT = fp8_kept_floats<D, NT, HL>();  // per warp (fp8_block.cuh)
+};
+
+}  // namespace
+
+// ------------------------------------------------------------------ per sequence
+// A unit is a sequence, a KV head and a tile of 4, 8, 16, 32 or 64 of its query heads; the units
+// are cut into pieces or ranges (decode_units.cuh).
+template <int D, int NT, int HL, int RT, bool LAZY>
+__global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_block_kernel(const UnitDecodeArgs a) {
+  using C = Fp8Cfg<D, NT, HL>;
+  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT, AHEAD = R - 1;
+  constexpr int kNewDoc = 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
+  // Per team, the blocks of two word chunks (64): id, and valid slots with kNewDoc where the block
+  // is not one of the document of the block before (or begins a chunk).
+  __shared__ int2 d_blk[TEAMS][64];
+  wait_for_launch_before();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / RT, rt = warp % RT;
+  const int ht = a.plan.units / a.Hkv;
+
+  UnitWalk w;
+  if (!w.begin(a, warp, lane)) return;
+  while (w.next(a)) {
+    const int s = w.s, seq_len = w.seq_len, nb = w.nb, lo = w.lo, hi = w.hi;
+    const int kvh = w.u / ht, head0 = (w.u - kvh * ht) * (C::ROWS * RT);
+    const int heads = min(C::ROWS * RT, a.G - head0);
+    const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
+    const int n = hi - lo;                                           // blocks of the part
+    const int m_pos = a.q_pos[s];
+    const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
+
+    Fp8QueryRows<NT> rows;
+    bool live[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rt * C::ROWS + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2));
+      live[nt] = r < heads;
+      rows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) + (q0 + (live[nt] ? r : 0)) * D;
+    }
+    const Fp8RawRows<D, NT> raw(rows, lane);  // loads that nothing waits for yet
+    float2 rate[HALF / 32];
+#pragma unroll
+    for (int j = 0; j < HALF / 32; ++j) rate[j] = a.rope[lane + 32 * j];
+
+    // ------------------------------------------------------------ first loads
+    const int per_team = (n + TEAMS - 1) / TEAMS;
+    const int kb0 = lo + team * per_team;
+    const int nk = max(0, min(lo + n, kb0 + per_team) - kb0);  // blocks of this team
+    const Fp8Loader<D> load(a.k_pool, a.v_pool, a.Hkv, kvh, lane);
+    const uint8_t* ring_p = smem + team * R * C::SLOT;
+    const uint32_t ring = smem_u32(ring_p);
+    uint32_t w_nxt = 0, wn_nxt = 0;
+    auto load_words = [&](int kc) {
+      const int k = kc + lane, b = kb0 + k;
+      w_nxt = k < nk ? wrow[b] : 0u;
+      wn_nxt = (k < nk && b + 1 < nb) ? wrow[b + 1] : 0u;
+    };
+    auto describe = [&](int kc) {  // the chunk of w_nxt, by every warp of the team alike
+      const LaneBlock r = describe_block(kc + lane < nk, kb0 + kc + lane, nb, seq_len, w_nxt, wn_nxt, a.id_bits,
+                                         a.num_pool_blocks, a.status);
+      // a block without keys is left out and did not have q rotated for its document
+      const int p_1 = __shfl_up_sync(0xffffffffu, r.nv > 0 ? r.p : INT_MIN, 1);
+      if (rt == 0)
+        d_blk[team][(kc + lane) & 63] = make_int2(r.phys < a.num_pool_blocks ? r.phys : 0,  // no keys in it: any block
+                                                  r.nv | (!LAZY || (lane > 0 && p_1 == r.p) ? 0 : kNewDoc));
+      __syncwarp();
+    };
+    load_words(0);
+    describe(0);
+    load_words(32);
+    if (RT > 1) team_sync(team, 32 * RT);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i < nk && i % RT == rt) load(ring + i * C::SLOT, d_blk[team][i].x, lane);
+      cp_async_commit();
+    }
+
+    // ------------------------------------------------------------ queries
+    fp8_scale_rows<D, NT>(rows, raw, live, a.scale_log2);
+    float2* cs = cs_all + warp * HALF;
+    float* kept = reinterpret_cast<float*>(cs_all + kWarps * HALF) + warp * C::KEPT;
+    Fp8Query<D, NT, HL> q;
+    auto rebuild = [&](int delta) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < HALF / 32; ++j) cs[lane + 32 * j] = rope_cs(rate[j], delta, a.status);
+      __syncwarp();
+      fp8_build_query<D, NT, HL>(q, rows, lane, [&](int) { return cs; });
+    };
+    // Rotated while the first records are on their way. Control: the pool holds absolute-position keys.
+    int p_cur = 0;  // the document that q is rotated for
+    if (nk > 0) {
+      if constexpr (LAZY) p_cur = decode_word(wrow[kb0], kb0, a.id_bits).p;
+      rebuild(m_pos - p_cur);
+    }
+
+    // ------------------------------------------------------------ main loop
+    Fp8State<D, NT, HL> st;
+    fp8_init(st);
+    for (int i = 0; i < nk; ++i) {
+      // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all
+      // of whose warps are done with block i - 1, whose stage is refilled.
+      cp_async_wait<AHEAD - 1>();
+      if (RT == 1) __syncwarp();
+      else team_sync(team, 32 * RT);
+      if ((i & 31) == 0) {
+        if (i + 32 < nk) {  // a chunk of words ahead, over the one that all are done with
+          describe(i + 32);
+          load_words(i + 64);
+        }
+        if (i > 0 && i % kFp8Flush == 0) fp8_flush(st, kept, i > kFp8Flush, lane);
+      }
+      const int j = i + AHEAD;
+      if (j < nk && j % RT == rt) load(ring + (j % R) * C::SLOT, d_blk[team][j & 63].x, lane);
+      cp_async_commit();  // a group a step, empty where another warp loads
+      const int info = d_blk[team][i & 63].y, nv = info & 31;
+      if (nv == 0) continue;  // the same for the whole team
+      if (LAZY && info >= kNewDoc) {
+        const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
+        if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
+      }
+      fp8_attend<D, NT, HL>(ring_p + (i % R) * C::SLOT, nv, q, st, lane, i >= kFp8Flush ? kept : nullptr);
+    }
+    if (nk > kFp8Flush) fp8_unflush(st, kept, lane);
+    fp8_finish(st);
+    cp_async_wait<0>();
+    __syncthreads();  // every team is done with its ring: the merge takes its place
+    float* red = reinterpret_cast<float*>(smem);
+    fp8_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
+    __syncthreads();
+    const bool whole = lo == 0 && hi == nb;
+    const size_t slot0 = (2 * (size_t)blockIdx.x + (lo == 0 ? 1 : 0)) * (C::ROWS * RT);
+    for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
+      const int row = idx / D, col = idx % D;  // row of tile row / ROWS, which warp row / ROWS of each team has
+      float M = -INFINITY;
+#pragma unroll
+      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * RT * C::ROWS + row) * C::RED + D]);
+      const float Mr = M == -INFINITY ? 0.f : M;  // no keys: all sums are 0 (or NaN, which stays)
+      float acc = 0.f, L = 0.f;
+#pragma unroll
+      for (int tm = 0; tm < TEAMS; ++tm) {
+        const float* src = red + (tm * RT * C::ROWS + row) * C::RED;
+        const float f = fast_ex2(src[D] - Mr);
+        acc += f * src[col];
+        L += f * src[D + 1];
+      }
+      if (whole) {
+        static_cast<__nv_bfloat16*>(a.out)[(q0 + row) * D + col] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+      } else {
+        a.ws_o[(slot0 + row) * D + col] = acc;
+        if (col == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * (slot0 + row)) = make_float2(M, L);
+      }
+    }
+    if (w.last()) return;
+    __syncthreads();  // the next part's loads and queries take the merge's place
+  }
+}
+
+// ------------------------------------------------------------------ shared runs
+// One CTA per (work item, KV head), for all of its up to 64 rows (members x heads).
+namespace {
+
+template <int D>
+struct Fp8SharedCfg {
+  static constexpr int SLOT = Fp8Loader<D>::STAGE;
+  static constexpr int ROWS = 2 * kWarps * 8;  // of a CTA
+  static constexpr int RED = D + 4;            // merge rows: o[D], m, l
+  static constexpr int STAGES = kShRing * kWarps;
+  static constexpr int BUF = STAGES * SLOT > ROWS * RED * 4 ? STAGES * SLOT : ROWS * RED * 4;
+  // the members' angles, then, once the queries are built, the warps' kept sums (fp8_block.cuh)
+  static constexpr int ANGLES = kMembers * (D / 2) * 8;
+  static constexpr int KEPT = kWarps * fp8_kept_floats<D, 2, 2>() * 4;
+  static constexpr int SMEM = BUF + (ANGLES > KEPT ? ANGLES : KEPT);
+};
+
+// What the CTA's warps share of an item.
+struct Fp8Item {
+  int rec[kItemInts];
+  int delta[kMembers], ok[kMembers];  // rotation offset of each member; it passed its checks
+  int2 d_blk[kWarps][64];             // per team, the blocks of two word chunks: id, valid slots
+};
+
+}  // namespace
+
+// The item's `rows` rows by teams of RT warps with NT tiles each.
+template <int D, int NT, int HL, bool LAZY>
+__device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
+                                                Fp8Item& it, uint8_t* smem, float2* cs_tab, int kvh, int rows, int RT) {
+  using C = Fp8SharedCfg<D>;
+  constexpr int HALF = D / 2, TILE = Fp8Rows<NT, HL>::ALL;
+  const int TEAMS = kWarps / RT, R = C::STAGES / TEAMS, AHEAD = R - 1;  // R = 2, 4 or 8
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / RT, rt = warp & (RT - 1);
+  const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3];
+
+  // ------------------------------------------------------------ first loads
+  const int per_team = (nblk + TEAMS - 1) / TEAMS;
+  const int kb0 = team * per_team;
+  const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
+  const Fp8Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
+  const uint8_t* ring_p = smem + team * R * C::SLOT;
+  const uint32_t ring = smem_u32(ring_p);
+  const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
+  const uint32_t id_mask = (1u << a.id_bits) - 1u;
+  const int* ids = it.rec + 8 + 4 * kMembers;  // the record's block ids
+  uint32_t w_nxt = 0u;
+  auto load_words = [&](int kc) {
+    if (kc + lane < nk) w_nxt = wrow[kc + lane];
+  };
+  // Chunk kc of the team's words (w_nxt) to its descriptors, by every warp of the team alike. The
+  // block word decides; where the record names the block too the two must agree.
+  auto describe = [&](int kc) {
+    const int k = kc + lane;
+    int phys = 0, nv = 0;  // no keys: any block of the pool
+    if (k < nk) {
+      const int ph = (int)(w_nxt & id_mask);
+      if (kb0 + k < LAZY_PLAN_ITEM_BLOCK_IDS && ids[kb0 + k] != ph) {
+        raise_status(a.status, LAZY_DEV_LAYOUT);
+      } else if (ph < a.num_pool_blocks) {
+        phys = ph;
+        nv = kb0 + k == nblk - 1 ? last_nv : kBlock;
+      } else {
+        raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
+      }
+    }
+    if (rt == 0) it.d_blk[team][k & 63] = make_int2(phys, nv);
+    __syncwarp();
+  };
+  load_words(0);
+  // First loads straight from the record's ids when it names all of them.
+  const bool rec_first = kb0 + min(AHEAD, nk) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  if (rec_first) {
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i < nk && (i & (RT - 1)) == rt) {
+        const int id = ids[kb0 + i];
+        load(ring + i * C::SLOT, id >= 0 && id < a.num_pool_blocks ? id : 0, lane);
+      }
+      cp_async_commit();
+    }
+  }
+  describe(0);
+  load_words(32);
+  if (RT > 1) team_sync(team, 32 * RT);
+  if (!rec_first) {
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i < nk && (i & (RT - 1)) == rt) load(ring + i * C::SLOT, it.d_blk[team][i].x, lane);
+      cp_async_commit();
+    }
+  }
+
+  // ------------------------------------------------------------ members
+  const int nmem = it.rec[4];
+  if (threadIdx.x < nmem) {
+    const int m = threadIdx.x, seq = it.rec[8 + 4 * m], bm = it.rec[8 + 4 * m + 1], slot = it.rec[8 + 4 * m + 2];
+    bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
+    int delta = 0;
+    if (good) {
+      const BlockInfo mi = decode_word(a.words[(size_t)seq * a.max_blocks + bm], bm, a.id_bits);
+      good = mi.phys == decode_word(a.words[(size_t)src * a.max_blocks + b0], b0, a.id_bits).phys;
+      const int qp = a.q_pos[seq];
+      delta = LAZY ? qp - mi.p : qp;
+    }
+    if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
+    it.ok[m] = good;
+    it.delta[m] = delta;
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads)
+    cs_tab[idx] = rope_cs(a.rope[idx % HALF], it.delta[idx / HALF], a.status);
+  __syncthreads();
+
+  // ------------------------------------------------------------ queries
+  auto mem_seq = [&](int m) { return it.rec[8 + 4 * m]; };
+  auto mem_slot = [&](int m) { return it.rec[8 + 4 * m + 2]; };
+  Fp8QueryRows<NT> qrows;
+  bool live[NT];
+  int mem[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = rt * TILE + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2)), rc = r < rows ? r : 0;
+    mem[nt] = rc / a.G;
+    live[nt] = r < rows && it.ok[mem[nt]];
+    qrows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) +
+                  ((live[nt] ? (size_t)mem_seq(mem[nt]) * a.Hq + (rc - mem[nt] * a.G) : 0) + (size_t)kvh * a.G) * D;
+  }
+  fp8_scale_rows<D, NT>(qrows, Fp8RawRows<D, NT>(qrows, lane), live, a.scale_log2);
+  Fp8Query<D, NT, HL> q;
+  fp8_build_query<D, NT, HL>(q, qrows, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
+
+  // ------------------------------------------------------------ main loop
+  float* kept = reinterpret_cast<float*>(cs_tab) + warp * fp8_kept_floats<D, NT, HL>();
+  if (per_team > kFp8Flush) __syncthreads();  // sums will be kept where the angles were
+  Fp8State<D, NT, HL> st;
+  fp8_init(st);
+  for (int i = 0; i < nk; ++i) {
+    // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all of
+    // whose warps are done with block i - 1, whose stage is refilled.
+    if (RT == 1) {
+      cp_async_wait<kShRing - 2>();
+      __syncwarp();
+    } else {
+      if (RT == 2) cp_async_wait<2 * kShRing - 2>();
+      else cp_async_wait<4 * kShRing - 2>();
+      team_sync(team, 32 * RT);
+    }
+    if ((i & 31) == 0) {  // a chunk of words ahead, over the one that all are done with
+      describe(i + 32);
+      load_words(i + 64);
+      if (i > 0 && i % kFp8Flush == 0) fp8_flush(st, kept, i > kFp8Flush, lane);
+    }
+    const int n = i + AHEAD;
+    if (n < nk && (n & (RT - 1)) == rt) load(ring + (n & (R - 1)) * C::SLOT, it.d_blk[team][n & 63].x, lane);
+    cp_async_commit();  // a group a step, empty where another warp loads
+    const int nv = it.d_blk[team][i & 63].y;
+    if (nv > 0) fp8_attend<D, NT, HL>(ring_p + (i & (R - 1)) * C::SLOT, nv, q, st, lane, i >= kFp8Flush ? kept : nullptr);
+  }
+  if (nk > kFp8Flush) fp8_unflush(st, kept, lane);
+  fp8_finish(st);
+  cp_async_wait<0>();
+  __syncthreads();  // every team is done with its ring: the merge takes its place
+
+  // ------------------------------------------------------------ partials
+  float* red = reinterpret_cast<float*>(smem);
+  fp8_store_partial(st, red + warp * TILE * C::RED, C::RED, lane);
+  __syncthreads();
+  constexpr int PER = D / 32;
+  for (int x = warp; x < rows; x += kWarps) {
+    const int m = x / a.G, h = x - m * a.G;
+    if (mem_slot(m) < 0 || mem_slot(m) >= a.num_slots) continue;
+    float M = -INFINITY, acc[PER], L = 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+    if (it.ok[m]) {  // a member that failed its checks leaves an empty partial
+      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * RT * TILE + x) * C::RED + D]);
+      const float Mr = M == -INFINITY ? 0.f : M;
+      for (int tm = 0; tm < TEAMS; ++tm) {
+        const float* row = red + (tm * RT * TILE + x) * C::RED;
+        const float w = fast_ex2(row[D] - Mr);
+        L += w * row[D + 1];
+#pragma unroll
+        for (int c = 0; c < PER; ++c) acc[c] += w * row[lane + 32 * c];
+      }
+      if (L != 0.f) M = Mr;  // all scores NaN: not an empty slot, which the combine would pass over
+    }
+    const size_t pidx = (size_t)mem_slot(m) * a.Hq + (size_t)kvh * a.G + h;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) a.ws_o[pidx * D + lane + 32 * c] = acc[c];
+    if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * pidx) = make_float2(M, L);
+  }
+}
+
+template <int D, bool LAZY>
+__global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
+                                                                              const uint8_t* v_pool) {
+  using C = Fp8SharedCfg<D>;
+  extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
+  float2* cs_tab = reinterpret_cast<float2*>(smem + C::BUF);  // [members][D / 2]
+  __shared__ __align__(16) Fp8Item it;
+  wait_for_launch_before();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int kvh = blockIdx.x % a.Hkv, item = blockIdx.x / a.Hkv;
+  if (threadIdx.x < kItemInts / 4)
+    reinterpret_cast<int4*>(it.rec)[threadIdx.x] =
+        reinterpret_cast<const int4*>(a.items)[(size_t)item * (kItemInts / 4) + threadIdx.x];
+  __syncthreads();
+  const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3], nmem = it.rec[4];
+  const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
+                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= C::ROWS;
+  if (!item_ok) {  // uniform over the CTA: nothing is loaded or written
+    if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
+    return;
+  }
+  const int n = nmem * a.G;
+  if (n <= 4) shared_fp8_rows<D, 1, 1, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, 1);
+  else if (n <= 8) shared_fp8_rows<D, 1, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, 1);
+  else shared_fp8_rows<D, 2, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, n <= 16 ? 1 : (n <= 32 ? 2 : 4));
+}
+
+// ------------------------------------------------------------------ launchers
+
+UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
+  int rows = 4;
+  while (rows < G && rows < 64) rows *= 2;
+  const int per_sm = rows < 16 ? Fp8Cfg<128, 1, 1>::CTAS : Fp8Cfg<128, 2, 2>::CTAS;
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm);
+}
+
+template <int D, int NT, int HL, int RT, bool LAZY>
+static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
+  using C = Fp8Cfg<D, NT, HL>;
+  constexpr int SMEM = C::BUF + kWarps * (D / 2) * 8 + kWarps * C::KEPT * 4;
+  cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, RT, LAZY>>(SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_behind(decode_fp8_block_kernel<D, NT, HL, RT, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
+}
+
+template <int D, bool LAZY>
+static cudaError_t launch_decode_d(const UnitDecodeArgs& a, cudaStream_t st) {
+  switch (a.plan.rows) {
+    case 4: return launch_decode_t<D, 1, 1, 1, LAZY>(a, st);
+    case 8: return launch_decode_t<D, 1, 2, 1, LAZY>(a, st);
+    case 16: return launch_decode_t<D, 2, 2, 1, LAZY>(a, st);
+    case 32: return launch_decode_t<D, 2, 2, 2, LAZY>(a, st);
+    default: return launch_decode_t<D, 2, 2, 4, LAZY>(a, st);
+  }
+}
+
+cudaError_t launch_decode_fp8_block(const UnitDecodeArgs& a, bool lazy, cudaStream_t st) {
+  if (a.D == 128) return lazy ? launch_decode_d<128, true>(a, st) : launch_decode_d<128, false>(a, st);
+  return lazy ? launch_decode_d<64, true>(a, st) : launch_decode_d<64, false>(a, st);
+}
+
+template <int D, bool LAZY>
+static cudaError_t launch_shared_t(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, cudaStream_t st) {
+  constexpr int SMEM = Fp8SharedCfg<D>::SMEM;
+  cudaError_t e = set_smem_once<decode_shared_fp8_block_kernel<D, LAZY>>(SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_behind(decode_shared_fp8_block_kernel<D, LAZY>, (unsigned)(a.num_items * a.Hkv), kThreads, SMEM, st, a,
+                       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool));
+}
+
+cudaError_t launch_decode_shared_fp8_block(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,
+                                           cudaStream_t st) {
+  if (a.num_items == 0) return cudaSuccess;
+  if (a.D == 128)
+    return lazy ? launch_shared_t<128, true>(a, k_pool, v_pool, st) : launch_shared_t<128, false>(a, k_pool, v_pool, st);
+  return lazy ? launch_shared_t<64, true>(a, k_pool, v_pool, st) : launch_shared_t<64, false>(a, k_pool, v_pool, st);
+}
+
+}  // namespace lazy

@@ -6,6 +6,7 @@
 #include <climits>
 
 #include "decode_block.cuh"
+#include "decode_units.cuh"
 #include "int4.cuh"
 #include "kernels.h"
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 //
 // The other parts go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that
 // begins in CTA c's places, 2 c for one that began before) and are merged by
-// combine_int4_kernel.
+// combine_units_kernel (decode_units.cu).
 //
 // Of a part the four warps take a quarter each. A warp is its own loader: a ring of RING
 // stages of two blocks, each refilled as soon as it was read. 64 sequences of 4160 tokens, 32
@@ -91,52 +92,8 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 // 32 heads on one KV head both tiles of 16 heads read the records (872 MB for 466), at 8 warps
 // an SM: 250 us, issue slots 51%, tensor 38%.
 
-namespace {
-
-constexpr int kMinPieceLog2 = 5;  // 32 blocks of a piece at least: one of 16384 tokens 17 us, with 16 or 64 19
-constexpr int kMaxPiece = 512;
-constexpr int kMinChunk = 16;   // blocks of a range at least
-constexpr int kMaxLook = 1024;  // sequences that every CTA looks through
-
-__device__ __forceinline__ int blocks_of(const Int4DecodeArgs& a, int s, int& seq_len) {
-  seq_len = a.seq_lens[s];
-  if (seq_len < 0 || seq_len > kBlock * a.max_blocks) {
-    raise_status(a.status, LAZY_DEV_BAD_LEN);
-    seq_len = seq_len < 0 ? 0 : kBlock * a.max_blocks;
-  }
-  return (seq_len + kBlock - 1) / kBlock;
-}
-
-// Blocks of a piece of a sequence of nb blocks.
-__host__ __device__ __forceinline__ int piece_of(const Int4Plan& p, int nb) {
-  if (p.splits == 1) return nb;
-  const int n = max(1, min(p.splits, nb >> p.least_log2));
-  return (int)((unsigned)(nb + n - 1) / (unsigned)n);
-}
-
-// Blocks of a range, of `total` in all.
-__device__ __forceinline__ int64_t chunk_of(const Int4DecodeArgs& a, int64_t total) {
-  const int64_t c = (total + a.plan.range_ctas - 1) / a.plan.range_ctas;
-  return c > kMinChunk ? c : kMinChunk;
-}
-
-// Whether the batch is cut into ranges: some sequence's pieces would be too long (every warp
-// looks by itself).
-__device__ __forceinline__ bool takes_ranges(const Int4DecodeArgs& a, int lane) {
-  if (a.plan.range_ctas == 0) return false;
-  if (a.B > kMaxLook) return true;
-  int longest = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    int len;
-    longest = max(longest, blocks_of(a, b, len));
-  }
-  return __reduce_max_sync(0xffffffffu, longest) > kMaxPiece * a.plan.splits;
-}
-
-}  // namespace
-
 template <int D, int NT, int HL, bool LAZY>
-__global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int4_kernel(const Int4DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int4_kernel(const UnitDecodeArgs a) {
   using C = Int4Cfg<D, NT, HL>;
   using G = Int4Geom<D>;
   constexpr int HALF = D / 2, R = C::RING;
@@ -151,72 +108,12 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
   wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int U = a.plan.units, ht = U / a.Hkv;
+  const int ht = a.plan.units / a.Hkv;
 
-  // ------------------------------------------------------------ the CTA's piece or range
-  int s = 0, seq_len = 0, nb = 0, u = 0, lo = 0, hi = 0;  // the part: blocks lo .. hi - 1 of unit u of s
-  int64_t at = 0, left = 0;  // place within sequence s (its units end to end); places left of the range
-  const bool ranges = takes_ranges(a, lane);
-  if (a.plan.range_ctas > 0 && blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B + 1] = ranges;
-  if (!ranges) {  // first pieces first: CTAs without one are the last, not between those of one SM
-    const unsigned units = (unsigned)a.B * U, piece = blockIdx.x / units, unit = blockIdx.x - piece * units;
-    s = unit / U;
-    u = unit - s * U;
-    nb = blocks_of(a, s, seq_len);
-    const int len = piece_of(a.plan, nb);
-    lo = piece * len;
-    hi = min(nb, lo + len);
-    if (piece > 0 && lo >= nb) return;
-  } else {  // every warp for itself: the total, then the sequence of the range's first place
-    int64_t total = 0;
-    int own = 0, inc = 0;  // of the last 32 sequences: the lane's blocks, and up to them
-    auto scan = [&](int b) {
-      int len;
-      inc = own = b + lane < a.B ? blocks_of(a, b + lane, len) : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-    };
-    for (int b = 0; b < a.B; b += 32) {
-      scan(b);
-      if (blockIdx.x == 0 && warp == 0 && b + lane < a.B) a.prefix[b + lane] = total + inc - own;
-      total += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.B] = total;
-    total *= U;
-    const int64_t chunk = chunk_of(a, total), first = blockIdx.x * chunk;
-    left = min(chunk, total - first);
-    if (left <= 0) return;
-    int64_t before = 0;
-    for (s = 0; s < a.B; s += 32) {
-      if (a.B > 32) scan(s);
-      const uint32_t past = __ballot_sync(0xffffffffu, (before + inc) * U > first);  // sequences that end behind it
-      if (past) {
-        const int l = __ffs(past) - 1;
-        s += l;
-        at = first - (before + __shfl_sync(0xffffffffu, inc, l) - __shfl_sync(0xffffffffu, own, l)) * U;
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-  }
-  while (true) {
-    // ------------------------------------------------------------ the next part
-    if (left > 0) {
-      if (s >= a.B) return;
-      nb = blocks_of(a, s, seq_len);
-      if (nb == 0 || at >= (int64_t)U * nb) {
-        at -= (int64_t)U * nb;
-        ++s;
-        continue;
-      }
-      u = (int)(at / nb), lo = (int)(at - (int64_t)u * nb);
-      hi = (int)min((int64_t)nb, lo + left);
-      at += hi - lo;
-      left -= hi - lo;
-    }
+  UnitWalk w;
+  if (!w.begin(a, warp, lane)) return;
+  while (w.next(a)) {
+    const int s = w.s, seq_len = w.seq_len, nb = w.nb, u = w.u, lo = w.lo, hi = w.hi;
     const int kvh = u / ht, head0 = (u - kvh * ht) * C::ROWS;
     const int heads = min(C::ROWS, a.G - head0);
     const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
@@ -371,143 +268,8 @@ __global__ void __launch_bounds__(kThreads, Int4Cfg<D, NT, HL>::CTAS) decode_int
         if (col == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * (slot0 + row)) = make_float2(M, L);
       }
     }
-    if (left <= 0) return;
+    if (w.last()) return;
     __syncthreads();  // the next part's loads and queries take the merge's place
-  }
-}
-
-// out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c over the parts of a unit of several pieces
-// or in several ranges; with ranges 0 for a sequence without blocks (with pieces its unit's CTA
-// writes that). A CTA looks after PAIRS (sequence, query head) pairs: a warp finds a pair's parts
-// and merges up to kCombineBatch of them by itself; more are shared by the CTA's warps. Launched
-// as a programmatic dependent of the decode kernel: it waits for that grid before it reads
-// anything.
-//
-// Up to kCombineAlone pairs, as many CTAs as are resident at once, get a CTA each: whole
-// calls of 32 heads took 21 us at 1 x 16384 tokens and at 4 x 4096, with PAIRS = 8 30 and 29.
-// Most of a large batch's pairs have nothing to merge, and CTAs that find that out come in
-// waves: at 64 x 4160 tokens PAIRS = 8 took 73.5 us, a CTA per pair 80.
-constexpr int kCombineWarps = 8, kCombineBatch = 8, kCombineAlone = 3 * 152;
-
-namespace {
-
-template <int D>
-struct Merged {
-  static constexpr int PER = D / 32;
-  float M, L, acc[PER];
-  // Parts first, first + step, ... of a row's n, a lane the columns lane + 32 i. Part i is CTA c0 + i stride's.
-  __device__ __forceinline__ Merged(const Int4DecodeArgs& a, int row, int c0, int n, int stride, int first, int step) {
-    const int lane = threadIdx.x & 31;
-    M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int cb = first; cb < n; cb += step * kCombineBatch) {
-      float2 ml[kCombineBatch];
-      float v[kCombineBatch][PER];
-#pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) {
-        const int c = cb + b * step;
-        ml[b] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[b][i] = 0.f;
-        if (c < n) {
-          const size_t p = (2 * ((size_t)c0 + (size_t)c * stride) + (c == 0 ? 1 : 0)) * a.plan.rows + row;
-          ml[b] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * p);
-#pragma unroll
-          for (int i = 0; i < PER; ++i) v[b][i] = a.ws_o[p * D + lane + 32 * i];
-        }
-      }
-      float Mn = M;
-#pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) Mn = fmaxf(Mn, ml[b].x);
-      const float Mr = Mn == -INFINITY ? 0.f : Mn;
-      const float r = fast_ex2(M - Mr);
-      L *= r;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] *= r;
-#pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) {
-        const float w = fast_ex2(ml[b].x - Mr);  // an empty part (m = -inf) weighs 0
-        L = fmaf(w, ml[b].y, L);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, v[b][i], acc[i]);
-      }
-      M = Mn;
-    }
-  }
-};
-
-}  // namespace
-
-template <int D, int PAIRS>
-__global__ void __launch_bounds__(32 * kCombineWarps) combine_int4_kernel(const Int4DecodeArgs a) {
-  constexpr int PER = D / 32;
-  __shared__ float red[kCombineWarps][D + 2];
-  __shared__ int2 parts[PAIRS];  // what the CTA's warps share: first part's CTA and parts; 0 or 1: nothing to merge
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t pair0 = (int64_t)blockIdx.x * PAIRS, pairs = (int64_t)a.B * a.Hq;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-  auto row_of = [&](int64_t pair) { return (int)(pair % a.Hq) % a.G % a.plan.rows; };
-  wait_for_launch_before();
-  const bool ranges = a.plan.range_ctas > 0 && a.prefix[a.B + 1] != 0;
-  const int stride = ranges ? 1 : a.B * a.plan.units;
-  if (warp < PAIRS) {
-    const int64_t pair = pair0 + warp;
-    int2 mine = make_int2(0, 0);
-    if (pair < pairs) {
-      const int s = (int)(pair / a.Hq), h = (int)(pair - (int64_t)s * a.Hq), kvh = h / a.G;
-      const int u = kvh * (a.plan.units / a.Hkv) + (h - kvh * a.G) / a.plan.rows;
-      if (ranges) {
-        const int64_t p0 = a.prefix[s], len = a.prefix[s + 1] - p0, lo = p0 * a.plan.units + u * len;
-        const int64_t chunk = chunk_of(a, a.prefix[a.B] * a.plan.units);
-        if (len == 0) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(0.f);
-        } else {
-          const int64_t c0 = lo / chunk;
-          mine = make_int2((int)c0, (int)((lo + len - 1) / chunk - c0) + 1);  // in one range: written there
-        }
-      } else {
-        int seq_len;
-        const int nb = blocks_of(a, s, seq_len), len = piece_of(a.plan, nb);
-        mine = make_int2(s * a.plan.units + u, nb > len ? (nb + len - 1) / len : 1);  // of one piece: written there
-      }
-      if (PAIRS > 1 && mine.y > 1 && mine.y <= kCombineBatch) {
-        const Merged<D> m(a, row_of(pair), mine.x, mine.y, stride, 0, 1);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) out[pair * D + lane + 32 * i] = __float2bfloat16_rn(m.L == 0.f ? 0.f : m.acc[i] / m.L);
-        mine.y = 0;
-      }
-    }
-    if (lane == 0) parts[warp] = mine;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < PAIRS; ++i) {
-    const int2 p = parts[i];
-    if (p.y <= 1) continue;
-    const Merged<D> m(a, row_of(pair0 + i), p.x, p.y, stride, warp, kCombineWarps);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) red[warp][lane + 32 * j] = m.acc[j];
-    if (lane == 0) {
-      red[warp][D] = m.M;
-      red[warp][D + 1] = m.L;
-    }
-    __syncthreads();
-    for (int col = threadIdx.x; col < D; col += 32 * kCombineWarps) {
-      float Ma = -INFINITY, x = 0.f, La = 0.f;
-#pragma unroll
-      for (int w = 0; w < kCombineWarps; ++w) Ma = fmaxf(Ma, red[w][D]);
-      if (Ma == -INFINITY) Ma = 0.f;
-#pragma unroll
-      for (int w = 0; w < kCombineWarps; ++w) {
-        const float f = fast_ex2(red[w][D] - Ma);
-        x += f * red[w][col];
-        La += f * red[w][D + 1];
-      }
-      out[(pair0 + i) * D + col] = __float2bfloat16_rn(La == 0.f ? 0.f : x / La);
-    }
-    __syncthreads();
   }
 }
 
@@ -763,33 +525,14 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
 
 // ------------------------------------------------------------------ launchers
 
-Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
-  Int4Plan p{};
-  p.rows = G <= 4 ? 4 : (G <= 8 ? 8 : 16);
-  p.units = Hkv * ((G + p.rows - 1) / p.rows);
-  const int mb = max_blocks > 0 ? max_blocks : 1;
-  const int64_t units = (int64_t)(B > 0 ? B : 1) * p.units;
-  const int64_t resident = (int64_t)sms * (p.rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS);
-  p.least_log2 = num_splits > 0 ? 0 : kMinPieceLog2;
-  p.splits = num_splits > 0 ? std::min(num_splits, mb)
-                            : (int)std::max<int64_t>(1, std::min<int64_t>(resident / units, mb >> kMinPieceLog2));
-  p.ctas = units * p.splits;
-  p.parts = p.splits > 1 ? p.ctas : 0;
-  if (num_splits <= 0 && mb > kMaxPiece * p.splits) {
-    p.range_ctas = std::min<int64_t>((units * mb + kMinChunk - 1) / kMinChunk, resident);
-    p.ctas = B > kMaxLook ? p.range_ctas : std::max(p.ctas, p.range_ctas);
-    p.parts = std::max(p.parts, p.range_ctas);
-  }
-  return p;
-}
-
-size_t decode_int4_workspace_bytes(const Int4Plan& p, int B, int D) {
-  if (p.parts == 0) return 0;
-  return (size_t)2 * p.parts * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(int64_t);
+UnitPlan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
+  const int rows = G <= 4 ? 4 : (G <= 8 ? 8 : 16);
+  const int per_sm = rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS;
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm);
 }
 
 template <int D, int NT, int HL, bool LAZY>
-static cudaError_t launch_decode_t(const Int4DecodeArgs& a, cudaStream_t st) {
+static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
   using C = Int4Cfg<D, NT, HL>;
   cudaError_t e = set_smem_once<decode_int4_kernel<D, NT, HL, LAZY>>(C::SMEM);
   if (e != cudaSuccess) return e;
@@ -797,24 +540,14 @@ static cudaError_t launch_decode_t(const Int4DecodeArgs& a, cudaStream_t st) {
 }
 
 template <int D, bool LAZY>
-static cudaError_t launch_decode_d(const Int4DecodeArgs& a, cudaStream_t st) {
+static cudaError_t launch_decode_d(const UnitDecodeArgs& a, cudaStream_t st) {
   if (a.plan.rows == 4) return launch_decode_t<D, 1, 1, LAZY>(a, st);
   return a.plan.rows == 8 ? launch_decode_t<D, 1, 2, LAZY>(a, st) : launch_decode_t<D, 2, 2, LAZY>(a, st);
 }
 
-cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t st) {
+cudaError_t launch_decode_int4(const UnitDecodeArgs& a, bool lazy, cudaStream_t st) {
   if (a.D == 128) return lazy ? launch_decode_d<128, true>(a, st) : launch_decode_d<128, false>(a, st);
   return lazy ? launch_decode_d<64, true>(a, st) : launch_decode_d<64, false>(a, st);
-}
-
-cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st) {
-  const long long pairs = (long long)a.B * a.Hq;
-  const bool one = pairs <= kCombineAlone;
-  const long long grid = one ? pairs : (pairs + kCombineWarps - 1) / kCombineWarps;
-  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  auto kern = a.D == 128 ? (one ? combine_int4_kernel<128, 1> : combine_int4_kernel<128, kCombineWarps>)
-                         : (one ? combine_int4_kernel<64, 1> : combine_int4_kernel<64, kCombineWarps>);
-  return launch_behind(kern, (unsigned)grid, 32 * kCombineWarps, 0, st, a);
 }
 
 template <int D, bool LAZY>

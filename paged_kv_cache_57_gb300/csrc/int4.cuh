@@ -53,12 +53,6 @@ __host__ __device__ __forceinline__ int int4_v_token(int r) { return (r & 8) + 2
 __device__ __forceinline__ float meta_scale(uint32_t m) { return __uint_as_float(m << 16); }
 __device__ __forceinline__ float meta_zero(uint32_t m) { return __uint_as_float(m & 0xffff0000u); }
 
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
 // A record in shared memory.
 struct SharedRecord {
   const uint8_t* p;
@@ -66,15 +60,6 @@ struct SharedRecord {
   __device__ __forceinline__ uint2 v2(int off) const { return *reinterpret_cast<const uint2*>(p + off); }
   __device__ __forceinline__ uint32_t v1(int off) const { return *reinterpret_cast<const uint32_t*>(p + off); }
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups of this thread have landed
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // A warp's copies of two blocks' records into a ring stage ([block][K, V]), 16 bytes a lane:
 // the rows of codes, then the four records' scales and zeros at once. (A bulk copy per
@@ -151,9 +136,6 @@ __device__ __forceinline__ int int4_word_dim(int t, int i) {
   constexpr int NG = Int4Geom<D>::NG, W = D / 32;
   return 64 * (i % NG) + 8 * ((W * t + i) / NG);
 }
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // A lane's own dims of its rows, loaded ahead of their use.
 template <int D, int NT>

@@ -102,6 +102,27 @@ struct PackArgs {
   int key_positions;         // offsets from each block's first key instead of its document's start
 };
 
+// New tokens of a batch's sequences (append_tokens.cu).
+struct AppendArgs {
+  const int32_t* new_lens;    // [B]
+  const int32_t* seq_lens;    // [B] slots in use
+  const int32_t* pos;         // [B] position of the next token
+  const int32_t* tail_start;  // [B] position of the sequence's own first token
+  const int32_t* free_blocks; // [num_free]
+  const int32_t* first_free;  // [1] or null
+  uint32_t* words;            // [B][max_blocks]
+  int32_t* seq_lens_out;      // [B]
+  int32_t* pos_out;           // [B]
+  int32_t* q_start;           // [B]
+  int32_t* cu_rows;           // [B + 1]
+  int32_t* block_indptr;      // [B + 1]
+  int32_t* slots;             // [num_rows]
+  int32_t* local_pos;         // [num_rows] or null
+  unsigned int* status;
+  int B, num_free, num_rows, doc_tokens, max_blocks, id_bits, num_pool_blocks, key_positions;
+  int vec;                    // slots and local_pos are 16-byte aligned
+};
+
 struct PrefillArgs {
   const int32_t* cu_seqlens_q;
   const int32_t* q_start;
@@ -223,6 +244,8 @@ inline int shared_rows_cap(int G, int D) { return (G >= 8 && D == 128) ? 128 : 6
 constexpr int kSharedTcSlots = 2 * 152;
 // The same of the int4 kernel.
 constexpr int kSharedInt4Slots = 4 * 152;
+// And of the kernel for e4m3 codes with block scales.
+constexpr int kSharedFp8BlockSlots = 3 * 152;
 
 // Host planner of the shared-run decode (shared_plan.cu). counts = {items, slots}.
 // chunk_blocks <= 0 picks the chunk from the batch: about auto_items items in all,
@@ -241,6 +264,8 @@ cudaError_t launch_rope_table(float2* table, int head_dim, double theta, const l
 cudaError_t launch_debug_rope(const float2* table, const int32_t* deltas, int n, int head_dim, float2* out,
                               unsigned int* status, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
+// *launches: kernels launched.
+cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st);
 cudaError_t launch_decode_f32(const DecodeArgs& a, bool lazy, cudaStream_t st);
 // alibi: null, or [Hq] ALiBi slopes (key-position words; no rotation).
 cudaError_t launch_decode_bf16(const DecodeArgs& a, const float* alibi, bool lazy, const CUtensorMap& kmap,
@@ -286,15 +311,17 @@ cudaError_t launch_shared_combine(const SharedDecodeArgs& a, cudaStream_t st);
 // kv_dtype: the pools' type (LAZY_F32 and LAZY_BF16 copy); vec: every row is 16-byte aligned.
 cudaError_t launch_cache_write(const CacheWriteArgs& a, int kv_dtype, bool vec, int sms, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadArgs& a, int kv_dtype, int sms, cudaStream_t st);
+// The same for LAZY_FP8_E4M3_BLOCK pools (cache_fp8_block.cu).
+cudaError_t launch_cache_write_fp8_block(const CacheWriteArgs& a, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_cache_read_fp8_block(const CacheReadArgs& a, int sms, cudaStream_t st);
 
-// int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool.
-// A unit is one sequence's blocks for one KV head and tile of `rows` query heads. Each is cut
-// into pieces of equal length, one per CTA, by its own sequence's length; or, where the longest
-// sequence would have pieces of more than 512 blocks (or the table allows it and the batch is
-// large), the units' blocks are laid end to end and cut into equal ranges, one per CTA. Both are
-// settled on the device.
-struct Int4Plan {
-  int rows;            // query heads of a unit: 4, 8 or 16
+// Per-sequence decodes over packed pools (decode_units.cuh). A unit is one sequence's blocks for
+// one KV head and tile of `rows` query heads. Each is cut into pieces of equal length, one per CTA,
+// by its own sequence's length; or, where the longest sequence would have pieces of more than 512
+// blocks (or the table allows it and the batch is large), the units' blocks are laid end to end and
+// cut into equal ranges, one per CTA. Both are settled on the device.
+struct UnitPlan {
+  int rows;            // query heads of a unit
   int units;           // units of a sequence: KV heads x head tiles
   int splits;          // pieces of a unit at most
   int least_log2;      // log2 of the blocks of a piece at least
@@ -302,17 +329,25 @@ struct Int4Plan {
   int64_t range_ctas;  // CTAs that share the batch as ranges; 0: no sequence can be that long
   int64_t parts;       // CTAs that may leave a part of a unit; 0: every unit is one piece, without a join
 };
-struct Int4DecodeArgs : DecodeArgs {
-  Int4Plan plan;
+struct UnitDecodeArgs : DecodeArgs {
+  UnitPlan plan;
   int64_t* prefix;  // with range_ctas: [B + 1] blocks of the sequences before each, and whether ranges were taken
 };
-// num_splits > 0: that many pieces of every unit (fewer of a sequence with fewer blocks); else chosen.
-// sms: the device's.
-Int4Plan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
-size_t decode_int4_workspace_bytes(const Int4Plan& plan, int B, int D);
+// num_splits > 0: that many pieces of every unit (fewer of a sequence with fewer blocks); else chosen
+// for the device's `resident` CTAs.
+UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident);
 // a.ws_o: [2 parts][rows][D], a.ws_ml: [2 parts][rows][2], then a.prefix, where there are parts.
-cudaError_t launch_decode_int4(const Int4DecodeArgs& a, bool lazy, cudaStream_t st);
-cudaError_t launch_combine_int4(const Int4DecodeArgs& a, cudaStream_t st);
+size_t unit_workspace_bytes(const UnitPlan& plan, int B, int D);
+cudaError_t launch_combine_units(const UnitDecodeArgs& a, cudaStream_t st);
+
+// int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool. sms: the device's.
+UnitPlan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
+cudaError_t launch_decode_int4(const UnitDecodeArgs& a, bool lazy, cudaStream_t st);
+// Pools of e4m3 codes with block scales (decode_fp8_block.cu): records of Fp8Geom<D>.
+UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
+cudaError_t launch_decode_fp8_block(const UnitDecodeArgs& a, bool lazy, cudaStream_t st);
+cudaError_t launch_decode_shared_fp8_block(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,
+                                           cudaStream_t st);
 cudaError_t launch_decode_shared_int4(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,
                                       cudaStream_t st);
 

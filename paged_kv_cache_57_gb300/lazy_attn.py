@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 import torch
@@ -24,8 +24,9 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 LAZY_OK, LAZY_ERR_INVALID_ARG, LAZY_ERR_UNSUPPORTED, LAZY_ERR_WORKSPACE, LAZY_ERR_LAYOUT, LAZY_ERR_CUDA, \
     LAZY_ERR_DEVICE = range(7)
-LAZY_F32, LAZY_BF16, LAZY_FP8_E4M3, LAZY_INT4 = 0, 1, 2, 3
-LAZY_DEV_BAD_BLOCK_ID, LAZY_DEV_POS_RANGE, LAZY_DEV_TIMEOUT, LAZY_DEV_LAYOUT, LAZY_DEV_BAD_LEN = 1, 2, 4, 8, 16
+LAZY_F32, LAZY_BF16, LAZY_FP8_E4M3, LAZY_INT4, LAZY_FP8_E4M3_BLOCK = 0, 1, 2, 3, 5
+LAZY_DEV_BAD_BLOCK_ID, LAZY_DEV_POS_RANGE, LAZY_DEV_TIMEOUT, LAZY_DEV_LAYOUT, LAZY_DEV_BAD_LEN, LAZY_DEV_NO_BLOCKS = \
+    1, 2, 4, 8, 16, 32
 BLOCK = 16
 
 EXPORTED = (
@@ -39,6 +40,7 @@ EXPORTED = (
     "lazy_attn_decode_alibi", "lazy_attn_debug_gather_withheld", "lazy_attn_prefill_alibi",
     "lazy_attn_decode_shared_partials", "lazy_attn_decode_shared_combine", "lazy_attn_mixed_workspace_bytes",
     "lazy_attn_mixed", "lazy_attn_pool_record_bytes", "lazy_attn_cache_write", "lazy_attn_cache_read",
+    "lazy_attn_append_tokens",
 )
 PLAN_MAX_MEMBERS = 16
 PLAN_ITEM_BLOCK_IDS = 32
@@ -102,6 +104,7 @@ _sig = {
     "lazy_attn_pool_record_bytes": (_sz, [_P]),
     "lazy_attn_cache_write": (ctypes.c_int, [_P, _vp, _i64, _i64, _vp, _i64, _i64, _i32] + [_vp] * 3 + [_vp]),
     "lazy_attn_cache_read": (ctypes.c_int, [_P, _vp, _vp, _i32] + [_vp] * 3 + [_vp]),
+    "lazy_attn_append_tokens": (ctypes.c_int, [_P] + [_vp] * 5 + [_i32, _vp, _i32, _i32] + [_vp] * 8 + [_vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -122,8 +125,8 @@ def make_params(*, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim:
                 sm_scale: float = 0.0, id_bits: int = 0, num_splits: int = 0, key_positions: bool = False,
                 kv_dtype: Optional[str] = None, k_scale: float = 0.0, v_scale: float = 0.0) -> Params:
     """kv_dtype "fp8_e4m3": pools of e4m3 codes (torch.float8_e4m3fn), values code * k_scale / v_scale.
-    "int4": pools of int4 records (torch.uint8, see empty_pools), which carry their own scales."""
-    kv = 0 if kv_dtype is None else {"fp8_e4m3": LAZY_FP8_E4M3, "int4": LAZY_INT4}[kv_dtype]
+    "int4" and "fp8_e4m3_block": pools of records (torch.uint8, see empty_pools), which carry their own scales."""
+    kv = 0 if kv_dtype is None else {"fp8_e4m3": LAZY_FP8_E4M3, "int4": LAZY_INT4, "fp8_e4m3_block": LAZY_FP8_E4M3_BLOCK}[kv_dtype]
     return Params(num_seqs, num_q_heads, num_kv_heads, head_dim, BLOCK, num_pool_blocks, max_blocks_per_seq,
                   id_bits, LAZY_BF16 if dtype == "bf16" else LAZY_F32, int(bool(lazy)), float(rope_theta),
                   float(sm_scale), num_splits, int(bool(key_positions)), kv, float(k_scale), float(v_scale))
@@ -157,25 +160,29 @@ def _tdt(p: Params):
     return torch.bfloat16 if p.dtype == LAZY_BF16 else torch.float32
 
 
+_RECORDS = (LAZY_INT4, LAZY_FP8_E4M3_BLOCK)  # kinds whose pools are records of bytes
+
+
 def _kvdt(p: Params):
     """torch dtype of the pools."""
-    if p.kv_dtype == LAZY_INT4:
+    if p.kv_dtype in _RECORDS:
         return torch.uint8
     return torch.float8_e4m3fn if p.kv_dtype == LAZY_FP8_E4M3 else _tdt(p)
 
 
 def _cache_pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
     """The pools' pointers, checked: type, device, size."""
-    rows, int4 = p.num_pool_blocks * p.num_kv_heads, p.kv_dtype == LAZY_INT4
-    n, dt = rows * p.head_dim * (9 if int4 else BLOCK), torch.uint8 if int4 else _kvdt(p)
+    rows, kv = p.num_pool_blocks * p.num_kv_heads, p.kv_dtype
+    n = rows * (p.head_dim * 9 if kv == LAZY_INT4 else p.head_dim * BLOCK + (32 if kv == LAZY_FP8_E4M3_BLOCK else 0))
+    dt = torch.uint8 if kv in _RECORDS else _kvdt(p)
     if k_pool.numel() < n or v_pool.numel() < n:
         raise ValueError(f"the pools must hold num_pool_blocks * num_kv_heads records ({n} elements)")
     return _dptr(k_pool, "k_pool", dt), _dptr(v_pool, "v_pool", dt)
 
 
 def _pools(p: Params, k_pool: torch.Tensor, v_pool: torch.Tensor):
-    """The decodes' pools. int4 records are plain bytes, which any uint8 tensor is: their number is checked too."""
-    if p.kv_dtype == LAZY_INT4:
+    """The decodes' pools. Records are plain bytes, which any uint8 tensor is: their number is checked too."""
+    if p.kv_dtype in _RECORDS:
         return _cache_pools(p, k_pool, v_pool)
     return _dptr(k_pool, "k_pool", _kvdt(p)), _dptr(v_pool, "v_pool", _kvdt(p))
 
@@ -277,6 +284,61 @@ def pack_block_words(p: Params, num_docs: int, seg_indptr: torch.Tensor, seg_doc
         _dptr(block_words, "block_words"), _dptr(seq_lens, "seq_lens", i32), _stream(stream))
     _check(rc, "pack_block_words")
     return block_words, seq_lens
+
+
+# ---------------------------------------------------------------- room for new tokens
+
+class AppendTables(NamedTuple):
+    """Outputs of append_tokens, int32 on the device; slots and local_pos have an entry for every row."""
+    seq_lens: torch.Tensor
+    pos: torch.Tensor
+    q_start: torch.Tensor
+    cu_rows: torch.Tensor
+    block_indptr: torch.Tensor
+    slots: torch.Tensor
+    local_pos: torch.Tensor
+
+    @classmethod
+    def empty(cls, p: Params, num_rows: int, device="cuda") -> "AppendTables":
+        """Uninitialised tables for p's sequences and num_rows rows."""
+        b = p.num_seqs
+        return cls(*(torch.empty(n, dtype=torch.int32, device=device) for n in (b, b, b, b + 1, b + 1, num_rows, num_rows)))
+
+
+def append_tokens(p: Params, new_lens: torch.Tensor, seq_lens: torch.Tensor, pos: torch.Tensor, tail_start: torch.Tensor,
+                  free_blocks: torch.Tensor, block_words: torch.Tensor, num_rows: Optional[int] = None,
+                  first_free: Optional[torch.Tensor] = None, doc_tokens: int = 4096, out: Optional[AppendTables] = None,
+                  stream=None) -> AppendTables:
+    """Room for new_lens[s] tokens behind every sequence (lazy_attn_append_tokens): words of the blocks taken from
+    free_blocks into block_words, and lengths, positions, row offsets and slots of num_rows rows (or of ``out``'s), whose
+    seq_lens and pos may be the inputs themselves. ``first_free`` is an earlier call's block_indptr[-1:]."""
+    i32, b = torch.int32, p.num_seqs
+    if out is None:
+        if num_rows is None:
+            raise ValueError("num_rows or out is needed")
+        out = AppendTables.empty(p, num_rows, device=block_words.device)
+    rows = out.slots.numel()
+    if num_rows is not None and num_rows != rows:
+        raise ValueError(f"out has {rows} rows, not {num_rows}")
+    for name, x, n in (("new_lens", new_lens, b), ("seq_lens", seq_lens, b), ("pos", pos, b), ("tail_start", tail_start, b),
+                       ("block_words", block_words, b * p.max_blocks_per_seq), ("out.seq_lens", out.seq_lens, b),
+                       ("out.pos", out.pos, b), ("out.q_start", out.q_start, b), ("out.cu_rows", out.cu_rows, b + 1),
+                       ("out.block_indptr", out.block_indptr, b + 1)):
+        if x.numel() < n:
+            raise ValueError(f"{name} must hold {n} elements")
+    if out.local_pos is not None and out.local_pos.numel() != rows:
+        raise ValueError("out.slots and out.local_pos must have as many rows")
+    if first_free is not None and first_free.numel() != 1:
+        raise ValueError("first_free must hold one element")
+    rc = _lib.lazy_attn_append_tokens(
+        ctypes.byref(p), _dptr(new_lens, "new_lens", i32), _dptr(seq_lens, "seq_lens", i32), _dptr(pos, "pos", i32),
+        _dptr(tail_start, "tail_start", i32), _dptr(free_blocks, "free_blocks", i32), free_blocks.numel(),
+        _dptr(first_free, "first_free", i32), int(doc_tokens), rows, _dptr(block_words, "block_words", i32),
+        _dptr(out.seq_lens, "out.seq_lens", i32), _dptr(out.pos, "out.pos", i32), _dptr(out.q_start, "out.q_start", i32),
+        _dptr(out.cu_rows, "out.cu_rows", i32), _dptr(out.block_indptr, "out.block_indptr", i32),
+        _dptr(out.slots, "out.slots", i32), _dptr(out.local_pos, "out.local_pos", i32), _stream(stream))
+    _check(rc, "append_tokens")
+    return out
 
 
 # ---------------------------------------------------------------- decode / prefill
@@ -496,11 +558,11 @@ def pool_record_bytes(p: Params) -> int:
 
 def empty_pools(p: Params, device="cuda"):
     """Uninitialised (k_pool, v_pool) of p's kind: [num_pool_blocks, Hkv, 16, d], or
-    [num_pool_blocks, Hkv, record] bytes for int4 pools."""
+    [num_pool_blocks, Hkv, record] bytes for pools of records."""
     n = pool_record_bytes(p)
     if n == 0:
         raise LazyAttnError(LAZY_ERR_INVALID_ARG, "empty_pools")
-    tail = (n,) if p.kv_dtype == LAZY_INT4 else (BLOCK, p.head_dim)
+    tail = (n,) if p.kv_dtype in _RECORDS else (BLOCK, p.head_dim)
     return tuple(torch.empty((p.num_pool_blocks, p.num_kv_heads) + tail, dtype=_kvdt(p), device=device)
                  for _ in range(2))
 
