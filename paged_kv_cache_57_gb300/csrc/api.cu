@@ -2,6 +2,7 @@
 // block-word packing, tensor-map encoding, split planning and kernel launches.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -576,7 +577,8 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
   // pools, a length that gives about one item per resident CTA. int4 (8 KV heads, 64-block
   // documents): 136 us against 156 with 32 blocks and 218 with 16; 8 sequences of 256-block
   // documents 45 against 44, 52 with 16, 108 with 256.
-  const int cb = chunk_blocks > 0 ? chunk_blocks : (cap == 128 || kv_records(p) ? 0 : 32);
+  const int most = kv_fp8_block(p) ? lazy::kFp8MaxRun : INT_MAX;
+  const int cb = chunk_blocks > 0 ? std::min(chunk_blocks, most) : (cap == 128 || kv_records(p) ? 0 : 32);
   const int slots = kv_int4(p) ? lazy::kSharedInt4Slots : kv_fp8_block(p) ? lazy::kSharedFp8BlockSlots : lazy::kSharedTcSlots;
   const int auto_items = std::max(1, slots / std::max(1, p->num_kv_heads));
   // small items spread through the launch: measured for the bf16 mma.sync kernel only

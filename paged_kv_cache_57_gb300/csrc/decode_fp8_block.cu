@@ -20,7 +20,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMembers = LAZY_PLAN_MAX_MEMBERS;
 constexpr int kItemInts = LAZY_PLAN_ITEM_INTS;
-constexpr int kShRing = 2;  // stages per warp of a team (shared runs)
 
 // The n threads of team t meet (barrier 0 is the CTA's).
 __device__ __forceinline__ void team_sync(int t, int n) { asm volatile("bar.sync %0, %1;" ::"r"(t + 1), "r"(n) : "memory"); }
@@ -29,11 +28,11 @@ template <int D, int NT, int HL>
 struct Fp8Cfg {
   static constexpr int ROWS = Fp8Rows<NT, HL>::ALL;  // of a warp
   static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
-  static constexpr int SLOT = Fp8Loader<D>::STAGE;
-  static constexpr int CTAS = NT == 1 ? 4 : 3;  // per SM
-  static constexpr int RING = 2;                // stages per warp of a team
-  static constexpr int BUF = kWarps * RING * SLOT > kWarps * ROWS * RED * 4 ? kWarps * RING * SLOT : kWarps * ROWS * RED * 4;
-  static constexpr int KEPT = fp8_kept_floats<D, NT, HL>();  // per warp (fp8_block.cuh)
+  static constexpr int SLOT = Fp8Loader<D>::STAGE;   // one block
+  static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // per SM
+  static constexpr int RING = NT == 4 ? 4 : 2;  // stages per warp of a team
+  static constexpr int SLOTS = kWarps * RING;
+  static constexpr int BUF = SLOTS * SLOT > kWarps * ROWS * RED * 4 ? SLOTS * SLOT : kWarps * ROWS * RED * 4;
 };
 
 }  // namespace
@@ -68,15 +67,13 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     const int m_pos = a.q_pos[s];
     const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
 
-    Fp8QueryRows<NT> rows;
+    const int row0 = rt * C::ROWS + (HL == 1 ? lane >> 3 : lane >> 2);  // the lane's first row, the others 8 on
+    const __nv_bfloat16* q_first = static_cast<const __nv_bfloat16*>(a.q) + q0 * D;
+    auto row = [&](int nt) { return q_first + (row0 + 8 * nt < heads ? row0 + 8 * nt : 0) * D; };
     bool live[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = rt * C::ROWS + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2));
-      live[nt] = r < heads;
-      rows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) + (q0 + (live[nt] ? r : 0)) * D;
-    }
-    const Fp8RawRows<D, NT> raw(rows, lane);  // loads that nothing waits for yet
+    for (int nt = 0; nt < NT; ++nt) live[nt] = row0 + 8 * nt < heads;
+    const Fp8RawRows<D, NT> raw(row, lane);  // loads that nothing waits for yet
     float2 rate[HALF / 32];
 #pragma unroll
     for (int j = 0; j < HALF / 32; ++j) rate[j] = a.rope[lane + 32 * j];
@@ -108,23 +105,24 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     describe(0);
     load_words(32);
     if (RT > 1) team_sync(team, 32 * RT);
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      if (i < nk && i % RT == rt) load(ring + i * C::SLOT, d_blk[team][i].x, lane);
+    auto load_block = [&](int j) {  // the warp's turn or not, one group
+      if (j < nk && j % RT == rt) load(ring + j % R * C::SLOT, d_blk[team][j & 63].x, lane);
       cp_async_commit();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load_block(i);
 
     // ------------------------------------------------------------ queries
-    fp8_scale_rows<D, NT>(rows, raw, live, a.scale_log2);
-    float2* cs = cs_all + warp * HALF;
-    float* kept = reinterpret_cast<float*>(cs_all + kWarps * HALF) + warp * C::KEPT;
     Fp8Query<D, NT, HL> q;
+    float mul[NT];
+    fp8_scale_rows<D, NT, HL>(q, mul, raw, live, a.scale_log2, lane);
+    float2* cs = cs_all + warp * HALF;
     auto rebuild = [&](int delta) {
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < HALF / 32; ++j) cs[lane + 32 * j] = rope_cs(rate[j], delta, a.status);
       __syncwarp();
-      fp8_build_query<D, NT, HL>(q, rows, lane, [&](int) { return cs; });
+      fp8_build_query<D, NT, HL>(q, mul, row, lane, [&](int) { return cs; });
     };
     // Rotated while the first records are on their way. Control: the pool holds absolute-position keys.
     int p_cur = 0;  // the document that q is rotated for
@@ -137,30 +135,29 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     Fp8State<D, NT, HL> st;
     fp8_init(st);
     for (int i = 0; i < nk; ++i) {
-      // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all
-      // of whose warps are done with block i - 1, whose stage is refilled.
+      // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all of
+      // whose warps are done with block i - 1, whose stage is refilled.
       cp_async_wait<AHEAD - 1>();
       if (RT == 1) __syncwarp();
       else team_sync(team, 32 * RT);
-      if ((i & 31) == 0) {
-        if (i + 32 < nk) {  // a chunk of words ahead, over the one that all are done with
-          describe(i + 32);
-          load_words(i + 64);
+      if ((i & 31) == 0 && i + 32 < nk) {  // a chunk of words ahead, over the one that all are done with
+        describe(i + 32);
+        load_words(i + 64);
+      }
+      load_block(i + AHEAD);
+      const uint8_t* stage[1] = {ring_p + i % R * C::SLOT};
+      const int info = d_blk[team][i & 63].y;
+      int nv[1] = {kBlock};
+      if (info != kBlock) {
+        nv[0] = info & 31;
+        if (nv[0] == 0) continue;  // the same for the whole team
+        if (LAZY && info > kNewDoc) {
+          const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
+          if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
         }
-        if (i > 0 && i % kFp8Flush == 0) fp8_flush(st, kept, i > kFp8Flush, lane);
       }
-      const int j = i + AHEAD;
-      if (j < nk && j % RT == rt) load(ring + (j % R) * C::SLOT, d_blk[team][j & 63].x, lane);
-      cp_async_commit();  // a group a step, empty where another warp loads
-      const int info = d_blk[team][i & 63].y, nv = info & 31;
-      if (nv == 0) continue;  // the same for the whole team
-      if (LAZY && info >= kNewDoc) {
-        const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
-        if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
-      }
-      fp8_attend<D, NT, HL>(ring_p + (i % R) * C::SLOT, nv, q, st, lane, i >= kFp8Flush ? kept : nullptr);
+      fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
     }
-    if (nk > kFp8Flush) fp8_unflush(st, kept, lane);
     fp8_finish(st);
     cp_async_wait<0>();
     __syncthreads();  // every team is done with its ring: the merge takes its place
@@ -204,12 +201,10 @@ struct Fp8SharedCfg {
   static constexpr int SLOT = Fp8Loader<D>::STAGE;
   static constexpr int ROWS = 2 * kWarps * 8;  // of a CTA
   static constexpr int RED = D + 4;            // merge rows: o[D], m, l
-  static constexpr int STAGES = kShRing * kWarps;
-  static constexpr int BUF = STAGES * SLOT > ROWS * RED * 4 ? STAGES * SLOT : ROWS * RED * 4;
-  // the members' angles, then, once the queries are built, the warps' kept sums (fp8_block.cuh)
-  static constexpr int ANGLES = kMembers * (D / 2) * 8;
-  static constexpr int KEPT = kWarps * fp8_kept_floats<D, 2, 2>() * 4;
-  static constexpr int SMEM = BUF + (ANGLES > KEPT ? ANGLES : KEPT);
+  static constexpr int NB = 2;      // blocks of a step
+  static constexpr int STEPS = 8;   // in the teams' rings
+  static constexpr int BUF = STEPS * NB * SLOT > ROWS * RED * 4 ? STEPS * NB * SLOT : ROWS * RED * 4;
+  static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;  // and the members' angles
 };
 
 // What the CTA's warps share of an item.
@@ -226,18 +221,20 @@ template <int D, int NT, int HL, bool LAZY>
 __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
                                                 Fp8Item& it, uint8_t* smem, float2* cs_tab, int kvh, int rows, int RT) {
   using C = Fp8SharedCfg<D>;
-  constexpr int HALF = D / 2, TILE = Fp8Rows<NT, HL>::ALL;
-  const int TEAMS = kWarps / RT, R = C::STAGES / TEAMS, AHEAD = R - 1;  // R = 2, 4 or 8
+  constexpr int HALF = D / 2, TILE = Fp8Rows<NT, HL>::ALL, NB = C::NB;
+  const int TEAMS = kWarps / RT, R = C::STEPS / TEAMS, AHEAD = R - 1;  // R = 2, 4 or 8
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / RT, rt = warp & (RT - 1);
   const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3];
 
   // ------------------------------------------------------------ first loads
-  const int per_team = (nblk + TEAMS - 1) / TEAMS;
+  // parts of whole steps
+  const int per_team = (nblk + NB * TEAMS - 1) / (NB * TEAMS) * NB;
   const int kb0 = team * per_team;
   const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
+  const int ns = (nk + NB - 1) / NB;                       // steps
   const Fp8Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
-  const uint8_t* ring_p = smem + team * R * C::SLOT;
+  const uint8_t* ring_p = smem + team * R * NB * C::SLOT;
   const uint32_t ring = smem_u32(ring_p);
   const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
   const uint32_t id_mask = (1u << a.id_bits) - 1u;
@@ -267,25 +264,27 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
   };
   load_words(0);
   // First loads straight from the record's ids when it names all of them.
-  const bool rec_first = kb0 + min(AHEAD, nk) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
-  if (rec_first) {
-    for (int i = 0; i < AHEAD; ++i) {
-      if (i < nk && (i & (RT - 1)) == rt) {
-        const int id = ids[kb0 + i];
-        load(ring + i * C::SLOT, id >= 0 && id < a.num_pool_blocks ? id : 0, lane);
-      }
-      cp_async_commit();
+  const bool rec_first = kb0 + min(NB * AHEAD, nk) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
+  auto load_step = [&](int j, auto id_of) {  // the warp's share of a step's blocks, as one group
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int k = NB * j + b;
+      if (k < nk && (k & (RT - 1)) == rt) load(ring + (k & (R * NB - 1)) * C::SLOT, id_of(k), lane);
     }
-  }
+    cp_async_commit();
+  };
+  auto described = [&](int k) { return it.d_blk[team][k & 63].x; };
+  if (rec_first)
+    for (int i = 0; i < AHEAD; ++i)
+      load_step(i, [&](int k) {
+        const int id = ids[kb0 + k];
+        return id >= 0 && id < a.num_pool_blocks ? id : 0;
+      });
   describe(0);
   load_words(32);
   if (RT > 1) team_sync(team, 32 * RT);
-  if (!rec_first) {
-    for (int i = 0; i < AHEAD; ++i) {
-      if (i < nk && (i & (RT - 1)) == rt) load(ring + i * C::SLOT, it.d_blk[team][i].x, lane);
-      cp_async_commit();
-    }
-  }
+  if (!rec_first)
+    for (int i = 0; i < AHEAD; ++i) load_step(i, described);
 
   // ------------------------------------------------------------ members
   const int nmem = it.rec[4];
@@ -311,7 +310,7 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
   // ------------------------------------------------------------ queries
   auto mem_seq = [&](int m) { return it.rec[8 + 4 * m]; };
   auto mem_slot = [&](int m) { return it.rec[8 + 4 * m + 2]; };
-  Fp8QueryRows<NT> qrows;
+  const __nv_bfloat16* qrow[NT];
   bool live[NT];
   int mem[NT];
 #pragma unroll
@@ -319,41 +318,44 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
     const int r = rt * TILE + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2)), rc = r < rows ? r : 0;
     mem[nt] = rc / a.G;
     live[nt] = r < rows && it.ok[mem[nt]];
-    qrows.q[nt] = static_cast<const __nv_bfloat16*>(a.q) +
-                  ((live[nt] ? (size_t)mem_seq(mem[nt]) * a.Hq + (rc - mem[nt] * a.G) : 0) + (size_t)kvh * a.G) * D;
+    qrow[nt] = static_cast<const __nv_bfloat16*>(a.q) +
+               ((live[nt] ? (size_t)mem_seq(mem[nt]) * a.Hq + (rc - mem[nt] * a.G) : 0) + (size_t)kvh * a.G) * D;
   }
-  fp8_scale_rows<D, NT>(qrows, Fp8RawRows<D, NT>(qrows, lane), live, a.scale_log2);
   Fp8Query<D, NT, HL> q;
-  fp8_build_query<D, NT, HL>(q, qrows, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
+  float mul[NT];
+  auto row = [&](int nt) { return qrow[nt]; };
+  fp8_scale_rows<D, NT, HL>(q, mul, Fp8RawRows<D, NT>(row, lane), live, a.scale_log2, lane);
+  fp8_build_query<D, NT, HL>(q, mul, row, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
 
   // ------------------------------------------------------------ main loop
-  float* kept = reinterpret_cast<float*>(cs_tab) + warp * fp8_kept_floats<D, NT, HL>();
-  if (per_team > kFp8Flush) __syncthreads();  // sums will be kept where the angles were
   Fp8State<D, NT, HL> st;
   fp8_init(st);
-  for (int i = 0; i < nk; ++i) {
-    // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all of
-    // whose warps are done with block i - 1, whose stage is refilled.
+  for (int i = 0; i < ns; ++i) {
+    // Step i has landed for the warps that loaded it and, behind the barrier, for the team, all of
+    // whose warps are done with step i - 1, whose stages are refilled.
     if (RT == 1) {
-      cp_async_wait<kShRing - 2>();
+      cp_async_wait<C::STEPS / 4 - 2>();
       __syncwarp();
     } else {
-      if (RT == 2) cp_async_wait<2 * kShRing - 2>();
-      else cp_async_wait<4 * kShRing - 2>();
+      if (RT == 2) cp_async_wait<C::STEPS / 2 - 2>();
+      else cp_async_wait<C::STEPS - 2>();
       team_sync(team, 32 * RT);
     }
-    if ((i & 31) == 0) {  // a chunk of words ahead, over the one that all are done with
-      describe(i + 32);
-      load_words(i + 64);
-      if (i > 0 && i % kFp8Flush == 0) fp8_flush(st, kept, i > kFp8Flush, lane);
+    const int k0 = NB * i;
+    if ((k0 & 31) == 0) {  // a chunk of words ahead, over the one that all are done with
+      describe(k0 + 32);
+      load_words(k0 + 64);
     }
-    const int n = i + AHEAD;
-    if (n < nk && (n & (RT - 1)) == rt) load(ring + (n & (R - 1)) * C::SLOT, it.d_blk[team][n & 63].x, lane);
-    cp_async_commit();  // a group a step, empty where another warp loads
-    const int nv = it.d_blk[team][i & 63].y;
-    if (nv > 0) fp8_attend<D, NT, HL>(ring_p + (i & (R - 1)) * C::SLOT, nv, q, st, lane, i >= kFp8Flush ? kept : nullptr);
+    load_step(i + AHEAD, described);
+    const uint8_t* stage[NB];
+    int nv[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      stage[b] = ring_p + ((k0 + b) & (R * NB - 1)) * C::SLOT;
+      nv[b] = it.d_blk[team][(k0 + b) & 63].y;
+    }
+    if (nv[0] > 0 || nv[NB - 1] > 0) fp8_attend<D, NT, HL, NB>(stage, nv, q, st, lane);
   }
-  if (nk > kFp8Flush) fp8_unflush(st, kept, lane);
   fp8_finish(st);
   cp_async_wait<0>();
   __syncthreads();  // every team is done with its ring: the merge takes its place
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(co
   __syncthreads();
   const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3], nmem = it.rec[4];
   const bool item_ok = src >= 0 && src < a.B && b0 >= 0 && nblk >= 1 && nblk <= a.max_blocks - b0 &&
-                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= C::ROWS;
+                       last_nv >= 1 && last_nv <= kBlock && nmem >= 1 && nmem <= kMembers && nmem * a.G <= C::ROWS && nblk <= kFp8MaxRun;
   if (!item_ok) {  // uniform over the CTA: nothing is loaded or written
     if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
     return;
@@ -420,14 +422,15 @@ __global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(co
 UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
   int rows = 4;
   while (rows < G && rows < 64) rows *= 2;
-  const int per_sm = rows < 16 ? Fp8Cfg<128, 1, 1>::CTAS : Fp8Cfg<128, 2, 2>::CTAS;
-  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm);
+  const int per_sm = rows <= 8 ? Fp8Cfg<128, 1, 1>::CTAS : Fp8Cfg<128, 2, 2>::CTAS;
+  const int teams = rows <= 16 ? 4 : 64 / rows;
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm, teams * kFp8MaxRun);
 }
 
 template <int D, int NT, int HL, int RT, bool LAZY>
 static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
   using C = Fp8Cfg<D, NT, HL>;
-  constexpr int SMEM = C::BUF + kWarps * (D / 2) * 8 + kWarps * C::KEPT * 4;
+  constexpr int SMEM = C::BUF + kWarps * (D / 2) * 8;
   cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, RT, LAZY>>(SMEM);
   if (e != cudaSuccess) return e;
   return launch_behind(decode_fp8_block_kernel<D, NT, HL, RT, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_units_kernel(const
   }
 }
 
-UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident) {
+UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident, int most) {
   UnitPlan p{};
   p.rows = rows;
   p.units = units;
@@ -151,10 +151,11 @@ UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, 
   p.least_log2 = num_splits > 0 ? 0 : kMinPieceLog2;
   p.splits = num_splits > 0 ? std::min(num_splits, mb)
                             : (int)std::max<int64_t>(1, std::min<int64_t>(resident / all, mb >> kMinPieceLog2));
+  if (num_splits > 0) p.splits = (int)std::max<int64_t>(p.splits, ((int64_t)mb + most - 1) / most);  // (else kMaxPiece or a range)
   p.ctas = all * p.splits;
   p.parts = p.splits > 1 ? p.ctas : 0;
   if (num_splits <= 0 && mb > kMaxPiece * p.splits) {
-    p.range_ctas = std::min<int64_t>((all * mb + kMinChunk - 1) / kMinChunk, resident);
+    p.range_ctas = std::max(std::min<int64_t>((all * mb + kMinChunk - 1) / kMinChunk, resident), (all * mb + most - 1) / most);
     p.ctas = B > kMaxLook ? p.range_ctas : std::max(p.ctas, p.range_ctas);
     p.parts = std::max(p.parts, p.range_ctas);
   }

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "decode_block.cuh"
+#include "kernels.h"
 
 namespace lazy {
 
@@ -54,12 +55,14 @@ struct Fp8Loader {
 
   // Block ph (inside the pool) to the stage at shared address `dst`.
   __device__ __forceinline__ void operator()(uint32_t dst, int ph, int lane) const {
-    const size_t off = (size_t)(uint32_t)ph * blk_bytes;
+    const uint8_t* kb = k + (uint64_t)(uint32_t)ph * blk_bytes;
+    const uint8_t* vb = v + (uint64_t)(uint32_t)ph * blk_bytes;
+    dst += 16 * lane;
 #pragma unroll
-    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + 16 * lane + 512 * c, k + off + 512 * c);
+    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + 512 * c, kb + 512 * c);
 #pragma unroll
-    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + 16 * lane + G::CODES + 512 * c, v + off + 512 * c);
-    if (lane < 2) cp_async4(dst + SCALES + 4 * lane, scale + off);
+    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + G::CODES + 512 * c, vb + 512 * c);
+    if (lane < 2) cp_async4(dst + SCALES - 12 * lane, scale + (uint64_t)(uint32_t)ph * blk_bytes);
   }
 };
 
@@ -82,31 +85,28 @@ struct Fp8Query {
   float f[NT][HL];
 };
 
-// The rows of the queries (bf16) that a lane reads, row 8 nt + g (or g / 2), with the factor that
-// scales them (softmax scale, log2 e, and over the row's power of two `pow2`, so that the largest
-// value is in 1..2; 0 for a row that is not there, whose pointer is another's).
-template <int NT>
-struct Fp8QueryRows {
-  const __nv_bfloat16* q[NT];
-  float mul[NT], pow2[NT];
-};
+// A lane reads the query rows (bf16) of the columns g of its tiles, row 8 nt + g (or g / 2); row(nt) points
+// at one (where there is none, at another). A row is scaled by mul: softmax scale and log2 e, over the row's power of
+// two, so that the largest value is in 1..2; 0 for a row that is not there.
 
 // A lane's own dims of its rows, loaded ahead of their use.
 template <int D, int NT>
 struct Fp8RawRows {
   uint4 x[NT][D / 32];
-  __device__ __forceinline__ explicit Fp8RawRows(const Fp8QueryRows<NT>& r, int lane) {
+  template <typename RowFn>
+  __device__ __forceinline__ Fp8RawRows(RowFn row, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        x[nt][i] = *reinterpret_cast<const uint4*>(r.q[nt] + 64 * (i / 2) + 16 * (lane & 3) + 8 * (i % 2));
+        x[nt][i] = *reinterpret_cast<const uint4*>(row(nt) + 64 * (i / 2) + 16 * (lane & 3) + 8 * (i % 2));
   }
 };
 
-// Fills mul and pow2 from the rows' values (all lanes).
-template <int D, int NT>
-__device__ __forceinline__ void fp8_scale_rows(Fp8QueryRows<NT>& r, const Fp8RawRows<D, NT>& raw, const bool (&live)[NT], float scale) {
+// Fills mul and q.f from the rows' values (all lanes).
+template <int D, int NT, int HL>
+__device__ __forceinline__ void fp8_scale_rows(Fp8Query<D, NT, HL>& q, float (&mul)[NT], const Fp8RawRows<D, NT>& raw,
+                                               const bool (&live)[NT], float scale, int lane) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     uint32_t mx = 0u;  // |bf16| compares as its bits
@@ -119,53 +119,55 @@ __device__ __forceinline__ void fp8_scale_rows(Fp8QueryRows<NT>& r, const Fp8Raw
     mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float m = fmaxf(bf16_lo(mx), bf16_hi(mx)) * scale;
     const uint32_t ex = min(max(__float_as_uint(m) >> 23, 27u), 227u);  // 2^(+-100)
-    r.pow2[nt] = __uint_as_float(ex << 23);
-    r.mul[nt] = live[nt] ? scale * __uint_as_float((254u - ex) << 23) : 0.f;
+    mul[nt] = live[nt] ? scale * __uint_as_float((254u - ex) << 23) : 0.f;
+#pragma unroll
+    for (int c = 0; c < HL; ++c)  // a lane of column 2t + c
+      q.f[nt][c] = __shfl_sync(0xffffffffu, __uint_as_float(ex << 23), 8 * (lane & 3) + 4 * c);
   }
 }
 
 // Rotates the rows by their angles: cs(nt) points at the (cos, sin) of the lane's row (shared
 // memory, 16-byte aligned). The rounding to f16 is off by 2^-11 of an operand.
-template <int D, int NT, int HL, typename CsFn>
-__device__ __forceinline__ void fp8_build_query(Fp8Query<D, NT, HL>& q, const Fp8QueryRows<NT>& rows, int lane, CsFn cs) {
+template <int D, int NT, int HL, typename RowFn, typename CsFn>
+__device__ __forceinline__ void fp8_build_query(Fp8Query<D, NT, HL>& q, const float (&mul)[NT], RowFn row, int lane, CsFn cs) {
   constexpr int HALF = D / 2;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2* ang = cs(nt);
-    const float mul = rows.mul[nt];
+    const __nv_bfloat16* src = row(nt);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       asm volatile("" ::: "memory");  // eight dims' loads at a time: registers
       const int base = 64 * (i / 2) + 16 * t + 8 * (i % 2);
       const float sgn = base < HALF ? -1.f : 1.f;
-      const uint4 x4 = *reinterpret_cast<const uint4*>(rows.q[nt] + base);
-      const uint4 y4 = *reinterpret_cast<const uint4*>(rows.q[nt] + (base ^ HALF));
+      const uint4 x4 = *reinterpret_cast<const uint4*>(src + base);
+      const uint4 y4 = *reinterpret_cast<const uint4*>(src + (base ^ HALF));
       const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const float4 c = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 2 * h);
-        const uint32_t b = pack_f16x2(fmaf(bf16_lo(x[h]), c.x, bf16_lo(y[h]) * (sgn * c.y)) * mul,
-                                      fmaf(bf16_hi(x[h]), c.z, bf16_hi(y[h]) * (sgn * c.w)) * mul);
+        const uint32_t b = pack_f16x2(fmaf(bf16_lo(x[h]), c.x, bf16_lo(y[h]) * (sgn * c.y)) * mul[nt],
+                                      fmaf(bf16_hi(x[h]), c.z, bf16_hi(y[h]) * (sgn * c.w)) * mul[nt]);
         q.b[nt][2 * i + h / 2][h % 2] = HL == 1 && (g & 1) ? 0u : b;
       }
     }
-#pragma unroll
-    for (int c = 0; c < HL; ++c) q.f[nt][c] = __shfl_sync(0xffffffffu, rows.pow2[nt], 8 * t + 4 * c);  // a lane of column 2t + c
   }
 }
 
-// Running state: per row the reference maximum as -m (log2 units; 0 before the first key) and
-// `top`, the score that refreshes it, the weight sum l (partial over the lanes of equal t until
-// fp8_finish), and O^T: o[i][nt] is product i's columns 2t, 2t + 1 for the dim 8 g + i in [0], [1] and
-// for 64 + 8 g + i (d = 64: 8 g + 4 + i) in [2], [3]. Weights times V's scale go to f16 over `inv`'s power of two,
-// which follows the scales as they grow: the largest scale is 2^4 then, at most 2^7 before
-// the reference moves, and weights at most 2^8. What f16 has below is for the long tails: a
-// weight keeps its 11 bits from 2^-18 of the largest scale, and is off by 2^-29 of that below.
+// Running state: per row nm, which puts a score s (log2 units) at a weight of 2^(s + nm) -- 2^kFp8Lift for the greatest
+// score when nm was set, at most 2^kFp8Most until it is set anew; +inf before the first key -- and the
+// weight sum l (partial over the lanes of equal t until fp8_finish), and O^T: o[i][nt] is product i's
+// columns 2t, 2t + 1 for the dim 8 g + i in [0], [1] and for 64 + 8 g + i (d = 64: 8 g + 4 + i) in
+// [2], [3]. Weights and V's scale over the power of two 1 / inv meet as f16: `inv` follows the scales as they
+// grow, the largest is 1 then, at most kFp8ScaleTop before the reference moves. What f16 has below
+// is for the long tails: a weight keeps its 11 bits from 2^-18 of the largest, and is off by 2^-29
+// of that (times the largest V scale) below.
+constexpr float kFp8Lift = 4.f, kFp8Most = 12.f, kFp8ScaleTop = 8.f;
 template <int D, int NT, int HL>
 struct Fp8State {
   float o[D / 16][NT][4];
-  float neg_m[NT][HL], top[NT][HL], l[NT][HL];
+  float nm[NT][HL], l[NT][HL];
   float inv, lim;  // the same in all lanes; a scale above lim moves the reference
 };
 
@@ -177,8 +179,7 @@ __device__ __forceinline__ void fp8_init(Fp8State<D, NT, HL>& st) {
     for (int i = 0; i < D / 16; ++i) st.o[i][nt][0] = st.o[i][nt][1] = st.o[i][nt][2] = st.o[i][nt][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < HL; ++c) {
-      st.neg_m[nt][c] = 0.f;
-      st.top[nt][c] = -INFINITY;
+      st.nm[nt][c] = INFINITY;
       st.l[nt][c] = 0.f;
     }
   }
@@ -186,109 +187,105 @@ __device__ __forceinline__ void fp8_init(Fp8State<D, NT, HL>& st) {
   st.lim = 0.f;
 }
 
-// The products truncate their running sums (2^-24 each time, always towards zero): 2^-13 of a
-// sum after 2048 blocks, next to the output's rounding of 2^-9. Longer runs move the sums to
-// shared memory, where they are added up by rounding additions, every kFp8Flush blocks: `kept`
-// is the warp's area, value n of lane l at 32 n + l (with HL = 1 only the columns that count).
-constexpr int kFp8Flush = 2048;
-template <int D, int NT, int HL>
-constexpr int fp8_kept_floats() { return 32 * (D / 16) * NT * 2 * HL; }
+// The products truncate their running sums (2^-24 each time, always towards zero): after
+// kFp8MaxRun = 16384 blocks a sum is off by 2^-11 or so of its size, a quarter of the output's
+// rounding. No warp sums more: pieces, ranges and items are cut there.
 
-// f(n, nt, c, o): value n of the kept ones, its row and its running sum.
-template <int D, int NT, int HL, typename Fn>
-__device__ __forceinline__ void fp8_each_kept(Fp8State<D, NT, HL>& st, Fn f) {
+// NB blocks of one document in ring stages: the first nv[b] slots of block b are keys (0 .. 16, the
+// same in all lanes; 0: the block is not there); what the others hold does not matter.
+template <int D, int NT, int HL, int NB>
+__device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], const int (&nv)[NB], const Fp8Query<D, NT, HL>& q,
+                                           Fp8State<D, NT, HL>& st, int lane) {
+  using G = Fp8Geom<D>;
+  const int g = lane >> 2, t = lane & 3;
+  bool partial = false;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
+  for (int b = 0; b < NB; ++b) partial |= nv[b] < kBlock;
+  float2 scale[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) scale[b] = *reinterpret_cast<const float2*>(stage[b] + Fp8Loader<D>::SCALES);
+
+  // Scores of keys g and g + 8 of each block over f[block]: p[block][tile][2 key + row]. The blocks' and
+  // tiles' products take turns, so that none waits for the one before it (one of each: even and odd
+  // ones).
+  constexpr int CH = NB * NT == 1 ? 2 : 1;
+  float p[NB][NT][4];
+  {
+    float odd[4];
+#pragma unroll
+    for (int jh = 0; jh < G::NG; ++jh) {
+      uint32_t x[NB][2][4];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 v = reinterpret_cast<const uint4*>(stage[b])[lane + 64 * jh + 32 * r];
+          x[b][r][0] = v.x, x[b][r][1] = v.y, x[b][r][2] = v.z, x[b][r][3] = v.w;
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t a[4];
+          e4m3x4_to_f16x4(x[b][0][i], a[0], a[2]);
+          e4m3x4_to_f16x4(x[b][1][i], a[1], a[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t* k = q.b[nt][4 * jh + i];
+            float(&sum)[4] = CH == 2 && i % 2 ? odd : p[b][nt];
+            if (jh == 0 && i < CH) mma_16816_f16_first(sum, a, k[0], k[1]);
+            else mma_16816_f16(sum, a, k[0], k[1]);
+          }
+        }
+    }
+    if (CH == 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[0][0][e] += odd[e];
+  }
+  float f[NB][NT][HL];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int c = 0; c < HL; ++c) f[b][nt][c] = q.f[nt][c] * scale[b].x;
+  if (partial) {
+    asm volatile("" ::: "memory");  // a branch, not selects on every block
 #pragma unroll
-        for (int c = 0; c < HL; ++c) f(((i * NT + nt) * 2 + r) * HL + c, nt, c, st.o[i][nt][2 * r + c]);
-}
-
-// Moves the running sums to the kept ones (which are there already: `again`).
-template <int D, int NT, int HL>
-__device__ __forceinline__ void fp8_flush(Fp8State<D, NT, HL>& st, float* kept, bool again, int lane) {
-  fp8_each_kept<D, NT, HL>(st, [&](int n, int, int, float& o) {
-    float* k = kept + 32 * n + lane;
-    *k = again ? *k + o : o;
-    o = 0.f;
-  });
-}
-
-// And back, at the end.
-template <int D, int NT, int HL>
-__device__ __forceinline__ void fp8_unflush(Fp8State<D, NT, HL>& st, const float* kept, int lane) {
-  fp8_each_kept<D, NT, HL>(st, [&](int n, int, int, float& o) { o += kept[32 * n + lane]; });
-}
-
-constexpr float kFp8RescaleLog2 = 8.f;  // a maximum is refreshed when it grows by more
-constexpr float kFp8ScaleTop = 128.f;   // the V scales' reference moves when one times inv is more
-
-// One block in a ring stage: its first nv slots are keys (1 .. 16, the same in all lanes); what
-// the others hold does not matter. `kept`: sums moved out of the state, to be rescaled with it (null: none).
-template <int D, int NT, int HL>
-__device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const Fp8Query<D, NT, HL>& q, Fp8State<D, NT, HL>& st,
-                                           int lane, float* kept) {
-  using G = Fp8Geom<D>;
-  const int g = lane >> 2, t = lane & 3;
-  const uint4* codes = reinterpret_cast<const uint4*>(stage) + lane;
-  const float2 scale = *reinterpret_cast<const float2*>(stage + Fp8Loader<D>::SCALES);
-
-  // Scores of keys g and g + 8, in log2 units: p[key][tile][row].
-  float acc[NT][4], p[2][NT][HL];
-#pragma unroll
-  for (int jh = 0; jh < G::NG; ++jh) {
-    const uint4 x4 = codes[64 * jh], y4 = codes[64 * jh + 32];
-    const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-      e4m3x4_to_f16x4(x[i], a[0], a[2]);
-      e4m3x4_to_f16x4(y[i], a[1], a[3]);
+    for (int b = 0; b < NB; ++b) {
+      if (nv[b] == 0) scale[b] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (jh == 0 && i == 0) mma_16816_f16_first(acc[nt], a, q.b[nt][0][0], q.b[nt][0][1]);
-        else mma_16816_f16(acc[nt], a, q.b[nt][4 * jh + i][0], q.b[nt][4 * jh + i][1]);
+#pragma unroll
+        for (int c = 0; c < HL; ++c) f[b][nt][c] = fmaxf(q.f[nt][c] * scale[b].x, 0x1p-126f);  // -inf stays -inf
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g + 8 * (e / 2) >= nv[b]) p[b][nt][e] = -INFINITY;
       }
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < HL; ++c) {
-      const float f = q.f[nt][c] * scale.x;
-      p[0][nt][c] = acc[nt][c] * f;
-      p[1][nt][c] = acc[nt][2 + c] * f;
-    }
-  if (nv < kBlock) {
-    asm volatile("" ::: "memory");  // a branch, not selects on every block
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < HL; ++c)
-          if (g + 8 * r >= nv) p[r][nt][c] = -INFINITY;
-  }
 
-  // Running maximum and V-scale reference: refreshed together, when some row's maximum or the
-  // scale outgrew its reference (a vote; the cross-lane maxima only then).
-  float mx[NT][HL];
-  bool grow = scale.y > st.lim;
+  // Maxima and the V-scale reference: refreshed together, when some row's weight or a scale would outgrow
+  // its reference (a vote; the cross-lane maxima only then).
+  float sm = scale[0].y;
+#pragma unroll
+  for (int b = 1; b < NB; ++b) sm = fmaxf(sm, scale[b].y);
+  bool grow = sm > st.lim;
+  auto top = [&](int nt, int c) {  // the lane's greatest score, over 2^-nm
+    float x = fmaf(fmaxf(p[0][nt][c], p[0][nt][2 + c]), f[0][nt][c], st.nm[nt][c]);
+#pragma unroll
+    for (int b = 1; b < NB; ++b) x = fmaxf(x, fmaf(fmaxf(p[b][nt][c], p[b][nt][2 + c]), f[b][nt][c], st.nm[nt][c]));
+    return x;
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < HL; ++c) {
-      mx[nt][c] = fmaxf(p[0][nt][c], p[1][nt][c]);
-      grow |= mx[nt][c] > st.top[nt][c];
-    }
+    for (int c = 0; c < HL; ++c) grow |= top(nt, c) > kFp8Most;
   if (__any_sync(0xffffffffu, grow)) {
-    if (scale.y > st.lim) {
-      // 2^(4 - e) for a scale 2^e. Kept a normal number.
-      const uint32_t ex = min(max(__float_as_uint(scale.y) >> 23, 8u), 252u);
-      const float inv = __uint_as_float((258u - ex) << 23), r = inv / st.inv;
+    if (sm > st.lim) {
+      // 2^-e for a scale 2^e. Kept a normal number.
+      const uint32_t ex = min(max(__float_as_uint(sm) >> 23, 4u), 250u);
+      const float inv = __uint_as_float((254u - ex) << 23), r = inv / st.inv;
       st.inv = inv;
       st.lim = kFp8ScaleTop / inv;
 #pragma unroll
@@ -297,80 +294,83 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const F
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) st.o[i][nt][e] *= r;
-      if (kept) fp8_each_kept<D, NT, HL>(st, [&](int n, int, int, float&) { kept[32 * n + lane] *= r; });
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < HL; ++c) {
-        float x = mx[nt][c];
+        float x = fmaxf(p[0][nt][c], p[0][nt][2 + c]) * f[0][nt][c];
+#pragma unroll
+        for (int b = 1; b < NB; ++b) x = fmaxf(x, fmaxf(p[b][nt][c], p[b][nt][2 + c]) * f[b][nt][c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        if (x > st.top[nt][c]) {
-          const float alpha = st.top[nt][c] == -INFINITY ? 0.f : fast_ex2(-st.neg_m[nt][c] - x);
-          st.neg_m[nt][c] = -x;
-          st.top[nt][c] = x + kFp8RescaleLog2;
+        if (x + st.nm[nt][c] > kFp8Most) {
+          const float nm = kFp8Lift - x, alpha = fast_ex2(nm - st.nm[nt][c]);  // 0 for the first key
+          st.nm[nt][c] = nm;
           st.l[nt][c] *= alpha;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             st.o[i][nt][c] *= alpha;
             st.o[i][nt][2 + c] *= alpha;
           }
-          if (kept)
-            fp8_each_kept<D, NT, HL>(st, [&](int n, int t2, int c2, float&) {
-              if (t2 == nt && c2 == c) kept[32 * n + lane] *= alpha;
-            });
         }
       }
   }
 
-  // Weights, their sum in fp32, and weights times V's scale (exact over its reference), rounded
-  // to f16 once: off by 2^-11 of a term, next to the codes' 4 bits. The k-order of O^T += C_v^T P^T
-  // is tokens 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
-  const float vs = scale.y * st.inv;
-  uint32_t pb[NT][2];
+  // Weights, their sum in fp32, and weights (rounded to f16: off by 2^-11, next to the codes' 4 bits)
+  // times V's scale over its reference, a power of two. The k-order of O^T += C_v^T P^T is tokens
+  // 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
+  uint32_t pb[NB][NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int b = 0; b < NB; ++b) {
+    const __half2 vs = __float2half2_rn(scale[b].y * st.inv);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < HL; ++c) {
-        p[r][nt][c] = fast_ex2(p[r][nt][c] + st.neg_m[nt][c]);
-        st.l[nt][c] += p[r][nt][c];
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int c = 0; c < HL; ++c) {
+          p[b][nt][2 * r + c] = fast_ex2(fmaf(p[b][nt][2 * r + c], f[b][nt][c], st.nm[nt][c]));
+          st.l[nt][c] += p[b][nt][2 * r + c];
+        }
+        const __half2 w = __hmul2(__floats2half2_rn(p[b][nt][2 * r], HL == 1 ? 0.f : p[b][nt][2 * r + HL - 1]), vs);
+        pb[b][nt][r] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&w));
       }
-      pb[nt][r] = transpose_8x8(pack_f16x2(p[r][nt][0] * vs, HL == 1 ? 0.f : p[r][nt][HL - 1] * vs));
-    }
+  }
 
   // Products 2 w and 2 w + 1 take the words w of the lane's chunks (d = 64: w and w + 2).
-  uint4 v4[2][G::NG];  // [tokens 2t, 2t + 1 or 2t + 8, 2t + 9][dims]
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int b = 0; b < NB; ++b) {
+    uint4 v4[2][G::NG];  // [tokens 2t, 2t + 1 or 2t + 8, 2t + 9][dims]
 #pragma unroll
-    for (int j = 0; j < G::NG; ++j) v4[r][j] = codes[G::CODES / 16 + 32 * (G::NG * r + j)];
-  if (nv < kBlock) {  // codes of slots without a key may be NaN
-    asm volatile("" ::: "memory");
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int tok = 2 * t + 8 * r;
-      const uint32_t keep = (tok < nv ? 0x00ff00ffu : 0u) | (tok + 1 < nv ? 0xff00ff00u : 0u);
+      for (int j = 0; j < G::NG; ++j) v4[r][j] = reinterpret_cast<const uint4*>(stage[b] + G::CODES)[lane + 32 * (G::NG * r + j)];
+    if (partial) {  // codes of slots without a key may be NaN
+      asm volatile("" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < G::NG; ++j) v4[r][j].x &= keep, v4[r][j].y &= keep, v4[r][j].z &= keep, v4[r][j].w &= keep;
-    }
-  }
+      for (int r = 0; r < 2; ++r) {
+        const int tok = 2 * t + 8 * r;
+        const uint32_t keep = (tok < nv[b] ? 0x00ff00ffu : 0u) | (tok + 1 < nv[b] ? 0xff00ff00u : 0u);
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    uint32_t a[2][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint32_t lo[4] = {v4[r][0].x, v4[r][0].y, v4[r][0].z, v4[r][0].w};
-      const uint32_t hi[4] = {v4[r][G::NG - 1].x, v4[r][G::NG - 1].y, v4[r][G::NG - 1].z, v4[r][G::NG - 1].w};
-      e4m3x4_to_f16x4(lo[w], a[0][2 * r], a[1][2 * r]);
-      e4m3x4_to_f16x4(hi[G::NG == 2 ? w : w + 2], a[0][2 * r + 1], a[1][2 * r + 1]);
+        for (int j = 0; j < G::NG; ++j) v4[r][j].x &= keep, v4[r][j].y &= keep, v4[r][j].z &= keep, v4[r][j].w &= keep;
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t a[2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_16816_f16(st.o[2 * w + e][nt], a[e], pb[nt][0], pb[nt][1]);
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t lo[4] = {v4[r][0].x, v4[r][0].y, v4[r][0].z, v4[r][0].w};
+        const uint32_t hi[4] = {v4[r][G::NG - 1].x, v4[r][G::NG - 1].y, v4[r][G::NG - 1].z, v4[r][G::NG - 1].w};
+        e4m3x4_to_f16x4(lo[w], a[0][2 * r], a[1][2 * r]);
+        e4m3x4_to_f16x4(hi[G::NG == 2 ? w : w + 2], a[0][2 * r + 1], a[1][2 * r + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(st.o[2 * w + e][nt], a[e], pb[b][nt][0], pb[b][nt][1]);
+    }
   }
 }
 
@@ -403,7 +403,7 @@ __device__ __forceinline__ void fp8_store_partial(const Fp8State<D, NT, HL>& st,
               make_float4(st.o[i][nt][2 * h + c] * r, st.o[i + 1][nt][2 * h + c] * r, st.o[i + 2][nt][2 * h + c] * r,
                           st.o[i + 3][nt][2 * h + c] * r);
       if (g == 0) {
-        row[D] = st.top[nt][c] == -INFINITY ? -INFINITY : -st.neg_m[nt][c];
+        row[D] = -st.nm[nt][c];
         row[D + 1] = st.l[nt][c];
       }
     }

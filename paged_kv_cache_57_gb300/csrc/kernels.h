@@ -334,8 +334,8 @@ struct UnitDecodeArgs : DecodeArgs {
   int64_t* prefix;  // with range_ctas: [B + 1] blocks of the sequences before each, and whether ranges were taken
 };
 // num_splits > 0: that many pieces of every unit (fewer of a sequence with fewer blocks); else chosen
-// for the device's `resident` CTAs.
-UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident);
+// for the device's `resident` CTAs. No piece or range has more than `most` blocks.
+UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident, int most = 1 << 30);
 // a.ws_o: [2 parts][rows][D], a.ws_ml: [2 parts][rows][2], then a.prefix, where there are parts.
 size_t unit_workspace_bytes(const UnitPlan& plan, int B, int D);
 cudaError_t launch_combine_units(const UnitDecodeArgs& a, cudaStream_t st);
@@ -343,7 +343,9 @@ cudaError_t launch_combine_units(const UnitDecodeArgs& a, cudaStream_t st);
 // int4 pools (decode_int4.cu): records of Int4Geom<D> behind a.k_pool / a.v_pool. sms: the device's.
 UnitPlan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
 cudaError_t launch_decode_int4(const UnitDecodeArgs& a, bool lazy, cudaStream_t st);
-// Pools of e4m3 codes with block scales (decode_fp8_block.cu): records of Fp8Geom<D>.
+// Pools of e4m3 codes with block scales (decode_fp8_block.cu): records of Fp8Geom<D>. A warp adds up
+// at most kFp8MaxRun blocks (fp8_block.cuh).
+constexpr int kFp8MaxRun = 16384;
 UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms);
 cudaError_t launch_decode_fp8_block(const UnitDecodeArgs& a, bool lazy, cudaStream_t st);
 cudaError_t launch_decode_shared_fp8_block(const SharedDecodeArgs& a, const void* k_pool, const void* v_pool, bool lazy,
