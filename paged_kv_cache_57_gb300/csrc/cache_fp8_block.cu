@@ -161,7 +161,7 @@ __device__ __forceinline__ void write_run(const uint8_t* src, int64_t step, cons
 
 // A warp per (W tokens, K or V, KV head): the runs that begin among the tokens.
 template <int D, bool VEC, int W>
-__global__ void __launch_bounds__(kThreads) cache_write_fp8_block_kernel(const CacheWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) cache_write_fp8_block_kernel(const CacheWriteArgs a) {
   __shared__ int rowtok_all[kWarps][kBlock];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* rowtok = rowtok_all[warp];

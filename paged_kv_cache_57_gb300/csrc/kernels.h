@@ -121,6 +121,7 @@ struct AppendArgs {
   unsigned int* status;
   int B, num_free, num_rows, doc_tokens, max_blocks, id_bits, num_pool_blocks, key_positions;
   int vec;                    // slots and local_pos are 16-byte aligned
+  uint32_t doc_mul, doc_shift;  // division by doc_tokens (the launch fills them)
 };
 
 struct PrefillArgs {

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple, Optional
+from typing import Optional
 
 import numpy as np
 import torch
@@ -132,10 +132,10 @@ def make_params(*, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim:
                   float(sm_scale), num_splits, int(bool(key_positions)), kv, float(k_scale), float(v_scale))
 
 
-def _dptr(t: Optional[torch.Tensor], name: str, dtype=None, device_required=True):
+def _dptr(t: Optional[torch.Tensor], name: str, dtype=None):
     if t is None:
         return None
-    if device_required and not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -144,14 +144,14 @@ def _dptr(t: Optional[torch.Tensor], name: str, dtype=None, device_required=True
     return t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it (3 us of a call's 10), where torch has the call.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current stream's handle without a Stream object around it (3 us of a call's 10), where torch has the calls.
+_raw_stream, _raw_device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -288,21 +288,46 @@ def pack_block_words(p: Params, num_docs: int, seg_indptr: torch.Tensor, seg_doc
 
 # ---------------------------------------------------------------- room for new tokens
 
-class AppendTables(NamedTuple):
-    """Outputs of append_tokens, int32 on the device; slots and local_pos have an entry for every row."""
-    seq_lens: torch.Tensor
-    pos: torch.Tensor
-    q_start: torch.Tensor
-    cu_rows: torch.Tensor
-    block_indptr: torch.Tensor
-    slots: torch.Tensor
-    local_pos: torch.Tensor
+class AppendTables:
+    """Outputs of append_tokens, int32 and contiguous, on one device: seq_lens, pos, q_start [B]; cu_rows, block_indptr
+    [B + 1]; slots and local_pos (or None) with an entry for every row. A step's tables are made once and filled by every
+    call, so they are looked at here and not there."""
+    __slots__ = ("seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos", "rows", "num_seqs", "_ptrs")
+
+    def __init__(self, seq_lens: torch.Tensor, pos: torch.Tensor, q_start: torch.Tensor, cu_rows: torch.Tensor,
+                 block_indptr: torch.Tensor, slots: torch.Tensor, local_pos: Optional[torch.Tensor] = None):
+        self.seq_lens, self.pos, self.q_start = seq_lens, pos, q_start
+        self.cu_rows, self.block_indptr, self.slots, self.local_pos = cu_rows, block_indptr, slots, local_pos
+        self.rows = slots.numel()
+        self.num_seqs = min(seq_lens.numel(), pos.numel(), q_start.numel(), cu_rows.numel() - 1, block_indptr.numel() - 1)
+        if local_pos is not None and local_pos.numel() != self.rows:
+            raise ValueError("slots and local_pos must have as many rows")
+        ptrs = []
+        for name in self.__slots__[:7]:
+            x = getattr(self, name)
+            if x is not None and (x.dtype != torch.int32 or not x.is_contiguous() or x.device != slots.device):
+                raise ValueError(f"{name} must be a contiguous int32 tensor on the other tables' device")
+            ptrs.append(ctypes.c_void_p(None if x is None else x.data_ptr()))
+        self._ptrs = tuple(ptrs) if slots.is_cuda else None
+
+    def __iter__(self):
+        return iter((self.seq_lens, self.pos, self.q_start, self.cu_rows, self.block_indptr, self.slots, self.local_pos))
+
+    def replace(self, **tables) -> "AppendTables":
+        """The same tables but for those given."""
+        return AppendTables(**{**{n: getattr(self, n) for n in self.__slots__[:7]}, **tables})
 
     @classmethod
     def empty(cls, p: Params, num_rows: int, device="cuda") -> "AppendTables":
         """Uninitialised tables for p's sequences and num_rows rows."""
         b = p.num_seqs
         return cls(*(torch.empty(n, dtype=torch.int32, device=device) for n in (b, b, b, b + 1, b + 1, num_rows, num_rows)))
+
+
+def _i32_in(x: torch.Tensor, name: str, n: int) -> int:
+    if x.numel() < n:
+        raise ValueError(f"{name} must hold {n} elements")
+    return _dptr(x, name, torch.int32)
 
 
 def append_tokens(p: Params, new_lens: torch.Tensor, seq_lens: torch.Tensor, pos: torch.Tensor, tail_start: torch.Tensor,
@@ -312,32 +337,26 @@ def append_tokens(p: Params, new_lens: torch.Tensor, seq_lens: torch.Tensor, pos
     """Room for new_lens[s] tokens behind every sequence (lazy_attn_append_tokens): words of the blocks taken from
     free_blocks into block_words, and lengths, positions, row offsets and slots of num_rows rows (or of ``out``'s), whose
     seq_lens and pos may be the inputs themselves. ``first_free`` is an earlier call's block_indptr[-1:]."""
-    i32, b = torch.int32, p.num_seqs
+    b = p.num_seqs
     if out is None:
         if num_rows is None:
             raise ValueError("num_rows or out is needed")
         out = AppendTables.empty(p, num_rows, device=block_words.device)
-    rows = out.slots.numel()
-    if num_rows is not None and num_rows != rows:
-        raise ValueError(f"out has {rows} rows, not {num_rows}")
-    for name, x, n in (("new_lens", new_lens, b), ("seq_lens", seq_lens, b), ("pos", pos, b), ("tail_start", tail_start, b),
-                       ("block_words", block_words, b * p.max_blocks_per_seq), ("out.seq_lens", out.seq_lens, b),
-                       ("out.pos", out.pos, b), ("out.q_start", out.q_start, b), ("out.cu_rows", out.cu_rows, b + 1),
-                       ("out.block_indptr", out.block_indptr, b + 1)):
-        if x.numel() < n:
-            raise ValueError(f"{name} must hold {n} elements")
-    if out.local_pos is not None and out.local_pos.numel() != rows:
-        raise ValueError("out.slots and out.local_pos must have as many rows")
+    elif num_rows is not None and num_rows != out.rows:
+        raise ValueError(f"out has {out.rows} rows, not {num_rows}")
+    if out.num_seqs < b:
+        raise ValueError(f"out has tables for {out.num_seqs} sequences, not {b}")
+    if out._ptrs is None:
+        raise ValueError("out must be CUDA tensors")
     if first_free is not None and first_free.numel() != 1:
         raise ValueError("first_free must hold one element")
     rc = _lib.lazy_attn_append_tokens(
-        ctypes.byref(p), _dptr(new_lens, "new_lens", i32), _dptr(seq_lens, "seq_lens", i32), _dptr(pos, "pos", i32),
-        _dptr(tail_start, "tail_start", i32), _dptr(free_blocks, "free_blocks", i32), free_blocks.numel(),
-        _dptr(first_free, "first_free", i32), int(doc_tokens), rows, _dptr(block_words, "block_words", i32),
-        _dptr(out.seq_lens, "out.seq_lens", i32), _dptr(out.pos, "out.pos", i32), _dptr(out.q_start, "out.q_start", i32),
-        _dptr(out.cu_rows, "out.cu_rows", i32), _dptr(out.block_indptr, "out.block_indptr", i32),
-        _dptr(out.slots, "out.slots", i32), _dptr(out.local_pos, "out.local_pos", i32), _stream(stream))
-    _check(rc, "append_tokens")
+        ctypes.byref(p), _i32_in(new_lens, "new_lens", b), _i32_in(seq_lens, "seq_lens", b), _i32_in(pos, "pos", b),
+        _i32_in(tail_start, "tail_start", b), _dptr(free_blocks, "free_blocks", torch.int32), free_blocks.numel(),
+        _dptr(first_free, "first_free", torch.int32), doc_tokens, out.rows,
+        _i32_in(block_words, "block_words", b * p.max_blocks_per_seq), *out._ptrs, _stream(stream))
+    if rc != LAZY_OK:
+        raise LazyAttnError(rc, "append_tokens")
     return out
 
 
@@ -585,7 +604,7 @@ def cache_write(p: Params, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     if not (k.is_cuda and v.is_cuda) or k.dtype != dt or v.dtype != dt:
         raise ValueError(f"k and v must be {dt} CUDA tensors")
     sk, sv = k.stride(), v.stride()
-    if k.shape != shape or v.shape != shape or ((sk[2] != 1 or sv[2] != 1) and k.numel()):
+    if k.shape != shape or v.shape != shape or (not sk[2] == sv[2] == 1 and k.numel()):
         raise ValueError(f"k and v must have shape {shape} and contiguous rows, got {tuple(k.shape)}, strides {sk} and "
                          f"{tuple(v.shape)}, strides {sv}")
     kp, vp = _cache_pools(p, k_pool, v_pool)

@@ -50,9 +50,9 @@ def compare(p, new, used, pos, start, free, words, rows, first=0, doc=4096, loca
         x.fill_(-77)
     seq_lens, at = i32(used), i32(pos)
     if inplace:
-        out = out._replace(seq_lens=seq_lens, pos=at)
+        out = out.replace(seq_lens=seq_lens, pos=at)
     if not local:
-        out = out._replace(local_pos=None)
+        out = out.replace(local_pos=None)
     got = L.append_tokens(p, i32(new), seq_lens, at, i32(start), i32(free) if len(free) else i32([0])[:0], w,
                           first_free=i32([first]) if first else None, doc_tokens=doc, out=out, stream=stream)
     assert got is out
@@ -82,6 +82,22 @@ def test_tables_match_the_model(batch, new_hi, ctx, tail, room, key_positions):
         if doc == 0 and not key_positions and new_hi > 8000:
             continue  # a document whose offsets leave their field: refused, see below
         compare(p, new, used, pos, start, free, words, int(new.sum()) + room, first=[0, 5, 7, 0][i], doc=doc, local=i != 2, inplace=i == 3)
+
+
+# a few long sequences among many short ones, a warp's and the grid's
+@pytest.mark.parametrize("batch,long", [(300, 3000), (300, 900), (2100, 40000), (260, 9), (1500, 1025)])
+def test_long_among_short(batch, long):
+    rng = np.random.default_rng(batch + long)
+    new, used, pos, start = requests(rng, batch, 3, 100, 40)
+    new[[1, batch // 2, batch - 1]] = long, long // 2, long - 1
+    need = int(sum(-(-(q - a + n) // 16) - -(-(q - a) // 16) for n, q, a in zip(new, pos, start)))
+    wide = int(max(-(-u // 16) + -(-n // 16) + 1 for u, n in zip(used, new)))
+    p = params(batch, wide, need + 50)
+    words = (rng.integers(0, 1 << 14, (batch, wide)) << 18 | rng.integers(0, need + 50, (batch, wide))).astype(np.uint32)
+    rows = int(new.sum())
+    free = rng.permutation(need + 50)[:need + 3]
+    for cut in (rows + 100, rows, rows - 5):
+        compare(p, new, used, pos, start, free, words, cut, doc=1024)
 
 
 def test_sequences_that_do_not_fit():
@@ -141,7 +157,7 @@ def test_unaligned_outputs_and_side_stream():
     w, ins = u32(words), [i32(x) for x in (new, used, pos, start)]
     fr = i32(free)
     big = [torch.full((rows + 8,), -5, dtype=torch.int32, device="cuda") for _ in range(2)]
-    out = L.AppendTables.empty(p, rows)._replace(slots=big[0][1:rows + 1], local_pos=big[1][3:rows + 3])
+    out = L.AppendTables.empty(p, rows).replace(slots=big[0][1:rows + 1], local_pos=big[1][3:rows + 3])
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     L.append_tokens(p, *ins, fr, w, out=out, stream=s)
@@ -180,7 +196,7 @@ class Server:
         self.words = torch.zeros(batch, wide, dtype=torch.int32, device="cuda")
         self.lens, self.pos, self.start = (torch.zeros(batch, dtype=torch.int32, device="cuda") for _ in range(3))
         self.free = i32(np.random.default_rng(1).permutation(400)[:350])
-        self.out = L.AppendTables.empty(self.p, cap)._replace(seq_lens=self.lens, pos=self.pos)
+        self.out = L.AppendTables.empty(self.p, cap).replace(seq_lens=self.lens, pos=self.pos)
         self.out.block_indptr.zero_()
         self.new = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.k, self.v = (torch.zeros(cap, 2, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
