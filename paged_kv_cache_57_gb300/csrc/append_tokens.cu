@@ -5,10 +5,9 @@
 // blocks: token i of them is row i % 16 of block b0 + i / 16. So all that couples the sequences
 // is two sums over the batch, of rows and of blocks taken from the free list. One CTA forms them
 // (append_scan_kernel), a thread a sequence, and where there is little to write, writes the rows too.
-// Else a second launch does, started behind the first one's back: a thread a sequence again where they have few
-// rows (append_seqs_kernel; long ones are shared by the warp, the longest by the grid), or, where a sequence has many, warps of 256 rows, which
-// find their sequence by a search in the rows' sums (append_rows_kernel). Latency bounds the small cases (64 sequences of a
-// token 3.3 us a call in a graph), the device's stores the large.
+// Else a second launch does, started behind the first one's back: a thread a row (append_row_kernel), or, of many,
+// warps of 256 rows (append_rows_kernel), that find their sequence by a search in the rows' sums. Latency bounds the
+// small cases (64 sequences of a token 3.4 us a call in a graph), the device's stores the large.
 #include <algorithm>
 #include <climits>
 
@@ -19,10 +18,10 @@ namespace lazy {
 
 namespace {
 
-constexpr int kRowThreads = 256, kSeqThreads = 128;
+constexpr int kRowThreads = 256;
+constexpr int kFewRows = 152 * 2048;  // a thread each is resident at once
 constexpr int kRowsPerWarp = 256;  // 3.2 million rows of 48 sequences 11.2 us, with 128 and 512 11.4, 1024 12.9
 constexpr int kOwnRows = 8;        // rows that a sequence's thread writes by itself
-constexpr int kWarpRows = 1024;    // and its warp
 constexpr int kOneDoc = 1 << 30;   // a document without an end
 
 __device__ __forceinline__ int blocks_for(int tokens) { return (int)(((unsigned)tokens + kBlock - 1) / kBlock); }
@@ -155,8 +154,8 @@ __device__ __forceinline__ void put_row(const AppendArgs& a, int r, int2 x) {
 }
 
 // The rows of a warp's sequences, each lane's own: s with the rows begin .. end - 1 (none: end <= begin). All
-// lanes call it. Few rows are their lane's, up to `most` the warp's.
-__device__ __forceinline__ void write_seqs(const AppendArgs& a, const SeqRows& q, int s, int begin, int end, int most) {
+// lanes call it. Few rows are their lane's, more are shared out.
+__device__ __forceinline__ void write_seqs(const AppendArgs& a, const SeqRows& q, int s, int begin, int end) {
   const int n = end - begin, lane = threadIdx.x & 31;
   if (n > 0 && n <= kOwnRows) {  // in one block of its own or two, of one document each
     const bool ok = q.shift != INT_MIN;
@@ -173,7 +172,7 @@ __device__ __forceinline__ void write_seqs(const AppendArgs& a, const SeqRows& q
       if (++local == a.doc_tokens) local = 0;
     }
   }
-  for (uint32_t left = __ballot_sync(0xffffffffu, n > kOwnRows && n <= most); left; left &= left - 1) {
+  for (uint32_t left = __ballot_sync(0xffffffffu, n > kOwnRows); left; left &= left - 1) {
     const int l = __ffs(left) - 1;
     auto of = [&](int x) { return __shfl_sync(0xffffffffu, x, l); };
     const SeqRows p{of(q.shift), of(q.start), of(q.b0), of(q.first), of(q.have)};
@@ -243,7 +242,7 @@ __global__ void append_scan_kernel(const AppendArgs a) {
     if (ROWS) {  // (one chunk)
       const int tail = s < a.B ? pos - a.tail_start[s] : 0, have = blocks_for(tail), begin = (int)(r - w.rows);
       const SeqRows q{ok ? tail - begin : INT_MIN, s < a.B ? a.tail_start[s] : 0, w.b0, first + (int)(b - w.blocks) - have, have};
-      write_seqs(a, q, s, begin, s < a.B ? (int)min(r, (int64_t)a.num_rows) : begin, INT_MAX);
+      write_seqs(a, q, s, begin, s < a.B ? (int)min(r, (int64_t)a.num_rows) : begin);
     }
     rows += all_r;
     blocks += all_b;
@@ -253,29 +252,17 @@ __global__ void append_scan_kernel(const AppendArgs a) {
     for (int r = (int)min(rows, (int64_t)a.num_rows) + threadIdx.x; r < a.num_rows; r += blockDim.x) put_row(a, r, make_int2(-1, 0));
 }
 
-__global__ void __launch_bounds__(kSeqThreads) append_seqs_kernel(const AppendArgs a) {
-  const int s = blockIdx.x * kSeqThreads + threadIdx.x;
+// A row a thread.
+__global__ void __launch_bounds__(kRowThreads) append_row_kernel(const AppendArgs a) {
+  const int r = blockIdx.x * kRowThreads + threadIdx.x;
   wait_for_launch_before();
-  int begin = 0, end = 0;
-  SeqRows q{INT_MIN, 0, 0, 0, 0};
-  if (s < a.B) {
-    begin = a.cu_rows[s];
-    end = min(a.cu_rows[s + 1], a.num_rows);
-    q = seq_rows(a, s, begin);
+  if (r >= a.num_rows) return;
+  int2 x = make_int2(-1, 0);
+  if (r < a.cu_rows[a.B]) {
+    const int s = seq_of(a.cu_rows, a.B, r);
+    x = one_row(a, seq_rows(a, s, a.cu_rows[s]), s, r);
   }
-  write_seqs(a, q, s, begin, end, kWarpRows);
-  // every warp looks for sequences of more, and takes its share of each
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kSeqThreads / 32);
-  for (int s0 = 0; s0 < a.B; s0 += 32) {
-    const int mine = s0 + lane, from = mine < a.B ? a.cu_rows[mine] : 0, to = mine < a.B ? min(a.cu_rows[mine + 1], a.num_rows) : 0;
-    for (uint32_t left = __ballot_sync(0xffffffffu, to - from > kWarpRows); left; left &= left - 1) {
-      const int l = __ffs(left) - 1, first = __shfl_sync(0xffffffffu, from, l), last = __shfl_sync(0xffffffffu, to, l);
-      const SeqRows p = seq_rows(a, s0 + l, first);
-      for (int64_t r = first + 32ll * (s >> 5) + lane; r < last; r += 32 * warps) put_row(a, (int)r, one_row(a, p, s0 + l, (int)r));
-    }
-  }
-  for (int64_t r = (int64_t)min(a.cu_rows[a.B], a.num_rows) + s; r < a.num_rows; r += (int64_t)gridDim.x * kSeqThreads)
-    put_row(a, (int)r, make_int2(-1, 0));
+  put_row(a, r, x);
 }
 
 // A warp takes kRowsPerWarp rows in a row, four a lane at a time.
@@ -350,7 +337,7 @@ cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st) {
   a.doc_shift = 0;
   while ((1ull << a.doc_shift) < d) ++a.doc_shift;
   a.doc_mul = (uint32_t)(((1ull << 32) * ((1ull << a.doc_shift) - d)) / d + 1);
-  // One CTA writes rows at an SM's rate: 1021 sequences of up to 8 took 10.7 us with the rows, 6.0 in two launches.
+  // One CTA writes rows at an SM's rate: 1021 sequences of up to 8 took 10.7 us that way.
   const bool one = a.B <= 256 && a.num_rows <= 1024;
   const unsigned threads = a.B >= 1024 ? 1024 : (one && a.num_rows > a.B ? 256 : (a.B <= 32 ? 32 : (a.B + 31) / 32 * 32));
   *launches = 1;
@@ -358,10 +345,7 @@ cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st) {
   cudaError_t e = launch_behind(append_scan_kernel<false>, 1, threads, 0, st, a);
   if (e != cudaSuccess || a.num_rows == 0) return e;
   *launches = 2;
-  if (a.num_rows < 64ll * a.B) {
-    const int64_t seqs = ((int64_t)a.B + kSeqThreads - 1) / kSeqThreads, rows = std::min(152, a.num_rows / 2048);
-    return launch_behind(append_seqs_kernel, (unsigned)std::max(seqs, rows), kSeqThreads, 0, st, a);
-  }
+  if (a.num_rows <= kFewRows) return launch_behind(append_row_kernel, (unsigned)((a.num_rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st, a);
   const int per = kRowThreads / 32 * kRowsPerWarp;
   return launch_behind(append_rows_kernel, (unsigned)(((int64_t)a.num_rows + per - 1) / per), kRowThreads, 0, st, a);
 }
