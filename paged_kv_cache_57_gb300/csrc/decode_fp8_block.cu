@@ -5,7 +5,9 @@
 //
 // Both kernels: four warps form 4 / RT teams of RT = 1, 2 or 4. A team takes a contiguous part of
 // the CTA's blocks through a ring of stages in shared memory; each of its warps has its own tile
-// of 4, 8 or 16 query rows. A block's copies are one warp's, in turn.
+// of 4, 8, 16 or 32 query rows. A block's K and V records are two bulk copies, which one lane starts
+// and the stage's mbarrier counts: a warp's own cp.async of them took 9 instructions a lane and block,
+// and an address for each. The stages' waits are bounded.
 #include <algorithm>
 #include <climits>
 
@@ -21,17 +23,15 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMembers = LAZY_PLAN_MAX_MEMBERS;
 constexpr int kItemInts = LAZY_PLAN_ITEM_INTS;
 
-// The n threads of team t meet (barrier 0 is the CTA's).
-__device__ __forceinline__ void team_sync(int t, int n) { asm volatile("bar.sync %0, %1;" ::"r"(t + 1), "r"(n) : "memory"); }
-
 template <int D, int NT, int HL>
 struct Fp8Cfg {
   static constexpr int ROWS = Fp8Rows<NT, HL>::ALL;  // of a warp
   static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
-  static constexpr int SLOT = Fp8Loader<D>::STAGE;   // one block
+  static constexpr int SLOT = Fp8Ring<D>::STAGE;     // one block
   static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // per SM
-  static constexpr int RING = NT == 4 ? 4 : 2;  // stages per warp of a team
+  static constexpr int RING = NT == 1 ? 2 : 4;                  // stages per warp of a team
   static constexpr int SLOTS = kWarps * RING;
+  static_assert(SLOTS <= kFp8Slots, "barriers");
   static constexpr int BUF = SLOTS * SLOT > kWarps * ROWS * RED * 4 ? SLOTS * SLOT : kWarps * ROWS * RED * 4;
 };
 
@@ -43,19 +43,25 @@ struct Fp8Cfg {
 template <int D, int NT, int HL, int RT, bool LAZY>
 __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_block_kernel(const UnitDecodeArgs a) {
   using C = Fp8Cfg<D, NT, HL>;
-  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT, AHEAD = R - 1;
+  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT, AHEAD = RT == 1 ? R - 1 : R - 2;
   constexpr int kNewDoc = 32;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
-  // Per team, the blocks of two word chunks (64): id, and valid slots with kNewDoc where the block
-  // is not one of the document of the block before (or begins a chunk).
-  __shared__ int2 d_blk[TEAMS][64];
+  uint32_t* q_all = reinterpret_cast<uint32_t*>(cs_all + kWarps * HALF);
+  __shared__ Fp8Bars bars;
+  if (threadIdx.x < C::SLOTS) {
+    mbar_init(&bars.full[threadIdx.x], 1);
+    mbar_init(&bars.empty[threadIdx.x], RT);
+    fence_barrier_init();
+  }
+  __syncthreads();
   wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / RT, rt = warp % RT;
   const int ht = a.plan.units / a.Hkv;
 
+  uint32_t used = 0;  // blocks that went through the ring before this part
   UnitWalk w;
   if (!w.begin(a, warp, lane)) return;
   while (w.next(a)) {
@@ -82,9 +88,12 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     const int per_team = (n + TEAMS - 1) / TEAMS;
     const int kb0 = lo + team * per_team;
     const int nk = max(0, min(lo + n, kb0 + per_team) - kb0);  // blocks of this team
-    const Fp8Loader<D> load(a.k_pool, a.v_pool, a.Hkv, kvh, lane);
-    const uint8_t* ring_p = smem + team * R * C::SLOT;
-    const uint32_t ring = smem_u32(ring_p);
+    const size_t head = (size_t)kvh * Fp8Geom<D>::REC;
+    const Fp8Ring<D> ring{static_cast<const uint8_t*>(a.k_pool) + head, static_cast<const uint8_t*>(a.v_pool) + head,
+                          (uint32_t)a.Hkv * Fp8Geom<D>::REC, smem + team * R * C::SLOT, &bars, team * R};
+    // A chunk of 32 blocks in the lanes: id, and valid slots with kNewDoc where the block is not one of the
+    // document of the block before (or begins a chunk).
+    int c_phys = 0, c_info = 0;
     uint32_t w_nxt = 0, wn_nxt = 0;
     auto load_words = [&](int kc) {
       const int k = kc + lane, b = kb0 + k;
@@ -96,33 +105,39 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
                                          a.num_pool_blocks, a.status);
       // a block without keys is left out and did not have q rotated for its document
       const int p_1 = __shfl_up_sync(0xffffffffu, r.nv > 0 ? r.p : INT_MIN, 1);
-      if (rt == 0)
-        d_blk[team][(kc + lane) & 63] = make_int2(r.phys < a.num_pool_blocks ? r.phys : 0,  // no keys in it: any block
-                                                  r.nv | (!LAZY || (lane > 0 && p_1 == r.p) ? 0 : kNewDoc));
-      __syncwarp();
+      c_phys = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block
+      c_info = r.nv | (!LAZY || (lane > 0 && p_1 == r.p) ? 0 : kNewDoc);
+    };
+    auto fill = [&](int j) {  // block j's stage is loaded, by the warp whose turn it is
+      if ((j & 31) == 0 && j < nk) {
+        describe(j);
+        load_words(j + 32);
+      }
+      if (j < nk && j % RT == rt) {
+        const uint32_t n_th = used + j, slot = n_th % R;
+        if (RT > 1 && n_th >= R && !ring.wait_empty(slot, (n_th / R + 1) & 1, a.status)) return false;
+        const int ph = __shfl_sync(0xffffffffu, c_phys, j & 31), info = __shfl_sync(0xffffffffu, c_info, j & 31);
+        if (lane == 0) ring.fill(slot, ph, info);
+      }
+      return true;
     };
     load_words(0);
-    describe(0);
-    load_words(32);
-    if (RT > 1) team_sync(team, 32 * RT);
-    auto load_block = [&](int j) {  // the warp's turn or not, one group
-      if (j < nk && j % RT == rt) load(ring + j % R * C::SLOT, d_blk[team][j & 63].x, lane);
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load_block(i);
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < AHEAD; ++i) ok &= fill(i);
 
     // ------------------------------------------------------------ queries
     Fp8Query<D, NT, HL> q;
     float mul[NT];
     fp8_scale_rows<D, NT, HL>(q, mul, raw, live, a.scale_log2, lane);
+    q.s = q_all + warp * (Fp8Query<D, NT, HL>::BYTES / 4) + 4 * lane;
     float2* cs = cs_all + warp * HALF;
     auto rebuild = [&](int delta) {
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < HALF / 32; ++j) cs[lane + 32 * j] = rope_cs(rate[j], delta, a.status);
       __syncwarp();
-      fp8_build_query<D, NT, HL>(q, mul, row, lane, [&](int) { return cs; });
+      fp8_build_query<D, NT, HL>(mul, row, lane, [&](int) { return cs; }, [&](int nt, int k, int h, uint32_t x) { q.set(nt, k, h, x); });
     };
     // Rotated while the first records are on their way. Control: the pool holds absolute-position keys.
     int p_cur = 0;  // the document that q is rotated for
@@ -135,31 +150,28 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     Fp8State<D, NT, HL> st;
     fp8_init(st);
     for (int i = 0; i < nk; ++i) {
-      // Block i has landed for the warp that loaded it and, behind the barrier, for the team, all of
-      // whose warps are done with block i - 1, whose stage is refilled.
-      cp_async_wait<AHEAD - 1>();
-      if (RT == 1) __syncwarp();
-      else team_sync(team, 32 * RT);
-      if ((i & 31) == 0 && i + 32 < nk) {  // a chunk of words ahead, over the one that all are done with
-        describe(i + 32);
-        load_words(i + 64);
+      const uint32_t n_th = used + i, slot = n_th % R;
+      ok = ok && fill(i + AHEAD) && ring.wait_full(slot, n_th / R & 1, a.status);
+      if (!ok) {
+        ring.drain(n_th, used + min(nk, i + AHEAD + 1), R, a.status);
+        break;
       }
-      load_block(i + AHEAD);
-      const uint8_t* stage[1] = {ring_p + i % R * C::SLOT};
-      const int info = d_blk[team][i & 63].y;
+      const uint8_t* stage[1] = {ring.base + slot * C::SLOT};
+      const int info = bars.info[team * R + slot];
       int nv[1] = {kBlock};
       if (info != kBlock) {
         nv[0] = info & 31;
-        if (nv[0] == 0) continue;  // the same for the whole team
         if (LAZY && info > kNewDoc) {
           const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
           if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
         }
       }
-      fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
+      if (nv[0] > 0) fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
+      __syncwarp();
+      if (RT > 1 && lane == 0) ring.release(slot);
     }
+    used += nk;
     fp8_finish(st);
-    cp_async_wait<0>();
     __syncthreads();  // every team is done with its ring: the merge takes its place
     float* red = reinterpret_cast<float*>(smem);
     fp8_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
@@ -187,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
         if (col == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * (slot0 + row)) = make_float2(M, L);
       }
     }
-    if (w.last()) return;
+    if (w.last() || !__syncthreads_and(ok)) return;
+    fence_proxy_async_smem();
     __syncthreads();  // the next part's loads and queries take the merge's place
   }
 }
@@ -198,12 +211,13 @@ namespace {
 
 template <int D>
 struct Fp8SharedCfg {
-  static constexpr int SLOT = Fp8Loader<D>::STAGE;
+  static constexpr int SLOT = Fp8Ring<D>::STAGE;
   static constexpr int ROWS = 2 * kWarps * 8;  // of a CTA
   static constexpr int RED = D + 4;            // merge rows: o[D], m, l
-  static constexpr int NB = 2;      // blocks of a step
-  static constexpr int STEPS = 8;   // in the teams' rings
-  static constexpr int BUF = STEPS * NB * SLOT > ROWS * RED * 4 ? STEPS * NB * SLOT : ROWS * RED * 4;
+  static constexpr int CTAS = 3;     // per SM
+  static constexpr int SLOTS = 16;   // stages of the teams' rings
+  static_assert(SLOTS <= kFp8Slots, "barriers");
+  static constexpr int BUF = SLOTS * SLOT > ROWS * RED * 4 ? SLOTS * SLOT : ROWS * RED * 4;
   static constexpr int SMEM = BUF + kMembers * (D / 2) * 8;  // and the members' angles
 };
 
@@ -211,7 +225,7 @@ struct Fp8SharedCfg {
 struct Fp8Item {
   int rec[kItemInts];
   int delta[kMembers], ok[kMembers];  // rotation offset of each member; it passed its checks
-  int2 d_blk[kWarps][64];             // per team, the blocks of two word chunks: id, valid slots
+  Fp8Bars bars;
 };
 
 }  // namespace
@@ -221,30 +235,29 @@ template <int D, int NT, int HL, bool LAZY>
 __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const uint8_t* k_pool, const uint8_t* v_pool,
                                                 Fp8Item& it, uint8_t* smem, float2* cs_tab, int kvh, int rows, int RT) {
   using C = Fp8SharedCfg<D>;
-  constexpr int HALF = D / 2, TILE = Fp8Rows<NT, HL>::ALL, NB = C::NB;
-  const int TEAMS = kWarps / RT, R = C::STEPS / TEAMS, AHEAD = R - 1;  // R = 2, 4 or 8
+  constexpr int HALF = D / 2, TILE = Fp8Rows<NT, HL>::ALL;
+  const int TEAMS = kWarps / RT, R = C::SLOTS / TEAMS;  // a power of two
+  const int AHEAD = RT == 1 ? R - 1 : R - 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / RT, rt = warp & (RT - 1);
   const int src = it.rec[0], b0 = it.rec[1], nblk = it.rec[2], last_nv = it.rec[3];
 
   // ------------------------------------------------------------ first loads
-  // parts of whole steps
-  const int per_team = (nblk + NB * TEAMS - 1) / (NB * TEAMS) * NB;
+  const int per_team = (nblk + TEAMS - 1) / TEAMS;
   const int kb0 = team * per_team;
   const int nk = max(0, min(nblk, kb0 + per_team) - kb0);  // blocks of the team
-  const int ns = (nk + NB - 1) / NB;                       // steps
-  const Fp8Loader<D> load(k_pool, v_pool, a.Hkv, kvh, lane);
-  const uint8_t* ring_p = smem + team * R * NB * C::SLOT;
-  const uint32_t ring = smem_u32(ring_p);
+  const size_t head = (size_t)kvh * Fp8Geom<D>::REC;
+  const Fp8Ring<D> ring{k_pool + head, v_pool + head, (uint32_t)a.Hkv * Fp8Geom<D>::REC, smem + team * R * C::SLOT, &it.bars, team * R};
   const uint32_t* wrow = a.words + (size_t)src * a.max_blocks + b0 + kb0;
   const uint32_t id_mask = (1u << a.id_bits) - 1u;
   const int* ids = it.rec + 8 + 4 * kMembers;  // the record's block ids
   uint32_t w_nxt = 0u;
+  int c_phys = 0, c_nv = 0;  // a chunk of 32 blocks in the lanes: id, valid slots
   auto load_words = [&](int kc) {
     if (kc + lane < nk) w_nxt = wrow[kc + lane];
   };
-  // Chunk kc of the team's words (w_nxt) to its descriptors, by every warp of the team alike. The
-  // block word decides; where the record names the block too the two must agree.
+  // Chunk kc of the team's words (w_nxt), by every warp of the team alike. The block word decides; where
+  // the record names the block too the two must agree.
   auto describe = [&](int kc) {
     const int k = kc + lane;
     int phys = 0, nv = 0;  // no keys: any block of the pool
@@ -259,105 +272,102 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
         raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
       }
     }
-    if (rt == 0) it.d_blk[team][k & 63] = make_int2(phys, nv);
-    __syncwarp();
+    c_phys = phys;
+    c_nv = nv;
   };
   load_words(0);
-  // First loads straight from the record's ids when it names all of them.
-  const bool rec_first = kb0 + min(NB * AHEAD, nk) <= LAZY_PLAN_ITEM_BLOCK_IDS;  // uniform over the team
-  auto load_step = [&](int j, auto id_of) {  // the warp's share of a step's blocks, as one group
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int k = NB * j + b;
-      if (k < nk && (k & (RT - 1)) == rt) load(ring + (k & (R * NB - 1)) * C::SLOT, id_of(k), lane);
-    }
-    cp_async_commit();
-  };
-  auto described = [&](int k) { return it.d_blk[team][k & 63].x; };
-  if (rec_first)
-    for (int i = 0; i < AHEAD; ++i)
-      load_step(i, [&](int k) {
-        const int id = ids[kb0 + k];
-        return id >= 0 && id < a.num_pool_blocks ? id : 0;
-      });
-  describe(0);
-  load_words(32);
-  if (RT > 1) team_sync(team, 32 * RT);
-  if (!rec_first)
-    for (int i = 0; i < AHEAD; ++i) load_step(i, described);
-
-  // ------------------------------------------------------------ members
-  const int nmem = it.rec[4];
-  if (threadIdx.x < nmem) {
-    const int m = threadIdx.x, seq = it.rec[8 + 4 * m], bm = it.rec[8 + 4 * m + 1], slot = it.rec[8 + 4 * m + 2];
-    bool good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
-    int delta = 0;
+  // What the queries need: loads that nothing waits for yet, so that all of the prologue's share one latency
+  // behind the record's. A member's seq, first block and slot, checked:
+  const int nmem = it.rec[4], me = threadIdx.x;
+  bool good = false;
+  uint32_t mem_word = 0u, src_word = 0u;
+  int mem_pos = 0;
+  if (me < nmem) {
+    const int seq = it.rec[8 + 4 * me], bm = it.rec[8 + 4 * me + 1], slot = it.rec[8 + 4 * me + 2];
+    good = seq >= 0 && seq < a.B && bm >= 0 && bm <= a.max_blocks - nblk && slot >= 0 && slot < a.num_slots;
     if (good) {
-      const BlockInfo mi = decode_word(a.words[(size_t)seq * a.max_blocks + bm], bm, a.id_bits);
-      good = mi.phys == decode_word(a.words[(size_t)src * a.max_blocks + b0], b0, a.id_bits).phys;
-      const int qp = a.q_pos[seq];
-      delta = LAZY ? qp - mi.p : qp;
+      mem_word = a.words[(size_t)seq * a.max_blocks + bm];
+      src_word = a.words[(size_t)src * a.max_blocks + b0];
+      mem_pos = a.q_pos[seq];
     }
-    if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
-    it.ok[m] = good;
-    it.delta[m] = delta;
   }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads)
-    cs_tab[idx] = rope_cs(a.rope[idx % HALF], it.delta[idx / HALF], a.status);
-  __syncthreads();
-
-  // ------------------------------------------------------------ queries
-  auto mem_seq = [&](int m) { return it.rec[8 + 4 * m]; };
-  auto mem_slot = [&](int m) { return it.rec[8 + 4 * m + 2]; };
+  static_assert(kThreads % HALF == 0, "a thread's angles are one frequency's");
+  const float2 rate = a.rope[threadIdx.x % HALF];
   const __nv_bfloat16* qrow[NT];
-  bool live[NT];
   int mem[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = rt * TILE + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2)), rc = r < rows ? r : 0;
     mem[nt] = rc / a.G;
-    live[nt] = r < rows && it.ok[mem[nt]];
+    const int seq = it.rec[8 + 4 * mem[nt]];
     qrow[nt] = static_cast<const __nv_bfloat16*>(a.q) +
-               ((live[nt] ? (size_t)mem_seq(mem[nt]) * a.Hq + (rc - mem[nt] * a.G) : 0) + (size_t)kvh * a.G) * D;
+               ((seq >= 0 && seq < a.B ? (size_t)seq * a.Hq + (rc - mem[nt] * a.G) : 0) + (size_t)kvh * a.G) * D;
   }
+  auto row = [&](int nt) { return qrow[nt]; };
+  const Fp8RawRows<D, NT> raw(row, lane);
+  auto fill = [&](int j) {  // block j's stage is loaded, by the warp whose turn it is
+    if ((j & 31) == 0 && j < nk) {
+      describe(j);
+      load_words(j + 32);
+    }
+    if (j < nk && (j & (RT - 1)) == rt) {
+      const int slot = j & (R - 1);
+      if (RT > 1 && j >= R && !ring.wait_empty(slot, (j / R + 1) & 1, a.status)) return false;
+      const int ph = __shfl_sync(0xffffffffu, c_phys, j & 31), nv = __shfl_sync(0xffffffffu, c_nv, j & 31);
+      if (lane == 0) ring.fill(slot, ph, nv);
+    }
+    return true;
+  };
+  bool ok = true;
+  if (kb0 + min(AHEAD, nk) <= LAZY_PLAN_ITEM_BLOCK_IDS) {  // straight from the record, which names them
+    for (int j = rt; j < min(AHEAD, nk); j += RT)
+      if (lane == 0) {
+        const int id = ids[kb0 + j];
+        ring.fill(j, id >= 0 && id < a.num_pool_blocks ? id : 0, kb0 + j == nblk - 1 ? last_nv : kBlock);
+      }
+    describe(0);
+    load_words(32);
+  } else {
+    for (int j = 0; j < AHEAD; ++j) ok &= fill(j);
+  }
+
+  // ------------------------------------------------------------ members and queries
+  if (me < nmem) {
+    const BlockInfo mi = decode_word(mem_word, it.rec[8 + 4 * me + 1], a.id_bits);
+    good = good && mi.phys == decode_word(src_word, b0, a.id_bits).phys;
+    if (!good) raise_status(a.status, LAZY_DEV_LAYOUT);
+    it.ok[me] = good;
+    it.delta[me] = !good ? 0 : (LAZY ? mem_pos - mi.p : mem_pos);
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < nmem * HALF; idx += kThreads) cs_tab[idx] = rope_cs(rate, it.delta[idx / HALF], a.status);
+  bool live[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) live[nt] = rt * TILE + (HL == 1 ? lane >> 3 : 8 * nt + (lane >> 2)) < rows && it.ok[mem[nt]];
   Fp8Query<D, NT, HL> q;
   float mul[NT];
-  auto row = [&](int nt) { return qrow[nt]; };
-  fp8_scale_rows<D, NT, HL>(q, mul, Fp8RawRows<D, NT>(row, lane), live, a.scale_log2, lane);
-  fp8_build_query<D, NT, HL>(q, mul, row, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; });
+  fp8_scale_rows<D, NT, HL>(q, mul, raw, live, a.scale_log2, lane);
+  __syncthreads();
+  fp8_build_query<D, NT, HL>(mul, row, lane, [&](int nt) { return cs_tab + mem[nt] * HALF; },
+                             [&](int nt, int k, int h, uint32_t x) { q.set(nt, k, h, x); });
 
   // ------------------------------------------------------------ main loop
   Fp8State<D, NT, HL> st;
   fp8_init(st);
-  for (int i = 0; i < ns; ++i) {
-    // Step i has landed for the warps that loaded it and, behind the barrier, for the team, all of
-    // whose warps are done with step i - 1, whose stages are refilled.
-    if (RT == 1) {
-      cp_async_wait<C::STEPS / 4 - 2>();
-      __syncwarp();
-    } else {
-      if (RT == 2) cp_async_wait<C::STEPS / 2 - 2>();
-      else cp_async_wait<C::STEPS - 2>();
-      team_sync(team, 32 * RT);
+  for (int i = 0; i < nk; ++i) {
+    const int slot = i & (R - 1);
+    ok = ok && fill(i + AHEAD) && ring.wait_full(slot, i / R & 1, a.status);
+    if (!ok) {
+      ring.drain(i, min(nk, i + AHEAD + 1), R, a.status);
+      break;
     }
-    const int k0 = NB * i;
-    if ((k0 & 31) == 0) {  // a chunk of words ahead, over the one that all are done with
-      describe(k0 + 32);
-      load_words(k0 + 64);
-    }
-    load_step(i + AHEAD, described);
-    const uint8_t* stage[NB];
-    int nv[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      stage[b] = ring_p + ((k0 + b) & (R * NB - 1)) * C::SLOT;
-      nv[b] = it.d_blk[team][(k0 + b) & 63].y;
-    }
-    if (nv[0] > 0 || nv[NB - 1] > 0) fp8_attend<D, NT, HL, NB>(stage, nv, q, st, lane);
+    const uint8_t* stage[1] = {ring.base + slot * C::SLOT};
+    const int nv[1] = {it.bars.info[team * R + slot]};
+    if (nv[0] > 0) fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
+    __syncwarp();
+    if (RT > 1 && lane == 0) ring.release(slot);
   }
   fp8_finish(st);
-  cp_async_wait<0>();
   __syncthreads();  // every team is done with its ring: the merge takes its place
 
   // ------------------------------------------------------------ partials
@@ -367,7 +377,8 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
   constexpr int PER = D / 32;
   for (int x = warp; x < rows; x += kWarps) {
     const int m = x / a.G, h = x - m * a.G;
-    if (mem_slot(m) < 0 || mem_slot(m) >= a.num_slots) continue;
+    const int slot = it.rec[8 + 4 * m + 2];
+    if (slot < 0 || slot >= a.num_slots) continue;
     float M = -INFINITY, acc[PER], L = 0.f;
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = 0.f;
@@ -383,7 +394,7 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
       }
       if (L != 0.f) M = Mr;  // all scores NaN: not an empty slot, which the combine would pass over
     }
-    const size_t pidx = (size_t)mem_slot(m) * a.Hq + (size_t)kvh * a.G + h;
+    const size_t pidx = (size_t)slot * a.Hq + (size_t)kvh * a.G + h;
 #pragma unroll
     for (int c = 0; c < PER; ++c) a.ws_o[pidx * D + lane + 32 * c] = acc[c];
     if (lane == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * pidx) = make_float2(M, L);
@@ -391,7 +402,7 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
 }
 
 template <int D, bool LAZY>
-__global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
+__global__ void __launch_bounds__(kThreads, Fp8SharedCfg<D>::CTAS) decode_shared_fp8_block_kernel(const SharedDecodeArgs a, const uint8_t* k_pool,
                                                                               const uint8_t* v_pool) {
   using C = Fp8SharedCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];            // the teams' rings, then the merge area
@@ -411,10 +422,15 @@ __global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(co
     if (threadIdx.x == 0) raise_status(a.status, LAZY_DEV_LAYOUT);
     return;
   }
-  const int n = nmem * a.G;
-  if (n <= 4) shared_fp8_rows<D, 1, 1, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, 1);
-  else if (n <= 8) shared_fp8_rows<D, 1, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, 1);
-  else shared_fp8_rows<D, 2, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, n <= 16 ? 1 : (n <= 32 ? 2 : 4));
+  const int n = nmem * a.G, RT = n <= 16 ? 1 : (n <= 32 ? 2 : 4);
+  if (threadIdx.x < C::SLOTS) {
+    mbar_init(&it.bars.full[threadIdx.x], 1);
+    mbar_init(&it.bars.empty[threadIdx.x], RT);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (n <= 8) shared_fp8_rows<D, 1, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, 1);
+  else shared_fp8_rows<D, 2, 2, LAZY>(a, k_pool, v_pool, it, smem, cs_tab, kvh, n, RT);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -422,15 +438,15 @@ __global__ void __launch_bounds__(kThreads, 3) decode_shared_fp8_block_kernel(co
 UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
   int rows = 4;
   while (rows < G && rows < 64) rows *= 2;
-  const int per_sm = rows <= 8 ? Fp8Cfg<128, 1, 1>::CTAS : Fp8Cfg<128, 2, 2>::CTAS;
-  const int teams = rows <= 16 ? 4 : 64 / rows;
-  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm, teams * kFp8MaxRun);
+  const int per_sm = rows <= 8 ? Fp8Cfg<128, 1, 1>::CTAS : (rows == 16 ? Fp8Cfg<128, 2, 2>::CTAS : Fp8Cfg<128, 4, 2>::CTAS);
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm,
+                    (rows == 64 ? 2 : 4) * kFp8MaxRun);
 }
 
 template <int D, int NT, int HL, int RT, bool LAZY>
 static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
   using C = Fp8Cfg<D, NT, HL>;
-  constexpr int SMEM = C::BUF + kWarps * (D / 2) * 8;
+  constexpr int SMEM = C::BUF + kWarps * ((D / 2) * 8 + Fp8Query<D, NT, HL>::BYTES);
   cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, RT, LAZY>>(SMEM);
   if (e != cudaSuccess) return e;
   return launch_behind(decode_fp8_block_kernel<D, NT, HL, RT, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
@@ -442,8 +458,8 @@ static cudaError_t launch_decode_d(const UnitDecodeArgs& a, cudaStream_t st) {
     case 4: return launch_decode_t<D, 1, 1, 1, LAZY>(a, st);
     case 8: return launch_decode_t<D, 1, 2, 1, LAZY>(a, st);
     case 16: return launch_decode_t<D, 2, 2, 1, LAZY>(a, st);
-    case 32: return launch_decode_t<D, 2, 2, 2, LAZY>(a, st);
-    default: return launch_decode_t<D, 2, 2, 4, LAZY>(a, st);
+    case 32: return launch_decode_t<D, 4, 2, 1, LAZY>(a, st);
+    default: return launch_decode_t<D, 4, 2, 2, LAZY>(a, st);
   }
 }
 

@@ -12,14 +12,14 @@
 //
 // The records lie in the order in which lanes need them: chunk 32 j + lane of a record is 16
 // bytes of lane's own fragments, whose neighbouring codes (dims of K, tokens of V) are the
-// pairs of f16 that an operand register holds. So a warp copies, and reads back, 512 bytes in
-// a row without a bank conflict, a lane reads only what it copied itself (no barrier before
-// it), and a conversion of two codes (exact: every e4m3 value is an f16 value) gives a
+// pairs of f16 that an operand register holds. So a warp reads 512 bytes in a row without a bank
+// conflict, and a conversion of two codes (exact: every e4m3 value is an f16 value) gives a
 // register of an operand: no transposes, masks or shuffles of codes.
 #pragma once
 
 #include "decode_block.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace lazy {
 
@@ -36,34 +36,50 @@ struct Fp8Geom {
 // 16 (t + 4 (j / 2)) .. + 15. V: dims 8 (g + 8 (j % NG)) .. + 7 of the tokens 2 (t + 4 (j / NG))
 // and that + 1, side by side.
 
-// A warp's copy of one block's records into a ring stage: K's codes, V's, then both scales.
+// A team's ring of stages. A stage is one block's K and V records, which one lane copies with two bulk copies; `full`
+// counts their bytes, `empty` the team's warps that are done with them. `info` goes with a stage: valid
+// slots, and what else its reader wants to know of it.
+constexpr int kFp8Slots = 16;  // stages of a CTA's rings at most
+struct Fp8Bars {
+  uint64_t full[kFp8Slots], empty[kFp8Slots];
+  int info[kFp8Slots];
+};
+
 template <int D>
-struct Fp8Loader {
+struct Fp8Ring {
   using G = Fp8Geom<D>;
-  static constexpr int SCALES = 2 * G::CODES;
-  static constexpr int STAGE = SCALES + 16;
-  const uint8_t *k, *v, *scale;  // the pools at the KV head, plus the lane's offset
+  static constexpr int STAGE = 2 * G::REC;
+  const uint8_t *k, *v;  // the pools at the KV head
   uint32_t blk_bytes;
+  uint8_t* base;         // the team's first stage
+  Fp8Bars* bars;         // of the CTA
+  int first;             // index of the team's first stage among them
 
-  __device__ __forceinline__ Fp8Loader(const void* k_pool, const void* v_pool, int hkv, int kvh, int lane) {
-    blk_bytes = (uint32_t)hkv * G::REC;
-    const size_t head = (size_t)kvh * G::REC;
-    k = static_cast<const uint8_t*>(k_pool) + head + 16 * lane;
-    v = static_cast<const uint8_t*>(v_pool) + head + 16 * lane;
-    scale = static_cast<const uint8_t*>((lane & 1) ? v_pool : k_pool) + head + G::SCALE;
+  // Block ph (inside the pool) to stage `slot`, by one lane.
+  __device__ __forceinline__ void fill(int slot, int ph, int info) const {
+    uint64_t* bar = &bars->full[first + slot];
+    bars->info[first + slot] = info;  // seen by those who see the barrier's phase
+    mbar_arrive_expect_tx(bar, STAGE);
+    const uint32_t dst = smem_u32(base) + slot * STAGE, b = smem_u32(bar);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(k + (uint64_t)(uint32_t)ph * blk_bytes), "n"(G::REC), "r"(b)
+                 : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst + G::REC),
+                 "l"(v + (uint64_t)(uint32_t)ph * blk_bytes), "n"(G::REC), "r"(b)
+                 : "memory");
   }
-
-  // Block ph (inside the pool) to the stage at shared address `dst`.
-  __device__ __forceinline__ void operator()(uint32_t dst, int ph, int lane) const {
-    const uint8_t* kb = k + (uint64_t)(uint32_t)ph * blk_bytes;
-    const uint8_t* vb = v + (uint64_t)(uint32_t)ph * blk_bytes;
-    dst += 16 * lane;
-#pragma unroll
-    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + 512 * c, kb + 512 * c);
-#pragma unroll
-    for (int c = 0; c < G::CHUNKS; ++c) cp_async16(dst + G::CODES + 512 * c, vb + 512 * c);
-    if (lane < 2) cp_async4(dst + SCALES - 12 * lane, scale + (uint64_t)(uint32_t)ph * blk_bytes);
+  __device__ __forceinline__ bool wait_full(int slot, uint32_t parity, unsigned int* status) const {
+    return warp_wait(&bars->full[first + slot], parity, status);
   }
+  __device__ __forceinline__ bool wait_empty(int slot, uint32_t parity, unsigned int* status) const {
+    return warp_wait(&bars->empty[first + slot], parity, status);
+  }
+  // A wait gave up: copies of the loads first .. last - 1 (counted through the ring of R) still land, or not within
+  // 10 ms each, before the CTA ends.
+  __device__ __noinline__ void drain(uint32_t first_load, uint32_t last_load, uint32_t R, unsigned int* status) const {
+    for (uint32_t n = first_load; n < last_load; ++n) warp_wait(&bars->full[first + n % R], n / R & 1, status, 10000000ull);
+  }
+  __device__ __forceinline__ void release(int slot) const { mbar_arrive(&bars->empty[first + slot]); }
 };
 
 // Query rows of a warp: NT tiles of 8, or (HL = 1, NT = 1) one tile of 4 in the products' even
@@ -79,17 +95,38 @@ struct Fp8Rows {
 // Query fragments: product 4 jh + i of a tile takes, in lane (g, t), column g's dims
 // 16 (t + 4 jh) + 4 i + 0, 1 (b0) and + 2, 3 (b1). A block's scores, in log2 units, are the products'
 // sums times f and K's scale; f is the row's power of two, for the rows that the lane sees.
+// Four tiles' fragments (64 registers, d = 128) lie in shared memory, a lane its own.
 template <int D, int NT, int HL>
 struct Fp8Query {
-  uint32_t b[NT][D / 16][2];
+  static constexpr bool kShared = NT == 4;
+  static constexpr int BYTES = kShared ? 32 * NT * (D / 16) * 8 : 0;  // of a warp
+  uint32_t b[kShared ? 1 : NT][kShared ? 1 : D / 16][2];
+  uint32_t* s;  // the lane's first word of the warp's area
   float f[NT][HL];
+
+  // Product k's fragments of all tiles.
+  __device__ __forceinline__ void get(int k, uint32_t (&x)[NT][2]) const {
+    if constexpr (kShared) {
+#pragma unroll
+      for (int nt = 0; nt + 1 < NT; nt += 2) {  // 16 bytes: two tiles' fragments
+        const uint4 v = *reinterpret_cast<const uint4*>(s + 128 * (k * (NT / 2) + nt / 2));
+        x[nt][0] = v.x, x[nt][1] = v.y, x[nt + 1][0] = v.z, x[nt + 1][1] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt][0] = b[nt][k][0], x[nt][1] = b[nt][k][1];
+    }
+  }
+  __device__ __forceinline__ void set(int nt, int k, int h, uint32_t v) {
+    if constexpr (kShared) s[128 * (k * (NT / 2) + nt / 2) + 2 * (nt % 2) + h] = v;
+    else b[nt][k][h] = v;
+  }
 };
 
 // A lane reads the query rows (bf16) of the columns g of its tiles, row 8 nt + g (or g / 2); row(nt) points
 // at one (where there is none, at another). A row is scaled by mul: softmax scale and log2 e, over the row's power of
-// two, so that the largest value is in 1..2; 0 for a row that is not there.
-
-// A lane's own dims of its rows, loaded ahead of their use.
+// two, so that the largest value is in 1..2; 0 for a row that is not there. Here a lane's own dims of its rows,
+// loaded ahead of their use.
 template <int D, int NT>
 struct Fp8RawRows {
   uint4 x[NT][D / 32];
@@ -127,9 +164,10 @@ __device__ __forceinline__ void fp8_scale_rows(Fp8Query<D, NT, HL>& q, float (&m
 }
 
 // Rotates the rows by their angles: cs(nt) points at the (cos, sin) of the lane's row (shared
-// memory, 16-byte aligned). The rounding to f16 is off by 2^-11 of an operand.
-template <int D, int NT, int HL, typename RowFn, typename CsFn>
-__device__ __forceinline__ void fp8_build_query(Fp8Query<D, NT, HL>& q, const float (&mul)[NT], RowFn row, int lane, CsFn cs) {
+// memory, 16-byte aligned); put(nt, k, h, x) takes word h of tile nt's fragment for product k. The rounding to f16 is
+// off by 2^-11 of an operand.
+template <int D, int NT, int HL, typename RowFn, typename CsFn, typename PutFn>
+__device__ __forceinline__ void fp8_build_query(const float (&mul)[NT], RowFn row, int lane, CsFn cs, PutFn put) {
   constexpr int HALF = D / 2;
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -149,7 +187,7 @@ __device__ __forceinline__ void fp8_build_query(Fp8Query<D, NT, HL>& q, const fl
         const float4 c = *reinterpret_cast<const float4*>(ang + (base & (HALF - 1)) + 2 * h);
         const uint32_t b = pack_f16x2(fmaf(bf16_lo(x[h]), c.x, bf16_lo(y[h]) * (sgn * c.y)) * mul[nt],
                                       fmaf(bf16_hi(x[h]), c.z, bf16_hi(y[h]) * (sgn * c.w)) * mul[nt]);
-        q.b[nt][2 * i + h / 2][h % 2] = HL == 1 && (g & 1) ? 0u : b;
+        put(nt, 2 * i + h / 2, h % 2, HL == 1 && (g & 1) ? 0u : b);
       }
     }
   }
@@ -203,7 +241,8 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
   for (int b = 0; b < NB; ++b) partial |= nv[b] < kBlock;
   float2 scale[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) scale[b] = *reinterpret_cast<const float2*>(stage[b] + Fp8Loader<D>::SCALES);
+  for (int b = 0; b < NB; ++b)
+    scale[b] = make_float2(*reinterpret_cast<const float*>(stage[b] + G::SCALE), *reinterpret_cast<const float*>(stage[b] + G::REC + G::SCALE));
 
   // Scores of keys g and g + 8 of each block over f[block]: p[block][tile][2 key + row]. The blocks' and
   // tiles' products take turns, so that none waits for the one before it (one of each: even and odd
@@ -223,7 +262,9 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
           x[b][r][0] = v.x, x[b][r][1] = v.y, x[b][r][2] = v.z, x[b][r][3] = v.w;
         }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        uint32_t k[NT][2];
+        q.get(4 * jh + i, k);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t a[4];
@@ -231,57 +272,83 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
           e4m3x4_to_f16x4(x[b][1][i], a[1], a[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t* k = q.b[nt][4 * jh + i];
             float(&sum)[4] = CH == 2 && i % 2 ? odd : p[b][nt];
-            if (jh == 0 && i < CH) mma_16816_f16_first(sum, a, k[0], k[1]);
-            else mma_16816_f16(sum, a, k[0], k[1]);
+            if (jh == 0 && i < CH) mma_16816_f16_first(sum, a, k[nt][0], k[nt][1]);
+            else mma_16816_f16(sum, a, k[nt][0], k[nt][1]);
           }
         }
+      }
     }
     if (CH == 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[0][0][e] += odd[e];
   }
-  float f[NB][NT][HL];
+  uint64_t f[NB][NT];  // pairs: the lane's rows (HL = 1: its row, for both keys)
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) f[b][nt] = f2_mul(f2(q.f[nt][0], q.f[nt][HL - 1]), f2(scale[b].x, scale[b].x));
+  // a pair of sums: row 2t, 2t + 1 of key r (HL = 1: keys g and g + 8 of the row)
+  auto pair = [&](int b, int nt, int r) { return HL == 1 ? f2(p[b][nt][0], p[b][nt][2]) : f2(p[b][nt][2 * r], p[b][nt][2 * r + 1]); };
+  auto set_pair = [&](int b, int nt, int r, uint64_t v) {
+    const float2 x = f2_split(v);
+    p[b][nt][HL == 1 ? 0 : 2 * r] = x.x;
+    p[b][nt][HL == 1 ? 2 : 2 * r + 1] = x.y;
+  };
+  auto mask = [&](float to) {  // the scores of slots that are no keys
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (g + 8 * (e / 2) >= nv[b])
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) p[b][nt][e] = to;
+  };
+  float sm = 0.f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (NB > 1 && nv[b] == 0) scale[b].y = 0.f;
+    sm = fmaxf(sm, scale[b].y);
+  }
+  const bool first = st.lim == 0.f;  // the same in all lanes
+  if (first) {
+    if (partial) mask(-INFINITY);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < HL; ++c) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)  // (-inf times a factor that is 0 would be NaN)
+          x = fmaxf(x, fmaxf(p[b][nt][c], p[b][nt][2 + c]) * fmaxf(q.f[nt][c] * scale[b].x, 0x1p-126f));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        st.nm[nt][c] = kFp8Lift - x;
+      }
+  }
+  // Exponents s + nm.
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < HL; ++c) f[b][nt][c] = q.f[nt][c] * scale[b].x;
+      for (int r = 0; r < HL; ++r) set_pair(b, nt, r, f2_fma(pair(b, nt, r), f[b][nt], f2(st.nm[nt][0], st.nm[nt][HL - 1])));
   if (partial) {
     asm volatile("" ::: "memory");  // a branch, not selects on every block
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (nv[b] == 0) scale[b] = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int c = 0; c < HL; ++c) f[b][nt][c] = fmaxf(q.f[nt][c] * scale[b].x, 0x1p-126f);  // -inf stays -inf
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (g + 8 * (e / 2) >= nv[b]) p[b][nt][e] = -INFINITY;
-      }
-    }
+    mask(-INFINITY);
   }
 
-  // Maxima and the V-scale reference: refreshed together, when some row's weight or a scale would outgrow
-  // its reference (a vote; the cross-lane maxima only then).
-  float sm = scale[0].y;
+  // References are refreshed together, when some weight or scale would outgrow its own (a vote; the
+  // cross-lane maxima only then).
+  float high = p[0][0][0];
 #pragma unroll
-  for (int b = 1; b < NB; ++b) sm = fmaxf(sm, scale[b].y);
-  bool grow = sm > st.lim;
-  auto top = [&](int nt, int c) {  // the lane's greatest score, over 2^-nm
-    float x = fmaf(fmaxf(p[0][nt][c], p[0][nt][2 + c]), f[0][nt][c], st.nm[nt][c]);
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int b = 1; b < NB; ++b) x = fmaxf(x, fmaf(fmaxf(p[b][nt][c], p[b][nt][2 + c]), f[b][nt][c], st.nm[nt][c]));
-    return x;
-  };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < HL; ++c) grow |= top(nt, c) > kFp8Most;
-  if (__any_sync(0xffffffffu, grow)) {
+    for (int nt = 0; nt < NT; ++nt) {
+      if constexpr (HL == 1) high = fmax3(high, p[b][nt][0], p[b][nt][2]);
+      else high = fmaxf(fmax3(high, p[b][nt][0], p[b][nt][1]), fmaxf(p[b][nt][2], p[b][nt][3]));
+    }
+  if (__any_sync(0xffffffffu, high > kFp8Most || sm > st.lim)) {
     if (sm > st.lim) {
       // 2^-e for a scale 2^e. Kept a normal number.
       const uint32_t ex = min(max(__float_as_uint(sm) >> 23, 4u), 250u);
@@ -299,15 +366,17 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < HL; ++c) {
-        float x = fmaxf(p[0][nt][c], p[0][nt][2 + c]) * f[0][nt][c];
+        float x = -INFINITY;
 #pragma unroll
-        for (int b = 1; b < NB; ++b) x = fmaxf(x, fmaxf(p[b][nt][c], p[b][nt][2 + c]) * f[b][nt][c]);
+        for (int b = 0; b < NB; ++b) x = fmax3(x, p[b][nt][c], p[b][nt][2 + c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        if (x + st.nm[nt][c] > kFp8Most) {
-          const float nm = kFp8Lift - x, alpha = fast_ex2(nm - st.nm[nt][c]);  // 0 for the first key
-          st.nm[nt][c] = nm;
+        if (x > kFp8Most) {
+          const float down = kFp8Lift - x, alpha = fast_ex2(down);
+          st.nm[nt][c] += down;
           st.l[nt][c] *= alpha;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) p[b][nt][c] += down, p[b][nt][2 + c] += down;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             st.o[i][nt][c] *= alpha;
@@ -325,17 +394,21 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
   for (int b = 0; b < NB; ++b) {
     const __half2 vs = __float2half2_rn(scale[b].y * st.inv);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 4; e += HL == 1 ? 2 : 1) p[b][nt][e] = fast_ex2(p[b][nt][e]);
+      if constexpr (HL == 1) {
+        st.l[nt][0] += p[b][nt][0] + p[b][nt][2];
+      } else {
+        const float2 sum = f2_split(f2_add(f2(st.l[nt][0], st.l[nt][HL - 1]), f2_add(pair(b, nt, 0), pair(b, nt, 1))));
+        st.l[nt][0] = sum.x, st.l[nt][HL - 1] = sum.y;
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-#pragma unroll
-        for (int c = 0; c < HL; ++c) {
-          p[b][nt][2 * r + c] = fast_ex2(fmaf(p[b][nt][2 * r + c], f[b][nt][c], st.nm[nt][c]));
-          st.l[nt][c] += p[b][nt][2 * r + c];
-        }
-        const __half2 w = __hmul2(__floats2half2_rn(p[b][nt][2 * r], HL == 1 ? 0.f : p[b][nt][2 * r + HL - 1]), vs);
+        const __half2 w = __hmul2(__floats2half2_rn(p[b][nt][2 * r], HL == 1 ? 0.f : p[b][nt][2 * r + 1]), vs);
         pb[b][nt][r] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&w));
       }
+    }
   }
 
   // Products 2 w and 2 w + 1 take the words w of the lane's chunks (d = 64: w and w + 2).
@@ -345,7 +418,7 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < G::NG; ++j) v4[r][j] = reinterpret_cast<const uint4*>(stage[b] + G::CODES)[lane + 32 * (G::NG * r + j)];
+      for (int j = 0; j < G::NG; ++j) v4[r][j] = reinterpret_cast<const uint4*>(stage[b] + G::REC)[lane + 32 * (G::NG * r + j)];
     if (partial) {  // codes of slots without a key may be NaN
       asm volatile("" ::: "memory");
 #pragma unroll
