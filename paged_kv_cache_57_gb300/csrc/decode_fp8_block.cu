@@ -156,17 +156,16 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
         ring.drain(n_th, used + min(nk, i + AHEAD + 1), R, a.status);
         break;
       }
-      const uint8_t* stage[1] = {ring.base + slot * C::SLOT};
       const int info = bars.info[team * R + slot];
-      int nv[1] = {kBlock};
+      int nv = kBlock;
       if (info != kBlock) {
-        nv[0] = info & 31;
+        nv = info & 31;
         if (LAZY && info > kNewDoc) {
           const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
           if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
         }
       }
-      if (nv[0] > 0) fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
+      if (nv > 0) fp8_attend<D, NT, HL>(ring.base + slot * C::SLOT, nv, q, st, lane);
       __syncwarp();
       if (RT > 1 && lane == 0) ring.release(slot);
     }
@@ -361,9 +360,8 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
       ring.drain(i, min(nk, i + AHEAD + 1), R, a.status);
       break;
     }
-    const uint8_t* stage[1] = {ring.base + slot * C::SLOT};
-    const int nv[1] = {it.bars.info[team * R + slot]};
-    if (nv[0] > 0) fp8_attend<D, NT, HL, 1>(stage, nv, q, st, lane);
+    const int nv = it.bars.info[team * R + slot];
+    if (nv > 0) fp8_attend<D, NT, HL>(ring.base + slot * C::SLOT, nv, q, st, lane);
     __syncwarp();
     if (RT > 1 && lane == 0) ring.release(slot);
   }

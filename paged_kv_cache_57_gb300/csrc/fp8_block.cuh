@@ -229,87 +229,65 @@ __device__ __forceinline__ void fp8_init(Fp8State<D, NT, HL>& st) {
 // kFp8MaxRun = 16384 blocks a sum is off by 2^-11 or so of its size, a quarter of the output's
 // rounding. No warp sums more: pieces, ranges and items are cut there.
 
-// NB blocks of one document in ring stages: the first nv[b] slots of block b are keys (0 .. 16, the
-// same in all lanes; 0: the block is not there); what the others hold does not matter.
-template <int D, int NT, int HL, int NB>
-__device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], const int (&nv)[NB], const Fp8Query<D, NT, HL>& q,
-                                           Fp8State<D, NT, HL>& st, int lane) {
+// A block in its stage: the first nv slots are keys (1 .. 16, the same in all lanes); what the others hold does not
+// matter.
+template <int D, int NT, int HL>
+__device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const Fp8Query<D, NT, HL>& q, Fp8State<D, NT, HL>& st,
+                                           int lane) {
   using G = Fp8Geom<D>;
   const int g = lane >> 2, t = lane & 3;
-  bool partial = false;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) partial |= nv[b] < kBlock;
-  float2 scale[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-    scale[b] = make_float2(*reinterpret_cast<const float*>(stage[b] + G::SCALE), *reinterpret_cast<const float*>(stage[b] + G::REC + G::SCALE));
+  const bool partial = nv < kBlock;
+  const float ks = *reinterpret_cast<const float*>(stage + G::SCALE), vs = *reinterpret_cast<const float*>(stage + G::REC + G::SCALE);
 
-  // Scores of keys g and g + 8 of each block over f[block]: p[block][tile][2 key + row]. The blocks' and
-  // tiles' products take turns, so that none waits for the one before it (one of each: even and odd
-  // ones).
-  constexpr int CH = NB * NT == 1 ? 2 : 1;
-  float p[NB][NT][4];
+  // Scores of keys g and g + 8 over f: p[tile][2 key + row]. The tiles' products take turns, so that
+  // none waits for the one before it (one tile: even and odd ones).
+  constexpr int CH = NT == 1 ? 2 : 1;
+  float p[NT][4];
   {
     float odd[4];
 #pragma unroll
     for (int jh = 0; jh < G::NG; ++jh) {
-      uint32_t x[NB][2][4];
+      uint32_t x[2][4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint4 v = reinterpret_cast<const uint4*>(stage[b])[lane + 64 * jh + 32 * r];
-          x[b][r][0] = v.x, x[b][r][1] = v.y, x[b][r][2] = v.z, x[b][r][3] = v.w;
-        }
+      for (int r = 0; r < 2; ++r) {
+        const uint4 v = reinterpret_cast<const uint4*>(stage)[lane + 64 * jh + 32 * r];
+        x[r][0] = v.x, x[r][1] = v.y, x[r][2] = v.z, x[r][3] = v.w;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t k[NT][2];
+        uint32_t k[NT][2], a[4];
         q.get(4 * jh + i, k);
+        e4m3x4_to_f16x4(x[0][i], a[0], a[2]);
+        e4m3x4_to_f16x4(x[1][i], a[1], a[3]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint32_t a[4];
-          e4m3x4_to_f16x4(x[b][0][i], a[0], a[2]);
-          e4m3x4_to_f16x4(x[b][1][i], a[1], a[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float(&sum)[4] = CH == 2 && i % 2 ? odd : p[b][nt];
-            if (jh == 0 && i < CH) mma_16816_f16_first(sum, a, k[nt][0], k[nt][1]);
-            else mma_16816_f16(sum, a, k[nt][0], k[nt][1]);
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          float(&sum)[4] = CH == 2 && i % 2 ? odd : p[nt];
+          if (jh == 0 && i < CH) mma_16816_f16_first(sum, a, k[nt][0], k[nt][1]);
+          else mma_16816_f16(sum, a, k[nt][0], k[nt][1]);
         }
       }
     }
     if (CH == 2)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[0][0][e] += odd[e];
+      for (int e = 0; e < 4; ++e) p[0][e] += odd[e];
   }
-  uint64_t f[NB][NT];  // pairs: the lane's rows (HL = 1: its row, for both keys)
+  uint64_t f[NT];  // pairs: the lane's rows (HL = 1: its row, for both keys)
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) f[b][nt] = f2_mul(f2(q.f[nt][0], q.f[nt][HL - 1]), f2(scale[b].x, scale[b].x));
+  for (int nt = 0; nt < NT; ++nt) f[nt] = f2_mul(f2(q.f[nt][0], q.f[nt][HL - 1]), f2(ks, ks));
   // a pair of sums: row 2t, 2t + 1 of key r (HL = 1: keys g and g + 8 of the row)
-  auto pair = [&](int b, int nt, int r) { return HL == 1 ? f2(p[b][nt][0], p[b][nt][2]) : f2(p[b][nt][2 * r], p[b][nt][2 * r + 1]); };
-  auto set_pair = [&](int b, int nt, int r, uint64_t v) {
+  auto pair = [&](int nt, int r) { return HL == 1 ? f2(p[nt][0], p[nt][2]) : f2(p[nt][2 * r], p[nt][2 * r + 1]); };
+  auto set_pair = [&](int nt, int r, uint64_t v) {
     const float2 x = f2_split(v);
-    p[b][nt][HL == 1 ? 0 : 2 * r] = x.x;
-    p[b][nt][HL == 1 ? 2 : 2 * r + 1] = x.y;
+    p[nt][HL == 1 ? 0 : 2 * r] = x.x;
+    p[nt][HL == 1 ? 2 : 2 * r + 1] = x.y;
   };
   auto mask = [&](float to) {  // the scores of slots that are no keys
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int e = 0; e < 4; ++e)
+      if (g + 8 * (e / 2) >= nv)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (g + 8 * (e / 2) >= nv[b])
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) p[b][nt][e] = to;
+        for (int nt = 0; nt < NT; ++nt) p[nt][e] = to;
   };
-  float sm = 0.f;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    if (NB > 1 && nv[b] == 0) scale[b].y = 0.f;
-    sm = fmaxf(sm, scale[b].y);
-  }
   const bool first = st.lim == 0.f;  // the same in all lanes
   if (first) {
     if (partial) mask(-INFINITY);
@@ -317,10 +295,7 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < HL; ++c) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)  // (-inf times a factor that is 0 would be NaN)
-          x = fmaxf(x, fmaxf(p[b][nt][c], p[b][nt][2 + c]) * fmaxf(q.f[nt][c] * scale[b].x, 0x1p-126f));
+        float x = fmaxf(p[nt][c], p[nt][2 + c]) * fmaxf(q.f[nt][c] * ks, 0x1p-126f);  // (-inf times 0 would be NaN)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
         st.nm[nt][c] = kFp8Lift - x;
@@ -328,11 +303,9 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
   }
   // Exponents s + nm.
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int r = 0; r < HL; ++r) set_pair(b, nt, r, f2_fma(pair(b, nt, r), f[b][nt], f2(st.nm[nt][0], st.nm[nt][HL - 1])));
+    for (int r = 0; r < HL; ++r) set_pair(nt, r, f2_fma(pair(nt, r), f[nt], f2(st.nm[nt][0], st.nm[nt][HL - 1])));
   if (partial) {
     asm volatile("" ::: "memory");  // a branch, not selects on every block
     mask(-INFINITY);
@@ -340,18 +313,16 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
 
   // References are refreshed together, when some weight or scale would outgrow its own (a vote; the
   // cross-lane maxima only then).
-  float high = p[0][0][0];
+  float high = p[0][0];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if constexpr (HL == 1) high = fmax3(high, p[b][nt][0], p[b][nt][2]);
-      else high = fmaxf(fmax3(high, p[b][nt][0], p[b][nt][1]), fmaxf(p[b][nt][2], p[b][nt][3]));
-    }
-  if (__any_sync(0xffffffffu, high > kFp8Most || sm > st.lim)) {
-    if (sm > st.lim) {
+  for (int nt = 0; nt < NT; ++nt) {
+    if constexpr (HL == 1) high = fmaxf(high, p[nt][2]);
+    else high = fmaxf(fmax3(high, p[nt][0], p[nt][1]), fmaxf(p[nt][2], p[nt][3]));
+  }
+  if (__any_sync(0xffffffffu, high > kFp8Most || vs > st.lim)) {
+    if (vs > st.lim) {
       // 2^-e for a scale 2^e. Kept a normal number.
-      const uint32_t ex = min(max(__float_as_uint(sm) >> 23, 4u), 250u);
+      const uint32_t ex = min(max(__float_as_uint(vs) >> 23, 4u), 250u);
       const float inv = __uint_as_float((254u - ex) << 23), r = inv / st.inv;
       st.inv = inv;
       st.lim = kFp8ScaleTop / inv;
@@ -366,17 +337,14 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < HL; ++c) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) x = fmax3(x, p[b][nt][c], p[b][nt][2 + c]);
+        float x = fmaxf(p[nt][c], p[nt][2 + c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
         if (x > kFp8Most) {
           const float down = kFp8Lift - x, alpha = fast_ex2(down);
           st.nm[nt][c] += down;
           st.l[nt][c] *= alpha;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) p[b][nt][c] += down, p[b][nt][2 + c] += down;
+          p[nt][c] += down, p[nt][2 + c] += down;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             st.o[i][nt][c] *= alpha;
@@ -389,61 +357,55 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* const (&stage)[NB], co
   // Weights, their sum in fp32, and weights (rounded to f16: off by 2^-11, next to the codes' 4 bits)
   // times V's scale over its reference, a power of two. The k-order of O^T += C_v^T P^T is tokens
   // 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
-  uint32_t pb[NB][NT][2];
+  uint32_t pb[NT][2];
+  const __half2 v_scale = __float2half2_rn(vs * st.inv);
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const __half2 vs = __float2half2_rn(scale[b].y * st.inv);
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int e = 0; e < 4; e += HL == 1 ? 2 : 1) p[nt][e] = fast_ex2(p[nt][e]);
+    if constexpr (HL == 1) {
+      st.l[nt][0] += p[nt][0] + p[nt][2];
+    } else {
+      const float2 sum = f2_split(f2_add(f2(st.l[nt][0], st.l[nt][HL - 1]), f2_add(pair(nt, 0), pair(nt, 1))));
+      st.l[nt][0] = sum.x, st.l[nt][HL - 1] = sum.y;
+    }
 #pragma unroll
-      for (int e = 0; e < 4; e += HL == 1 ? 2 : 1) p[b][nt][e] = fast_ex2(p[b][nt][e]);
-      if constexpr (HL == 1) {
-        st.l[nt][0] += p[b][nt][0] + p[b][nt][2];
-      } else {
-        const float2 sum = f2_split(f2_add(f2(st.l[nt][0], st.l[nt][HL - 1]), f2_add(pair(b, nt, 0), pair(b, nt, 1))));
-        st.l[nt][0] = sum.x, st.l[nt][HL - 1] = sum.y;
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const __half2 w = __hmul2(__floats2half2_rn(p[b][nt][2 * r], HL == 1 ? 0.f : p[b][nt][2 * r + 1]), vs);
-        pb[b][nt][r] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&w));
-      }
+    for (int r = 0; r < 2; ++r) {
+      const __half2 w = __hmul2(__floats2half2_rn(p[nt][2 * r], HL == 1 ? 0.f : p[nt][2 * r + 1]), v_scale);
+      pb[nt][r] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&w));
     }
   }
 
   // Products 2 w and 2 w + 1 take the words w of the lane's chunks (d = 64: w and w + 2).
+  uint4 v4[2][G::NG];  // [tokens 2t, 2t + 1 or 2t + 8, 2t + 9][dims]
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    uint4 v4[2][G::NG];  // [tokens 2t, 2t + 1 or 2t + 8, 2t + 9][dims]
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int j = 0; j < G::NG; ++j) v4[r][j] = reinterpret_cast<const uint4*>(stage + G::REC)[lane + 32 * (G::NG * r + j)];
+  if (partial) {  // codes of slots without a key may be NaN
+    asm volatile("" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < G::NG; ++j) v4[r][j] = reinterpret_cast<const uint4*>(stage[b] + G::REC)[lane + 32 * (G::NG * r + j)];
-    if (partial) {  // codes of slots without a key may be NaN
-      asm volatile("" ::: "memory");
+    for (int r = 0; r < 2; ++r) {
+      const int tok = 2 * t + 8 * r;
+      const uint32_t keep = (tok < nv ? 0x00ff00ffu : 0u) | (tok + 1 < nv ? 0xff00ff00u : 0u);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int tok = 2 * t + 8 * r;
-        const uint32_t keep = (tok < nv[b] ? 0x00ff00ffu : 0u) | (tok + 1 < nv[b] ? 0xff00ff00u : 0u);
+      for (int j = 0; j < G::NG; ++j) v4[r][j].x &= keep, v4[r][j].y &= keep, v4[r][j].z &= keep, v4[r][j].w &= keep;
+    }
+  }
 #pragma unroll
-        for (int j = 0; j < G::NG; ++j) v4[r][j].x &= keep, v4[r][j].y &= keep, v4[r][j].z &= keep, v4[r][j].w &= keep;
-      }
+  for (int w = 0; w < D / 32; ++w) {
+    uint32_t a[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t lo[4] = {v4[r][0].x, v4[r][0].y, v4[r][0].z, v4[r][0].w};
+      const uint32_t hi[4] = {v4[r][G::NG - 1].x, v4[r][G::NG - 1].y, v4[r][G::NG - 1].z, v4[r][G::NG - 1].w};
+      e4m3x4_to_f16x4(lo[w], a[0][2 * r], a[1][2 * r]);
+      e4m3x4_to_f16x4(hi[G::NG == 2 ? w : w + 2], a[0][2 * r + 1], a[1][2 * r + 1]);
     }
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      uint32_t a[2][4];
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t lo[4] = {v4[r][0].x, v4[r][0].y, v4[r][0].z, v4[r][0].w};
-        const uint32_t hi[4] = {v4[r][G::NG - 1].x, v4[r][G::NG - 1].y, v4[r][G::NG - 1].z, v4[r][G::NG - 1].w};
-        e4m3x4_to_f16x4(lo[w], a[0][2 * r], a[1][2 * r]);
-        e4m3x4_to_f16x4(hi[G::NG == 2 ? w : w + 2], a[0][2 * r + 1], a[1][2 * r + 1]);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(st.o[2 * w + e][nt], a[e], pb[b][nt][0], pb[b][nt][1]);
-    }
+      for (int nt = 0; nt < NT; ++nt) mma_16816_f16(st.o[2 * w + e][nt], a[e], pb[nt][0], pb[nt][1]);
   }
 }
 

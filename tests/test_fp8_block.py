@@ -106,6 +106,20 @@ def test_plan_keeps_items_of_at_most_64_rows():
     assert (items[:, 4] * 16 <= 64).all() and (items[:, 4] > 1).any()
 
 
+def test_long_sequences_and_items_are_cut():
+    # a warp adds up 16384 blocks at most: four teams of warps a CTA up to 32 query rows, two for more
+    L = _L()
+    for hq, most in ((4, 65536), (32, 65536), (33, 32768), (64, 32768)):
+        for wide in (most, most + 1):
+            p = _params(num_seqs=1, num_q_heads=hq, num_kv_heads=1, num_pool_blocks=8, max_blocks_per_seq=wide, num_splits=1)
+            assert (L.decode_workspace_bytes(p) > 0) == (wide > most), (hq, wide)
+    n = 40000
+    p = _params(num_seqs=1, num_q_heads=4, num_kv_heads=1, num_pool_blocks=n, max_blocks_per_seq=n)
+    i32 = lambda *x: np.array(x, dtype=np.int32)
+    items, _ = L.plan_shared_host(p, 1, i32(0, 1), i32(0), i32(16 * n), i32(0, n), np.arange(n, dtype=np.int32), chunk_blocks=n)
+    assert items[:, 2].max() == 16384 and items[:, 2].sum() == n
+
+
 # ---------------------------------------------------------------- the models
 
 @pytest.mark.parametrize("d", [64, 128])

@@ -393,9 +393,9 @@ def test_decode_query_sizes(qscale):
     check(decode(dv, kp, vp), M.attention(w, kv, vv), f"queries times {qscale}")
 
 
-# more than 2048 blocks of a warp: sums that are set aside, with maxima and V scales that keep growing behind them
+# thousands of blocks of a warp, with maxima and V scales that keep growing
 @pytest.mark.parametrize("hq,d", [(3, 128), (8, 64), (16, 64), (32, 64), (48, 128)])
-def test_long_runs_are_set_aside(hq, d):
+def test_long_runs(hq, d):
     docs = 2 if hq <= 16 else 1
     w = W.decode_zipf("f8long", batch=1, hq=hq, hkv=1, d=d, docs_per_seq=docs, doc_tokens=80000, pool_docs=docs, zipf_s=0.5, share=False,
                       seed=1832)
@@ -411,6 +411,22 @@ def test_long_runs_are_set_aside(hq, d):
     check(shared(dv, kp, vp, 5000), ref, "shared")
     dv.p.num_splits = 0
     check(decode(dv, kp, vp), ref, "split")
+
+
+def test_a_million_tokens():
+    # more blocks than the warps of a CTA add up: cut, whatever num_splits and chunk_blocks say
+    L = la()
+    w = W.decode_zipf("f8million", batch=1, hq=3, hkv=1, d=64, docs_per_seq=34, doc_tokens=32000, pool_docs=1, zipf_s=0.0, seed=1834)
+    w.v_pool = (1 + w.v_pool.double() / 4).to(torch.bfloat16)
+    dv, kp, vp, kv, vv = on_device(w, num_splits=1, id_bits=11)
+    assert dv.p.max_blocks_per_seq == 68000 and L.decode_workspace_bytes(dv.p) > 0
+    ref = M.attention(w, kv, vv)
+    check(decode(dv, kp, vp), ref, "per sequence")
+    check(shared(dv, kp, vp, 60000), ref, "shared")
+    plan = shared_plan(dv)
+    plan.items.view(-1)[2] = 16385  # an item longer than a warp adds up: refused
+    L.decode_shared(dv.p, dv.q, kp, vp, dv.words, dv.q_pos, dv.rope, plan)
+    assert L.device_status(clear=True) == L.LAZY_DEV_LAYOUT
 
 
 def test_low_scores_beside_parts_without_keys():
@@ -571,3 +587,45 @@ def test_width_of_the_table_changes_nothing(batch, hq, hkv, d, hi):
         p2 = la().make_params(num_seqs=batch, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, num_pool_blocks=dv.p.num_pool_blocks,
                               max_blocks_per_seq=wide, rope_theta=dw.rope_theta, kv_dtype=KIND)
         check(L.decode(p2, dv.q, kp, vp, words, dv.seq_lens, dv.q_pos, dv.rope), ref, f"{wide} words a sequence")
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (64, 4, 128), (64, 1, 64)])
+def test_captured_decodes_follow_their_inputs(hq, hkv, d):
+    # both decodes in one graph on one workspace; queries, lengths and positions change between replays
+    L = la()
+    w = W.decode_zipf("f8graph", batch=12, hq=hq, hkv=hkv, d=d, docs_per_seq=4, doc_tokens=320, pool_docs=6, zipf_s=1.0, suffix_tokens=40,
+                      seed=1861)
+    dv, kp, vp, kv, vv = on_device(w)
+    plan = shared_plan(dv)
+    n = max(L.decode_workspace_bytes(dv.p), L.decode_shared_workspace_bytes(dv.p, plan.num_slots))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    one, two = torch.empty_like(dv.q), torch.empty_like(dv.q)
+
+    def both():
+        L.decode(dv.p, dv.q, kp, vp, dv.words, dv.seq_lens, dv.q_pos, dv.rope, out=one, workspace=ws)
+        L.decode_shared(dv.p, dv.q, kp, vp, dv.words, dv.q_pos, dv.rope, plan, out=two, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    g = torch.Generator().manual_seed(5)
+    for i in range(3):
+        w.q = torch.randn(w.q.shape, generator=g).to(torch.bfloat16)
+        w.q_pos = w.q_pos + 17 * i
+        dv.q.copy_(w.q)
+        dv.q_pos.copy_(torch.from_numpy(np.asarray(w.q_pos, dtype=np.int32)))
+        ws.fill_(0xff)  # nothing is left over from a replay
+        graph.replay()
+        ref = M.attention(w, kv, vv)
+        check(one, ref, f"replay {i}")
+        check(two, ref, f"replay {i}, shared runs")
+    cut = dv.seq_lens.clone()  # shorter sequences: as an eager call of those lengths
+    dv.seq_lens.copy_(torch.clamp(cut - 333, min=0))
+    dv.seq_lens[3] = 0
+    graph.replay()
+    assert torch.equal(one.view(torch.int16), decode(dv, kp, vp).view(torch.int16)) and not one[3].any()
