@@ -256,7 +256,7 @@ constexpr int kSharedFp8BlockSlots = 3 * 152;
 int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_blocks, int num_docs, const int32_t* seg_indptr,
                      const int32_t* seg_doc, const int32_t* seg_len, const int32_t* doc_block_indptr,
                      const int32_t* doc_blocks, int chunk_blocks, int auto_items, int capacity, int32_t* items,
-                     int32_t* slot_indptr, int32_t* counts, bool spread_small = false, bool cost_of_rows = false);
+                     int32_t* slot_indptr, int32_t* counts, bool spread_small = false, bool cost_of_rows = false, bool alternate = false);
 
 // Every launcher returns the cudaError_t of its launch.
 // explicit_w (host, head_dim/2 rates in radians per position) overrides theta and scaling.

@@ -27,6 +27,11 @@
 // launch does not end on the long ones (32 x 16384 Zipf-drawn tokens 136 -> 129 us, 8 x 16384
 // of 256-block documents 44 -> 39; cutting wide items shorter instead cost more in partials
 // than it evened out, 143 us).
+// The kernel of e4m3 pools with block scales (alternate) is bound by memory on items of few rows and by
+// instructions on wide ones: the items longer than half the longest are taken from the two ends of that
+// order in turn, so that an SM has both at once; the short ones still come last (the same 32
+// sequences 120 -> 113 us, with 48 or 32 blocks an item 139 -> 135 and 136; 64 x 4096 tokens with private
+// tails of 4 blocks 50 -> 49; all items in two mixed streams 137 and 64).
 #include <algorithm>
 #include <utility>
 #include <vector>
@@ -38,7 +43,7 @@ namespace lazy {
 int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_blocks, int num_docs, const int32_t* seg_indptr,
                      const int32_t* seg_doc, const int32_t* seg_len, const int32_t* doc_block_indptr,
                      const int32_t* doc_blocks, int chunk_blocks, int auto_items, int capacity, int32_t* items,
-                     int32_t* slot_indptr, int32_t* counts, bool spread_small, bool cost_of_rows) {
+                     int32_t* slot_indptr, int32_t* counts, bool spread_small, bool cost_of_rows, bool alternate) {
   struct Occ {
     int seq, b0;
   };
@@ -133,6 +138,13 @@ int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_bl
   }
   if ((int64_t)its.size() > capacity) return LAZY_ERR_WORKSPACE;
   std::stable_sort(its.begin(), its.end(), [](const Item& x, const Item& y) { return x.cost > y.cost; });
+  if (alternate) {
+    int longest = 0;
+    for (const Item& it : its) longest = std::max(longest, it.nb);
+    const auto end = std::stable_partition(its.begin(), its.end(), [&](const Item& it) { return 2 * it.nb > longest; });
+    const std::vector<Item> big(its.begin(), end);
+    for (size_t k = 0; k < big.size(); ++k) its[k] = k % 2 ? big[big.size() - 1 - k / 2] : big[k / 2];
+  }
   // Items of at most kSmall blocks (a sequence's private tail, say) cost an item's fixed
   // latency for little data; spread evenly through the launch instead of ending it, they
   // run beside streaming items, and the launch does not end on a wave of them.

@@ -106,6 +106,23 @@ def test_plan_keeps_items_of_at_most_64_rows():
     assert (items[:, 4] * 16 <= 64).all() and (items[:, 4] > 1).any()
 
 
+def test_plan_takes_long_items_from_both_ends():
+    L = _L()
+    w = W.decode_zipf("order8", batch=16, hq=16, hkv=2, d=128, docs_per_seq=4, doc_tokens=640, pool_docs=9, zipf_s=1.0, suffix_tokens=50, seed=78)
+    p = _params(num_seqs=16, num_q_heads=16, num_kv_heads=2, num_pool_blocks=w.num_pool_blocks, max_blocks_per_seq=w.max_blocks_per_seq)
+    for chunk in (0, 3, 40):
+        items, slots = L.plan_shared_host(p, len(w.doc_len), w.seg_indptr, w.seg_doc, w.seg_len, w.doc_block_indptr, w.doc_blocks, chunk_blocks=chunk)
+        nb, rows = items[:, 2], items[:, 4] * 8
+        cost = nb * np.array([1, 2, 4])[np.searchsorted([8, 16], rows)]
+        long = 2 * nb > nb.max()
+        n = int(long.sum())
+        assert 0 < n and long[:n].all() and (np.diff(cost[n:]) <= 0).all()
+        assert (np.diff(cost[:n:2]) <= 0).all() and (np.diff(cost[1:n:2]) >= 0).all() and cost[:n:2].min() >= cost[1:n:2].max(initial=0)
+        # every member's slots once, in the order of its partials
+        taken = [(int(m[0]), int(m[2])) for it in items for m in it[8:8 + 4 * it[4]].reshape(-1, 4)]
+        assert sorted(x for _, x in taken) == list(range(int(slots[-1]))) and all(slots[s] <= x < slots[s + 1] for s, x in taken)
+
+
 def test_long_sequences_and_items_are_cut():
     # a warp adds up 16384 blocks at most: four teams of warps a CTA up to 32 query rows, two for more
     L = _L()
