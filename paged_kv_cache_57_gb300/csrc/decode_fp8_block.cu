@@ -322,10 +322,12 @@ __device__ __forceinline__ void shared_fp8_rows(const SharedDecodeArgs& a, const
     for (int j = rt; j < min(AHEAD, nk); j += RT)
       if (lane == 0) {
         const int id = ids[kb0 + j];
-        ring.fill(j, id >= 0 && id < a.num_pool_blocks ? id : 0, kb0 + j == nblk - 1 ? last_nv : kBlock);
+        ring.fill(j, id >= 0 && id < a.num_pool_blocks ? id : 0, 0);
       }
     describe(0);
     load_words(32);
+    __syncwarp();
+    if (lane < AHEAD && (lane & (RT - 1)) == rt) it.bars.info[team * R + lane] = c_nv;  // seen behind the barriers below
   } else {
     for (int j = 0; j < AHEAD; ++j) ok &= fill(j);
   }

@@ -498,6 +498,51 @@ def test_device_errors_are_reported():
     assert L.device_status(clear=True) == L.LAZY_DEV_LAYOUT
 
 
+# a block whose word and whose item disagree, or which is not in the pool, is left out of shared runs too
+@pytest.mark.parametrize("batch,hq", [(1, 4), (1, 16), (3, 8), (4, 16)])
+@pytest.mark.parametrize("at", [0, 1, 4, 9])
+def test_shared_items_leave_bad_blocks_out(batch, hq, at):
+    L = la()
+    w = W.decode_zipf("f8badrec", batch=batch, hq=hq, hkv=1, d=128, docs_per_seq=1, doc_tokens=160, pool_docs=1, zipf_s=0.5, seed=1871)
+    blocks = w.doc_blocks[:10].astype(int)
+    dv, kp, vp, kv, vv = on_device(w)
+
+    def kept(out, what):  # what the other nine blocks give
+        want = torch.zeros((batch, hq, 128), dtype=torch.float64, device="cuda")
+        bound = torch.zeros_like(want)
+        keep = torch.arange(160, device="cuda") // 16 != at
+        f = torch.as_tensor(w.rope_theta ** (-2.0 * np.arange(64) / 128), dtype=torch.float64, device="cuda")
+        k = kv[torch.as_tensor(blocks, device="cuda")].reshape(160, 128)[keep]
+        v = vv[torch.as_tensor(blocks, device="cuda")].reshape(160, 128)[keep]
+        for b in range(batch):
+            d = (float(w.q_pos[b]) - float(w.seq_pos0[b])) * f
+            q = w.q[b].double().cuda()
+            r = torch.cat((q[:, :64] * d.cos() - q[:, 64:] * d.sin(), q[:, :64] * d.sin() + q[:, 64:] * d.cos()), -1)
+            wt = torch.softmax(r @ k.T * 128 ** -0.5, -1)
+            want[b] = wt @ v
+            # the terms of the model's bound: query's rounding (2^-11 of each dim: scores off by e, weights by 2 e and a
+            # little), weights' (2^-11), sums (2^-18), f16's least step, the output's (2^-8)
+            e = 128 ** -0.5 * (2.0 ** -11 + 2.0 ** -24 * 128 ** 0.5) * q.norm(dim=-1) * k.norm(dim=-1).max()
+            spread = torch.einsum("ht,htd->hd", wt, (v[None] - want[b][:, None]).abs())
+            bound[b] = (2.0 ** -8 * want[b].abs() + torch.expm1(2 * e)[:, None] * spread + (2.0 ** -11 + 2.0 ** -18) * (wt @ v.abs())
+                        + 160 * 2.0 ** -28 * v.abs().max())
+        check(out, (want, bound), what)
+
+    plan = shared_plan(dv)
+    assert plan.num_items == 1 and plan.items_host[0, 2] == 10
+    other = blocks[(at + 1) % 10]
+    plan.items.view(-1, L.PLAN_ITEM_INTS)[0, 72 + at] = int(other)
+    if at > 0:
+        kept(L.decode_shared(dv.p, dv.q, kp, vp, dv.words, dv.q_pos, dv.rope, plan), "record")
+        assert L.device_status(clear=True) == L.LAZY_DEV_LAYOUT
+    last = dv.p.num_pool_blocks
+    plan.items.view(-1, L.PLAN_ITEM_INTS)[0, 72 + at] = last
+    words = dv.words.clone()
+    words[:, at] = (words[:, at] & ~0x3FFFF) | last
+    kept(L.decode_shared(dv.p, dv.q, kp, vp, words, dv.q_pos, dv.rope, plan), "id")
+    assert L.device_status(clear=True) == L.LAZY_DEV_BAD_BLOCK_ID
+
+
 # a block that is not in the pool is left out, and the document's others are attended at their own positions
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 64), (32, 1, 128)])
 @pytest.mark.parametrize("bad", [0, 3, 10])
