@@ -270,7 +270,8 @@ int lazy_attn_pack_block_words(const lazy_attn_params *p, int32_t num_docs, cons
  * LAZY_DEV_LAYOUT (pos and tail_start do not fit seq_lens, the table or a word's offset field is
  * full, *first_free outside the list). An id outside the pool sets LAZY_DEV_BAD_BLOCK_ID; its
  * rows get slots of -1.
- * Outputs other than the two named must not overlap inputs. num_seqs may be 0. */
+ * Outputs other than the two named, and block_indptr's last entry as first_free, must not
+ * overlap inputs. num_seqs may be 0. */
 int lazy_attn_append_tokens(const lazy_attn_params *p, const int32_t *new_lens, const int32_t *seq_lens,
                             const int32_t *pos, const int32_t *tail_start, const int32_t *free_blocks,
                             int32_t num_free, const int32_t *first_free, int32_t doc_tokens, int32_t num_rows,

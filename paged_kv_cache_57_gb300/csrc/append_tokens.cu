@@ -7,7 +7,8 @@
 // (append_scan_kernel), a thread a sequence, and where there is little to write, writes the rows too.
 // Else a second launch does, started behind the first one's back: a thread a row (append_row_kernel), or, of many,
 // warps of 256 rows (append_rows_kernel), that find their sequence by a search in the rows' sums. Latency bounds the
-// small cases (64 sequences of a token 3.4 us a call in a graph), the device's stores the large.
+// small cases (64 sequences of a token 3.4 us a call in a graph, 6.8 a call from Python), the device's
+// stores and the rows' arithmetic the large (2.6 million rows 11.0 us, 21 MB, issue slots 63%).
 #include <algorithm>
 #include <climits>
 
@@ -19,8 +20,10 @@ namespace lazy {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kFewRows = 152 * 2048;  // a thread each is resident at once
-constexpr int kRowsPerWarp = 256;  // 3.2 million rows of 48 sequences 11.2 us, with 128 and 512 11.4, 1024 12.9
+// A thread a row up to what is resident at once: 6000 rows of 1021 sequences 8.5 us, in warps of 256 rows
+// 15.9; 2.6 million rows of 48 20.4 and 11.0.
+constexpr int kFewRows = 152 * 2048;
+constexpr int kRowsPerWarp = 256;  // 2.6 million rows of 48 sequences 11.2 us, with 128 and 512 11.4, 1024 12.9
 constexpr int kOwnRows = 8;        // rows that a sequence's thread writes by itself
 constexpr int kOneDoc = 1 << 30;   // a document without an end
 
@@ -337,7 +340,8 @@ cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st) {
   a.doc_shift = 0;
   while ((1ull << a.doc_shift) < d) ++a.doc_shift;
   a.doc_mul = (uint32_t)(((1ull << 32) * ((1ull << a.doc_shift) - d)) / d + 1);
-  // One CTA writes rows at an SM's rate: 1021 sequences of up to 8 took 10.7 us that way.
+  // One CTA writes rows at an SM's rate: 1021 sequences of up to 8 took 10.7 us that way, for 8.5; but 64
+  // sequences of a token 6.8, with a second launch 8.5.
   const bool one = a.B <= 256 && a.num_rows <= 1024;
   const unsigned threads = a.B >= 1024 ? 1024 : (one && a.num_rows > a.B ? 256 : (a.B <= 32 ? 32 : (a.B + 31) / 32 * 32));
   *launches = 1;

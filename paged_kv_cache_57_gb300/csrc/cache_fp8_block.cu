@@ -8,6 +8,10 @@
 // lane's rows give its own chunks whole), takes the maximum across the warp, and writes the
 // chunks that hold one of the rows. The other rows' codes are touched only where the scale
 // grows: a power of two, so that a code of 4 bits changes only where it falls below e4m3's least step.
+// A step's 64 tokens of 8 heads take 2.8 us in a graph (latency: slots, rows, record), 16384 tokens of
+// documents 22.5 us, 4.5 TB/s, with issue slots 60% busy: converting is what bounds it.
+//
+// Read: 1024 blocks of 8 heads 17.0 us, 5.9 TB/s: memory.
 #include "fp8_block.cuh"
 #include "kernels.h"
 
@@ -276,7 +280,9 @@ cudaError_t write_w(const CacheWriteArgs& a, bool vec, cudaStream_t st) {
 }
 
 // A window of one token finds every run at once, but in a document fifteen warps of sixteen find that
-// theirs began before; windows of a block's length waste none, and take the runs among them in turn.
+// theirs began before; windows of a block's length waste none, and take the runs among them in turn. 64
+// tokens of 64 sequences took 2.8 us with windows of one token and 24.6 with 16, 16384 tokens of documents 54.5 and
+// 22.5 (8 heads); 4378 of 2 heads 4.2 and 4.7. Windows of one up to what is resident four times over.
 template <int D>
 cudaError_t write_d(const CacheWriteArgs& a, bool vec, int sms, cudaStream_t st) {
   return (int64_t)a.num_tokens * 2 * a.Hkv <= (int64_t)sms * 128 ? write_w<D, 1>(a, vec, st) : write_w<D, kBlock>(a, vec, st);

@@ -6,8 +6,17 @@
 // Both kernels: four warps form 4 / RT teams of RT = 1, 2 or 4. A team takes a contiguous part of
 // the CTA's blocks through a ring of stages in shared memory; each of its warps has its own tile
 // of 4, 8, 16 or 32 query rows. A block's K and V records are two bulk copies, which one lane starts
-// and the stage's mbarrier counts: a warp's own cp.async of them took 9 instructions a lane and block,
-// and an address for each. The stages' waits are bounded.
+// and the stage's mbarrier counts, every wait with a limit: a warp's own cp.async of them, nine
+// instructions and their addresses in every lane, took 94 us where these take 86.
+//
+// Measured (8 KV heads of 128 dims unless said; calls in a row). Per sequence: 64 of 4096 tokens, 32 heads, 545 MB,
+// 86 us, 6.3 TB/s: memory; one of 16384, 64 heads, 13.5 us: the chain of a piece, the join and two
+// launches; 48 of 256 to 131072, 32 heads on one, 838 MB, 235 us, 3.5 TB/s: instructions. There an
+// mma.sync m16n8k16 holds its scheduler for 8 cycles, so that a block of 32 rows costs an SM 144 cycles of products
+// beside 116 of softmax and loop, for 180 of memory. Shared runs: 64 sequences of 4096 tokens, Zipf-drawn, 48 us
+// for 151 MB, of which the prologue of an item (record, members, angles, queries) and the join are about
+// 12; 32 of 16384, 64 heads, 112 us for 386 MB: alone, items of up to 16 rows take 68 us, bound by
+// memory, the wider ones 71, by instructions.
 #include <algorithm>
 #include <climits>
 
@@ -28,8 +37,10 @@ struct Fp8Cfg {
   static constexpr int ROWS = Fp8Rows<NT, HL>::ALL;  // of a warp
   static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
   static constexpr int SLOT = Fp8Ring<D>::STAGE;     // one block
-  static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // per SM
-  static constexpr int RING = NT == 1 ? 2 : 4;                  // stages per warp of a team
+  // Per SM, as registers allow. 32 and 64 rows as two or four warps with 16 each, at three CTAs: 234 to 244 us
+  // for the 235 above, with twice or four times the conversions.
+  static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
+  static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp of a team
   static constexpr int SLOTS = kWarps * RING;
   static_assert(SLOTS <= kFp8Slots, "barriers");
   static constexpr int BUF = SLOTS * SLOT > kWarps * ROWS * RED * 4 ? SLOTS * SLOT : kWarps * ROWS * RED * 4;
@@ -213,6 +224,8 @@ struct Fp8SharedCfg {
   static constexpr int SLOT = Fp8Ring<D>::STAGE;
   static constexpr int ROWS = 2 * kWarps * 8;  // of a CTA
   static constexpr int RED = D + 4;            // merge rows: o[D], m, l
+  // Four CTAs an SM with 8 stages and the queries of 16 rows in shared memory: 115 us for 119 on the 32 long sequences,
+  // 55 for 49 on the 64 short ones.
   static constexpr int CTAS = 3;     // per SM
   static constexpr int SLOTS = 16;   // stages of the teams' rings
   static_assert(SLOTS <= kFp8Slots, "barriers");

@@ -61,29 +61,7 @@ __device__ __forceinline__ void int4_store_partial(const Int4State<D, NT, HL>& s
 // A unit is a sequence, a KV head and a tile of 4, 8 or 16 of its query heads. Tiles of 8
 // where 4 would do take 83 us against 77 on 64 x 4160 tokens, tiles of 8 instead of 16 345
 // against 258 on 32 heads per KV head.
-//
-// Equal pieces: a unit is cut into pieces of the same length, one CTA each: as many as let all
-// units fill the resident CTAs once, of at least 32 blocks by the sequence's own length
-// (a block table is as wide as a captured step may need; CTAs that its sequence leaves without
-// a piece end at once). Units of one piece are written out, without parts and a join.
-//
-// Ranges: where a piece would be longer than kMaxPiece, the length of the longest sequence
-// says too little about the others. The units' blocks are laid end to end and cut into equal
-// ranges, one per resident CTA: batches of any lengths give every CTA the same work. A CTA
-// goes through its range unit by unit; a unit that lies in one range is written out. Where the
-// table's width does not rule ranges out every CTA looks for the longest sequence, in batches of
-// up to kMaxLook; larger ones are cut into ranges (tables of 4096 blocks, 32 heads on 8, us with the
-// look and with ranges at once: 512 sequences of 64 tokens 56 61, of 1024 134 150; 1024 of 64
-// 123 110, of 256 158 154, of 1024 272 290; 2048 of 64 303 213, of 1024 582 563).
-//
-// Measured from HBM (pieces, ranges; us), 32 heads on 8: 64 sequences of 256 blocks 63 68, of 512
-// 118 113, of 600 139 130, of 1000 225 210, of 2000 439 397; of up to 512 106 96, of up to 1024
-// 189 138; 4 of 8192 (pieces of 432) 105 109. 32 heads on one: 16 of 2000 (pieces of 106) 63 69,
-// 48 of up to 3750 (pieces of 1250) 215 145.
-//
-// The other parts go to the workspace (at most two per CTA: slot 2 c + 1 for a unit that
-// begins in CTA c's places, 2 c for one that began before) and are merged by
-// combine_units_kernel (decode_units.cu).
+// Units are cut into pieces or ranges (decode_units.cuh).
 //
 // Of a part the four warps take a quarter each. A warp is its own loader: a ring of RING
 // stages of two blocks, each refilled as soon as it was read. 64 sequences of 4160 tokens, 32
