@@ -674,3 +674,41 @@ def test_captured_decodes_follow_their_inputs(hq, hkv, d):
     dv.seq_lens[3] = 0
     graph.replay()
     assert torch.equal(one.view(torch.int16), decode(dv, kp, vp).view(torch.int16)) and not one[3].any()
+
+
+def test_records_behind_4_gb():
+    # the same records at the end of pools of more than 2^32 bytes: written, read back and attended to, bit for bit
+    L = la()
+    w = W.decode_zipf("f8far", batch=4, hq=32, hkv=8, d=128, docs_per_seq=3, doc_tokens=200, pool_docs=5, zipf_s=1.0, suffix_tokens=9, seed=1881)
+    dv, kp, vp, kv, vv = on_device(w)
+    n, n_far = w.num_pool_blocks, 1 << 18
+    far = torch.arange(n_far - 1, n_far - 1 - n, -1, device="cuda")  # where block b goes
+    p = L.make_params(num_seqs=4, num_q_heads=32, num_kv_heads=8, head_dim=128, num_pool_blocks=n_far,
+                      max_blocks_per_seq=dv.p.max_blocks_per_seq, rope_theta=w.rope_theta, kv_dtype=KIND)
+    big = L.empty_pools(p)
+    assert big[0].numel() > 1 << 32
+    for x, small in zip(big, (kp, vp)):
+        x.fill_(0x7f)
+        x[far] = small
+    words = dv.words & ~0x3FFFF | far[(dv.words & 0x3FFFF).long()].int()
+    for b in range(4):  # words behind the sequences stay 0
+        words[b, (int(dv.seq_lens[b]) + 15) // 16:] = 0
+    one = L.decode(p, dv.q, *big, words, dv.seq_lens, dv.q_pos, dv.rope)
+    assert torch.equal(one.view(torch.int16), decode(dv, kp, vp).view(torch.int16))
+    two = shared(dv, kp, vp)
+    check(two, M.attention(w, kv, vv), "shared")
+    w.doc_blocks, w.num_pool_blocks = (n_far - 1 - w.doc_blocks).astype(w.doc_blocks.dtype), n_far
+    dv.p, dv.words = p, words
+    assert torch.equal(shared(dv, *big).view(torch.int16), two.view(torch.int16))
+    rng = np.random.default_rng(4)
+    k, v = rows("normal", 16 * n, 8, 128, rng).cuda(), rows("outliers", 16 * n, 8, 128, rng).cuda()
+    slots = torch.arange(16 * n, dtype=torch.int32, device="cuda")
+    L.cache_write(p, k, v, 16 * far[slots.long() // 16].int() + slots % 16, *big)
+    q = params(8, 128, n)
+    near = L.empty_pools(q)
+    L.cache_write(q, k, v, slots, *near)
+    for x, y in zip(big, near):
+        same_records(x[far], y.cpu().numpy(), 128)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")
+    for x, y in zip(L.cache_read(p, *big, far.int()), L.cache_read(q, *near, ids)):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
