@@ -11,7 +11,7 @@
 //
 // Measured (8 KV heads of 128 dims unless said; calls in a row). Per sequence: 64 of 4096 tokens, 32 heads, 545 MB,
 // 86 us, 6.3 TB/s: memory; one of 16384, 64 heads, 13.5 us: the chain of a piece, the join and two
-// launches; 48 of 256 to 131072, 32 heads on one, 838 MB, 235 us, 3.5 TB/s: instructions. There an
+// launches; 48 of 256 to 131072, 32 heads on one, 829 MB, 230 us, 3.6 TB/s: instructions. There an
 // mma.sync m16n8k16 holds its scheduler for 8 cycles, so that a block of 32 rows costs an SM 144 cycles of products
 // beside 116 of softmax and loop, for 180 of memory. Shared runs: 64 sequences of 4096 tokens, Zipf-drawn, 48 us
 // for 151 MB, of which the prologue of an item (record, members, angles, queries) and the join are about
@@ -38,7 +38,7 @@ struct Fp8Cfg {
   static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
   static constexpr int SLOT = Fp8Ring<D>::STAGE;     // one block
   // Per SM, as registers allow. 32 and 64 rows as two or four warps with 16 each, at three CTAs: 234 to 244 us
-  // for the 235 above, with twice or four times the conversions.
+  // for 235 at the time, with twice or four times the conversions.
   static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
   static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp of a team
   static constexpr int SLOTS = kWarps * RING;
@@ -54,7 +54,10 @@ struct Fp8Cfg {
 template <int D, int NT, int HL, int RT, bool LAZY>
 __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_block_kernel(const UnitDecodeArgs a) {
   using C = Fp8Cfg<D, NT, HL>;
-  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT, AHEAD = RT == 1 ? R - 1 : R - 2;
+  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT;
+  // Blocks are started PAIR at a time, AHEAD of the one in work; EARLY before the first. (One at a time took 32 rows'
+  // 235 us for 230; in the shared decode pairs brought nothing.)
+  constexpr int PAIR = RT == 1 && R >= 4 ? 2 : 1, AHEAD = RT == 1 && PAIR == 1 ? R - 1 : R - 2, EARLY = PAIR == 2 ? R : AHEAD;
   constexpr int kNewDoc = 32;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
@@ -119,23 +122,23 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
       c_phys = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block
       c_info = r.nv | (!LAZY || (lane > 0 && p_1 == r.p) ? 0 : kNewDoc);
     };
-    auto fill = [&](int j) {  // block j's stage is loaded, by the warp whose turn it is
+    auto fill = [&](int j) {  // the stages of blocks j .. j + PAIR - 1 are loaded, by the warp whose turn it is
       if ((j & 31) == 0 && j < nk) {
         describe(j);
         load_words(j + 32);
       }
       if (j < nk && j % RT == rt) {
-        const uint32_t n_th = used + j, slot = n_th % R;
-        if (RT > 1 && n_th >= R && !ring.wait_empty(slot, (n_th / R + 1) & 1, a.status)) return false;
-        const int ph = __shfl_sync(0xffffffffu, c_phys, j & 31), info = __shfl_sync(0xffffffffu, c_info, j & 31);
-        if (lane == 0) ring.fill(slot, ph, info);
+        const uint32_t n_th = used + j;
+        if (RT > 1 && n_th >= R && !ring.wait_empty(n_th % R, (n_th / R + 1) & 1, a.status)) return false;
+        const int off = lane - (j & 31);  // by the lanes that hold the blocks
+        if (off >= 0 && off < PAIR && j + off < nk) ring.fill((n_th + off) % R, c_phys, c_info);
       }
       return true;
     };
     load_words(0);
     bool ok = true;
 #pragma unroll 1
-    for (int i = 0; i < AHEAD; ++i) ok &= fill(i);
+    for (int i = 0; i < EARLY; i += PAIR) ok &= fill(i);
 
     // ------------------------------------------------------------ queries
     Fp8Query<D, NT, HL> q;
@@ -162,9 +165,10 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     fp8_init(st);
     for (int i = 0; i < nk; ++i) {
       const uint32_t n_th = used + i, slot = n_th % R;
-      ok = ok && fill(i + AHEAD) && ring.wait_full(slot, n_th / R & 1, a.status);
+      if (PAIR == 1 || (i % 2 == 0 && i > 0)) ok = ok && fill(i + AHEAD);
+      ok = ok && ring.wait_full(slot, n_th / R & 1, a.status);
       if (!ok) {
-        ring.drain(n_th, used + min(nk, i + AHEAD + 1), R, a.status);
+        ring.drain(n_th, used + min(nk, i + R), R, a.status);
         break;
       }
       const int info = bars.info[team * R + slot];
