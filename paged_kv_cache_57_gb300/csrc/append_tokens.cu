@@ -243,7 +243,8 @@ __global__ void append_scan_kernel(const AppendArgs a) {
       a.block_indptr[0] = first;
     }
     if (ROWS) {  // (one chunk)
-      const int tail = s < a.B ? pos - a.tail_start[s] : 0, have = blocks_for(tail), begin = (int)(r - w.rows);
+      const int tail = s < a.B ? pos - a.tail_start[s] : 0, have = blocks_for(tail);
+      const int begin = (int)min(r - w.rows, (int64_t)a.num_rows);  // the rows' sum may leave 32 bits
       const SeqRows q{ok ? tail - begin : INT_MIN, s < a.B ? a.tail_start[s] : 0, w.b0, first + (int)(b - w.blocks) - have, have};
       write_seqs(a, q, s, begin, s < a.B ? (int)min(r, (int64_t)a.num_rows) : begin);
     }

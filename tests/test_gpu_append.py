@@ -144,6 +144,26 @@ def test_sequences_that_do_not_fit():
     assert L.device_status(clear=True) == 0
 
 
+@pytest.mark.parametrize("batch,rows", [(6, 20), (6, 2000), (300, 20)])
+def test_rows_whose_sum_leaves_32_bits(batch, rows):
+    # one CTA's rows, a thread a row, more sequences than one CTA writes the rows of
+    L = la()
+    top = 2 ** 31 - 1
+    new = np.zeros(batch, np.int64)
+    new[:6] = [3, top, top, top, 5, 0]
+    p = params(batch, 4, 600)
+    buf = torch.full((2, rows + 64), -5, dtype=torch.int32, device="cuda")
+    out = L.AppendTables.empty(p, rows).replace(slots=buf[0, 32:32 + rows], local_pos=buf[1, 32:32 + rows])
+    zero, words = i32([0] * batch), u32(np.zeros((batch, 4), np.uint32))
+    L.append_tokens(p, i32(new), zero, zero, zero, i32(np.arange(600)), words, out=out)
+    assert L.device_status(clear=True) == L.LAZY_DEV_LAYOUT | L.LAZY_DEV_BAD_LEN
+    assert (buf[:, :32] == -5).all() and (buf[:, 32 + rows:] == -5).all()
+    assert out.slots[:3].tolist() == [0, 1, 2] and (out.slots[3:] == -1).all()
+    assert out.local_pos[:3].tolist() == [0, 1, 2] and not out.local_pos[3:].any()
+    cu = np.minimum(np.cumsum([0, *new]), top)
+    assert out.cu_rows.tolist() == cu.tolist() and out.seq_lens.tolist() == [3] + [0] * (batch - 1)
+
+
 def test_unaligned_outputs_and_side_stream():
     L = la()
     rng = np.random.default_rng(4)
