@@ -310,6 +310,11 @@ class AppendTables:
             ptrs.append(ctypes.c_void_p(None if x is None else x.data_ptr()))
         self._ptrs = tuple(ptrs) if slots.is_cuda else None
 
+    def __setattr__(self, name, value):
+        if hasattr(self, "_ptrs"):
+            raise AttributeError("the tables are fixed: replace() makes others")
+        object.__setattr__(self, name, value)
+
     def __iter__(self):
         return iter((self.seq_lens, self.pos, self.q_start, self.cu_rows, self.block_indptr, self.slots, self.local_pos))
 

@@ -234,6 +234,17 @@ def test_append_binding_checks_shapes():
         L.append_tokens(p, **ok)
 
 
+def test_append_tables_are_fixed():
+    # a call writes where the tables were when they were made
+    L = _L()
+    t = L.AppendTables.empty(_params(kv_dtype=None), 5, "cpu")
+    for name in ("slots", "pos", "rows", "_ptrs"):
+        with pytest.raises(AttributeError):
+            setattr(t, name, getattr(t, name))
+    other = t.replace(pos=torch.zeros(2, dtype=torch.int32))
+    assert other.slots is t.slots and other.pos is not t.pos
+
+
 @pytest.mark.parametrize("key_positions", [False, True])
 def test_model_appends_what_the_packer_packs(key_positions):
     # requests from nothing, one document each: the words and lengths of the packer, whose documents are the blocks given
