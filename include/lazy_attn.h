@@ -320,7 +320,9 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  * or, for R = 128 and for pools of records (int4, e4m3 with block scales), about one item per
  * resident CTA (2 x 152 / num_kv_heads items, int4: 4 x 152 / num_kv_heads, e4m3 with block
  * scales: 3 x 152 / num_kv_heads): the sets' blocks summed, divided
- * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. It writes
+ * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. For e4m3 with block scales a block of a
+ * set of more than 16 rows counts as two, of more than 32 as four, and the length of such a set's
+ * chunks is that part of 16 .. 256; a document is cut into equal chunks of about that length. It writes
  *   items_host [num_items][LAZY_PLAN_ITEM_INTS] int32, one work item each:
  *     [0] src_seq, [1] b0, [2] nblk, [3] last_valid, [4] nmem, [5] c0, [6..7] 0:
  *         nblk logical blocks of sequence src_seq from block b0, all full but
@@ -557,8 +559,7 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale where that
  * is more (weights over the row's largest in the part). Sums and maxima are fp32. A warp adds up
  * at most 16384 blocks: lazy_attn_decode cuts longer sequences whatever num_splits says (with
- * num_splits 1 too tables of more than 65536 blocks, or 32768 for more than 32 query heads a KV
- * head, take a workspace), lazy_attn_plan_shared_host limits chunk_blocks to that, and an item of more blocks sets
+ * num_splits 1 too tables of more than 65536 blocks take a workspace), lazy_attn_plan_shared_host limits chunk_blocks to that, and an item of more blocks sets
  * LAZY_DEV_LAYOUT and leaves its slots as they were. */
 
 /* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold

@@ -3,7 +3,7 @@
 // arithmetic of a block is in fp8_block.cuh; the query rows of a KV head are its heads (per
 // sequence), or members x heads (shared).
 //
-// Both kernels: four warps form 4 / RT teams of RT = 1, 2 or 4. A team takes a contiguous part of
+// Four warps form 4 / RT teams of RT = 1 (per sequence: always), 2 or 4. A team takes a contiguous part of
 // the CTA's blocks through a ring of stages in shared memory; each of its warps has its own tile
 // of 4, 8, 16 or 32 query rows. A block's K and V records are two bulk copies, which one lane starts
 // and the stage's mbarrier counts, every wait with a limit: a warp's own cp.async of them, nine
@@ -37,8 +37,8 @@ struct Fp8Cfg {
   static constexpr int ROWS = Fp8Rows<NT, HL>::ALL;  // of a warp
   static constexpr int RED = D + 4;                  // merge rows: o[D], m, l
   static constexpr int SLOT = Fp8Ring<D>::STAGE;     // one block
-  // Per SM, as registers allow. 32 and 64 rows as two or four warps with 16 each, at three CTAs: 234 to 244 us
-  // for 235 at the time, with twice or four times the conversions.
+  // Per SM, as registers allow. 32 rows as two warps of a team with 16 each, at three CTAs: 234 to 244 us for
+  // 235 at the time, with twice the conversions.
   static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
   static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp of a team
   static constexpr int SLOTS = kWarps * RING;
@@ -49,15 +49,15 @@ struct Fp8Cfg {
 }  // namespace
 
 // ------------------------------------------------------------------ per sequence
-// A unit is a sequence, a KV head and a tile of 4, 8, 16, 32 or 64 of its query heads; the units
-// are cut into pieces or ranges (decode_units.cuh).
-template <int D, int NT, int HL, int RT, bool LAZY>
+// A unit is a sequence, a KV head and a tile of 4, 8, 16 or 32 of its query heads; the units
+// are cut into pieces or ranges (decode_units.cuh). Of a part each warp takes a quarter, by itself.
+template <int D, int NT, int HL, bool LAZY>
 __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_block_kernel(const UnitDecodeArgs a) {
   using C = Fp8Cfg<D, NT, HL>;
-  constexpr int HALF = D / 2, TEAMS = kWarps / RT, R = C::RING * RT;
+  constexpr int HALF = D / 2, R = C::RING;
   // Blocks are started PAIR at a time, AHEAD of the one in work; EARLY before the first. (One at a time took 32 rows'
   // 235 us for 230; in the shared decode pairs brought nothing.)
-  constexpr int PAIR = RT == 1 && R >= 4 ? 2 : 1, AHEAD = RT == 1 && PAIR == 1 ? R - 1 : R - 2, EARLY = PAIR == 2 ? R : AHEAD;
+  constexpr int PAIR = R >= 4 ? 2 : 1, AHEAD = R - PAIR, EARLY = PAIR == 2 ? R : AHEAD;
   constexpr int kNewDoc = 32;
   extern __shared__ __align__(128) uint8_t smem[];
   float2* cs_all = reinterpret_cast<float2*>(smem + C::BUF);
@@ -65,14 +65,12 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
   __shared__ Fp8Bars bars;
   if (threadIdx.x < C::SLOTS) {
     mbar_init(&bars.full[threadIdx.x], 1);
-    mbar_init(&bars.empty[threadIdx.x], RT);
     fence_barrier_init();
   }
   __syncthreads();
   wait_for_launch_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = warp / RT, rt = warp % RT;
   const int ht = a.plan.units / a.Hkv;
 
   uint32_t used = 0;  // blocks that went through the ring before this part
@@ -80,14 +78,14 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
   if (!w.begin(a, warp, lane)) return;
   while (w.next(a)) {
     const int s = w.s, seq_len = w.seq_len, nb = w.nb, lo = w.lo, hi = w.hi;
-    const int kvh = w.u / ht, head0 = (w.u - kvh * ht) * (C::ROWS * RT);
-    const int heads = min(C::ROWS * RT, a.G - head0);
+    const int kvh = w.u / ht, head0 = (w.u - kvh * ht) * C::ROWS;
+    const int heads = min(C::ROWS, a.G - head0);
     const size_t q0 = (size_t)s * a.Hq + (size_t)kvh * a.G + head0;  // the first row's head
     const int n = hi - lo;                                           // blocks of the part
     const int m_pos = a.q_pos[s];
     const uint32_t* wrow = a.words + (size_t)s * a.max_blocks;
 
-    const int row0 = rt * C::ROWS + (HL == 1 ? lane >> 3 : lane >> 2);  // the lane's first row, the others 8 on
+    const int row0 = HL == 1 ? lane >> 3 : lane >> 2;  // the lane's first row, the others 8 on
     const __nv_bfloat16* q_first = static_cast<const __nv_bfloat16*>(a.q) + q0 * D;
     auto row = [&](int nt) { return q_first + (row0 + 8 * nt < heads ? row0 + 8 * nt : 0) * D; };
     bool live[NT];
@@ -99,12 +97,12 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     for (int j = 0; j < HALF / 32; ++j) rate[j] = a.rope[lane + 32 * j];
 
     // ------------------------------------------------------------ first loads
-    const int per_team = (n + TEAMS - 1) / TEAMS;
-    const int kb0 = lo + team * per_team;
-    const int nk = max(0, min(lo + n, kb0 + per_team) - kb0);  // blocks of this team
+    const int per_warp = (n + kWarps - 1) / kWarps;
+    const int kb0 = lo + warp * per_warp;
+    const int nk = max(0, min(lo + n, kb0 + per_warp) - kb0);  // blocks of this warp
     const size_t head = (size_t)kvh * Fp8Geom<D>::REC;
     const Fp8Ring<D> ring{static_cast<const uint8_t*>(a.k_pool) + head, static_cast<const uint8_t*>(a.v_pool) + head,
-                          (uint32_t)a.Hkv * Fp8Geom<D>::REC, smem + team * R * C::SLOT, &bars, team * R};
+                          (uint32_t)a.Hkv * Fp8Geom<D>::REC, smem + warp * R * C::SLOT, &bars, warp * R};
     // A chunk of 32 blocks in the lanes: id, and valid slots with kNewDoc where the block is not one of the
     // document of the block before (or begins a chunk).
     int c_phys = 0, c_info = 0;
@@ -114,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
       w_nxt = k < nk ? wrow[b] : 0u;
       wn_nxt = (k < nk && b + 1 < nb) ? wrow[b + 1] : 0u;
     };
-    auto describe = [&](int kc) {  // the chunk of w_nxt, by every warp of the team alike
+    auto describe = [&](int kc) {  // the chunk of w_nxt
       const LaneBlock r = describe_block(kc + lane < nk, kb0 + kc + lane, nb, seq_len, w_nxt, wn_nxt, a.id_bits,
                                          a.num_pool_blocks, a.status);
       // a block without keys is left out and did not have q rotated for its document
@@ -122,23 +120,17 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
       c_phys = r.phys < a.num_pool_blocks ? r.phys : 0;  // no keys in it: any block
       c_info = r.nv | (!LAZY || (lane > 0 && p_1 == r.p) ? 0 : kNewDoc);
     };
-    auto fill = [&](int j) {  // the stages of blocks j .. j + PAIR - 1 are loaded, by the warp whose turn it is
+    auto fill = [&](int j) {  // the stages of blocks j .. j + PAIR - 1 are loaded, by the lanes that hold the blocks
       if ((j & 31) == 0 && j < nk) {
         describe(j);
         load_words(j + 32);
       }
-      if (j < nk && j % RT == rt) {
-        const uint32_t n_th = used + j;
-        if (RT > 1 && n_th >= R && !ring.wait_empty(n_th % R, (n_th / R + 1) & 1, a.status)) return false;
-        const int off = lane - (j & 31);  // by the lanes that hold the blocks
-        if (off >= 0 && off < PAIR && j + off < nk) ring.fill((n_th + off) % R, c_phys, c_info);
-      }
-      return true;
+      const int off = lane - (j & 31);
+      if (off >= 0 && off < PAIR && j + off < nk) ring.fill((used + j + off) % R, c_phys, c_info);
     };
     load_words(0);
-    bool ok = true;
 #pragma unroll 1
-    for (int i = 0; i < EARLY; i += PAIR) ok &= fill(i);
+    for (int i = 0; i < EARLY; i += PAIR) fill(i);
 
     // ------------------------------------------------------------ queries
     Fp8Query<D, NT, HL> q;
@@ -163,15 +155,16 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     // ------------------------------------------------------------ main loop
     Fp8State<D, NT, HL> st;
     fp8_init(st);
+    bool ok = true;
     for (int i = 0; i < nk; ++i) {
       const uint32_t n_th = used + i, slot = n_th % R;
-      if (PAIR == 1 || (i % 2 == 0 && i > 0)) ok = ok && fill(i + AHEAD);
-      ok = ok && ring.wait_full(slot, n_th / R & 1, a.status);
+      if (PAIR == 1 || (i % 2 == 0 && i > 0)) fill(i + AHEAD);
+      ok = ring.wait_full(slot, n_th / R & 1, a.status);
       if (!ok) {
         ring.drain(n_th, used + min(nk, i + R), R, a.status);
         break;
       }
-      const int info = bars.info[team * R + slot];
+      const int info = bars.info[warp * R + slot];
       int nv = kBlock;
       if (info != kBlock) {
         nv = info & 31;
@@ -181,27 +174,26 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
         }
       }
       if (nv > 0) fp8_attend<D, NT, HL>(ring.base + slot * C::SLOT, nv, q, st, lane);
-      __syncwarp();
-      if (RT > 1 && lane == 0) ring.release(slot);
+      __syncwarp();  // the stage is free
     }
     used += nk;
     fp8_finish(st);
-    __syncthreads();  // every team is done with its ring: the merge takes its place
+    __syncthreads();  // every warp is done with its ring: the merge takes its place
     float* red = reinterpret_cast<float*>(smem);
     fp8_store_partial(st, red + warp * C::ROWS * C::RED, C::RED, lane);
     __syncthreads();
     const bool whole = lo == 0 && hi == nb;
-    const size_t slot0 = (2 * (size_t)blockIdx.x + (lo == 0 ? 1 : 0)) * (C::ROWS * RT);
+    const size_t slot0 = (2 * (size_t)blockIdx.x + (lo == 0 ? 1 : 0)) * C::ROWS;
     for (int idx = threadIdx.x; idx < heads * D; idx += kThreads) {
-      const int row = idx / D, col = idx % D;  // row of tile row / ROWS, which warp row / ROWS of each team has
+      const int row = idx / D, col = idx % D;
       float M = -INFINITY;
 #pragma unroll
-      for (int tm = 0; tm < TEAMS; ++tm) M = fmaxf(M, red[(tm * RT * C::ROWS + row) * C::RED + D]);
+      for (int tm = 0; tm < kWarps; ++tm) M = fmaxf(M, red[(tm * C::ROWS + row) * C::RED + D]);
       const float Mr = M == -INFINITY ? 0.f : M;  // no keys: all sums are 0 (or NaN, which stays)
       float acc = 0.f, L = 0.f;
 #pragma unroll
-      for (int tm = 0; tm < TEAMS; ++tm) {
-        const float* src = red + (tm * RT * C::ROWS + row) * C::RED;
+      for (int tm = 0; tm < kWarps; ++tm) {
+        const float* src = red + (tm * C::ROWS + row) * C::RED;
         const float f = fast_ex2(src[D] - Mr);
         acc += f * src[col];
         L += f * src[D + 1];
@@ -452,31 +444,41 @@ __global__ void __launch_bounds__(kThreads, Fp8SharedCfg<D>::CTAS) decode_shared
 
 // ------------------------------------------------------------------ launchers
 
+// 32 rows a warp read and convert a block once for twice the rows, but their queries take longer to build and to
+// merge; worth it for long batches, going by the table's width: 48 sequences of 256 to 131072 tokens, 32 heads on
+// one, 230 us, as two units of 16 rows 281; 45 of 40000 to 79000 195 and 207; but 53 of 1665 to 3331 34 and 26,
+// one of 8000 25 and 13, one of 20 22 and 10. (64 rows as two warps with 32 each: 258 us where units of 32 take 184,
+// 80 sequences of 10000 to 20000 tokens, 64 heads on one.)
+constexpr int64_t kWideBlocks = 1 << 16;
+
+// Pieces of at least 16 blocks; 32 for 32 rows (128 sequences of 1000 tokens 27 us, with 16 31). With 32 for the
+// others one sequence of 16384 tokens, 32 heads on 2, takes 14.8 us, with 16 12.4 and with 8 13.2; two of 1475, 32 on
+// 8, 13.1, 10.7 and 10.4; eight of 2048, 64 on 8, 15.9, 16.1 and 25.5 (more parts than a warp of the join merges).
 UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
+  const int most = (int64_t)B * max_blocks * Hkv >= kWideBlocks ? 32 : 16;
   int rows = 4;
-  while (rows < G && rows < 64) rows *= 2;
+  while (rows < G && rows < most) rows *= 2;
   const int per_sm = rows <= 8 ? Fp8Cfg<128, 1, 1>::CTAS : (rows == 16 ? Fp8Cfg<128, 2, 2>::CTAS : Fp8Cfg<128, 4, 2>::CTAS);
-  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm,
-                    (rows == 64 ? 2 : 4) * kFp8MaxRun);
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm, rows == 32 ? 5 : 4,
+                    kWarps * kFp8MaxRun);
 }
 
-template <int D, int NT, int HL, int RT, bool LAZY>
+template <int D, int NT, int HL, bool LAZY>
 static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
   using C = Fp8Cfg<D, NT, HL>;
   constexpr int SMEM = C::BUF + kWarps * ((D / 2) * 8 + Fp8Query<D, NT, HL>::BYTES);
-  cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, RT, LAZY>>(SMEM);
+  cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, LAZY>>(SMEM);
   if (e != cudaSuccess) return e;
-  return launch_behind(decode_fp8_block_kernel<D, NT, HL, RT, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
+  return launch_behind(decode_fp8_block_kernel<D, NT, HL, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
 }
 
 template <int D, bool LAZY>
 static cudaError_t launch_decode_d(const UnitDecodeArgs& a, cudaStream_t st) {
   switch (a.plan.rows) {
-    case 4: return launch_decode_t<D, 1, 1, 1, LAZY>(a, st);
-    case 8: return launch_decode_t<D, 1, 2, 1, LAZY>(a, st);
-    case 16: return launch_decode_t<D, 2, 2, 1, LAZY>(a, st);
-    case 32: return launch_decode_t<D, 4, 2, 1, LAZY>(a, st);
-    default: return launch_decode_t<D, 4, 2, 2, LAZY>(a, st);
+    case 4: return launch_decode_t<D, 1, 1, LAZY>(a, st);
+    case 8: return launch_decode_t<D, 1, 2, LAZY>(a, st);
+    case 16: return launch_decode_t<D, 2, 2, LAZY>(a, st);
+    default: return launch_decode_t<D, 4, 2, LAZY>(a, st);
   }
 }
 

@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_shared_int4_kernel(const S
 UnitPlan plan_decode_int4(int B, int G, int Hkv, int max_blocks, int num_splits, int sms) {
   const int rows = G <= 4 ? 4 : (G <= 8 ? 8 : 16);
   const int per_sm = rows < 16 ? Int4Cfg<128, 1, 1>::CTAS : Int4Cfg<128, 2, 2>::CTAS;
-  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm);
+  return plan_units(B, rows, Hkv * ((G + rows - 1) / rows), max_blocks, num_splits, (int64_t)sms * per_sm, kMinPieceLog2);
 }
 
 template <int D, int NT, int HL, bool LAZY>

@@ -142,15 +142,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_units_kernel(const
   }
 }
 
-UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident, int most) {
+UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident, int least_log2, int most) {
   UnitPlan p{};
   p.rows = rows;
   p.units = units;
   const int mb = max_blocks > 0 ? max_blocks : 1;
   const int64_t all = (int64_t)(B > 0 ? B : 1) * units;
-  p.least_log2 = num_splits > 0 ? 0 : kMinPieceLog2;
+  p.least_log2 = num_splits > 0 ? 0 : least_log2;
   p.splits = num_splits > 0 ? std::min(num_splits, mb)
-                            : (int)std::max<int64_t>(1, std::min<int64_t>(resident / all, mb >> kMinPieceLog2));
+                            : (int)std::max<int64_t>(1, std::min<int64_t>(resident / all, mb >> least_log2));
   if (num_splits > 0) p.splits = (int)std::max<int64_t>(p.splits, ((int64_t)mb + most - 1) / most);  // (else kMaxPiece or a range)
   p.ctas = all * p.splits;
   p.parts = p.splits > 1 ? p.ctas : 0;

@@ -31,7 +31,10 @@
 // instructions on wide ones: the items longer than half the longest are taken from the two ends of that
 // order in turn, so that an SM has both at once; the short ones still come last (the same 32
 // sequences 120 -> 113 us, with 48 or 32 blocks an item 139 -> 135 and 136; 64 x 4096 tokens with private
-// tails of 4 blocks 50 -> 49; all items in two mixed streams 137 and 64).
+// tails of 4 blocks 50 -> 49; all items in two mixed streams 137 and 64). Its automatic lengths count a block
+// of a wide set as two (up to 32 rows) or four, and cut a document into equal parts, which matters where items
+// are few: 29 x up to 14336 tokens, 15 heads on 5, 68 -> 36 us, one document of 4096 tokens in 32 sequences 42 -> 36
+// (parts of that length and a rest instead: 16 x 4096 of 256-token documents 30 -> 37).
 #include <algorithm>
 #include <utility>
 #include <vector>
@@ -99,14 +102,23 @@ int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_bl
   struct Set {
     int group, first, n, rt, cb;
   };
-  int cb = chunk_blocks;
-  if (cb <= 0) {  // about auto_items items: 32 .. 256 blocks, a multiple of 4 (one key tile)
+  // What a block of a set of n members takes, in blocks of a narrow one.
+  auto share = [&](int n) { return !alternate || n * G <= 16 ? 1 : (n * G <= 32 ? 2 : 4); };
+  int64_t per = 0;
+  if (chunk_blocks <= 0) {  // about auto_items items of equal work
     int64_t total = 0;
-    for (int gi = 0; gi < ng; ++gi)
-      total += (int64_t)((keys[gi].second + kBlk - 1) / kBlk) * ((gsize(gi) + per_set - 1) / per_set);
-    const int64_t per = (total + std::max(1, auto_items) - 1) / std::max(1, auto_items);
-    cb = (int)std::min<int64_t>(256, std::max<int64_t>(32, (per + 3) / 4 * 4));
+    for (int gi = 0; gi < ng; ++gi) {
+      const int sets_of = gsize(gi) / per_set, rest = gsize(gi) % per_set;
+      total += (int64_t)((keys[gi].second + kBlk - 1) / kBlk) * (sets_of * share(per_set) + (rest > 0 ? share(rest) : 0));
+    }
+    per = (total + std::max(1, auto_items) - 1) / std::max(1, auto_items);
   }
+  // 32 (alternate: 16 of a narrow set's) .. 256 blocks, a multiple of 4 (one key tile)
+  auto chunk_of = [&](int n) {
+    if (chunk_blocks > 0) return chunk_blocks;
+    const int w = share(n);
+    return (int)std::min<int64_t>(256, std::max<int64_t>((alternate ? 16 : 32) / w, (per / w + 3) / 4 * 4));
+  };
   std::vector<Set> sets;
   std::vector<int> nslots(B, 0);
   for (int gi = 0; gi < ng; ++gi) {
@@ -115,6 +127,11 @@ int plan_shared_host(int B, int G, int rows_cap, int max_blocks, int num_pool_bl
       const int n = std::min(per_set, gsize(gi) - j0);
       const int rows = n * G;
       const int rt = !cost_of_rows || rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+      int cb = chunk_of(n);
+      if (alternate && chunk_blocks <= 0) {  // equal parts, as many as that length suggests
+        const int parts = std::max(1, (nbk + cb / 2) / cb);
+        cb = ((nbk + parts - 1) / parts + 3) / 4 * 4;
+      }
       sets.push_back(Set{gi, gstart[gi] + j0, n, rt, cb});
       for (int j = 0; j < n; ++j) nslots[occ[gstart[gi] + j0 + j].seq] += (nbk + cb - 1) / cb;
     }

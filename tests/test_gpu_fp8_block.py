@@ -528,7 +528,7 @@ def test_shared_items_leave_bad_blocks_out(batch, hq, at):
                         + 160 * 2.0 ** -28 * v.abs().max())
         check(out, (want, bound), what)
 
-    plan = shared_plan(dv)
+    plan = shared_plan(dv, 10)
     assert plan.num_items == 1 and plan.items_host[0, 2] == 10
     other = blocks[(at + 1) % 10]
     plan.items.view(-1, L.PLAN_ITEM_INTS)[0, 72 + at] = int(other)
