@@ -557,10 +557,11 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * block whose row 0 is written begins anew: its other rows, unless written too, are 0.
  * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
  * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale where that
- * is more (weights over the row's largest in the part). Sums and maxima are fp32. A warp adds up
- * at most 16384 blocks: lazy_attn_decode cuts longer sequences whatever num_splits says (with
- * num_splits 1 too tables of more than 65536 blocks take a workspace), lazy_attn_plan_shared_host limits chunk_blocks to that, and an item of more blocks sets
- * LAZY_DEV_LAYOUT and leaves its slots as they were. */
+ * is more (weights over the row's largest in the part). Sums and maxima are fp32. A warp adds up at
+ * most 16384 blocks: lazy_attn_decode cuts longer sequences whatever num_splits says (with num_splits
+ * 1 too tables of more than 65536 blocks take a workspace), lazy_attn_plan_shared_host limits
+ * chunk_blocks to that, and an item of more blocks sets LAZY_DEV_LAYOUT and leaves its slots as they
+ * were. */
 
 /* Bytes of one (block, KV head) of a pool of p's kind: k_pool and v_pool hold
  * num_pool_blocks * Hkv times that. 0 on bad params. */

@@ -350,7 +350,8 @@ cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st) {
   cudaError_t e = launch_behind(append_scan_kernel<false>, 1, threads, 0, st, a);
   if (e != cudaSuccess || a.num_rows == 0) return e;
   *launches = 2;
-  if (a.num_rows <= kFewRows) return launch_behind(append_row_kernel, (unsigned)((a.num_rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st, a);
+  if (a.num_rows <= kFewRows)
+    return launch_behind(append_row_kernel, (unsigned)((a.num_rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st, a);
   const int per = kRowThreads / 32 * kRowsPerWarp;
   return launch_behind(append_rows_kernel, (unsigned)(((int64_t)a.num_rows + per - 1) / per), kRowThreads, 0, st, a);
 }

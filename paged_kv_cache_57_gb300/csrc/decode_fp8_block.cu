@@ -40,7 +40,7 @@ struct Fp8Cfg {
   // Per SM, as registers allow. 32 rows as two warps of a team with 16 each, at three CTAs: 234 to 244 us for
   // 235 at the time, with twice the conversions.
   static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
-  static constexpr int RING = NT == 1 ? 2 : 4;  // stages per warp of a team
+  static constexpr int RING = NT == 1 ? 2 : 4;  // stages of a warp
   static constexpr int SLOTS = kWarps * RING;
   static_assert(SLOTS <= kFp8Slots, "barriers");
   static constexpr int BUF = SLOTS * SLOT > kWarps * ROWS * RED * 4 ? SLOTS * SLOT : kWarps * ROWS * RED * 4;
