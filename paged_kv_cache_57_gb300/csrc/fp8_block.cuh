@@ -222,7 +222,7 @@ __device__ __forceinline__ void fp8_init(Fp8State<D, NT, HL>& st) {
     }
   }
   st.inv = 1.f;
-  st.lim = 0.f;
+  st.lim = -1.f;
 }
 
 // The products truncate their running sums (2^-24 each time, always towards zero): after
@@ -288,7 +288,7 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const F
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) p[nt][e] = to;
   };
-  const bool first = st.lim == 0.f;  // the same in all lanes
+  const bool first = st.lim < 0.f;  // the same in all lanes (a scale of 0, of a pool that nothing wrote, counts too)
   if (first) {
     if (partial) mask(-INFINITY);
 #pragma unroll

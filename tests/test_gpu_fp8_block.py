@@ -712,3 +712,21 @@ def test_records_behind_4_gb():
     ids = torch.arange(n, dtype=torch.int32, device="cuda")
     for x, y in zip(L.cache_read(p, *big, far.int()), L.cache_read(q, *near, ids)):
         assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (8, 1, 64), (16, 1, 128), (64, 1, 128)])
+def test_blocks_of_zero_bytes_are_keys_and_values_of_zero(hq, hkv, d):
+    # as a pool is that was cleared and not written: codes and scales of 0
+    w = W.decode_zipf("f8zero", batch=3, hq=hq, hkv=hkv, d=d, docs_per_seq=3, doc_tokens=140, pool_docs=4, zipf_s=0.7, seed=1891)
+    dv, kp, vp, kv, vv = on_device(w)
+    for doc in range(4):  # the first blocks of two documents, a later one of the others
+        a = int(w.doc_block_indptr[doc])
+        for b in ([0, 1, 2] if doc % 2 else [1, 5]):
+            blk = int(w.doc_blocks[a + b])
+            kp[blk], vp[blk], kv[blk], vv[blk] = 0, 0, 0, 0
+    ref = M.attention(w, kv, vv)
+    for splits in (0, 1, 3):
+        dv.p.num_splits = splits
+        check(decode(dv, kp, vp), ref, f"splits {splits}")
+    check(shared(dv, kp, vp), ref, "shared")
+    check(shared(dv, kp, vp, 2), ref, "shared, short items")
