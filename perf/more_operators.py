@@ -76,15 +76,6 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    """One more case. Block words of 32 bits do not hold every layout (the packer refuses documents or pools that are too long
-    for their fields): such a draw is drawn again."""
-    while True:
-        case = _draw(rng)
-        if case["op"] in ("tables", "write") or _fits_words(case):
-            return case
-
-
-def _draw(rng):
     op = rng.choice(["tables", "write", "decode", "decode", "shared"])
     if op == "tables":
         batch = _log(rng, 1, 4096)
@@ -167,20 +158,6 @@ def _used_blocks(seqs):
         for doc, n in segs:
             used[doc] = max(used.get(doc, 0), _blocks(n))
     return sum(used.values()), sum(_blocks(n) for s in seqs for _, n in s), sum(n for s in seqs for _, n in s)
-
-
-def _fits_words(case):
-    """Whether the blocks' ids and offsets fit the words' fields."""
-    seqs, doc_len = _segments(case)
-    if sum(_blocks(doc_len[doc]) for doc in {doc for segs in seqs for doc, _ in segs}) > 1 << ID_BITS:
-        return False
-    for segs in seqs:
-        b = p = 0
-        for _, n in segs:
-            if BLOCK * (b + _blocks(n) - 1) - p >= 1 << 31 - ID_BITS:
-                return False
-            b, p = b + _blocks(n), p + n
-    return True
 
 
 def _documents(case):
