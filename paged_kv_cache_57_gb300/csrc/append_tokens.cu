@@ -33,12 +33,13 @@ __device__ __forceinline__ int blocks_for(int tokens) { return (int)(((unsigned)
 struct Want {
   int rows, blocks;  // new tokens; blocks from the free list
   int b0;            // block of its own first token
+  int start;         // tail_start, which may be the place of pos_out
   bool ok;           // the tokens can be added, room in the free list and the rows permitting
 };
 
 __device__ __forceinline__ Want want_of(const AppendArgs& a, int s, int& len, int& pos) {
-  Want w{0, 0, 0, false};
   const int n = a.new_lens[s], start = a.tail_start[s];
+  Want w{0, 0, 0, start, false};
   len = a.seq_lens[s];
   pos = a.pos[s];
   if (n <= 0) {
@@ -215,7 +216,7 @@ __global__ void append_scan_kernel(const AppendArgs a) {
   for (int c = 0; c < a.B || c == 0; c += blockDim.x) {
     const int s = c + threadIdx.x;
     int len = 0, pos = 0;
-    Want w{0, 0, 0, false};
+    Want w{0, 0, 0, 0, false};
     if (s < a.B) w = want_of(a, s, len, pos);
     int64_t r = w.rows, b = w.blocks, all_r, all_b;
     scan2(r, b, part, all_r, all_b);
@@ -231,7 +232,7 @@ __global__ void append_scan_kernel(const AppendArgs a) {
     const int64_t given = given_s;
     if (s < a.B) {
       // (every value of the sequence that an output may take the place of has been read)
-      a.seq_lens_out[s] = ok ? kBlock * w.b0 + (pos - a.tail_start[s]) + w.rows : len;
+      a.seq_lens_out[s] = ok ? kBlock * w.b0 + (pos - w.start) + w.rows : len;
       a.pos_out[s] = ok ? pos + w.rows : pos;
       a.q_start[s] = pos;
       const int cu = (int)(r < INT_MAX ? r : INT_MAX);
@@ -243,9 +244,9 @@ __global__ void append_scan_kernel(const AppendArgs a) {
       a.block_indptr[0] = first;
     }
     if (ROWS) {  // (one chunk)
-      const int tail = s < a.B ? pos - a.tail_start[s] : 0, have = blocks_for(tail);
+      const int tail = pos - w.start, have = blocks_for(tail);
       const int begin = (int)min(r - w.rows, (int64_t)a.num_rows);  // the rows' sum may leave 32 bits
-      const SeqRows q{ok ? tail - begin : INT_MIN, s < a.B ? a.tail_start[s] : 0, w.b0, first + (int)(b - w.blocks) - have, have};
+      const SeqRows q{ok ? tail - begin : INT_MIN, w.start, w.b0, first + (int)(b - w.blocks) - have, have};
       write_seqs(a, q, s, begin, s < a.B ? (int)min(r, (int64_t)a.num_rows) : begin);
     }
     rows += all_r;
@@ -350,6 +351,7 @@ cudaError_t launch_append_tokens(AppendArgs a, int* launches, cudaStream_t st) {
   cudaError_t e = launch_behind(append_scan_kernel<false>, 1, threads, 0, st, a);
   if (e != cudaSuccess || a.num_rows == 0) return e;
   *launches = 2;
+  if (a.tail_start == a.pos_out) a.tail_start = a.q_start;  // (= pos) was overwritten; q_start has its values
   if (a.num_rows <= kFewRows)
     return launch_behind(append_row_kernel, (unsigned)((a.num_rows + kRowThreads - 1) / kRowThreads), kRowThreads, 0, st, a);
   const int per = kRowThreads / 32 * kRowsPerWarp;
