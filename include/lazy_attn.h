@@ -103,7 +103,7 @@ typedef struct {
   int32_t num_kv_heads;       /* Hkv >= 1 */
   int32_t head_dim;           /* d: 64 or 128 */
   int32_t block_size;         /* must be 16 */
-  int32_t num_pool_blocks;    /* rows of k_pool / v_pool, < 2^id_bits */
+  int32_t num_pool_blocks;    /* rows of k_pool / v_pool, <= 2^id_bits */
   int32_t max_blocks_per_seq; /* row stride of block_words */
   int32_t id_bits;            /* 8..24; 0 selects the default 18 */
   int32_t dtype;              /* lazy_dtype of q, pools and out */
@@ -269,7 +269,8 @@ int lazy_attn_pack_block_words(const lazy_attn_params *p, int32_t num_docs, cons
  * either), LAZY_DEV_BAD_LEN (negative new_lens, seq_lens outside the table, rows past num_rows),
  * LAZY_DEV_LAYOUT (pos and tail_start do not fit seq_lens, the table or a word's offset field is
  * full, *first_free outside the list). An id outside the pool sets LAZY_DEV_BAD_BLOCK_ID; its
- * rows get slots of -1.
+ * rows get slots of -1. In a pool of 2^id_bits blocks, where a word cannot mark such an id, the
+ * sequence's tokens are not added then, and the blocks that it was given are passed over.
  * Outputs other than the two named, and block_indptr's last entry as first_free, must not
  * overlap inputs. num_seqs may be 0. */
 int lazy_attn_append_tokens(const lazy_attn_params *p, const int32_t *new_lens, const int32_t *seq_lens,

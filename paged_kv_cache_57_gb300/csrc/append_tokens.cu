@@ -105,6 +105,22 @@ __device__ __forceinline__ void scan2(int64_t& x, int64_t& y, int64_t (&part)[2]
   if (warp > 0) x += bx, y += by;
 }
 
+// Whether the n ids from free_blocks[at] on are blocks of the pool, for the lanes with `mine`. All lanes call it.
+__device__ __forceinline__ bool ids_good(const AppendArgs& a, bool mine, int at, int n) {
+  const int lane = threadIdx.x & 31;
+  bool good = true;
+  for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+    const int l = __ffs(left) - 1, from = __shfl_sync(0xffffffffu, at, l), count = __shfl_sync(0xffffffffu, n, l);
+    bool bad = false;
+    for (int j = lane; j < count; j += 32) {
+      const int id = a.free_blocks[from + j];
+      bad |= id < 0 || id >= a.num_pool_blocks;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == l) good = false;
+  }
+  return good;
+}
+
 // a / d for 0 <= a < 2^31 (a.doc_mul, a.doc_shift: the launch fills them).
 __device__ __forceinline__ int doc_of(const AppendArgs& a, int at) {
   return (int)((__umulhi((unsigned)at, a.doc_mul) + (unsigned)at) >> a.doc_shift);
@@ -223,10 +239,16 @@ __global__ void append_scan_kernel(const AppendArgs a) {
     r += rows;
     b += blocks;
     const bool fits_rows = r <= a.num_rows, fits_blocks = w.blocks == 0 || first + b <= a.num_free;
-    const bool ok = w.ok && fits_rows && fits_blocks;
+    bool ok = w.ok && fits_rows && fits_blocks;
     if (w.ok && !ok) {
       raise_status(a.status, fits_rows ? LAZY_DEV_NO_BLOCKS : LAZY_DEV_BAD_LEN);
       if (w.blocks > 0) atomicMin(reinterpret_cast<unsigned long long*>(&given_s), (unsigned long long)(b - w.blocks));
+    }
+    // A word marks a bad id by the greatest of its field. Where that is a block of the pool, a sequence
+    // that is given a bad id gets no tokens: the next call's would go into that block.
+    if (a.num_pool_blocks >> a.id_bits != 0 && !ids_good(a, ok && w.blocks > 0, (int)(first + b - w.blocks), w.blocks)) {
+      raise_status(a.status, LAZY_DEV_BAD_BLOCK_ID);
+      ok = false;
     }
     __syncthreads();
     const int64_t given = given_s;

@@ -41,3 +41,46 @@ def test_chunks_that_begin_at_pos_in_place(batch, new_hi):
     got = (w, out.seq_lens, out.pos, out.q_start, out.cu_rows, out.block_indptr, out.slots, out.local_pos)
     for name, g, x in zip(("words", "seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos"), got, want):
         assert np.array_equal(g.cpu().numpy(), np.ascontiguousarray(x).view(np.int32)), name
+
+
+# ids outside the pool where every id of the words' field is a block: no word can say that a block is none. One CTA's rows,
+# a thread a row; a document of more ids than a warp looks at at once
+@pytest.mark.parametrize("batch,new_hi,room", [(6, 60, 0), (6, 60, 2000), (300, 1, 0), (3, 1200, 0)])
+@pytest.mark.parametrize("key_positions", [False, True])
+def test_bad_ids_of_a_full_field_add_nothing(batch, new_hi, room, key_positions):
+    L = la()
+    rng = np.random.default_rng(batch + new_hi)
+    p = params(batch, 80, 256, bits=8, key_positions=key_positions)
+    new = np.where(np.arange(batch) % 3 == 2, 0, rng.integers(1, new_hi + 1, batch))
+    zero = np.zeros(batch, np.int64)
+    new[np.cumsum(-(-new // 16)) > 250] = 0
+    need = -(-new // 16)
+    at = np.cumsum(need) - need
+    free = rng.permutation(256)[:int(need.sum()) + 4]
+    bad = [0, int(np.argmax(np.where(np.arange(batch) > 0, need, 0)))]  # the first and the longest other
+    broken = free.copy()
+    broken[at[bad[0]]], broken[at[bad[1]] + need[bad[1]] - 1] = 256, -3
+    words = rng.integers(0, 1 << 31, (batch, 80)).astype(np.uint32)
+    rows = int(new.sum()) + room
+    want = list(A.append(new, zero, zero, zero, free, words, rows, max_blocks=80, id_bits=8, pool=256, doc=1024, key_positions=key_positions))
+    assert want[-1] == 0
+    for s in bad:  # as it was, but for its place in the list and among the rows
+        want[0][s], want[1][s], want[2][s] = words[s], 0, 0
+        want[6][want[4][s]:want[4][s + 1]], want[7][want[4][s]:want[4][s + 1]] = -1, 0
+    w, lens, pos, start = u32(words), i32(zero), i32(zero), i32(zero)
+    out = L.AppendTables.empty(p, rows).replace(seq_lens=lens, pos=pos)
+
+    def call(n, first):
+        L.append_tokens(p, i32(n), lens, pos, start, i32(broken), w, first_free=first, doc_tokens=1024, out=out)
+
+    call(new, None)
+    assert L.device_status(clear=True) == L.LAZY_DEV_BAD_BLOCK_ID
+    got = (w, out.seq_lens, out.pos, out.q_start, out.cu_rows, out.block_indptr, out.slots, out.local_pos)
+    for name, g, x in zip(("words", "seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos"), got, want):
+        assert np.array_equal(g.cpu().numpy(), np.ascontiguousarray(x).view(np.int32)), name
+    # the next call's tokens go into a block of the list's, not into the pool's last one
+    again = np.zeros(batch, np.int64)
+    again[bad[0]] = 2
+    call(again, out.block_indptr[-1:])
+    block = int(free[int(need.sum())])
+    assert L.device_status(clear=True) == 0 and out.slots[:2].tolist() == [16 * block, 16 * block + 1]
