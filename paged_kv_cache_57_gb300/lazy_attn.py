@@ -291,8 +291,9 @@ def pack_block_words(p: Params, num_docs: int, seg_indptr: torch.Tensor, seg_doc
 class AppendTables:
     """Outputs of append_tokens, int32 and contiguous, on one device: seq_lens, pos, q_start [B]; cu_rows, block_indptr
     [B + 1]; slots and local_pos (or None) with an entry for every row. A step's tables are made once and filled by every
-    call, so they are looked at here and not there."""
-    __slots__ = ("seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos", "rows", "num_seqs", "_ptrs")
+    call, so they are looked at here and not there. seq_lens, pos and q_start may be longer; the sums may not, since
+    their last entries are the batch's (block_indptr[-1:] is the next call's first_free)."""
+    __slots__ = ("seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos", "rows", "num_seqs", "_ptrs", "_sums")
 
     def __init__(self, seq_lens: torch.Tensor, pos: torch.Tensor, q_start: torch.Tensor, cu_rows: torch.Tensor,
                  block_indptr: torch.Tensor, slots: torch.Tensor, local_pos: Optional[torch.Tensor] = None):
@@ -300,6 +301,7 @@ class AppendTables:
         self.cu_rows, self.block_indptr, self.slots, self.local_pos = cu_rows, block_indptr, slots, local_pos
         self.rows = slots.numel()
         self.num_seqs = min(seq_lens.numel(), pos.numel(), q_start.numel(), cu_rows.numel() - 1, block_indptr.numel() - 1)
+        self._sums = max(cu_rows.numel(), block_indptr.numel()) - 1
         if local_pos is not None and local_pos.numel() != self.rows:
             raise ValueError("slots and local_pos must have as many rows")
         ptrs = []
@@ -351,6 +353,8 @@ def append_tokens(p: Params, new_lens: torch.Tensor, seq_lens: torch.Tensor, pos
         raise ValueError(f"out has {out.rows} rows, not {num_rows}")
     if out.num_seqs < b:
         raise ValueError(f"out has tables for {out.num_seqs} sequences, not {b}")
+    if out._sums != b:
+        raise ValueError(f"out's cu_rows and block_indptr must have {b + 1} entries: slices of them make tables for fewer sequences")
     if out._ptrs is None:
         raise ValueError("out must be CUDA tensors")
     if first_free is not None and first_free.numel() != 1:

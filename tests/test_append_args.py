@@ -1,6 +1,9 @@
 """CPU: arguments of append_tokens that are refused."""
 import ctypes
 
+import pytest
+import torch
+
 
 
 def _L():
@@ -21,3 +24,18 @@ def test_pos_out_in_the_place_of_another_tail_start():
     rc = L._lib.lazy_attn_append_tokens(ctypes.byref(_params()), new, lens, pos, start, free, 4, None, 16, 8, words, len_out, start, q_start, cu,
                                         indptr, slots, None, None)
     assert rc == L.LAZY_ERR_INVALID_ARG
+
+
+def test_sums_of_more_sequences_than_the_call_has():
+    # block_indptr[-1:] goes on where the call ended: an entry that the call does not write would hand blocks out twice
+    L = _L()
+    p, big = _params(), _params(num_seqs=3)
+    z = lambda n: torch.zeros(n, dtype=torch.int32)
+    args = dict(new_lens=z(2), seq_lens=z(2), pos=z(2), tail_start=z(2), free_blocks=z(9), block_words=z(8))
+    t = L.AppendTables.empty(big, 5, "cpu")
+    small = dict(cu_rows=t.cu_rows[:3], block_indptr=t.block_indptr[:3])
+    for out in (t, t.replace(cu_rows=t.cu_rows[:3]), t.replace(block_indptr=t.block_indptr[:3])):
+        with pytest.raises(ValueError, match="must have 3 entries"):
+            L.append_tokens(p, **args, out=out)
+    with pytest.raises(ValueError, match="CUDA"):  # on to the next check
+        L.append_tokens(p, **args, out=t.replace(**small))

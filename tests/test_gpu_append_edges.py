@@ -84,3 +84,17 @@ def test_bad_ids_of_a_full_field_add_nothing(batch, new_hi, room, key_positions)
     call(again, out.block_indptr[-1:])
     block = int(free[int(need.sum())])
     assert L.device_status(clear=True) == 0 and out.slots[:2].tolist() == [16 * block, 16 * block + 1]
+
+
+def test_a_smaller_batch_in_slices_of_the_tables_goes_on_in_the_list():
+    L = la()
+    big, p = params(5, 8, 40), params(2, 8, 40)
+    t = L.AppendTables.empty(big, 64)
+    z5, z2, free = i32([0] * 5), i32([0] * 2), i32(np.random.default_rng(2).permutation(40))
+    L.append_tokens(big, i32([17, 1, 16, 0, 3]), z5, z5, z5, free, u32(np.zeros((5, 8), np.uint32)), out=t)
+    taken = set((t.slots[:37] // 16).tolist())
+    assert int(t.block_indptr[-1]) == len(taken) == 5
+    first = t.block_indptr[-1:].clone()
+    t = t.replace(cu_rows=t.cu_rows[:3], block_indptr=t.block_indptr[:3])
+    L.append_tokens(p, i32([20, 2]), z2, z2, z2, free, u32(np.zeros((2, 8), np.uint32)), first_free=first, out=t)
+    assert int(t.block_indptr[-1]) == 8 and not taken & set((t.slots[:22] // 16).tolist()) and int(t.cu_rows[-1]) == 22
