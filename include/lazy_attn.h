@@ -555,7 +555,8 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * block's e before. Codes are x / 2^e to the nearest (ties to even, saturated at +-448); infinities
  * and NaN are written as NaN. The rows that the call does not write keep their codes, rounded again
  * where e grew (which changes a code only where it falls below e4m3's least normal number). A
- * block whose row 0 is written begins anew: its other rows, unless written too, are 0.
+ * block whose row 0 is written begins anew: its other rows, unless written too, are 0. So does one
+ * whose scale is no 2^e of that range, which no call wrote.
  * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
  * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale where that
  * is more (weights over the row's largest in the part). Sums and maxima are fp32. A warp adds up at

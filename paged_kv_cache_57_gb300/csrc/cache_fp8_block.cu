@@ -25,9 +25,9 @@ constexpr int kExpMin = -100, kExpMax = 119;  // 448 * 2^119 is bf16's last bina
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// e of a record's scale; what no call wrote is brought into range.
-__device__ __forceinline__ int exponent_of(float scale) {
-  return min(max((int)((__float_as_uint(scale) >> 23) & 255u) - 127, kExpMin), kExpMax);
+// Whether a record's scale is one that a write leaves: 2^e of the range. (A pool that nothing wrote holds anything.)
+__device__ __forceinline__ bool is_scale(uint32_t bits) {
+  return (bits & 0x7fffffu) == 0u && bits >> 23 >= (uint32_t)(kExpMin + 127) && bits >> 23 <= (uint32_t)(kExpMax + 127);
 }
 
 // The least e with m <= 448 * 2^e = 1.75 * 2^(e + 8), for bf16 bits m of a finite value >= 0.
@@ -116,8 +116,9 @@ __device__ __forceinline__ void write_run(const uint8_t* src, int64_t step, cons
       m = abs_max(m, x[n][i]);
     }
   }
-  const bool anew = rowmask & 1u;
-  const int e_old = anew ? kExpMin : exponent_of(*reinterpret_cast<const float*>(rec + G::SCALE));
+  const uint32_t was = rowmask & 1u ? 0u : *reinterpret_cast<const uint32_t*>(rec + G::SCALE);
+  const bool anew = !is_scale(was);
+  const int e_old = anew ? kExpMin : (int)(was >> 23) - 127;
   m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
   if (m >= 0x7f80u) {  // infinities and NaN do not count, and are written as NaN
     m = 0u;
