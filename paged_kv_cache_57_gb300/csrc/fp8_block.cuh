@@ -354,11 +354,11 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const F
       }
   }
 
-  // Weights, their sum in fp32, and weights (rounded to f16: off by 2^-11, next to the codes' 4 bits)
-  // times V's scale over its reference, a power of two. The k-order of O^T += C_v^T P^T is tokens
+  // Weights, their sum in fp32, and weights times V's scale over its reference, a power of two, rounded to f16 once
+  // (off by 2^-11, next to the codes' 4 bits). The k-order of O^T += C_v^T P^T is tokens
   // 2t, 2t + 1 (b0), 2t + 8, 2t + 9 (b1).
   uint32_t pb[NT][2];
-  const __half2 v_scale = __float2half2_rn(vs * st.inv);
+  const float v_scale = vs * st.inv;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -371,8 +371,8 @@ __device__ __forceinline__ void fp8_attend(const uint8_t* stage, int nv, const F
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const __half2 w = __hmul2(__floats2half2_rn(p[nt][2 * r], HL == 1 ? 0.f : p[nt][2 * r + 1]), v_scale);
-      pb[nt][r] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&w));
+      const float2 w = HL == 1 ? make_float2(p[nt][2 * r] * v_scale, 0.f) : f2_split(f2_mul(pair(nt, r), f2(v_scale, v_scale)));
+      pb[nt][r] = transpose_8x8(pack_f16x2(w.x, w.y));
     }
   }
 

@@ -48,3 +48,39 @@ def test_writes_behind_row_0_of_blocks_that_nothing_wrote(hkv, d, docs):
         scatter(slots, y, src, is_v)
         y[untouched] = old[untouched]
         same_records(x, y, d)
+
+
+# Weights times V scales are rounded once: a block of weight 1 whose scale is 2^-25 of the part's largest (the least step of
+# f16 is 2^-24) keeps its values. All scores are 0, so that every weight is 1; the header's bound on a product that is rounded to
+# f16 is 2^-11 of it, or 2^-29 of the largest scale. Codes are whole powers of two: with weights and scales they are exact, and so are
+# the sums. A warp's part has the blocks of both scales (one warp: one split of at most 4 blocks a warp).
+@pytest.mark.parametrize("hq", [4, 8, 16, 32])
+@pytest.mark.parametrize("down", [14, 20, 24, 25, 27])
+@pytest.mark.parametrize("shared", [False, True])
+def test_small_v_scales_beside_large_ones(hq, down, shared):
+    L = la()
+    d, nb = 128, 8
+    p = L.make_params(num_seqs=1, num_q_heads=hq, num_kv_heads=1, head_dim=d, num_pool_blocks=nb, max_blocks_per_seq=nb, kv_dtype="fp8_e4m3_block",
+                      num_splits=1)
+    kp, vp = L.empty_pools(p)
+    k = torch.zeros(16 * nb, 1, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    big = torch.arange(16 * nb, device="cuda") // 16 % 2 == 0
+    v[big, 0, 0] = 256.0                   # scale 1, in the first dim
+    v[~big, 0, 1:] = 256.0 * 2.0 ** -down  # scale 2^-down, in the others
+    L.cache_write(p, k, v, torch.arange(16 * nb, dtype=torch.int32, device="cuda"), kp, vp)
+    q = torch.zeros(1, hq, d, dtype=torch.bfloat16, device="cuda")
+    words = torch.arange(nb, dtype=torch.int32, device="cuda")[None].contiguous()
+    lens = torch.tensor([16 * nb], dtype=torch.int32, device="cuda")
+    rope = L.rope_table_init(p)
+    if shared:
+        one = np.array([0, 1], np.int32)
+        items, slots = L.plan_shared_host(p, 1, one, [0], [16 * nb], [0, nb], np.arange(nb, dtype=np.int32), chunk_blocks=nb)
+        out = L.decode_shared(p, q, kp, vp, words, lens, rope, L.SharedPlan(items, slots))
+    else:
+        out = L.decode(p, q, kp, vp, words, lens, lens, rope)
+    out = out.double()[0]
+    assert (out[:, 0] == 128).all()
+    want = 128 * 2.0 ** -down
+    # half of the keys have a weight of 1 and a product that is off by 2^-29 at most (f16's least step: 2^-25 with weights of 2^4), times 256
+    assert ((out[:, 1:] - want).abs() <= 128 * 2.0 ** -29 + 2.0 ** -8 * want).all(), out[0, 1].item() / want
