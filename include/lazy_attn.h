@@ -559,7 +559,10 @@ int lazy_attn_mixed(const lazy_attn_params *p_dec, const void *q_dec, const uint
  * whose scale is no 2^e of that range, which no call wrote.
  * The decodes on them (at most 65535 KV heads) round rotated queries to f16 (2^-11 of each), and
  * weight times V scale: to 2^-11 of the product, or to 2^-29 of the part's largest V scale where that
- * is more (weights over the row's largest in the part). Sums and maxima are fp32. A warp adds up at
+ * is more (weights over the row's largest in the part). Sums and maxima are fp32. The products' sums are
+ * truncated, by up to 2^-23 of the sum a block that a warp takes: over 512 blocks at most in
+ * lazy_attn_decode, and over an item's blocks in lazy_attn_decode_shared (with up to 16 query rows a
+ * quarter of them, with up to 32 half); lengths that the planner chooses have 384 at most. A warp adds up at
  * most 16384 blocks: lazy_attn_decode cuts longer sequences whatever num_splits says (with num_splits
  * 1 too tables of more than 65536 blocks take a workspace), lazy_attn_plan_shared_host limits
  * chunk_blocks to that, and an item of more blocks sets LAZY_DEV_LAYOUT and leaves its slots as they

@@ -51,7 +51,8 @@ struct Fp8Cfg {
 // ------------------------------------------------------------------ per sequence
 // A unit is a sequence, a KV head and a tile of 4, 8, 16 or 32 of its query heads; the units
 // are cut into pieces or ranges (decode_units.cuh). Of a part each warp takes a quarter, by itself.
-template <int D, int NT, int HL, bool LAZY>
+// LONG: a warp may have more than kFp8Keep blocks of a part.
+template <int D, int NT, int HL, bool LAZY, bool LONG>
 __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_block_kernel(const UnitDecodeArgs a) {
   using C = Fp8Cfg<D, NT, HL>;
   constexpr int HALF = D / 2, R = C::RING;
@@ -156,26 +157,35 @@ __global__ void __launch_bounds__(kThreads, Fp8Cfg<D, NT, HL>::CTAS) decode_fp8_
     Fp8State<D, NT, HL> st;
     fp8_init(st);
     bool ok = true;
-    for (int i = 0; i < nk; ++i) {
-      const uint32_t n_th = used + i, slot = n_th % R;
-      if (PAIR == 1 || (i % 2 == 0 && i > 0)) fill(i + AHEAD);
-      ok = ring.wait_full(slot, n_th / R & 1, a.status);
-      if (!ok) {
-        ring.drain(n_th, used + min(nk, i + R), R, a.status);
-        break;
-      }
-      const int info = bars.info[warp * R + slot];
-      int nv = kBlock;
-      if (info != kBlock) {
-        nv = info & 31;
-        if (LAZY && info > kNewDoc) {
-          const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
-          if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
+    Fp8Kept<D, NT, HL> kept;  // (LONG)
+    kept.any = false;
+    int i = 0;
+#pragma unroll 1
+    for (int end = LONG ? min(nk, kFp8Keep) : nk;; end = min(nk, end + kFp8Keep)) {
+      for (; i < end; ++i) {
+        const uint32_t n_th = used + i, slot = n_th % R;
+        if (PAIR == 1 || (i % 2 == 0 && i > 0)) fill(i + AHEAD);
+        ok = ring.wait_full(slot, n_th / R & 1, a.status);
+        if (!ok) {
+          ring.drain(n_th, used + min(nk, i + R), R, a.status);
+          break;
         }
+        const int info = bars.info[warp * R + slot];
+        int nv = kBlock;
+        if (info != kBlock) {
+          nv = info & 31;
+          if (LAZY && info > kNewDoc) {
+            const int p = decode_word(wrow[kb0 + i], kb0 + i, a.id_bits).p;
+            if (p != p_cur) rebuild(a.q_pos[s] - (p_cur = p));
+          }
+        }
+        if (nv > 0) fp8_attend<D, NT, HL>(ring.base + slot * C::SLOT, nv, q, st, lane);
+        __syncwarp();  // the stage is free
       }
-      if (nv > 0) fp8_attend<D, NT, HL>(ring.base + slot * C::SLOT, nv, q, st, lane);
-      __syncwarp();  // the stage is free
+      if (!LONG || !ok || end == nk) break;
+      kept.keep(st);
     }
+    if (LONG) kept.give_back(st);
     used += nk;
     fp8_finish(st);
     __syncthreads();  // every warp is done with its ring: the merge takes its place
@@ -463,23 +473,28 @@ UnitPlan plan_decode_fp8_block(int B, int G, int Hkv, int max_blocks, int num_sp
                     kWarps * kFp8MaxRun);
 }
 
-template <int D, int NT, int HL, bool LAZY>
+template <int D, int NT, int HL, bool LAZY, bool LONG>
 static cudaError_t launch_decode_t(const UnitDecodeArgs& a, cudaStream_t st) {
   using C = Fp8Cfg<D, NT, HL>;
   constexpr int SMEM = C::BUF + kWarps * ((D / 2) * 8 + Fp8Query<D, NT, HL>::BYTES);
-  cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, LAZY>>(SMEM);
+  cudaError_t e = set_smem_once<decode_fp8_block_kernel<D, NT, HL, LAZY, LONG>>(SMEM);
   if (e != cudaSuccess) return e;
-  return launch_behind(decode_fp8_block_kernel<D, NT, HL, LAZY>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
+  return launch_behind(decode_fp8_block_kernel<D, NT, HL, LAZY, LONG>, (unsigned)a.plan.ctas, kThreads, SMEM, st, a);
+}
+
+template <int D, bool LAZY, bool LONG>
+static cudaError_t launch_decode_l(const UnitDecodeArgs& a, cudaStream_t st) {
+  switch (a.plan.rows) {
+    case 4: return launch_decode_t<D, 1, 1, LAZY, LONG>(a, st);
+    case 8: return launch_decode_t<D, 1, 2, LAZY, LONG>(a, st);
+    case 16: return launch_decode_t<D, 2, 2, LAZY, LONG>(a, st);
+    default: return launch_decode_t<D, 4, 2, LAZY, LONG>(a, st);
+  }
 }
 
 template <int D, bool LAZY>
 static cudaError_t launch_decode_d(const UnitDecodeArgs& a, cudaStream_t st) {
-  switch (a.plan.rows) {
-    case 4: return launch_decode_t<D, 1, 1, LAZY>(a, st);
-    case 8: return launch_decode_t<D, 1, 2, LAZY>(a, st);
-    case 16: return launch_decode_t<D, 2, 2, LAZY>(a, st);
-    default: return launch_decode_t<D, 4, 2, LAZY>(a, st);
-  }
+  return longest_part(a.plan, a.B, a.max_blocks) > kWarps * kFp8Keep ? launch_decode_l<D, LAZY, true>(a, st) : launch_decode_l<D, LAZY, false>(a, st);
 }
 
 cudaError_t launch_decode_fp8_block(const UnitDecodeArgs& a, bool lazy, cudaStream_t st) {

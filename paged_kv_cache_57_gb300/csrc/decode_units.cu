@@ -162,6 +162,12 @@ UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, 
   return p;
 }
 
+int64_t longest_part(const UnitPlan& p, int B, int max_blocks) {
+  if (p.range_ctas == 0) return ((int64_t)max_blocks + p.splits - 1) / p.splits;
+  const int64_t chunk = ((int64_t)B * p.units * max_blocks + p.range_ctas - 1) / p.range_ctas;
+  return std::max<int64_t>(kMaxPiece, std::min<int64_t>(max_blocks, chunk));
+}
+
 size_t unit_workspace_bytes(const UnitPlan& p, int B, int D) {
   if (p.parts == 0) return 0;
   return (size_t)2 * p.parts * p.rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(int64_t);

@@ -45,6 +45,12 @@ struct Fp8Bars {
   int info[kFp8Slots];
 };
 
+// A wait gave up: copies of the loads first .. last - 1 (counted through the ring of R) still land, or not within
+// 10 ms each, before the CTA ends. (By value: a ring whose address is taken lies in memory.)
+static __device__ __noinline__ void fp8_drain(uint64_t* full, uint32_t first_load, uint32_t last_load, uint32_t R, unsigned int* status) {
+  for (uint32_t n = first_load; n < last_load; ++n) warp_wait(&full[n % R], n / R & 1, status, 10000000ull);
+}
+
 template <int D>
 struct Fp8Ring {
   using G = Fp8Geom<D>;
@@ -74,10 +80,8 @@ struct Fp8Ring {
   __device__ __forceinline__ bool wait_empty(int slot, uint32_t parity, unsigned int* status) const {
     return warp_wait(&bars->empty[first + slot], parity, status);
   }
-  // A wait gave up: copies of the loads first .. last - 1 (counted through the ring of R) still land, or not within
-  // 10 ms each, before the CTA ends.
-  __device__ __noinline__ void drain(uint32_t first_load, uint32_t last_load, uint32_t R, unsigned int* status) const {
-    for (uint32_t n = first_load; n < last_load; ++n) warp_wait(&bars->full[first + n % R], n / R & 1, status, 10000000ull);
+  __device__ __forceinline__ void drain(uint32_t first_load, uint32_t last_load, uint32_t R, unsigned int* status) const {
+    fp8_drain(&bars->full[first], first_load, last_load, R, status);
   }
   __device__ __forceinline__ void release(int slot) const { mbar_arrive(&bars->empty[first + slot]); }
 };
@@ -225,9 +229,64 @@ __device__ __forceinline__ void fp8_init(Fp8State<D, NT, HL>& st) {
   st.lim = -1.f;
 }
 
-// The products truncate their running sums (2^-24 each time, always towards zero): after
-// kFp8MaxRun = 16384 blocks a sum is off by 2^-11 or so of its size, a quarter of the output's
-// rounding. No warp sums more: pieces, ranges and items are cut there.
+// The products truncate their running sums (by up to 2^-23 a block, always towards zero). In lazy_attn_decode a warp's sums
+// leave the accumulators every kFp8Keep blocks (2^-14 at most by then) for local memory, where they are added with rounding,
+// and their references with them; registers hold no second set. The kernel for parts that long is one of its own: with the way
+// out in the others' code one sequence of 16384 tokens took 14.2 us for 13.6, and shared items 120 for 112 (32 x 16384 tokens), which
+// keep theirs: of the lengths that the planner takes (384 blocks at most) 2^-14. No warp sums more than kFp8MaxRun = 16384 blocks:
+// pieces, ranges and items are cut there. 16 sequences of 262144 tokens: 32 heads on 8 1242 us for 1230 without the way
+// out, 64 on 4 662 for 623 (its registers spill); 48 with 32 on one 714 for 705.
+constexpr int kFp8Keep = 512;
+template <int D, int NT, int HL>
+struct Fp8Kept {
+  static constexpr int SUMS = D / 16 * NT * 2 * HL;  // (HL = 1: of the columns that count)
+  volatile float o[SUMS], nm[NT * HL], inv;          // volatile: stays in memory
+  bool any;
+
+  // f(sum, place, row's tile, row).
+  template <typename Fn>
+  static __device__ __forceinline__ void each(Fp8State<D, NT, HL>& st, Fn f) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < HL; ++c) f(st.o[i][nt][2 * h + c], ((i * NT + nt) * 2 + h) * HL + c, nt, c);
+  }
+  // What the kept sums weigh by the state's references, per row.
+  __device__ __forceinline__ void weights(const Fp8State<D, NT, HL>& st, float (&w)[NT][HL]) const {
+    const float r = st.inv / inv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < HL; ++c) w[nt][c] = fast_ex2(st.nm[nt][c] - nm[nt * HL + c]) * r;
+  }
+  __device__ __forceinline__ void keep(Fp8State<D, NT, HL>& st) {
+    if (st.lim < 0.f) return;  // no block yet (the same in all lanes)
+    if (any) {
+      float w[NT][HL];
+      weights(st, w);
+      each(st, [&](float& x, int n, int nt, int c) { o[n] = fmaf(o[n], w[nt][c], x), x = 0.f; });
+    } else {
+      each(st, [&](float& x, int n, int, int) { o[n] = x, x = 0.f; });
+    }
+    any = true;
+    inv = st.inv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < HL; ++c) nm[nt * HL + c] = st.nm[nt][c];
+  }
+  // And back, at the end.
+  __device__ __forceinline__ void give_back(Fp8State<D, NT, HL>& st) const {
+    if (!any) return;
+    float w[NT][HL];
+    weights(st, w);
+    each(st, [&](float& x, int n, int nt, int c) { x = fmaf(o[n], w[nt][c], x); });
+  }
+};
 
 // A block in its stage: the first nv slots are keys (1 .. 16, the same in all lanes); what the others hold does not
 // matter.

@@ -337,6 +337,8 @@ struct UnitDecodeArgs : DecodeArgs {
 // num_splits > 0: that many pieces of every unit (fewer of a sequence with fewer blocks); else chosen
 // for the device's `resident` CTAs. No piece or range has more than `most` blocks.
 UnitPlan plan_units(int B, int rows, int units, int max_blocks, int num_splits, int64_t resident, int least_log2, int most = 1 << 30);
+// Blocks of a piece or range at most.
+int64_t longest_part(const UnitPlan& plan, int B, int max_blocks);
 // a.ws_o: [2 parts][rows][D], a.ws_ml: [2 parts][rows][2], then a.prefix, where there are parts.
 size_t unit_workspace_bytes(const UnitPlan& plan, int B, int D);
 cudaError_t launch_combine_units(const UnitDecodeArgs& a, cudaStream_t st);
