@@ -1,11 +1,14 @@
-"""GPU: tables of new tokens where the arrays of a call are one another's, or end beside one another."""
+"""GPU: tables of new tokens where the arrays of a call are one another's, end beside one another or hold bad ids, and a server's
+steps against what its pools hold."""
 import numpy as np
 import pytest
 import torch
 
 import append_model as A
+import fp8_block_model as M
 from gpu_util import la
-from test_gpu_append import i32, params, u32
+from test_gpu_append import THETA, Server, i32, params, u32
+from test_gpu_fp8_block import check, same_records, scatter
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +101,86 @@ def test_a_smaller_batch_in_slices_of_the_tables_goes_on_in_the_list():
     t = t.replace(cu_rows=t.cu_rows[:3], block_indptr=t.block_indptr[:3])
     L.append_tokens(p, i32([20, 2]), z2, z2, z2, free, u32(np.zeros((2, 8), np.uint32)), first_free=first, out=t)
     assert int(t.block_indptr[-1]) == 8 and not taken & set((t.slots[:22] // 16).tolist()) and int(t.cu_rows[-1]) == 22
+
+
+class Held:
+    """What fp8_block_model.attention asks of a workload, of a server's sequences: documents of srv.doc tokens behind one another."""
+
+    def __init__(self, srv, words, lens, q):
+        self.num_seqs, self.num_q_heads, self.num_kv_heads, self.head_dim, self.rope_theta = srv.batch, srv.hq, srv.hkv, srv.d, THETA
+        self.q, self.q_pos, self.seq_pos0 = q, lens, np.zeros(srv.batch, np.int64)
+        ids = words & (1 << 18) - 1
+        self.segs, self.doc_blocks, self.doc_block_indptr = [], [], [0]
+        for s, n in enumerate(lens):
+            self.segs.append([])
+            for a in range(0, int(n), srv.doc):
+                self.segs[s].append((len(self.doc_block_indptr) - 1, min(srv.doc, int(n) - a)))
+                self.doc_blocks += ids[s, a // 16:-(-min(int(n), a + srv.doc) // 16)].tolist()
+                self.doc_block_indptr.append(len(self.doc_blocks))
+        self.doc_blocks = np.array(self.doc_blocks)
+
+    def seq_segments(self, s):
+        return self.segs[s]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_captured_steps_against_what_the_pools_hold(d):
+    # tables, records and both decodes of every step: tables against the model of them, records byte for byte, outputs within the
+    # elementwise bound of 64-bit attention over the records' values
+    L = la()
+    batch, cap = 5, 300
+    srv = Server("fp8_e4m3_block", batch, d, cap, 60)
+    g = torch.Generator("cuda").manual_seed(17)
+    words, lens, free = np.zeros((batch, 60), np.uint32), np.zeros(batch, np.int64), srv.free.cpu().numpy()
+    pools, first, start = [x.cpu().numpy() for x in srv.pools], 0, np.zeros(batch, np.int64)
+    q_in = torch.zeros(batch, 8, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q_in)
+    ws = torch.empty(max(256, L.decode_workspace_bytes(srv.p)), dtype=torch.uint8, device="cuda")
+
+    def step():
+        srv.step()
+        srv.attend(q_in, out, ws)
+
+    def follow(new, run):
+        nonlocal words, lens, first
+        srv.new.copy_(i32(new))
+        srv.rows(new, g)
+        q_in.copy_(torch.randn(batch, 8, d, generator=g, device="cuda").to(torch.bfloat16))
+        run()
+        want = A.append(new, lens, lens, start, free, words, cap, max_blocks=60, id_bits=18, pool=400, first=first, doc=srv.doc)
+        assert want[-1] == 0
+        for name, got, x in zip(("words", "seq_lens", "pos", "q_start", "cu_rows", "block_indptr", "slots", "local_pos"), (srv.words, *srv.out), want):
+            assert np.array_equal(got.cpu().numpy(), np.ascontiguousarray(x).view(np.int32)), name
+        words, lens, first = want[0], want[1].astype(np.int64), int(want[5][-1])
+        total = int(sum(new))
+        for x, y, rows, is_v in zip(srv.pools, pools, (srv.k, srv.v), (False, True)):
+            scatter(want[6][:total], y, rows[:total].cpu(), is_v)
+            same_records(x, y, d)
+
+    def attention():
+        values = [torch.from_numpy(np.nan_to_num(M.values(y, d, is_v))).cuda() for y, is_v in zip(pools, (False, True))]
+        w = Held(srv, words, lens, q_in)
+        return w, M.attention(w, *values)
+
+    follow([100, 1, 64, 16, 0], step)
+    want, bound = attention()[1]
+    check(out[:4], (want[:4], bound[:4]), "prompts")
+    assert not out[4].any()  # a sequence without a token
+    srv.new.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(24):
+        follow([(i + s) % 4 if s < 4 else 1 for s in range(batch)], graph.replay)
+        w, ref = attention()
+        check(out, ref, f"step {i}")
+    docs = [n for s in range(batch) for _, n in w.segs[s]]
+    seg = np.cumsum([0] + [len(s) for s in w.segs])
+    items, slots = L.plan_shared_host(srv.p, len(docs), seg, np.arange(len(docs)), docs, w.doc_block_indptr, w.doc_blocks)
+    two = L.decode_shared(srv.p, q_in, *srv.pools, srv.words, srv.pos, srv.rope, L.SharedPlan(items, slots))
+    check(two, ref, "shared")
