@@ -238,8 +238,9 @@ int lazy_attn_pack_block_words(const lazy_attn_params *p, int32_t num_docs, cons
                                uint32_t *block_words, int32_t *seq_lens, lazy_stream_t stream);
 
 /* ---------------------------------------------------------------- room for new tokens
- * The tables of a step, from the sequences' lengths alone and on the device: a captured step
- * needs no host in between. Every sequence s gets new_lens[s] tokens (a prompt, a chunk of one,
+ * The tables of a step, from the sequences' lengths alone and on the device: a captured step of these
+ * tables, the pool writes and lazy_attn_decode needs no host in between (the shared-run decode's plan is the
+ * host's). Every sequence s gets new_lens[s] tokens (a prompt, a chunk of one,
  * a decoded token, drafts; 0: none) behind what it holds. Its own tokens start at position
  * tail_start[s] and lie in blocks of their own, behind the blocks of the documents that it cites:
  * token i of them (position tail_start[s] + i) is row i % 16 of logical block b0 + i / 16, where
@@ -321,9 +322,10 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  * or, for R = 128 and for pools of records (int4, e4m3 with block scales), about one item per
  * resident CTA (2 x 152 / num_kv_heads items, int4: 4 x 152 / num_kv_heads, e4m3 with block
  * scales: 3 x 152 / num_kv_heads): the sets' blocks summed, divided
- * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. For e4m3 with block scales a block of a
- * set of more than 16 rows counts as two, of more than 32 as four, and the length of such a set's
- * chunks is that part of 16 .. 256; a document is cut into equal chunks of about that length. It writes
+ * by that count, rounded up to a multiple of 4 and kept within 32 .. 256. For e4m3 with block scales a set has a
+ * weight w: 1 up to 16 query rows, 2 up to 32, else 4. The blocks are summed times w, that sum over the
+ * count is divided by w again, rounded up to a multiple of 4 and kept within 16 / w .. 256; and a document is cut
+ * into equal chunks, as many as bring them nearest to that length (up to half as long again). It writes
  *   items_host [num_items][LAZY_PLAN_ITEM_INTS] int32, one work item each:
  *     [0] src_seq, [1] b0, [2] nblk, [3] last_valid, [4] nmem, [5] c0, [6..7] 0:
  *         nblk logical blocks of sequence src_seq from block b0, all full but
@@ -341,7 +343,8 @@ int lazy_attn_decode(const lazy_attn_params *p, const void *q, const void *k_poo
  *     slot_indptr[s+1]-1;
  *   counts_host [2] = {num_items, num_slots}.
  * Items are ordered by decreasing block count, for pools of records times 1, 2 or 4 for up to 8,
- * up to 16 or more query rows (ties in the order of first appearance of their document).
+ * up to 16 or more query rows (ties in the order of first appearance of their document). For e4m3 with block scales
+ * the items of more than half the longest one's blocks come first, taken from the two ends of that order in turn.
  * `capacity` bounds the item count (the number
  * of logical blocks in the batch always suffices). Returns LAZY_ERR_LAYOUT on the
  * packer's layout errors, and LAZY_ERR_WORKSPACE if capacity is too small.

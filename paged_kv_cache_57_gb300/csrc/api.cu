@@ -574,11 +574,11 @@ int lazy_attn_plan_shared_host(const lazy_attn_params* p, int32_t num_docs, cons
   if (c.G > 64) return LAZY_ERR_UNSUPPORTED;
   // quantised pools run on mma.sync kernels (items of at most 64 rows) at every ratio
   const int cap = kv_quantised(p) ? 64 : lazy::shared_rows_cap(c.G, p->head_dim);
-  // 0: 32 blocks for the bf16 and e4m3 mma.sync kernel; for the tensor-core kernel and int4
-  // pools, a length that gives about one item per resident CTA. int4 (8 KV heads, 64-block
+  // 0: 32 blocks for the bf16 and e4m3 mma.sync kernel; for the tensor-core kernel and pools of
+  // records, a length that gives about one item per resident CTA (shared_plan.cu). int4 (8 KV heads, 64-block
   // documents): 136 us against 156 with 32 blocks and 218 with 16; 8 sequences of 256-block
   // documents 45 against 44, 52 with 16, 108 with 256.
-  const int most = kv_fp8_block(p) ? lazy::kFp8MaxRun : INT_MAX;
+  const int most = kv_fp8_block(p) ? lazy::kFp8MaxRun : INT_MAX;  // blocks that a warp may add up
   const int cb = chunk_blocks > 0 ? std::min(chunk_blocks, most) : (cap == 128 || kv_records(p) ? 0 : 32);
   const int slots = kv_int4(p) ? lazy::kSharedInt4Slots : kv_fp8_block(p) ? lazy::kSharedFp8BlockSlots : lazy::kSharedTcSlots;
   const int auto_items = std::max(1, slots / std::max(1, p->num_kv_heads));

@@ -343,7 +343,8 @@ def append_tokens(p: Params, new_lens: torch.Tensor, seq_lens: torch.Tensor, pos
                   stream=None) -> AppendTables:
     """Room for new_lens[s] tokens behind every sequence (lazy_attn_append_tokens): words of the blocks taken from
     free_blocks into block_words, and lengths, positions, row offsets and slots of num_rows rows (or of ``out``'s), whose
-    seq_lens and pos may be the inputs themselves. ``first_free`` is an earlier call's block_indptr[-1:]."""
+    seq_lens and pos may be the inputs themselves (tail_start may be pos, too). ``first_free`` is an earlier call's
+    block_indptr[-1:]."""
     b = p.num_seqs
     if out is None:
         if num_rows is None:
@@ -608,7 +609,9 @@ def token_slots(blocks, first: int, count: int) -> np.ndarray:
 def cache_write(p: Params, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pool: torch.Tensor,
                 v_pool: torch.Tensor, stream=None) -> None:
     """Writes rows k, v [T, Hkv, d] (any token and head strides, d contiguous) into the slots
-    [T] int32 of the pools, in the pools' type (lazy_attn_cache_write)."""
+    [T] int32 of the pools, in the pools' type (lazy_attn_cache_write). With "fp8_e4m3_block" the tokens
+    that go into one block lie within 32 consecutive entries of slots, as append_tokens leaves them and
+    the tokens of a document in their order do; nothing tells of others, whose records are unspecified."""
     dt, shape = _tdt(p), (slots.numel(), p.num_kv_heads, p.head_dim)
     if not (k.is_cuda and v.is_cuda) or k.dtype != dt or v.dtype != dt:
         raise ValueError(f"k and v must be {dt} CUDA tensors")
