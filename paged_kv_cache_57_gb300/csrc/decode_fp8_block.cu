@@ -10,12 +10,12 @@
 // instructions and their addresses in every lane, took 94 us where these take 86.
 //
 // Measured (8 KV heads of 128 dims unless said; calls in a row). Per sequence: 64 of 4096 tokens, 32 heads, 545 MB,
-// 86 us, 6.3 TB/s: memory; one of 16384, 64 heads, 13.5 us: the chain of a piece, the join and two
-// launches; 48 of 256 to 131072, 32 heads on one, 829 MB, 230 us, 3.6 TB/s: instructions. There an
+// 85 us, 6.4 TB/s: memory; one of 16384, 64 heads, 13.7 us: the chain of a piece, the join and two
+// launches; 48 of 256 to 131072, 32 heads on one, 829 MB, 227 us, 3.6 TB/s: instructions. There an
 // mma.sync m16n8k16 holds its scheduler for 8 cycles, so that a block of 32 rows costs an SM 144 cycles of products
 // beside 116 of softmax and loop, for 180 of memory. Shared runs: 64 sequences of 4096 tokens, Zipf-drawn, 48 us
 // for 151 MB, of which the prologue of an item (record, members, angles, queries) and the join are about
-// 12; 32 of 16384, 64 heads, 112 us for 386 MB: alone, items of up to 16 rows take 68 us, bound by
+// 12 (the rest was not taken apart); 32 of 16384, 64 heads, 112 us for 386 MB: alone, items of up to 16 rows take 68 us, bound by
 // memory, the wider ones 71, by instructions.
 #include <algorithm>
 #include <climits>
