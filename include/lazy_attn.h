@@ -252,7 +252,8 @@ int lazy_attn_pack_block_words(const lazy_attn_params *p, int32_t num_docs, cons
  *   pos         [B] position of the next token: tail_start plus the sequence's own tokens so far
  *   tail_start  [B]; = pos: its own tokens begin with this call, in a fresh block (a prefill
  *               chunk, which has to be a document of its own, is given that way, with
- *               doc_tokens 0 or at least its length). May be the array pos itself, pos_out too
+ *               doc_tokens 0 or at least its length). May be the array pos itself, pos_out too,
+ *               but not another one that the call writes
  *   free_blocks [num_free] physical ids; the call takes them in order from index *first_free
  *               (device; NULL: 0), sequence by sequence, one as a token enters its row 0
  *   block_words [B][max_blocks_per_seq]: the words of the blocks taken are written (in either

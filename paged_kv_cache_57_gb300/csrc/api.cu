@@ -398,7 +398,9 @@ int lazy_attn_append_tokens(const lazy_attn_params* p, const int32_t* new_lens, 
   if (!cu_rows || !block_indptr || (num_free > 0 && !free_blocks) || (num_rows > 0 && !slots)) return LAZY_ERR_INVALID_ARG;
   if (p->num_seqs > 0 && (!new_lens || !seq_lens || !pos || !tail_start || !block_words || !seq_lens_out || !pos_out || !q_start))
     return LAZY_ERR_INVALID_ARG;
-  if (p->num_seqs > 0 && pos_out == tail_start && pos != tail_start) return LAZY_ERR_INVALID_ARG;
+  // the rows' launch reads tail_start behind the one that writes the lengths; where it was pos, q_start has its values
+  if (p->num_seqs > 0 && ((pos_out == tail_start && pos != tail_start) || (seq_lens_out == tail_start && pos_out != tail_start)))
+    return LAZY_ERR_INVALID_ARG;
   unsigned int* st = status_ptr();
   if (!st) return LAZY_ERR_CUDA;
   lazy::AppendArgs a{new_lens, seq_lens, pos, tail_start, free_blocks, first_free, block_words, seq_lens_out, pos_out, q_start,

@@ -18,12 +18,14 @@ def _params(**kw):
     return _L().make_params(**{**base, **kw})
 
 
-def test_pos_out_in_the_place_of_another_tail_start():
+def test_lengths_in_the_place_of_tail_start():
+    # but for pos itself, whose old values the call keeps in q_start
     L = _L()
-    new, lens, pos, start, free, words, len_out, q_start, cu, indptr, slots = (ctypes.c_void_p(1 << 20 | i << 12) for i in range(11))
-    rc = L._lib.lazy_attn_append_tokens(ctypes.byref(_params()), new, lens, pos, start, free, 4, None, 16, 8, words, len_out, start, q_start, cu,
-                                        indptr, slots, None, None)
-    assert rc == L.LAZY_ERR_INVALID_ARG
+    new, lens, pos, start, free, words, len_out, pos_out, q_start, cu, indptr, slots = (ctypes.c_void_p(1 << 20 | i << 12) for i in range(12))
+    for l, p in ((len_out, start), (start, pos_out), (start, pos)):
+        rc = L._lib.lazy_attn_append_tokens(ctypes.byref(_params()), new, lens, pos, start, free, 4, None, 16, 8, words, l, p, q_start, cu,
+                                            indptr, slots, None, None)
+        assert rc == L.LAZY_ERR_INVALID_ARG
 
 
 def test_sums_of_more_sequences_than_the_call_has():
